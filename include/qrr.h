@@ -322,6 +322,83 @@ qrr_status qrr_attention_decode_fp8(const void* q, int32_t B, int32_t Hq, int32_
                                     size_t workspace_bytes, int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* NVFP4 key/value cache in pages, and attention over it ("QeRL: Beyond
+ * Efficiency", abstract: NVFP4 for rollout; "NVIDIA NeMo RL behaalt 48% ...",
+ * section "Praktische prestatiewinsten": low precision extended to the KV
+ * cache and the attention operations).  The pages of the sources give no
+ * format for a 4-bit cache; it takes the weights' NVFP4 layout above, one
+ * cached row (one token, one KV head) at a time.
+ *
+ * qrr_kv_nvfp4 describes a cache; it is a HOST struct, read during the call.
+ *   k_codes, v_codes    uint8 [num_pages][Hkv][page][D/2], E2M1 codes, even
+ *                       index in the low nibble
+ *   k_scales, v_scales  uint8 [num_pages][Hkv][page][D/16], E4M3 bytes
+ *   k_gs, v_gs          fp32 [Hkv] global scales (> 0; they take the place of a
+ *                       weight's tensor scale), or NULL for 1.  The caller
+ *                       picks them (an absmax / 2688 seen so far, say): a
+ *                       block whose absmax exceeds 2688 gs saturates.
+ *   page_table          int32 [B][max_pages]: token p of sequence b is slot
+ *                       p % page of page page_table[b][p / page].  Sequences
+ *                       may share pages that none of them writes.
+ *   D                   64 or 128;  page a power of two, at least 16
+ * Element: e2m1(code) * e4m3(scale) * gs.
+ *
+ * Rows of a call.  cu int32 [B + 1], ascending, or NULL: sequence b brings the
+ * rows cu[b] .. cu[b + 1] - 1 of the call's T rows (NULL: T = B, one row
+ * each); row cu[b] + i stands at position pos[b] + i (pos int32 [B]).  A
+ * position below 0 is no token: nothing is written, zeros are read, its
+ * attention sees nothing.  Rows outside cu[0] .. cu[B] - 1 are left alone.  A
+ * position at or above max_pages * page, a page number outside
+ * [0, num_pages) or offsets that leave [0, T] raise QRR_DEV_BAD_INDEX; such a
+ * row is not written to the cache, and reads zeros.  T <= 2^30 and
+ * max_pages * page <= 2^30.
+ *
+ * qrr_kv_append_nvfp4: quantizes rows k_new, v_new (bf16, row t at base + t ld
+ * elements, Hkv heads of D values, ld a multiple of 8): per 16 values
+ *   s = e4m3_rne(amax / (6 gs)), d = fp32(s gs), code = e2m1_rne(x / d)
+ * (as qrr_quantize_nvfp4 with s_t = gs).  No two rows may name one slot.
+ * qrr_kv_read_nvfp4: the rows' values bf16_rn(fp32(e2m1 * e4m3) * gs) into
+ * k_out, v_out bf16 [T][Hkv][D]. */
+typedef struct qrr_kv_nvfp4 {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_gs;
+  const float* v_gs;
+  const int32_t* page_table;
+  int32_t num_pages, Hkv, page, D, B, max_pages;
+} qrr_kv_nvfp4;
+
+qrr_status qrr_kv_append_nvfp4(const qrr_kv_nvfp4* cache, const void* k_new, const void* v_new, int64_t T,
+                               int64_t ld_k, int64_t ld_v, const int32_t* cu, const int32_t* pos,
+                               int32_t* dev_status, void* stream);
+qrr_status qrr_kv_read_nvfp4(const qrr_kv_nvfp4* cache, int64_t T, const int32_t* cu, const int32_t* pos,
+                             void* k_out, void* v_out, int32_t* dev_status, void* stream);
+
+/* qrr_attention_nvfp4: for each row (a query token) and query head h, KV head
+ * h / (Hq / Hkv),
+ *   out = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q . k_j),
+ *   lse = log(sum_j p_j)
+ * over the cached positions j <= pos[b] + i (the row's own token included:
+ * append first).  A row that sees nothing gives zeros and lse -inf.
+ *   q    bf16, row t at q + t ld_q elements, Hq heads of D; ld_q % 8 == 0
+ *   scale > 0 and finite (1 / sqrt(D), usually)
+ *   max_new  host bound on cu[b + 1] - cu[b] (1 where cu is NULL); a sequence
+ *            with more rows raises QRR_DEV_BAD_INDEX, its outputs unspecified
+ *   out  bf16 [T][Hq][D];  lse fp32 [T][Hq] or NULL
+ *   workspace  qrr_attention_nvfp4_workspace_bytes(cache, T, Hq, max_new)
+ * Hq a multiple of Hkv.  Cached values convert exactly; the query is carried
+ * in f16 after a power of two a row (exact for values within 2^-29 of the
+ * row's largest); p is rounded to f16, all sums are fp32.  Work is cut over
+ * the cached tokens and joined in a fixed order: results do not depend on
+ * timing. */
+size_t qrr_attention_nvfp4_workspace_bytes(const qrr_kv_nvfp4* cache, int64_t T, int32_t Hq, int32_t max_new);
+qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t T, int64_t ld_q, int32_t Hq,
+                               const int32_t* cu, const int32_t* pos, int32_t max_new, float scale, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Token log-probabilities and token-level importance-sampling weights
  * ("NVIDIA NeMo RL behaalt 48% ...", the paragraph on importance sampling in
  * "Waarom dit belangrijk is voor AI-economie": the shift between the

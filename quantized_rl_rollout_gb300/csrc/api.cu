@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "kv_nvfp4.cuh"
 #include "linear.cuh"
 #include "quant.cuh"
 #include "tc.cuh"
@@ -771,6 +772,87 @@ qrr_status qrr_attention_decode_fp8(const void* q, int32_t B, int32_t Hq, int32_
   float* po = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + round_up(rows * 8));
   return from_cuda(launch_attention_decode_fp8(q, k_cache, k_scales, v_cache, v_scales, lens, B, Hq, Hkv, Lmax, out,
                                                pm, pl, po, dev_status, as_stream(stream)));
+}
+
+// A cache description, and the rows of a call on it.
+static qrr_status check_kv_nvfp4(const qrr_kv_nvfp4* c, int64_t T, const int32_t* cu, const int32_t* pos) {
+  if (!c || c->num_pages < 0 || c->Hkv < 0 || c->page <= 0 || c->D <= 0 || c->B < 0 || c->max_pages < 0 || T < 0)
+    return QRR_ERR_INVALID_ARG;
+  if ((c->D != 64 && c->D != 128) || c->page < 16 || (c->page & (c->page - 1)) != 0) return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (T > kMaxTokens || static_cast<int64_t>(c->max_pages) * c->page > kMaxTokens || c->Hkv > 65536)
+    return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (T * 2 * c->Hkv * (c->D / 16) > static_cast<int64_t>(INT32_MAX) * 256) return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (!cu && T != c->B) return QRR_ERR_INVALID_ARG;
+  if (T > 0 && c->Hkv > 0 && !pos && c->B > 0) return QRR_ERR_INVALID_ARG;
+  if (T > 0 && c->Hkv > 0 && static_cast<int64_t>(c->B) * c->max_pages > 0 && !c->page_table)
+    return QRR_ERR_INVALID_ARG;
+  if (T > 0 && c->Hkv > 0 && c->num_pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+    return QRR_ERR_INVALID_ARG;
+  auto a4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales) ||
+      !a4(c->k_gs) || !a4(c->v_gs) || !a4(c->page_table) || !a4(cu) || !a4(pos))
+    return QRR_ERR_MISALIGNED;
+  return QRR_OK;
+}
+
+static KvNvfp4 kv_view(const qrr_kv_nvfp4& c) {
+  int shift = 0;
+  while ((1 << shift) < c.page) ++shift;
+  return KvNvfp4{c.k_codes, c.k_scales, c.v_codes, c.v_scales, c.k_gs, c.v_gs, c.page_table,
+                 c.num_pages, c.Hkv, shift, c.D, c.B, c.max_pages};
+}
+
+qrr_status qrr_kv_append_nvfp4(const qrr_kv_nvfp4* cache, const void* k_new, const void* v_new, int64_t T,
+                               int64_t ld_k, int64_t ld_v, const int32_t* cu, const int32_t* pos, int32_t* dev_status,
+                               void* stream) {
+  const qrr_status st = check_kv_nvfp4(cache, T, cu, pos);
+  if (st != QRR_OK) return st;
+  const int64_t row = static_cast<int64_t>(cache->Hkv) * cache->D;
+  if (T * row > 0 && (!k_new || !v_new)) return QRR_ERR_INVALID_ARG;
+  if (T > 1 && (ld_k < row || ld_v < row)) return QRR_ERR_INVALID_ARG;
+  if (ld_k % 8 != 0 || ld_v % 8 != 0 || !aligned16(k_new) || !aligned16(v_new)) return QRR_ERR_MISALIGNED;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  return from_cuda(launch_kv_append_nvfp4(kv_view(*cache), KvRows{cu, pos, T}, k_new, v_new, ld_k, ld_v, dev_status,
+                                          as_stream(stream)));
+}
+
+qrr_status qrr_kv_read_nvfp4(const qrr_kv_nvfp4* cache, int64_t T, const int32_t* cu, const int32_t* pos, void* k_out,
+                             void* v_out, int32_t* dev_status, void* stream) {
+  const qrr_status st = check_kv_nvfp4(cache, T, cu, pos);
+  if (st != QRR_OK) return st;
+  if (T * cache->Hkv > 0 && (!k_out || !v_out)) return QRR_ERR_INVALID_ARG;
+  if (!aligned16(k_out) || !aligned16(v_out)) return QRR_ERR_MISALIGNED;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  return from_cuda(launch_kv_read_nvfp4(kv_view(*cache), KvRows{cu, pos, T}, k_out, v_out, dev_status,
+                                        as_stream(stream)));
+}
+
+size_t qrr_attention_nvfp4_workspace_bytes(const qrr_kv_nvfp4* cache, int64_t T, int32_t Hq, int32_t max_new) {
+  if (!cache || T < 0 || Hq < 0 || max_new < 0 || cache->Hkv <= 0 || (cache->D != 64 && cache->D != 128) || cache->B < 0)
+    return 0;
+  return attention_nvfp4_ws_bytes(cache->D, T, cache->B, Hq, cache->Hkv, max_new);
+}
+
+qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t T, int64_t ld_q, int32_t Hq,
+                               const int32_t* cu, const int32_t* pos, int32_t max_new, float scale, void* out,
+                               float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  const qrr_status st = check_kv_nvfp4(cache, T, cu, pos);
+  if (st != QRR_OK) return st;
+  if (Hq < 0 || cache->Hkv <= 0 || max_new < 0 || (!cu && max_new != 1)) return QRR_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || scale == INFINITY) return QRR_ERR_INVALID_ARG;
+  if (Hq % cache->Hkv != 0 || max_new > kMaxTokens / (Hq > 0 ? Hq : 1)) return QRR_ERR_UNSUPPORTED_SHAPE;
+  const int64_t row = static_cast<int64_t>(Hq) * cache->D;
+  if (T * row > 0 && (!q || !out)) return QRR_ERR_INVALID_ARG;
+  if (T > 1 && ld_q < row) return QRR_ERR_INVALID_ARG;
+  if (ld_q % 8 != 0 || !aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(lse) & 3u))
+    return QRR_ERR_MISALIGNED;
+  if (!workspace || workspace_bytes < qrr_attention_nvfp4_workspace_bytes(cache, T, Hq, max_new))
+    return QRR_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QRR_ERR_MISALIGNED;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  AttnNvfp4Args a{kv_view(*cache), KvRows{cu, pos, T}, static_cast<const uint16_t*>(q), ld_q, Hq, max_new, scale,
+                  static_cast<uint16_t*>(out), lse, static_cast<uint8_t*>(workspace), dev_status};
+  return from_cuda(launch_attention_nvfp4(a, as_stream(stream)));
 }
 
 qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const int32_t* tokens,

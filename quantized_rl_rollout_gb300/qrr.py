@@ -52,6 +52,14 @@ class LinearDesc(ctypes.Structure):
                 ("y", _c_p)]
 
 
+class KvNvfp4Desc(ctypes.Structure):
+    """Mirror of ``qrr_kv_nvfp4``."""
+
+    _fields_ = [("k_codes", _c_p), ("k_scales", _c_p), ("v_codes", _c_p), ("v_scales", _c_p), ("k_gs", _c_p),
+                ("v_gs", _c_p), ("page_table", _c_p), ("num_pages", _c_i32), ("Hkv", _c_i32), ("page", _c_i32),
+                ("D", _c_i32), ("B", _c_i32), ("max_pages", _c_i32)]
+
+
 # symbol -> (restype, argtypes)
 SIGNATURES = {
     "qrr_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -81,6 +89,11 @@ SIGNATURES = {
     "qrr_attention_decode_fp8_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32]),
     "qrr_attention_decode_fp8": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i32, _c_p,
                                                 _c_p, _c_sz, _c_p, _c_p]),
+    "qrr_kv_append_nvfp4": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p]),
+    "qrr_kv_read_nvfp4": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "qrr_attention_nvfp4_workspace_bytes": (_c_sz, [_c_p, _c_i64, _c_i32, _c_i32]),
+    "qrr_attention_nvfp4": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_p, _c_i32, ctypes.c_float, _c_p,
+                                           _c_p, _c_p, _c_sz, _c_p, _c_p]),
     "qrr_lora_backward_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32]),
     "qrr_lora_backward_nvfp4": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i32,
                                                ctypes.c_float, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
@@ -491,3 +504,144 @@ def attention_decode_fp8(q, k_cache, k_scales, v_cache, v_scales, lens, out=None
                                           workspace.numel(), _ptr(dev_status), _stream(stream)),
            "qrr_attention_decode_fp8")
     return out
+
+
+class KvCacheNvfp4:
+    """A paged NVFP4 key/value cache over buffers of the caller's, checked once.
+
+    ``k_codes``, ``v_codes`` uint8 [pages, Hkv, page, D/2]; ``k_scales``,
+    ``v_scales`` uint8 [pages, Hkv, page, D/16]; ``page_table`` int32
+    [B, max_pages]; ``k_gs``, ``v_gs`` fp32 [Hkv] global scales or None (1).
+    The tensors are kept, not copied: their contents may change between calls
+    (new pages in the table, say), their storage may not."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, page_table, k_gs=None, v_gs=None):
+        for t, name in ((k_codes, "k_codes"), (k_scales, "k_scales"), (v_codes, "v_codes"), (v_scales, "v_scales")):
+            _need(t, torch.uint8, name)
+        _need(page_table, torch.int32, "page_table")
+        if k_codes.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("k_codes must be [pages, Hkv, page, D/2] and page_table [B, max_pages]")
+        pages, hkv, page, half = k_codes.shape
+        if v_codes.shape != k_codes.shape:
+            raise ValueError("k_codes and v_codes must have the same shape")
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            if tuple(t.shape) != (pages, hkv, page, half // 8):
+                raise ValueError(f"{name} must be {[pages, hkv, page, half // 8]}, got {list(t.shape)}")
+        for t, name in ((k_gs, "k_gs"), (v_gs, "v_gs")):
+            if t is not None:
+                _need(t, torch.float32, name)
+                if t.numel() != hkv:
+                    raise ValueError(f"{name} must have one value a KV head")
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, page_table, k_gs, v_gs)
+        self.device = k_codes.device
+        self.pages, self.hkv, self.page, self.dim = pages, hkv, page, 2 * half
+        self.batch, self.max_pages = page_table.shape
+        self.desc = KvNvfp4Desc(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_gs), _ptr(v_gs),
+                                _ptr(page_table), pages, hkv, page, 2 * half, self.batch, self.max_pages)
+        self._addr = ctypes.addressof(self.desc)
+
+    @classmethod
+    def empty(cls, pages, hkv, page, dim, page_table, k_gs=None, v_gs=None):
+        """A cache with buffers of its own, all zeros."""
+        dev = page_table.device
+        codes = [torch.zeros(pages, hkv, page, dim // 2, dtype=torch.uint8, device=dev) for _ in range(2)]
+        scales = [torch.zeros(pages, hkv, page, dim // 16, dtype=torch.uint8, device=dev) for _ in range(2)]
+        return cls(codes[0], scales[0], codes[1], scales[1], page_table, k_gs, v_gs)
+
+
+def _for_stream(t, stream):
+    """``t``, allocated here, kept from being reused before ``stream`` (another than the current one, if given) is done."""
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
+    return t
+
+
+def _kv_rows(cache, pos, cu, t):
+    if pos.dtype is not torch.int32 or not pos.is_cuda or not pos.is_contiguous() or pos.numel() != cache.batch:
+        raise ValueError(f"pos must be a contiguous CUDA int32 tensor of {cache.batch} values")
+    if cu is None:
+        if t != cache.batch:
+            raise ValueError(f"without cu there is one row a sequence: {cache.batch}, got {t}")
+    elif cu.dtype is not torch.int32 or not cu.is_cuda or not cu.is_contiguous() or cu.numel() != cache.batch + 1:
+        raise ValueError(f"cu must be a contiguous CUDA int32 tensor of {cache.batch + 1} values")
+
+
+def _head_rows(x, heads, dim, name):
+    """Row stride of bf16 rows [T, heads, dim] whose heads are contiguous (a slice of a wider projection will do)."""
+    if x.dtype is not torch.bfloat16 or not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {list(x.shape)}")
+    s = x.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if x.shape[0] > 1 else heads * dim
+
+
+def kv_append_nvfp4(k_new, v_new, cache, pos, cu=None, dev_status=None, stream=None):
+    """Quantize rows [T, Hkv, D] of keys and values into the cache: sequence b's rows cu[b] .. cu[b + 1] - 1 (row b
+    alone without ``cu``) at the positions pos[b], pos[b] + 1, ... (see ``qrr_kv_append_nvfp4``)."""
+    ld_k = _head_rows(k_new, cache.hkv, cache.dim, "k_new")
+    ld_v = _head_rows(v_new, cache.hkv, cache.dim, "v_new")
+    t = k_new.shape[0]
+    if v_new.shape[0] != t:
+        raise ValueError("k_new and v_new must have the same rows")
+    _kv_rows(cache, pos, cu, t)
+    _check(lib().qrr_kv_append_nvfp4(cache._addr, k_new.data_ptr(), v_new.data_ptr(), t, ld_k, ld_v, _ptr(cu),
+                                     pos.data_ptr(), _ptr(dev_status), _stream(stream)), "qrr_kv_append_nvfp4")
+
+
+def kv_read_nvfp4(cache, pos, cu=None, rows=None, k=None, v=None, dev_status=None, stream=None):
+    """(k, v) bf16 [rows, Hkv, D]: the cached values at pos[b], pos[b] + 1, ... of every sequence, as many as ``cu``
+    gives it (one without ``cu``); ``rows`` is cu[B], which the host cannot see without waiting for the GPU."""
+    if rows is None:
+        if cu is not None and k is None:
+            raise ValueError("rows is needed with cu")
+        rows = cache.batch if k is None else k.shape[0]
+    _kv_rows(cache, pos, cu, rows)
+    shape = (rows, cache.hkv, cache.dim)
+    k = _for_stream(torch.empty(shape, dtype=torch.bfloat16, device=cache.device), stream) if k is None else k
+    v = _for_stream(torch.empty(shape, dtype=torch.bfloat16, device=cache.device), stream) if v is None else v
+    for x, name in ((k, "k"), (v, "v")):
+        if x.dtype is not torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.shape != shape:
+            raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor {list(shape)}")
+    _check(lib().qrr_kv_read_nvfp4(cache._addr, rows, _ptr(cu), pos.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   _ptr(dev_status), _stream(stream)), "qrr_kv_read_nvfp4")
+    return k, v
+
+
+def attention_nvfp4_workspace_bytes(cache, rows, hq, max_new=1) -> int:
+    return int(lib().qrr_attention_nvfp4_workspace_bytes(cache._addr, int(rows), int(hq), int(max_new)))
+
+
+def attention_nvfp4(q, cache, pos, cu=None, max_new=None, scale=None, return_lse=False, out=None, lse=None,
+                    workspace=None, dev_status=None, stream=None):
+    """Attention of query rows q [T, Hq, D] over the NVFP4 cache: row cu[b] + i sees the positions up to pos[b] + i.
+
+    ``max_new`` bounds the rows of a sequence (needed with ``cu``); ``scale`` is
+    1/sqrt(D) unless given.  Returns out bf16 [T, Hq, D], or (out, lse fp32
+    [T, Hq]) when ``return_lse`` is set or ``lse`` is given."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, D], got {list(q.shape)}")
+    t, hq, d = q.shape
+    ld_q = _head_rows(q, hq, cache.dim, "q")
+    _kv_rows(cache, pos, cu, t)
+    if max_new is None:
+        if cu is not None:
+            raise ValueError("max_new is needed with cu")
+        max_new = 1
+    if scale is None:
+        scale = d ** -0.5
+    out = _for_stream(torch.empty(t, hq, d, dtype=torch.bfloat16, device=q.device), stream) if out is None else out
+    if out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous() or out.shape != q.shape:
+        raise ValueError(f"out must be a contiguous CUDA bfloat16 tensor {list(q.shape)}")
+    if lse is None:
+        lse = _for_stream(torch.empty(t, hq, dtype=torch.float32, device=q.device), stream) if return_lse else None
+    elif lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (t, hq):
+        raise ValueError(f"lse must be a contiguous CUDA float32 tensor {[t, hq]}")
+    if workspace is None:
+        workspace = _for_stream(_workspace(attention_nvfp4_workspace_bytes(cache, t, hq, max_new), q.device), stream)
+    _check(lib().qrr_attention_nvfp4(cache._addr, q.data_ptr(), t, ld_q, hq, _ptr(cu), pos.data_ptr(), int(max_new),
+                                     float(scale), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
+                                     _ptr(dev_status), _stream(stream)), "qrr_attention_nvfp4")
+    return out if lse is None else (out, lse)
