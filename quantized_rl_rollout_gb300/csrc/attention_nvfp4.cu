@@ -30,55 +30,19 @@
 // and is only moved when some score exceeds it by 15, so p = 2^(s - m) stays
 // within f16, the row's largest p is at least 2^7, and a p keeps f16's full 11
 // bits down to 2^-21 of that (an absolute 2^-32 of it below).
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "kv_nvfp4.cuh"
+#include "attention_nvfp4.cuh"
 #include "tc.cuh"
 
 namespace qrr {
+
+using namespace attn4;
 
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kCtasPerSm = 4;
-constexpr int kMaxSms = 160;       // of the workspace's size; the grid is capped to it
-constexpr int kMinTiles = 8;       // tiles of a range: two a warp
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNone = -1.0e30f;  // reference of a row that has seen nothing
-constexpr float kLift = 7.0f, kRoom = 15.0f;  // the reference lies kLift under the largest score and moves above kRoom
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Two E4M3 bytes -> f16x2 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(b));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+constexpr int kMinTiles = 8;  // tiles of a range: two a warp
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t r;
@@ -127,49 +91,18 @@ struct Tile {
   int live;  // tokens of the tile that exist (0..16)
 };
 
-struct Item {
-  int b, rt, h;     // sequence, row tile, KV head
-  int first, n;     // its rows
-  int pos;          // position of its first row
-  int last;         // last visible position of the sequence's last row (-1: none)
-  int tiles;        // tiles of the item (at least 1)
+struct Item : Seq {
+  int b, rt, h;  // sequence, row tile, KV head
+  int tiles;     // tiles of the item (at least 1)
 };
 
-// Workspace: [records][m, l, o of the pieces]; piece 2 k is CTA k's first when
-// it continues an item, piece 2 k + 1 its last when it starts one that the
-// next CTA continues.
-struct Record {
-  int cont;        // piece 2 k is there
-  int cont_more;   // and the next CTA continues the same item
-  int start;       // piece 2 k + 1 is there
-  int b, rt, h, first, n;
-};
-
-struct Params {
-  KvNvfp4 c;
-  KvRows r;
-  const uint16_t* q;
-  int64_t ld_q;
-  int Hq, G, max_new;
-  float scale;
-  uint16_t* out;
-  float* lse;
-  Record* rec;
-  float *pm, *pl, *po;  // [piece][rows], [piece][rows], [piece][rows][D]
-  int32_t* status;
-};
-
-// The sequence's rows, row tiles and tiles.
+// Sequence b's row tiles (none if it has more rows than this kernel takes).
 template <int RT>
 __device__ __forceinline__ void seq_item(const Params& p, int b, Item& it, int& rts) {
-  if (!kv_rows_of(p.r, b, it.first, it.n) || it.n > p.max_new) flag(p.status, QRR_DEV_BAD_INDEX);
-  it.n = min(it.n, p.max_new);
-  it.pos = min(__ldg(p.r.pos + b), kMaxTokens);  // with at most kMaxTokens rows: sums stay in 32 bits
-  const int last = it.pos + it.n - 1, cap = static_cast<int>(p.c.capacity());
-  if (it.n > 0 && last >= cap) flag(p.status, QRR_DEV_BAD_INDEX);
-  it.last = min(max(last, -1), cap - 1);
+  static_cast<Seq&>(it) = seq_of(p, b);
   it.tiles = max(1, (it.last + 16) >> 4);
-  rts = (it.n * p.G + RT - 1) / RT;
+  const int64_t rows = static_cast<int64_t>(it.n) * p.G;
+  rts = rows > kFewRows ? 0 : static_cast<int>((rows + RT - 1) / RT);
 }
 
 template <int D>
@@ -240,8 +173,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
     mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
     mx = max(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
     if (mx >= 0x7F80u) flag(p.status, QRR_DEV_NONFINITE);
-    // 2^e with mx 2^-e in [2^14, 2^15)
-    const int e = mx == 0u || mx >= 0x7F80u ? 0 : (mx >= 0x80u ? static_cast<int>(mx >> 7) - 127 : 31 - __clz(mx) - 133) - 14;
+    const int e = query_exp(mx);
     const Pow2Scaler sc(e);
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
@@ -490,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4
       }
       if (!cut0 && !cut1) {
         const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
-        const int64_t orow = static_cast<int64_t>(it.first + row / p.G) * p.Hq + it.h * p.G + row % p.G;
+        const int64_t orow = out_row(p, it.first, it.h, row);
         const __nv_bfloat162 u = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), v = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
         *reinterpret_cast<uint2*>(p.out + orow * D + d) =
             make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
@@ -502,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4
       }
     }
     if (cut0) rec.cont = 1, rec.cont_more = cut1;
-    else if (cut1) rec.start = 1, rec.b = it.b, rec.rt = it.rt, rec.h = it.h, rec.first = it.first, rec.n = it.n;
+    else if (cut1) rec.start = 1, rec.rt = it.rt, rec.h = it.h, rec.first = it.first, rec.n = it.n;
     __syncthreads();
     left -= t1 - t0;
     t0 = 0;
@@ -515,71 +447,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4
   if (tid == 0) p.rec[blockIdx.x] = rec;
 }
 
-// Joins the pieces of the item that starts in range k and is continued by the
-// next ones: a warp a row, in the order of the ranges.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) attn_nvfp4_join_kernel(const Params p, int ranges) {
-  constexpr int RT = 8 * NT, V = D / 32;
-  const int k = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Record rec = p.rec[k];
-  if (!rec.start) return;
-  int last = k + 1;
-  while (last + 1 < ranges && p.rec[last].cont_more) ++last;
-  const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  for (int r = warp; r < RT; r += 8) {
-    const int row = rec.rt * RT + r;
-    if (row >= rec.n * p.G) break;
-    auto piece = [&](int i) { return static_cast<int64_t>(i == k ? 2 * k + 1 : 2 * i) * RT + r; };
-    float m = kNone;
-    for (int i = k; i <= last; ++i) m = fmaxf(m, p.pm[piece(i)]);
-    float l = 0.0f, o[V] = {};
-    for (int i = k; i <= last; ++i) {
-      const int64_t pr = piece(i);
-      const float a = ex2(p.pm[pr] - m);
-      l += a * p.pl[pr];
-#pragma unroll
-      for (int d = 0; d < V; ++d) o[d] += a * p.po[pr * D + 32 * d + lane];
-    }
-    const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
-    const int64_t orow = static_cast<int64_t>(rec.first + row / p.G) * p.Hq + rec.h * p.G + row % p.G;
-#pragma unroll
-    for (int d = 0; d < V; ++d)
-      reinterpret_cast<__nv_bfloat16*>(p.out)[orow * D + 32 * d + lane] = __float2bfloat16_rn(o[d] * inv);
-    if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
-  }
-}
-
 namespace {
-
-constexpr size_t kAlign = 256;
-size_t up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 template <int D, int NT>
 cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   constexpr int RT = 8 * NT;
-  Params p{a.c, a.r, a.q, a.ld_q, a.Hq, a.Hq / a.c.Hkv, a.max_new, a.scale, a.out, a.lse};
-  uint8_t* w = a.ws;
-  const size_t rows = static_cast<size_t>(2) * grid * RT;
-  p.rec = reinterpret_cast<Record*>(w);
-  w += up(sizeof(Record) * grid);
-  p.pm = reinterpret_cast<float*>(w);
-  w += up(rows * 4);
-  p.pl = reinterpret_cast<float*>(w);
-  w += up(rows * 4);
-  p.po = reinterpret_cast<float*>(w);
-  p.status = a.status;
+  const Params p = make_params(a, a.ws, grid, RT);
   attn_nvfp4_kernel<D, NT><<<grid, kThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  attn_nvfp4_join_kernel<D, NT><<<grid, 256, 0, stream>>>(p, grid);
+  join_kernel<D, RT><<<dim3(grid, NT), 256, 0, stream>>>(p, grid);
   return cudaGetLastError();
 }
 
+// Whether some sequence may have few rows, or many (see kFewRows).
+bool any_few(int G) { return G <= kFewRows; }
+bool any_many(int64_t max_new, int G) { return max_new * G > kFewRows; }
+
+size_t few_ws_bytes(int D) { return ws_bytes(D, kMaxSms * kCtasPerSm, kFewRows); }
+
 }  // namespace
 
-size_t attention_nvfp4_ws_bytes(int D, int64_t, int, int, int, int64_t) {
-  const size_t grid = kMaxSms * kCtasPerSm, rows = 2 * grid * 16;
-  return up(sizeof(Record) * grid) + 2 * up(rows * 4) + up(rows * D * 4);
+size_t attention_nvfp4_ws_bytes(int D, int64_t, int, int Hq, int Hkv, int64_t max_new) {
+  const int G = Hq / Hkv;
+  return few_ws_bytes(D) + (any_many(max_new, G) ? attention_nvfp4_tc_ws_bytes(D) : 0);
 }
 
 cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) {
@@ -587,10 +478,14 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
   int dev = 0, sms = kSMs;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int G = a.Hq / a.c.Hkv;
-  const bool one = static_cast<int64_t>(a.max_new) * G <= 8;
-  const int grid = (sms < kMaxSms ? sms : kMaxSms) * (one ? kCtasPerSm : 2);
-  if (a.c.D == 128) return one ? launch<128, 1>(a, grid, stream) : launch<128, 2>(a, grid, stream);
-  return one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream);
+  if (any_few(G)) {
+    const bool one = static_cast<int64_t>(a.max_new) * G <= 8;
+    const int grid = (sms < kMaxSms ? sms : kMaxSms) * (one ? kCtasPerSm : 2);
+    const cudaError_t e = a.c.D == 128 ? (one ? launch<128, 1>(a, grid, stream) : launch<128, 2>(a, grid, stream))
+                                       : (one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream));
+    if (e != cudaSuccess) return e;
+  }
+  return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D), stream) : cudaSuccess;
 }
 
 }  // namespace qrr

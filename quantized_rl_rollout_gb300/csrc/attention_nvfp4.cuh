@@ -1,0 +1,163 @@
+// What the two kernels of attention over the paged NVFP4 cache share: few rows a
+// sequence (attention_nvfp4.cu) and many (attention_nvfp4_tc.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv_nvfp4.cuh"
+
+namespace qrr {
+
+namespace attn4 {
+
+constexpr int kMaxSms = 160;       // of the workspace's size; grids are capped to it
+constexpr int kFewRows = 16;       // a sequence with at most this many rows a KV head takes the first kernel
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNone = -1.0e30f;  // reference of a row that has seen nothing
+constexpr float kLift = 7.0f, kRoom = 15.0f;  // the reference lies kLift under the largest score and moves above kRoom
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two E4M3 bytes -> f16x2 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// The exponent e that brings a row whose largest |bf16| has the bits mx into
+// f16: mx 2^-e in [2^14, 2^15) (0 for a zero or a non-finite row).
+__device__ __forceinline__ int query_exp(uint32_t mx) {
+  if (mx == 0u || mx >= 0x7F80u) return 0;
+  return (mx >= 0x80u ? static_cast<int>(mx >> 7) - 127 : 31 - __clz(static_cast<int>(mx)) - 133) - 14;
+}
+
+// Pieces of items that cross ranges.  Piece 2 k is range k's first when it
+// continues an item, piece 2 k + 1 its last when it starts one that the next
+// range continues.
+struct Record {
+  int cont;       // piece 2 k is there
+  int cont_more;  // and the next range continues the same item
+  int start;      // piece 2 k + 1 is there
+  int rt, h, first, n;  // its row tile, KV head, the sequence's rows
+};
+
+struct Params {
+  KvNvfp4 c;
+  KvRows r;
+  const uint16_t* q;
+  int64_t ld_q;
+  int Hq, G, max_new;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  Record* rec;
+  float *pm, *pl, *po;  // [piece][row], [piece][row], [piece][row][D]
+  int32_t* status;
+};
+
+// A sequence as the kernels see it: its rows, the position of the first, the
+// last visible position of the last (-1: none).
+struct Seq {
+  int first, n, pos, last;
+};
+
+__device__ __forceinline__ Seq seq_of(const Params& p, int b) {
+  Seq s;
+  if (!kv_rows_of(p.r, b, s.first, s.n) || s.n > p.max_new) flag(p.status, QRR_DEV_BAD_INDEX);
+  s.n = min(s.n, p.max_new);
+  s.pos = min(__ldg(p.r.pos + b), kMaxTokens);  // with at most kMaxTokens rows: sums stay in 32 bits
+  const int last = s.pos + s.n - 1, cap = static_cast<int>(p.c.capacity());
+  if (s.n > 0 && last >= cap) flag(p.status, QRR_DEV_BAD_INDEX);
+  s.last = min(max(last, -1), cap - 1);
+  return s;
+}
+
+// Output row of row `row` (token row / G, head of the group row % G).
+__device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, int row) {
+  return static_cast<int64_t>(first + row / p.G) * p.Hq + h * p.G + row % p.G;
+}
+
+// Joins the pieces of the item that starts in range k = blockIdx.x and is
+// continued by the next ones: a warp a row, in the order of the ranges.  RT:
+// rows of a piece.
+template <int D, int RT>
+__global__ void __launch_bounds__(256) join_kernel(const Params p, int ranges) {
+  constexpr int V = D / 32;
+  const int k = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Record rec = p.rec[k];
+  if (!rec.start) return;
+  const int row = rec.rt * RT + r;
+  if (row >= rec.n * p.G) return;
+  int last = k + 1;
+  while (last + 1 < ranges && p.rec[last].cont_more) ++last;
+  const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
+  auto piece = [&](int i) { return static_cast<int64_t>(i == k ? 2 * k + 1 : 2 * i) * RT + r; };
+  float m = kNone;
+  for (int i = k; i <= last; ++i) m = fmaxf(m, p.pm[piece(i)]);
+  float l = 0.0f, o[V] = {};
+  for (int i = k; i <= last; ++i) {
+    const int64_t pr = piece(i);
+    const float a = ex2(p.pm[pr] - m);
+    l += a * p.pl[pr];
+#pragma unroll
+    for (int d = 0; d < V; ++d) o[d] += a * p.po[pr * D + 32 * d + lane];
+  }
+  const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+  const int64_t orow = out_row(p, rec.first, rec.h, row);
+#pragma unroll
+  for (int d = 0; d < V; ++d)
+    reinterpret_cast<__nv_bfloat16*>(p.out)[orow * D + 32 * d + lane] = __float2bfloat16_rn(o[d] * inv);
+  if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+}
+
+// Workspace of `ranges` ranges whose pieces have `rt` rows.
+inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+inline size_t ws_bytes(int D, int ranges, int rt) {
+  const size_t rows = static_cast<size_t>(2) * ranges * rt;
+  return align256(sizeof(Record) * ranges) + 2 * align256(rows * 4) + align256(rows * D * 4);
+}
+inline Params make_params(const AttnNvfp4Args& a, uint8_t* w, int ranges, int rt) {
+  Params p{a.c, a.r, a.q, a.ld_q, a.Hq, a.Hq / a.c.Hkv, a.max_new, a.scale, a.out, a.lse};
+  const size_t rows = static_cast<size_t>(2) * ranges * rt;
+  p.rec = reinterpret_cast<Record*>(w);
+  w += align256(sizeof(Record) * ranges);
+  p.pm = reinterpret_cast<float*>(w);
+  w += align256(rows * 4);
+  p.pl = reinterpret_cast<float*>(w);
+  w += align256(rows * 4);
+  p.po = reinterpret_cast<float*>(w);
+  p.status = a.status;
+  return p;
+}
+
+}  // namespace attn4
+
+// Many rows a sequence (attention_nvfp4_tc.cu); ws: its own part.
+size_t attention_nvfp4_tc_ws_bytes(int D);
+cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream);
+
+}  // namespace qrr

@@ -1,0 +1,610 @@
+// Attention over the paged NVFP4 key/value cache, many query rows a sequence
+// (prompts, new turns): the formulas of attention_nvfp4.cu on the 5th-generation
+// tensor cores.
+//
+// An item is 256 rows of a sequence and a KV head (row = new token x G + query
+// head of the group), as two tiles of 128; its keys and values come in tiles of
+// 128 tokens.  The key tiles of all items form one sequence that is cut in
+// equal ranges, one a CTA (one CTA an SM), as in the other kernel; pieces of
+// items that cross ranges go to the workspace and are joined afterwards.
+//
+// A CTA's warps:
+//   0..3, 4..7  softmax of row tile 0 and 1: a thread a row.  Loads its query
+//               row as f16 (a power of two a row) into shared memory, then for
+//               every key tile turns the scores in tensor memory into weights
+//               (f16, over the scores' own columns), and at the end scales and
+//               stores the row.
+//   8..11       codes and scales -> f16 key and value tiles in shared memory
+//               (code x block scale is exact), two stages each, 128-byte
+//               swizzled; the codes of the next tile are fetched meanwhile.
+//   12          issues the MMAs: S_i = Q_i K^T (M128 N128), O_i += P_i V
+//               (P from tensor memory, V MN-major).  Order per key tile:
+//               PV_0, S_0 of the next, PV_1, S_1 of the next, so one tile's
+//               softmax runs under the other's MMAs.
+// Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
+//
+// A row's weights are formed with the running reference in one pass over its
+// scores; only when a score exceeds it by kRoom (and on a row's first tile) the
+// pass is repeated with a new one and the row's output so far is scaled.
+#include "attention_nvfp4.cuh"
+#include "tc.cuh"
+
+namespace qrr {
+
+using namespace attn4;
+
+namespace {
+
+constexpr int kThreads = 13 * 32;
+constexpr int kRows = 256;  // rows of an item
+constexpr int kTok = 128;   // tokens of a key tile
+constexpr int kMinTiles = 4;  // key tiles of a range
+constexpr int kSeqs = 1024;   // sequences whose tile counts are kept in shared memory
+constexpr uint32_t kTmemCols = 512;
+
+template <int D>
+struct Smem {
+  static constexpr int kTile = 128 * D * 2;  // bytes of a query, key or value tile
+  uint8_t q[2][kTile], k[2][kTile], v[2][kTile];
+  uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done;
+  uint32_t tmem;
+  int abort;
+  int64_t total;
+  int32_t seq_tiles[kSeqs];
+  int64_t part[kThreads / 32];
+  int64_t start_off;
+  int start_b;
+};
+
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// The wait for this thread's tensor-memory loads, with the loaded registers as
+// operands so that no use of them moves above it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                 "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Items of a sequence: row tiles of 256 (none if it has few rows), and the key
+// tiles of one (at least 1).
+__device__ __forceinline__ int row_tiles(const Params& p, const Seq& s) {
+  const int64_t rows = static_cast<int64_t>(s.n) * p.G;
+  return rows <= kFewRows ? 0 : static_cast<int>((rows + kRows - 1) / kRows);
+}
+__device__ __forceinline__ int last_seen(const Params& p, const Seq& s, int qt) {
+  return min(s.pos + (min((qt + 1) * kRows, s.n * p.G) - 1) / p.G, s.last);
+}
+__device__ __forceinline__ int key_tiles(const Params& p, const Seq& s, int qt) {
+  return max(1, (last_seen(p, s, qt) + kTok) / kTok);
+}
+
+// Key tiles of one KV head of sequence b over all its row tiles, by a warp.
+__device__ __forceinline__ int seq_key_tiles(const Params& p, int b, int lane) {
+  const Seq s = seq_of(p, b);
+  const int qts = row_tiles(p, s);
+  int sum = 0;
+  for (int qt = lane; qt < qts; qt += 32) sum += key_tiles(p, s, qt);
+  return __reduce_add_sync(0xFFFFFFFFu, sum);
+}
+
+// The walk over a range's pieces of items; every thread of the CTA makes it.
+struct Walk {
+  Seq s;
+  int b, h, qt, qts, tiles;  // current item and its key tiles
+  int t0, t1;                // the piece's key tiles
+  int64_t left;              // tiles of the range from t0 on
+  __device__ __forceinline__ void piece(const Params& p) {
+    tiles = key_tiles(p, s, qt);
+    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + left));
+  }
+  __device__ __forceinline__ void begin(const Params& p, int b_, int64_t off, int64_t left_) {
+    b = b_;
+    left = left_;
+    s = seq_of(p, b);
+    qts = row_tiles(p, s);
+    int per = 0;  // of one head
+    for (int i = 0; i < qts; ++i) per += key_tiles(p, s, i);
+    h = static_cast<int>(off / per);
+    int rest = static_cast<int>(off - static_cast<int64_t>(h) * per);
+    for (qt = 0; qt + 1 < qts; ++qt) {
+      const int n = key_tiles(p, s, qt);
+      if (rest < n) break;
+      rest -= n;
+    }
+    t0 = rest;
+    piece(p);
+  }
+  __device__ __forceinline__ bool next(const Params& p) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++qt == qts) {
+      qt = 0;
+      if (++h == p.c.Hkv) {
+        h = 0;
+        do {
+          if (++b >= p.c.B) return false;
+          s = seq_of(p, b);
+          qts = row_tiles(p, s);
+        } while (qts == 0);
+      }
+    }
+    piece(p);
+    return true;
+  }
+};
+
+// ---- codes -> f16 tiles ------------------------------------------------------
+
+// What a thread of the four converting warps holds of a tile: of every pass,
+// one chunk of 32 values of one token.
+template <int D>
+struct Codes {
+  static constexpr int kPerRow = D / 32, kRowsPass = 128 / kPerRow;
+  uint4 w[kPerRow];
+  uint32_t s[kPerRow];  // its two block scales
+};
+
+template <int D>
+__device__ __forceinline__ void fetch(const Params& p, const uint8_t* codes, const uint8_t* scales, const int32_t* table,
+                                      int h, int tile, int last, int tid, Codes<D>& x) {
+  using C = Codes<D>;
+  const int c = tid % C::kPerRow, r0 = tid / C::kPerRow;
+#pragma unroll
+  for (int i = 0; i < C::kPerRow; ++i) {
+    const int tok = tile * kTok + i * C::kRowsPass + r0;
+    x.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    x.s[i] = 0u;
+    if (tok <= last) {
+      const int pg = __ldg(table + (tok >> p.c.page_shift));
+      if (pg >= 0 && pg < p.c.num_pages) {
+        const int64_t row = kv_row(p.c, pg, h, tok & ((1 << p.c.page_shift) - 1));
+        x.w[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * (D / 2)) + c);
+        x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + row * (D / 16)) + c);
+      } else {
+        flag(p.status, QRR_DEV_BAD_INDEX);
+      }
+    }
+  }
+}
+
+// Row r of a tile lies at 128 r in each of its D / 64 column halves of 16 KB,
+// its 16-byte pieces at their index exclusive-or r % 8.
+template <int D>
+__device__ __forceinline__ void convert(const Codes<D>& x, uint8_t* tile, int tid) {
+  using C = Codes<D>;
+  const int c = tid % C::kPerRow, r0 = tid / C::kPerRow;
+#pragma unroll
+  for (int i = 0; i < C::kPerRow; ++i) {
+    const int r = i * C::kRowsPass + r0;
+    const uint32_t s2 = e4m3x2_to_f16x2(x.s[i]);
+    const uint32_t w[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
+    uint4 o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t f[4];
+      f16x2x4_from_e2m1x8(w[k], f);
+      const uint32_t sc = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
+      o[k] = make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
+    }
+    uint8_t* half = tile + (c >> 1) * (128 * 128) + r * 128;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      // the two column halves have the same banks: their lanes write in another order
+      const bool swap = (c >> 1) != 0;
+      const uint4 y = swap ? o[k ^ 2] : o[k];
+      const int piece = (4 * (c & 1) + k) ^ (swap ? 2 : 0);
+      *reinterpret_cast<uint4*>(half + ((piece ^ (r & 7)) << 4)) = y;
+    }
+  }
+}
+
+// ---- softmax -------------------------------------------------------------------
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 32 scores of a row -> weights 2^(s f - m): f16 pairs, their fp32 sums, the
+// largest score.  MASK: only the first `n` of them are seen.
+template <bool MASK>
+__device__ __forceinline__ void weights(uint32_t (&r)[32], int n, uint64_t f2, uint64_t nm2, float& mx, uint64_t& sum,
+                                        uint32_t* out) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a = __uint_as_float(r[2 * i]), b = __uint_as_float(r[2 * i + 1]);
+    if (MASK) {
+      a = 2 * i < n ? a : -INFINITY;
+      b = 2 * i + 1 < n ? b : -INFINITY;
+    }
+    mx = max3(mx, a, b);
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(f2), "l"(nm2));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+    a = ex2(a);
+    b = ex2(b);
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(x));
+    out[i] = f16x2(a, b);
+  }
+}
+
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<D>& sh = *reinterpret_cast<Smem<D>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* abort = &sh.abort;
+
+  // ---- this CTA's range of the key tiles
+  const int B = p.c.B;
+  int64_t mine = 0;
+  for (int b = warp; b < B; b += kThreads / 32) {
+    const int n = seq_key_tiles(p, b, lane);
+    if (lane == 0 && b < kSeqs) sh.seq_tiles[b] = n;
+    mine += n;
+  }
+  if (lane == 0) sh.part[warp] = mine;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 4);
+      mbar_init(&sh.k_full[i], 4);
+      mbar_init(&sh.k_empty[i], 1);
+      mbar_init(&sh.v_full[i], 4);
+      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.o_full[i], 1);
+    }
+    mbar_init(&sh.done, 1);
+    sh.abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += sh.part[w];
+  total *= p.c.Hkv;
+  const int64_t per = max(static_cast<int64_t>(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
+  const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
+  Record rec{};
+  if (begin >= end) {
+    if (tid == 0) p.rec[blockIdx.x] = rec;
+    return;
+  }
+  if (warp == 12) {
+    tmem_alloc(&sh.tmem, kTmemCols);
+    // the sequence that the range begins in
+    int64_t off = begin;
+    int found = -1;
+    for (int b0 = 0; b0 < B && found < 0; b0 += 32) {
+      int n = 0;
+      if (b0 + 32 <= kSeqs) n = b0 + lane < B ? sh.seq_tiles[b0 + lane] : 0;
+      else
+        for (int i = 0; i < 32 && b0 + i < B; ++i) {
+          const int x = seq_key_tiles(p, b0 + i, lane);
+          if (lane == i) n = x;
+        }
+      const int64_t own = static_cast<int64_t>(n) * p.c.Hkv;
+      int64_t incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, off >= incl - own && off < incl);
+      if (in) {
+        found = __ffs(static_cast<int>(in)) - 1;
+        off -= __shfl_sync(0xFFFFFFFFu, incl - own, found);
+        found += b0;
+      } else {
+        off -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+      }
+    }
+    if (lane == 0) {
+      sh.start_b = found;
+      sh.start_off = off;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  Walk w;
+  w.begin(p, sh.start_b, sh.start_off, end - begin);
+
+  if (warp < 8) {
+    // ---------------- softmax ----------------
+    const int tile = warp >> 2, r = tid & 127;
+    const uint32_t ts = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * tile;
+    const uint32_t to = ts + 256;
+    uint32_t s_phase = 0, o_phase = 0;
+    bool ok = true;
+    do {
+      const int row0 = w.qt * kRows + 128 * tile, rows = w.s.n * p.G;
+      if (row0 < rows) {
+        const int row = row0 + r;
+        const bool in = row < rows;
+        // ---- the query row, as f16
+        uint32_t mx = 0u;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + (w.s.first + row / p.G) * p.ld_q + static_cast<int64_t>(w.h * p.G + row % p.G) * D);
+        if (in)
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) mx = max(mx, absmax_bits8(__ldg(src + i)));
+        if (mx >= 0x7F80u) flag(p.status, QRR_DEV_NONFINITE);
+        const int e = query_exp(mx);
+        const Pow2Scaler sc(e);
+        uint8_t* dst = sh.q[tile] + r * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (in) x = __ldg(src + i);
+          const uint4 y = make_uint4(f16x2(sc(bf16_lo(x.x)), sc(bf16_hi(x.x))), f16x2(sc(bf16_lo(x.y)), sc(bf16_hi(x.y))),
+                                     f16x2(sc(bf16_lo(x.z)), sc(bf16_hi(x.z))), f16x2(sc(bf16_lo(x.w)), sc(bf16_hi(x.w))));
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4)) = y;
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.q_full[tile]);
+        // at least the smallest normal value: a masked score times it stays -inf
+        const float f = fmaxf(p.scale * kLog2e * (p.c.kg ? __ldg(p.c.kg + w.h) : 1.0f) * ldexpf(1.0f, e), 1.17549435e-38f);
+        const uint64_t f2 = twice(f);
+        // rows behind the last one are never read: they need no mask
+        const int lim = in ? min(w.s.pos + row / p.G, w.s.last) : 0x7FFFFFFF;
+        const int lim_warp = __reduce_min_sync(0xFFFFFFFFu, lim);
+        float m = kNone, l = 0.0f;
+        for (int j = w.t0; j < w.t1 && ok; ++j) {
+          if (!mbar_wait(&sh.s_full[tile], s_phase, abort, p.status)) {
+            ok = false;
+            break;
+          }
+          s_phase ^= 1;
+          tc_fence_after();
+          const int seen = lim - kTok * j + 1;  // of this tile's tokens
+          const bool mask = kTok * j + kTok - 1 > lim_warp;
+          uint32_t pk[64];
+          float top;
+          uint64_t sum;
+          auto pass = [&] {
+            top = -INFINITY;
+            sum = 0ull;
+            const uint64_t nm2 = twice(-m);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[32];
+              tmem_ld32(ts + 32 * c, x);
+              tmem_ld_wait32(x);
+              if (mask) weights<true>(x, seen - 32 * c, f2, nm2, top, sum, pk + 16 * c);
+              else weights<false>(x, 0, f2, nm2, top, sum, pk + 16 * c);
+            }
+          };
+          pass();
+          const bool move = top * f > m + kRoom;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            const float m1 = move ? top * f - kLift : m, a = ex2(m - m1);
+            m = m1;
+            l *= a;
+            if (j > w.t0) {
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(to + 32 * c, x);
+                tmem_ld_wait32(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * a);
+                tmem_st32(to + 32 * c, x);
+              }
+            }
+            pass();
+          }
+          float s0, s1;
+          asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum));
+          l += s0 + s1;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = pk[32 * c + i];
+            tmem_st32(ts + 32 * c, x);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.p_full[tile]);
+        }
+        if (!ok) break;
+        // ---- the row's result
+        if (!mbar_wait(&sh.o_full[tile], o_phase, abort, p.status)) break;
+        o_phase ^= 1;
+        tc_fence_after();
+        const bool cut0 = w.t0 > 0, cut1 = w.t1 < w.tiles;
+        if (!cut0 && !cut1) {
+          const float vg = p.c.vg ? __ldg(p.c.vg + w.h) : 1.0f;
+          const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+          const int64_t orow = out_row(p, w.s.first, w.h, in ? row : row0);
+          uint4* out = reinterpret_cast<uint4*>(p.out + orow * D);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(to + 32 * c, x);
+            tmem_ld_wait32(x);
+            uint32_t y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 v2 = __floats2bfloat162_rn(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
+              y[i] = *reinterpret_cast<const uint32_t*>(&v2);
+            }
+            if (in)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) out[4 * c + i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          }
+          if (in && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+        } else {
+          const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRows + 128 * tile + r;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(to + 32 * c, x);
+            tmem_ld_wait32(x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(p.po + pr * D + 32 * c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          }
+          p.pm[pr] = m;
+          p.pl[pr] = l;
+        }
+        tc_fence_before();
+      }
+      if (tid == 0) {
+        if (w.t0 > 0) rec.cont = 1, rec.cont_more = w.t1 < w.tiles;
+        else if (w.t1 < w.tiles) rec.start = 1, rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
+      }
+    } while (w.next(p));
+    if (tid == 0) p.rec[blockIdx.x] = rec;
+  } else if (warp < 12) {
+    // ---------------- codes -> key and value tiles ----------------
+    const int t = tid - 256;
+    int use = 0;
+    bool ok = true;
+    do {
+      const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
+      const int last = last_seen(p, w.s, w.qt);
+      Codes<D> x, y;
+      fetch<D>(p, p.c.kc, p.c.ks, table, w.h, w.t0, last, t, x);
+      for (int j = w.t0; j < w.t1 && ok; ++j, ++use) {
+        const int st = use & 1;
+        const uint32_t parity = ((use >> 1) - 1) & 1;
+        fetch<D>(p, p.c.vc, p.c.vs, table, w.h, j, last, t, y);
+        if (use >= 2 && !mbar_wait(&sh.k_empty[st], parity, abort, p.status)) {
+          ok = false;
+          break;
+        }
+        convert<D>(x, sh.k[st], t);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.k_full[st]);
+        if (j + 1 < w.t1) fetch<D>(p, p.c.kc, p.c.ks, table, w.h, j + 1, last, t, x);
+        if (use >= 2 && !mbar_wait(&sh.v_empty[st], parity, abort, p.status)) {
+          ok = false;
+          break;
+        }
+        convert<D>(y, sh.v[st], t);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.v_full[st]);
+      }
+    } while (ok && w.next(p));
+  } else {
+    // ---------------- MMA issuer ----------------
+    if (elect_one()) {
+      constexpr uint32_t id_s = make_idesc(kFmtF16, kFmtF16, 128, kTok);
+      constexpr uint32_t id_o = make_idesc_major(kFmtF16, kFmtF16, 128, D, false, true);
+      int use = 0, use0 = 0;
+      uint32_t p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+      bool ok = true;
+      do {
+        const int tiles = w.qt * kRows + 128 < w.s.n * p.G ? 2 : 1;  // row tiles with rows
+        const int n = w.t1 - w.t0;
+        use0 = use;
+        auto scores = [&](int i, int st) {
+          const uint32_t a = smem_u32(sh.q[i]), b = smem_u32(sh.k[st]);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
+            mma_bf16_ss(tmem + 128 * i, sw128_desc(a + off), sw128_desc(b + off), id_s, k > 0);
+          }
+          mma_commit(&sh.s_full[i]);
+        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+          if (!ok || !mbar_wait(bar, parity, abort, p.status)) {
+            ok = false;
+            return false;
+          }
+          tc_fence_after();
+          return true;
+        };
+        for (int i = 0; i < tiles; ++i) {
+          if (!wait(&sh.q_full[i], q_phase[i])) break;
+          q_phase[i] ^= 1;
+          if (i == 0 && !wait(&sh.k_full[use & 1], (use >> 1) & 1)) break;
+          scores(i, use & 1);
+        }
+        if (ok) mma_commit(&sh.k_empty[use & 1]);
+        for (int j = 0; j < n && ok; ++j, ++use) {
+          const int st = use & 1;
+          for (int i = 0; i < tiles; ++i) {
+            if (!wait(&sh.p_full[i], p_phase[i])) break;
+            p_phase[i] ^= 1;
+            if (i == 0 && !wait(&sh.v_full[st], (use >> 1) & 1)) break;
+            uint64_t b[8];
+            const uint32_t v = smem_u32(sh.v[st]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = sw128_mn_desc(v + k * 2048, 128 * 128);
+            mma8_ts(tmem + 256 + 128 * i, tmem + 128 * i, b, id_o, j > 0);
+            if (i + 1 == tiles) mma_commit(&sh.v_empty[st]);
+            if (j + 1 == n) mma_commit(&sh.o_full[i]);
+            else {
+              const int su = use + 1;
+              if (i == 0 && !wait(&sh.k_full[su & 1], (su >> 1) & 1)) break;
+              scores(i, su & 1);
+              if (i + 1 == tiles) mma_commit(&sh.k_empty[su & 1]);
+            }
+          }
+        }
+        use = use0 + n;
+      } while (ok && w.next(p));
+      mma_commit(&sh.done);
+      volatile int no_abort = 0;
+      mbar_wait(&sh.done, 0, &no_abort, p.status);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+namespace {
+
+template <int D>
+cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
+  constexpr int smem = static_cast<int>(sizeof(Smem<D>)) + 1024;
+  static_assert(smem <= 227 * 1024, "shared memory");
+  const cudaError_t at = cudaFuncSetAttribute(attn_nvfp4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (at != cudaSuccess) return at;
+  int dev = 0, sms = kSMs;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int grid = sms < kMaxSms ? sms : kMaxSms;
+  const Params p = make_params(a, ws, grid, kRows);
+  attn_nvfp4_tc_kernel<D><<<grid, kThreads, smem, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  join_kernel<D, kRows><<<dim3(grid, kRows / 8), 256, 0, stream>>>(p, grid);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attention_nvfp4_tc_ws_bytes(int D) { return ws_bytes(D, kMaxSms, kRows); }
+
+cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
+  return a.c.D == 128 ? launch<128>(a, ws, stream) : launch<64>(a, ws, stream);
+}
+
+}  // namespace qrr
