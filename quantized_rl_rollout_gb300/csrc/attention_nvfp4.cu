@@ -162,7 +162,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
     uint32_t w[D / 8] = {};
     uint32_t mx = 0u;
     if (in) {
-      const uint16_t* src = p.q + (it.first + r / p.G) * p.ld_q + static_cast<int64_t>(it.h * p.G + r % p.G) * D + c * (D / 4);
+      const uint16_t* src = p.q + (it.first + p.byG.div(r)) * p.ld_q + static_cast<int64_t>(it.h * p.G + p.byG.mod(r)) * D + c * (D / 4);
 #pragma unroll
       for (int i = 0; i < D / 32; ++i) {
         const uint4 x = __ldg(reinterpret_cast<const uint4*>(src) + i);
@@ -180,7 +180,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
 #pragma unroll
       for (int i = 0; i < 2; ++i) s.q[nt][j][i] = f16x2(sc(bf16_lo(w[2 * j + i])), sc(bf16_hi(w[2 * j + i])));
     const float f = p.scale * kLog2e * kg * ldexpf(1.0f, e);
-    const int lim = in ? min(it.pos + r / p.G, it.last) : -1;
+    const int lim = in ? min(it.pos + p.byG.div(r), it.last) : -1;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       s.f[nt][x] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * c + x));
@@ -369,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4
     // what the rows of this tile see at most, and at least (rows behind the
     // last one are never read again: they need no mask)
     const int r_end = min((it.rt + 1) * RT, it.n * p.G);
-    const int see = min(it.pos + (r_end - 1) / p.G, it.last);
-    const int sure = min(it.pos + it.rt * RT / p.G, it.last);
+    const int see = min(it.pos + p.byG.div(r_end - 1), it.last);
+    const int sure = min(it.pos + p.byG.div(it.rt * RT), it.last);
     const int stop = min(t1, (see + 16) >> 4);
     const int32_t* table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
     Tile<D> x, y;

@@ -65,12 +65,28 @@ struct Record {
   int rt, h, first, n;  // its row tile, KV head, the sequence's rows
 };
 
+// x / d for 0 <= x < 2^31 by a multiplication (T. Granlund, P. Montgomery,
+// "Division by invariant integers using multiplication", PLDI 1994).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d_) : d(d_), mul(0), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int div(int x) const {
+    return static_cast<int>((__umulhi(mul, static_cast<uint32_t>(x)) + static_cast<uint32_t>(x)) >> shift);
+  }
+  __device__ __forceinline__ int mod(int x) const { return x - div(x) * static_cast<int>(d); }
+};
+
 struct Params {
   KvNvfp4 c;
   KvRows r;
   const uint16_t* q;
   int64_t ld_q;
   int Hq, G, max_new;
+  FastDiv byG;
   float scale;
   uint16_t* out;
   float* lse;
@@ -98,7 +114,7 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
 
 // Output row of row `row` (token row / G, head of the group row % G).
 __device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, int row) {
-  return static_cast<int64_t>(first + row / p.G) * p.Hq + h * p.G + row % p.G;
+  return static_cast<int64_t>(first + p.byG.div(row)) * p.Hq + h * p.G + p.byG.mod(row);
 }
 
 // Joins the pieces of the item that starts in range k = blockIdx.x and is
@@ -141,7 +157,8 @@ inline size_t ws_bytes(int D, int ranges, int rt) {
   return align256(sizeof(Record) * ranges) + 2 * align256(rows * 4) + align256(rows * D * 4);
 }
 inline Params make_params(const AttnNvfp4Args& a, uint8_t* w, int ranges, int rt) {
-  Params p{a.c, a.r, a.q, a.ld_q, a.Hq, a.Hq / a.c.Hkv, a.max_new, a.scale, a.out, a.lse};
+  const int G = a.Hq / a.c.Hkv;
+  Params p{a.c, a.r, a.q, a.ld_q, a.Hq, G, a.max_new, FastDiv(static_cast<uint32_t>(G)), a.scale, a.out, a.lse};
   const size_t rows = static_cast<size_t>(2) * ranges * rt;
   p.rec = reinterpret_cast<Record*>(w);
   w += align256(sizeof(Record) * ranges);

@@ -46,6 +46,9 @@ template <int D>
 struct Smem {
   static constexpr int kTile = 128 * D * 2;  // bytes of a query, key or value tile
   uint8_t q[2][kTile], k[2][kTile], v[2][kTile];
+  // codes and scales of the next three key or value tiles
+  uint8_t raw[3][64 * D];
+  uint8_t raw_s[3][8 * D];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done;
   uint32_t tmem;
   int abort;
@@ -68,6 +71,12 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
                  "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
 // Items of a sequence: row tiles of 256 (none if it has few rows), and the key
 // tiles of one (at least 1).
 __device__ __forceinline__ int row_tiles(const Params& p, const Seq& s) {
@@ -75,7 +84,7 @@ __device__ __forceinline__ int row_tiles(const Params& p, const Seq& s) {
   return rows <= kFewRows ? 0 : static_cast<int>((rows + kRows - 1) / kRows);
 }
 __device__ __forceinline__ int last_seen(const Params& p, const Seq& s, int qt) {
-  return min(s.pos + (min((qt + 1) * kRows, s.n * p.G) - 1) / p.G, s.last);
+  return min(s.pos + p.byG.div(min((qt + 1) * kRows, s.n * p.G) - 1), s.last);
 }
 __device__ __forceinline__ int key_tiles(const Params& p, const Seq& s, int qt) {
   return max(1, (last_seen(p, s, qt) + kTok) / kTok);
@@ -105,14 +114,31 @@ struct Walk {
     left = left_;
     s = seq_of(p, b);
     qts = row_tiles(p, s);
-    int per = 0;  // of one head
-    for (int i = 0; i < qts; ++i) per += key_tiles(p, s, i);
+    const int lane = threadIdx.x & 31;
+    const int64_t per = seq_key_tiles(p, b, lane);  // of one head
     h = static_cast<int>(off / per);
-    int rest = static_cast<int>(off - static_cast<int64_t>(h) * per);
-    for (qt = 0; qt + 1 < qts; ++qt) {
-      const int n = key_tiles(p, s, qt);
-      if (rest < n) break;
-      rest -= n;
+    int rest = static_cast<int>(off - h * per);
+    for (qt = 0;; qt += 32) {  // 32 row tiles at a time
+      const int own = qt + lane < qts ? key_tiles(p, s, qt + lane) : 0;
+      int incl = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t in = __ballot_sync(0xFFFFFFFFu, rest >= incl - own && rest < incl);
+      if (in) {
+        const int k = __ffs(static_cast<int>(in)) - 1;
+        rest -= __shfl_sync(0xFFFFFFFFu, incl - own, k);
+        qt += k;
+        break;
+      }
+      rest -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+      if (qt + 32 >= qts) {  // not reached: off lies in the sequence
+        qt = max(qts - 1, 0);
+        rest = 0;
+        break;
+      }
     }
     t0 = rest;
     piece(p);
@@ -139,65 +165,97 @@ struct Walk {
 
 // ---- codes -> f16 tiles ------------------------------------------------------
 
-// What a thread of the four converting warps holds of a tile: of every pass,
-// one chunk of 32 values of one token.
+// The converting warps' own walk, ahead of the tiles that they convert: the
+// codes and scales of a key or value tile into slot `slot` of the raw ring by
+// asynchronous copies.  A warp copies what it will convert itself: in pass i
+// rows [32 i + 8 warp, + 8) (D = 64: two groups of 8), a lane's chunk of 32
+// values of row lane % 8.
 template <int D>
-struct Codes {
-  static constexpr int kPerRow = D / 32, kRowsPass = 128 / kPerRow;
-  uint4 w[kPerRow];
-  uint32_t s[kPerRow];  // its two block scales
-};
-
-template <int D>
-__device__ __forceinline__ void fetch(const Params& p, const uint8_t* codes, const uint8_t* scales, const int32_t* table,
-                                      int h, int tile, int last, int tid, Codes<D>& x) {
-  using C = Codes<D>;
-  const int c = tid % C::kPerRow, r0 = tid / C::kPerRow;
-#pragma unroll
-  for (int i = 0; i < C::kPerRow; ++i) {
-    const int tok = tile * kTok + i * C::kRowsPass + r0;
-    x.w[i] = make_uint4(0u, 0u, 0u, 0u);
-    x.s[i] = 0u;
-    if (tok <= last) {
-      const int pg = __ldg(table + (tok >> p.c.page_shift));
-      if (pg >= 0 && pg < p.c.num_pages) {
-        const int64_t row = kv_row(p.c, pg, h, tok & ((1 << p.c.page_shift) - 1));
-        x.w[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * (D / 2)) + c);
-        x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + row * (D / 16)) + c);
-      } else {
-        flag(p.status, QRR_DEV_BAD_INDEX);
-      }
-    }
+struct Feed {
+  static constexpr int kPasses = D / 32, kRowsPass = 128 / kPasses;
+  Walk w;
+  int j, slot, last;
+  bool value, more;
+  int64_t row[kPasses];  // cache rows of the lane, -1 for none
+  __device__ __forceinline__ static int chunk(int t) { return (t >> 3) % kPasses; }
+  __device__ __forceinline__ static int row_of(int t, int i) {
+    const int lane = t & 31;
+    return i * kRowsPass + (t >> 5) * (kRowsPass / 4) + (lane & 7) + (D == 64 ? 8 * (lane >> 4) : 0);
   }
-}
+  __device__ __forceinline__ void begin(const Params& p, const Walk& from) {
+    w = from;
+    j = w.t0;
+    last = last_seen(p, w.s, w.qt);
+    slot = 0;
+    value = false;
+    more = true;
+  }
+  __device__ __forceinline__ void issue(const Params& p, Smem<D>& sh, int t) {
+    if (more) {
+      if (!value) {
+        const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+          const int tok = j * kTok + row_of(t, i);
+          row[i] = -1;
+          if (tok <= last) {
+            const int pg = __ldg(table + (tok >> p.c.page_shift));
+            if (pg >= 0 && pg < p.c.num_pages) row[i] = kv_row(p.c, pg, w.h, tok & ((1 << p.c.page_shift) - 1));
+            else flag(p.status, QRR_DEV_BAD_INDEX);
+          }
+        }
+      }
+      const uint8_t* codes = value ? p.c.vc : p.c.kc;
+      const uint8_t* scales = value ? p.c.vs : p.c.ks;
+      const int c = chunk(t);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        // a row that is not there is filled with zeros
+        const uint32_t to = smem_u32(sh.raw[slot] + (i * 128 + t) * 16);
+        const int n = row[i] >= 0 ? 16 : 0;
+        const int64_t at = row[i] >= 0 ? row[i] : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(codes + at * (D / 2) + c * 16), "r"(n)
+                     : "memory");
+        if (c == 0) {
+          const uint32_t ts = smem_u32(sh.raw_s[slot] + row_of(t, i) * (D / 16));
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(ts), "l"(scales + at * (D / 16)), "n"(D / 16),
+                       "r"(n ? D / 16 : 0)
+                       : "memory");
+        }
+      }
+      slot = slot == 2 ? 0 : slot + 1;
+      if (value && ++j == w.t1) {
+        more = w.next(p);
+        j = w.t0;
+        last = last_seen(p, w.s, w.qt);
+      }
+      value = !value;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
 
 // Row r of a tile lies at 128 r in each of its D / 64 column halves of 16 KB,
 // its 16-byte pieces at their index exclusive-or r % 8.
 template <int D>
-__device__ __forceinline__ void convert(const Codes<D>& x, uint8_t* tile, int tid) {
-  using C = Codes<D>;
-  const int c = tid % C::kPerRow, r0 = tid / C::kPerRow;
+__device__ __forceinline__ void convert(const Smem<D>& sh, int slot, uint8_t* tile, int t) {
+  using F = Feed<D>;
+  const int c = F::chunk(t), x = t & 7;
+  uint8_t* half = tile + (c >> 1) * (128 * 128);
 #pragma unroll
-  for (int i = 0; i < C::kPerRow; ++i) {
-    const int r = i * C::kRowsPass + r0;
-    const uint32_t s2 = e4m3x2_to_f16x2(x.s[i]);
-    const uint32_t w[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
-    uint4 o[4];
+  for (int i = 0; i < F::kPasses; ++i) {
+    const int r = F::row_of(t, i);
+    const uint4 w4 = *reinterpret_cast<const uint4*>(sh.raw[slot] + (i * 128 + t) * 16);
+    const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sh.raw_s[slot] + r * (D / 16) + 2 * c));
+    const uint32_t sc[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
+    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t f[4];
       f16x2x4_from_e2m1x8(w[k], f);
-      const uint32_t sc = __byte_perm(s2, s2, k < 2 ? 0x1010 : 0x3232);
-      o[k] = make_uint4(hmul2(f[0], sc), hmul2(f[1], sc), hmul2(f[2], sc), hmul2(f[3], sc));
-    }
-    uint8_t* half = tile + (c >> 1) * (128 * 128) + r * 128;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // the two column halves have the same banks: their lanes write in another order
-      const bool swap = (c >> 1) != 0;
-      const uint4 y = swap ? o[k ^ 2] : o[k];
-      const int piece = (4 * (c & 1) + k) ^ (swap ? 2 : 0);
-      *reinterpret_cast<uint4*>(half + ((piece ^ (r & 7)) << 4)) = y;
+      const uint32_t s = sc[k >> 1];
+      *reinterpret_cast<uint4*>(half + r * 128 + (((4 * (c & 1) + k) ^ x) << 4)) =
+          make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
     }
   }
 }
@@ -211,18 +269,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // 32 scores of a row -> weights 2^(s f - m): f16 pairs, their fp32 sums, the
-// largest score.  MASK: only the first `n` of them are seen.
-template <bool MASK>
-__device__ __forceinline__ void weights(uint32_t (&r)[32], int n, uint64_t f2, uint64_t nm2, float& mx, uint64_t& sum,
-                                        uint32_t* out) {
+// largest score.
+__device__ __forceinline__ void weights(const uint32_t (&r)[32], uint64_t f2, uint64_t nm2, float& top, uint64_t& sum,
+                                        uint32_t (&out)[16]) {
+  float mx[2] = {-INFINITY, -INFINITY};
+  uint64_t acc[2] = {0ull, 0ull};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float a = __uint_as_float(r[2 * i]), b = __uint_as_float(r[2 * i + 1]);
-    if (MASK) {
-      a = 2 * i < n ? a : -INFINITY;
-      b = 2 * i + 1 < n ? b : -INFINITY;
-    }
-    mx = max3(mx, a, b);
+    mx[i & 1] = max3(mx[i & 1], a, b);
     uint64_t x;
     asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
     asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(f2), "l"(nm2));
@@ -230,9 +285,11 @@ __device__ __forceinline__ void weights(uint32_t (&r)[32], int n, uint64_t f2, u
     a = ex2(a);
     b = ex2(b);
     asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
-    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(x));
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc[i & 1]) : "l"(x));
     out[i] = f16x2(a, b);
   }
+  top = fmaxf(mx[0], mx[1]);
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(sum) : "l"(acc[0]), "l"(acc[1]));
 }
 
 __device__ __forceinline__ uint64_t twice(float x) {
@@ -331,6 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     const int tile = warp >> 2, r = tid & 127;
     const uint32_t ts = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 128 * tile;
     const uint32_t to = ts + 256;
+    // the warp's 32 rows of the query tile, by 16-byte pieces: lanes `sub` and
+    // `piece` of a copy of kAtOnce rows
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+    const int piece = lane % kLanes, sub = lane / kLanes;
+    uint8_t* const stage = sh.q[tile];
+    auto at = [&](int rr, int pc) { return stage + (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4); };
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true;
     do {
@@ -338,24 +401,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
       if (row0 < rows) {
         const int row = row0 + r;
         const bool in = row < rows;
-        // ---- the query row, as f16
+        // ---- the warp's query rows: copied as they are, kLanes lanes a row,
+        // then turned into f16 in place, a thread a row.  (Loops that run once
+        // a piece are kept rolled: straight code would wait for its own
+        // instructions, 9000 cycles in the place of 2500.)
+        {
+#pragma unroll 2
+          for (int i = 0; i < kLanes; ++i) {
+            const int rr = 32 * (warp & 3) + i * kAtOnce + sub, rq = row0 + rr;
+            const bool there = rq < rows;
+            const uint16_t* src = p.q + (w.s.first + p.byG.div(there ? rq : 0)) * p.ld_q +
+                                  static_cast<int64_t>(w.h * p.G + p.byG.mod(there ? rq : 0)) * D + piece * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at(rr, piece))), "l"(src),
+                         "r"(there ? 16 : 0)
+                         : "memory");
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+        }
         uint32_t mx = 0u;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            p.q + (w.s.first + row / p.G) * p.ld_q + static_cast<int64_t>(w.h * p.G + row % p.G) * D);
-        if (in)
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) mx = max(mx, absmax_bits8(__ldg(src + i)));
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) mx = max(mx, absmax_bits8(*reinterpret_cast<const uint4*>(at(r, i))));
         if (mx >= 0x7F80u) flag(p.status, QRR_DEV_NONFINITE);
         const int e = query_exp(mx);
         const Pow2Scaler sc(e);
-        uint8_t* dst = sh.q[tile] + r * 128;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (in) x = __ldg(src + i);
-          const uint4 y = make_uint4(f16x2(sc(bf16_lo(x.x)), sc(bf16_hi(x.x))), f16x2(sc(bf16_lo(x.y)), sc(bf16_hi(x.y))),
-                                     f16x2(sc(bf16_lo(x.z)), sc(bf16_hi(x.z))), f16x2(sc(bf16_lo(x.w)), sc(bf16_hi(x.w))));
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * (128 * 128) + (((i & 7) ^ (r & 7)) << 4)) = y;
+#pragma unroll 2
+        for (int i = 0; i < kLanes; ++i) {
+          uint4* y = reinterpret_cast<uint4*>(at(r, i));
+          const uint4 x = *y;
+          *y = make_uint4(f16x2(sc(bf16_lo(x.x)), sc(bf16_hi(x.x))), f16x2(sc(bf16_lo(x.y)), sc(bf16_hi(x.y))),
+                          f16x2(sc(bf16_lo(x.z)), sc(bf16_hi(x.z))), f16x2(sc(bf16_lo(x.w)), sc(bf16_hi(x.w))));
         }
         fence_async_shared();
         __syncwarp();
@@ -364,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         const float f = fmaxf(p.scale * kLog2e * (p.c.kg ? __ldg(p.c.kg + w.h) : 1.0f) * ldexpf(1.0f, e), 1.17549435e-38f);
         const uint64_t f2 = twice(f);
         // rows behind the last one are never read: they need no mask
-        const int lim = in ? min(w.s.pos + row / p.G, w.s.last) : 0x7FFFFFFF;
+        const int lim = in ? min(w.s.pos + p.byG.div(row), w.s.last) : 0x7FFFFFFF;
         const int lim_warp = __reduce_min_sync(0xFFFFFFFFu, lim);
         float m = kNone, l = 0.0f;
         for (int j = w.t0; j < w.t1 && ok; ++j) {
@@ -376,50 +451,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
           tc_fence_after();
           const int seen = lim - kTok * j + 1;  // of this tile's tokens
           const bool mask = kTok * j + kTok - 1 > lim_warp;
-          uint32_t pk[64];
-          float top;
-          uint64_t sum;
-          auto pass = [&] {
-            top = -INFINITY;
-            sum = 0ull;
-            const uint64_t nm2 = twice(-m);
+          // 32 columns at a time; weights 32 c .. 32 c + 31 go to the columns
+          // 16 c .. 16 c + 15, whose scores have been loaded by then
+          auto chunk = [&](uint32_t (&x)[32], int c) {
+            if (mask)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              tmem_ld32(ts + 32 * c, x);
-              tmem_ld_wait32(x);
-              if (mask) weights<true>(x, seen - 32 * c, f2, nm2, top, sum, pk + 16 * c);
-              else weights<false>(x, 0, f2, nm2, top, sum, pk + 16 * c);
-            }
-          };
-          pass();
-          const bool move = top * f > m + kRoom;
-          if (__any_sync(0xFFFFFFFFu, move)) {
-            const float m1 = move ? top * f - kLift : m, a = ex2(m - m1);
-            m = m1;
-            l *= a;
-            if (j > w.t0) {
+              for (int i = 0; i < 32; ++i) x[i] = i < seen - 32 * c ? x[i] : 0xFF800000u;
+            uint32_t y[16];
+            float top;
+            uint64_t sum;
+            while (true) {
+              weights(x, f2, twice(-m), top, sum, y);
+              const bool move = top * f > m + kRoom;
+              if (!__any_sync(0xFFFFFFFFu, move)) break;
+              // a new reference: scale what the row has so far, and form the
+              // chunk's weights again
+              const float m1 = move ? top * f - kLift : m, a = ex2(m - m1);
+              m = m1;
+              l *= a;
+              const uint32_t a2 = f16x2(a, a);
+#pragma unroll 1
+              for (int k = 0; k < c; ++k) {
+                uint32_t z[16];
+                tmem_ld16(ts + 16 * k, z);
+                tmem_ld_wait16(z);
 #pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld32(to + 32 * c, x);
-                tmem_ld_wait32(x);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * a);
-                tmem_st32(to + 32 * c, x);
+                for (int i = 0; i < 16; ++i) z[i] = hmul2(z[i], a2);
+                tmem_st16(ts + 16 * k, z);
               }
+              if (j > w.t0)
+#pragma unroll 1
+                for (int k = 0; k < D / 16; ++k) {
+                  uint32_t z[16];
+                  tmem_ld16(to + 16 * k, z);
+                  tmem_ld_wait16(z);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) z[i] = __float_as_uint(__uint_as_float(z[i]) * a);
+                  tmem_st16(to + 16 * k, z);
+                }
+              tmem_st_wait();
             }
-            pass();
-          }
-          float s0, s1;
-          asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum));
-          l += s0 + s1;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = pk[32 * c + i];
-            tmem_st32(ts + 32 * c, x);
+            float s0, s1;
+            asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(sum));
+            l += s0 + s1;
+            tmem_st16(ts + 16 * c, y);
+          };
+          uint32_t xa[32], xb[32];
+          tmem_ld32(ts, xa);
+          tmem_ld_wait32(xa);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+            tmem_ld32(ts + 32 * c + 32, xb);
+            chunk(xa, c);
+            tmem_ld_wait32(xb);
+            tmem_ld32(ts + 64, xa);  // (the last time for nothing)
+            chunk(xb, c + 1);
+            tmem_ld_wait32(xa);
           }
           tmem_st_wait();
           tc_fence_before();
@@ -431,13 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         if (!mbar_wait(&sh.o_full[tile], o_phase, abort, p.status)) break;
         o_phase ^= 1;
         tc_fence_after();
+        // through the warp's rows of the query tile, which no MMA reads any
+        // more, so that lanes store neighbouring bytes
         const bool cut0 = w.t0 > 0, cut1 = w.t1 < w.tiles;
         if (!cut0 && !cut1) {
           const float vg = p.c.vg ? __ldg(p.c.vg + w.h) : 1.0f;
           const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
-          const int64_t orow = out_row(p, w.s.first, w.h, in ? row : row0);
-          uint4* out = reinterpret_cast<uint4*>(p.out + orow * D);
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
             tmem_ld32(to + 32 * c, x);
@@ -448,25 +535,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
               const __nv_bfloat162 v2 = __floats2bfloat162_rn(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
               y[i] = *reinterpret_cast<const uint32_t*>(&v2);
             }
-            if (in)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) out[4 * c + i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(at(r, 4 * c + i)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
-          if (in && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+          if (in && p.lse) p.lse[out_row(p, w.s.first, w.h, row)] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+          __syncwarp();
+#pragma unroll 2
+          for (int i = 0; i < kLanes; ++i) {
+            const int rr = 32 * (warp & 3) + i * kAtOnce + sub;
+            if (row0 + rr < rows)
+              reinterpret_cast<uint4*>(p.out + out_row(p, w.s.first, w.h, row0 + rr) * D)[piece] =
+                  *reinterpret_cast<const uint4*>(at(rr, piece));
+          }
         } else {
-          const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRows + 128 * tile + r;
+          const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRows + 128 * tile;
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll 1
+            for (int c = 0; c < D / 64; ++c) {
+              uint32_t x[32];
+              tmem_ld32(to + (D / 2) * half + 32 * c, x);
+              tmem_ld_wait32(x);
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld32(to + 32 * c, x);
-            tmem_ld_wait32(x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(p.po + pr * D + 32 * c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(at(r, 8 * c + i)) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            }
+            __syncwarp();
+#pragma unroll 2
+            for (int i = 0; i < kLanes; ++i) {
+              const int rr = 32 * (warp & 3) + i * kAtOnce + sub;
+              reinterpret_cast<uint4*>(p.po + (pr + rr) * D + (D / 2) * half)[piece] = *reinterpret_cast<const uint4*>(at(rr, piece));
+            }
+            __syncwarp();
           }
-          p.pm[pr] = m;
-          p.pl[pr] = l;
+          p.pm[pr + r] = m;
+          p.pl[pr + r] = l;
         }
+        __syncwarp();
         tc_fence_before();
       }
       if (tid == 0) {
@@ -478,36 +584,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
   } else if (warp < 12) {
     // ---------------- codes -> key and value tiles ----------------
     const int t = tid - 256;
-    int use = 0;
+    Feed<D> feed;
+    feed.begin(p, w);
+    feed.issue(p, sh, t);
+    feed.issue(p, sh, t);
+    int use = 0, slot = 0;
     bool ok = true;
+    auto half = [&](uint8_t* tile, uint64_t* empty, uint64_t* full) {
+      feed.issue(p, sh, t);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      __syncwarp();
+      if (use >= 2 && !mbar_wait(empty, ((use >> 1) - 1) & 1, abort, p.status)) return false;
+      convert<D>(sh, slot, tile, t);
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full);
+      slot = slot == 2 ? 0 : slot + 1;
+      return true;
+    };
     do {
-      const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
-      const int last = last_seen(p, w.s, w.qt);
-      Codes<D> x, y;
-      fetch<D>(p, p.c.kc, p.c.ks, table, w.h, w.t0, last, t, x);
       for (int j = w.t0; j < w.t1 && ok; ++j, ++use) {
         const int st = use & 1;
-        const uint32_t parity = ((use >> 1) - 1) & 1;
-        fetch<D>(p, p.c.vc, p.c.vs, table, w.h, j, last, t, y);
-        if (use >= 2 && !mbar_wait(&sh.k_empty[st], parity, abort, p.status)) {
-          ok = false;
-          break;
-        }
-        convert<D>(x, sh.k[st], t);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.k_full[st]);
-        if (j + 1 < w.t1) fetch<D>(p, p.c.kc, p.c.ks, table, w.h, j + 1, last, t, x);
-        if (use >= 2 && !mbar_wait(&sh.v_empty[st], parity, abort, p.status)) {
-          ok = false;
-          break;
-        }
-        convert<D>(y, sh.v[st], t);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.v_full[st]);
+        ok = half(sh.k[st], &sh.k_empty[st], &sh.k_full[st]) && half(sh.v[st], &sh.v_empty[st], &sh.v_full[st]);
       }
     } while (ok && w.next(p));
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ---------------- MMA issuer ----------------
     if (elect_one()) {
