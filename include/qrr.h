@@ -388,7 +388,7 @@ qrr_status qrr_kv_read_nvfp4(const qrr_kv_nvfp4* cache, int64_t T, const int32_t
  *            with more rows raises QRR_DEV_BAD_INDEX, its outputs unspecified
  *   out  bf16 [T][Hq][D];  lse fp32 [T][Hq] or NULL
  *   workspace  qrr_attention_nvfp4_workspace_bytes(cache, T, Hq, max_new)
- * Hq a multiple of Hkv.  Cached values convert exactly; the query is carried
+ * Hq a multiple of Hkv, T * Hq < 2^31.  Cached values convert exactly; the query is carried
  * in f16 after a power of two a row (exact for values within 2^-29 of the
  * row's largest); p is rounded to f16, all sums are fp32.  Work is cut over
  * the cached tokens and joined in a fixed order: results do not depend on

@@ -841,6 +841,7 @@ qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t
   if (Hq < 0 || cache->Hkv <= 0 || max_new < 0 || (!cu && max_new != 1)) return QRR_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || scale == INFINITY) return QRR_ERR_INVALID_ARG;
   if (Hq % cache->Hkv != 0 || max_new > kMaxTokens / (Hq > 0 ? Hq : 1)) return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (T * Hq > INT32_MAX) return QRR_ERR_UNSUPPORTED_SHAPE;  // rows of out and lse
   const int64_t row = static_cast<int64_t>(Hq) * cache->D;
   if (T * row > 0 && (!q || !out)) return QRR_ERR_INVALID_ARG;
   if (T > 1 && ld_q < row) return QRR_ERR_INVALID_ARG;

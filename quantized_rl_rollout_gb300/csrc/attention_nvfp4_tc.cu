@@ -16,11 +16,14 @@
 //               stores the row.
 //   8..11       codes and scales -> f16 key and value tiles in shared memory
 //               (code x block scale is exact), two stages each, 128-byte
-//               swizzled; the codes of the next tile are fetched meanwhile.
+//               swizzled.
 //   12          issues the MMAs: S_i = Q_i K^T (M128 N128), O_i += P_i V
 //               (P from tensor memory, V MN-major).  Order per key tile:
 //               PV_0, S_0 of the next, PV_1, S_1 of the next, so one tile's
 //               softmax runs under the other's MMAs.
+//   13          fetches codes and scales by bulk copies, a run of tokens in one
+//               page each, into a ring of three raw tiles (keys and values in
+//               turn), running ahead over the ends of items.
 // Tensor memory: S_0, S_1, O_0, O_1 of 128 columns each.
 //
 // A row's weights are formed with the running reference in one pass over its
@@ -35,7 +38,7 @@ using namespace attn4;
 
 namespace {
 
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr int kRows = 256;  // rows of an item
 constexpr int kTok = 128;   // tokens of a key tile
 constexpr int kMinTiles = 4;  // key tiles of a range
@@ -49,6 +52,7 @@ struct Smem {
   // codes and scales of the next three key or value tiles
   uint8_t raw[3][64 * D];
   uint8_t raw_s[3][8 * D];
+  uint64_t raw_full[3], raw_empty[3];
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done;
   uint32_t tmem;
   int abort;
@@ -165,100 +169,50 @@ struct Walk {
 
 // ---- codes -> f16 tiles ------------------------------------------------------
 
-// The converting warps' own walk, ahead of the tiles that they convert: the
-// codes and scales of a key or value tile into slot `slot` of the raw ring by
-// asynchronous copies.  A warp copies what it will convert itself: in pass i
-// rows [32 i + 8 warp, + 8) (D = 64: two groups of 8), a lane's chunk of 32
-// values of row lane % 8.
+// A lane's share of a raw tile, and its conversion.  Row r of a tile lies at
+// 128 r in each of its D / 64 column halves of 16 KB, its 16-byte pieces at
+// their index exclusive-or r % 8.  A thread takes a chunk of 32 values of one
+// row in each of D / 32 passes.
 template <int D>
-struct Feed {
+struct Codes {
   static constexpr int kPasses = D / 32, kRowsPass = 128 / kPasses;
-  Walk w;
-  int j, slot, last;
-  bool value, more;
-  int64_t row[kPasses];  // cache rows of the lane, -1 for none
-  __device__ __forceinline__ static int chunk(int t) { return (t >> 3) % kPasses; }
-  __device__ __forceinline__ static int row_of(int t, int i) {
-    const int lane = t & 31;
-    return i * kRowsPass + (t >> 5) * (kRowsPass / 4) + (lane & 7) + (D == 64 ? 8 * (lane >> 4) : 0);
-  }
-  __device__ __forceinline__ void begin(const Params& p, const Walk& from) {
-    w = from;
-    j = w.t0;
-    last = last_seen(p, w.s, w.qt);
-    slot = 0;
-    value = false;
-    more = true;
-  }
-  __device__ __forceinline__ void issue(const Params& p, Smem<D>& sh, int t) {
-    if (more) {
-      if (!value) {
-        const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
+  uint4 w[kPasses];
+  uint32_t s[kPasses];  // the chunk's two block scales
+  // rows from `live` on have no token: their scales count as zero (what lies
+  // there may be anything)
+  __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, int live, int t) {
+    const int c = t % kPasses;
 #pragma unroll
-        for (int i = 0; i < kPasses; ++i) {
-          const int tok = j * kTok + row_of(t, i);
-          row[i] = -1;
-          if (tok <= last) {
-            const int pg = __ldg(table + (tok >> p.c.page_shift));
-            if (pg >= 0 && pg < p.c.num_pages) row[i] = kv_row(p.c, pg, w.h, tok & ((1 << p.c.page_shift) - 1));
-            else flag(p.status, QRR_DEV_BAD_INDEX);
-          }
-        }
-      }
-      const uint8_t* codes = value ? p.c.vc : p.c.kc;
-      const uint8_t* scales = value ? p.c.vs : p.c.ks;
-      const int c = chunk(t);
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        // a row that is not there is filled with zeros
-        const uint32_t to = smem_u32(sh.raw[slot] + (i * 128 + t) * 16);
-        const int n = row[i] >= 0 ? 16 : 0;
-        const int64_t at = row[i] >= 0 ? row[i] : 0;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(codes + at * (D / 2) + c * 16), "r"(n)
-                     : "memory");
-        if (c == 0) {
-          const uint32_t ts = smem_u32(sh.raw_s[slot] + row_of(t, i) * (D / 16));
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(ts), "l"(scales + at * (D / 16)), "n"(D / 16),
-                       "r"(n ? D / 16 : 0)
-                       : "memory");
-        }
-      }
-      slot = slot == 2 ? 0 : slot + 1;
-      if (value && ++j == w.t1) {
-        more = w.next(p);
-        j = w.t0;
-        last = last_seen(p, w.s, w.qt);
-      }
-      value = !value;
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = i * kRowsPass + t / kPasses;
+      w[i] = *reinterpret_cast<const uint4*>(codes + r * (D / 2) + 16 * c);
+      s[i] = *reinterpret_cast<const uint16_t*>(scales + r * (D / 16) + 2 * c);
+      if (r >= live) s[i] = 0u;
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  __device__ __forceinline__ void convert(uint8_t* tile, int t) const {
+    const int c = t % kPasses, r0 = t / kPasses;
+    // the two column halves have the same banks: lanes of the second one take
+    // their words in another order
+    const bool swap = c >= 2;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const int r = i * kRowsPass + r0;
+      const uint32_t s2 = e4m3x2_to_f16x2(s[i]);
+      const uint32_t sc[2] = {__byte_perm(s2, s2, swap ? 0x3232 : 0x1010), __byte_perm(s2, s2, swap ? 0x1010 : 0x3232)};
+      const uint32_t ww[4] = {swap ? w[i].z : w[i].x, swap ? w[i].w : w[i].y, swap ? w[i].x : w[i].z, swap ? w[i].y : w[i].w};
+      uint8_t* row = tile + (c >> 1) * (128 * 128) + r * 128;
+      const int x = (4 * (c & 1)) ^ (swap ? 2 : 0) ^ (r & 7);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t f[4];
+        f16x2x4_from_e2m1x8(ww[k], f);
+        const uint32_t y = sc[k >> 1];
+        *reinterpret_cast<uint4*>(row + ((x ^ k) << 4)) = make_uint4(hmul2(f[0], y), hmul2(f[1], y), hmul2(f[2], y), hmul2(f[3], y));
+      }
+    }
   }
 };
-
-// Row r of a tile lies at 128 r in each of its D / 64 column halves of 16 KB,
-// its 16-byte pieces at their index exclusive-or r % 8.
-template <int D>
-__device__ __forceinline__ void convert(const Smem<D>& sh, int slot, uint8_t* tile, int t) {
-  using F = Feed<D>;
-  const int c = F::chunk(t), x = t & 7;
-  uint8_t* half = tile + (c >> 1) * (128 * 128);
-#pragma unroll
-  for (int i = 0; i < F::kPasses; ++i) {
-    const int r = F::row_of(t, i);
-    const uint4 w4 = *reinterpret_cast<const uint4*>(sh.raw[slot] + (i * 128 + t) * 16);
-    const uint32_t s2 = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sh.raw_s[slot] + r * (D / 16) + 2 * c));
-    const uint32_t sc[2] = {__byte_perm(s2, s2, 0x1010), __byte_perm(s2, s2, 0x3232)};
-    const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t f[4];
-      f16x2x4_from_e2m1x8(w[k], f);
-      const uint32_t s = sc[k >> 1];
-      *reinterpret_cast<uint4*>(half + r * 128 + (((4 * (c & 1) + k) ^ x) << 4)) =
-          make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
-    }
-  }
-}
 
 // ---- softmax -------------------------------------------------------------------
 
@@ -298,6 +252,16 @@ __device__ __forceinline__ uint64_t twice(float x) {
   return r;
 }
 
+// Two bf16 values times a power of two, as f16.
+__device__ __forceinline__ uint32_t scaled_f16x2(uint32_t w, uint64_t sc) {
+  uint64_t x;
+  float a, b;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(bf16_lo(w)), "f"(bf16_hi(w)));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(sc));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+  return f16x2(a, b);
+}
+
 }  // namespace
 
 template <int D>
@@ -317,6 +281,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
   }
   if (lane == 0) sh.part[warp] = mine;
   if (tid == 0) {
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 4);
       mbar_init(&sh.k_full[i], 4);
@@ -401,19 +369,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
       if (row0 < rows) {
         const int row = row0 + r;
         const bool in = row < rows;
+        const int token = w.s.first + (in ? p.byG.div(row) : 0), head = w.h * p.G + (in ? p.byG.mod(row) : 0);
         // ---- the warp's query rows: copied as they are, kLanes lanes a row,
         // then turned into f16 in place, a thread a row.  (Loops that run once
         // a piece are kept rolled: straight code would wait for its own
         // instructions, 9000 cycles in the place of 2500.)
         {
-#pragma unroll 2
+#pragma unroll 4
           for (int i = 0; i < kLanes; ++i) {
-            const int rr = 32 * (warp & 3) + i * kAtOnce + sub, rq = row0 + rr;
-            const bool there = rq < rows;
-            const uint16_t* src = p.q + (w.s.first + p.byG.div(there ? rq : 0)) * p.ld_q +
-                                  static_cast<int64_t>(w.h * p.G + p.byG.mod(there ? rq : 0)) * D + piece * 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at(rr, piece))), "l"(src),
-                         "r"(there ? 16 : 0)
+            const int from = i * kAtOnce + sub;  // the copied row's own lane
+            const int tq = __shfl_sync(0xFFFFFFFFu, token, from), hq = __shfl_sync(0xFFFFFFFFu, head, from);
+            const uint16_t* src = p.q + tq * p.ld_q + hq * D + piece * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at(32 * (warp & 3) + from, piece))),
+                         "l"(src), "r"(row0 + 32 * (warp & 3) + from < rows ? 16 : 0)
                          : "memory");
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
@@ -423,14 +391,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
 #pragma unroll 4
         for (int i = 0; i < kLanes; ++i) mx = max(mx, absmax_bits8(*reinterpret_cast<const uint4*>(at(r, i))));
         if (mx >= 0x7F80u) flag(p.status, QRR_DEV_NONFINITE);
-        const int e = query_exp(mx);
-        const Pow2Scaler sc(e);
-#pragma unroll 2
+        const int e = max(query_exp(mx), -127);  // one factor 2^-e (a row below 2^-113 comes out smaller)
+        const uint64_t sc = twice(__uint_as_float(static_cast<uint32_t>(127 - e) << 23));
+#pragma unroll 4
         for (int i = 0; i < kLanes; ++i) {
           uint4* y = reinterpret_cast<uint4*>(at(r, i));
           const uint4 x = *y;
-          *y = make_uint4(f16x2(sc(bf16_lo(x.x)), sc(bf16_hi(x.x))), f16x2(sc(bf16_lo(x.y)), sc(bf16_hi(x.y))),
-                          f16x2(sc(bf16_lo(x.z)), sc(bf16_hi(x.z))), f16x2(sc(bf16_lo(x.w)), sc(bf16_hi(x.w))));
+          *y = make_uint4(scaled_f16x2(x.x, sc), scaled_f16x2(x.y, sc), scaled_f16x2(x.z, sc), scaled_f16x2(x.w, sc));
         }
         fence_async_shared();
         __syncwarp();
@@ -539,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
             for (int i = 0; i < 4; ++i)
               *reinterpret_cast<uint4*>(at(r, 4 * c + i)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
           }
-          if (in && p.lse) p.lse[out_row(p, w.s.first, w.h, row)] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+          const int orow = token * p.Hq + head;
+          if (in && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
           __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
           for (int i = 0; i < kLanes; ++i) {
-            const int rr = 32 * (warp & 3) + i * kAtOnce + sub;
-            if (row0 + rr < rows)
-              reinterpret_cast<uint4*>(p.out + out_row(p, w.s.first, w.h, row0 + rr) * D)[piece] =
-                  *reinterpret_cast<const uint4*>(at(rr, piece));
+            const int from = i * kAtOnce + sub, rr = 32 * (warp & 3) + from;
+            const int64_t to_row = __shfl_sync(0xFFFFFFFFu, orow, from);
+            if (row0 + rr < rows) reinterpret_cast<uint4*>(p.out + to_row * D)[piece] = *reinterpret_cast<const uint4*>(at(rr, piece));
           }
         } else {
           const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRows + 128 * tile;
@@ -562,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
                 *reinterpret_cast<uint4*>(at(r, 8 * c + i)) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
             }
             __syncwarp();
-#pragma unroll 2
+#pragma unroll 4
             for (int i = 0; i < kLanes; ++i) {
               const int rr = 32 * (warp & 3) + i * kAtOnce + sub;
               reinterpret_cast<uint4*>(p.po + (pr + rr) * D + (D / 2) * half)[piece] = *reinterpret_cast<const uint4*>(at(rr, piece));
@@ -584,31 +551,70 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
   } else if (warp < 12) {
     // ---------------- codes -> key and value tiles ----------------
     const int t = tid - 256;
-    Feed<D> feed;
-    feed.begin(p, w);
-    feed.issue(p, sh, t);
-    feed.issue(p, sh, t);
-    int use = 0, slot = 0;
+    int use = 0, slot = 0, turn = 0;
     bool ok = true;
-    auto half = [&](uint8_t* tile, uint64_t* empty, uint64_t* full) {
-      feed.issue(p, sh, t);
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
+    auto half = [&](uint8_t* tile, uint64_t* empty, uint64_t* full, int live) {
+      if (!mbar_wait(&sh.raw_full[slot], turn & 1, abort, p.status)) return false;
+      Codes<D> x;
+      x.load(sh.raw[slot], sh.raw_s[slot], live, t);
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.raw_empty[slot]);
       if (use >= 2 && !mbar_wait(empty, ((use >> 1) - 1) & 1, abort, p.status)) return false;
-      convert<D>(sh, slot, tile, t);
+      x.convert(tile, t);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
-      slot = slot == 2 ? 0 : slot + 1;
+      if (++slot == 3) slot = 0, ++turn;
       return true;
     };
     do {
+      const int last = last_seen(p, w.s, w.qt);
       for (int j = w.t0; j < w.t1 && ok; ++j, ++use) {
-        const int st = use & 1;
-        ok = half(sh.k[st], &sh.k_empty[st], &sh.k_full[st]) && half(sh.v[st], &sh.v_empty[st], &sh.v_full[st]);
+        const int st = use & 1, live = last + 1 - kTok * j;
+        ok = half(sh.k[st], &sh.k_empty[st], &sh.k_full[st], live) && half(sh.v[st], &sh.v_empty[st], &sh.v_full[st], live);
       }
     } while (ok && w.next(p));
-    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 13) {
+    // ---------------- codes and scales into the ring ----------------
+    const int run = min(1 << p.c.page_shift, kTok);  // tokens of a copy: of one page
+    int slot = 0, n = 0;
+    bool ok = true;
+    do {
+      const int last = last_seen(p, w.s, w.qt);
+      const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
+      for (int j = w.t0; j < w.t1 && ok; ++j) {
+        const int tok = kTok * j + lane * run;
+        int rows = lane * run < kTok ? min(max(last + 1 - tok, 0), run) : 0;
+        int64_t row = 0;
+        if (rows > 0) {
+          const int pg = __ldg(table + (tok >> p.c.page_shift));
+          if (pg >= 0 && pg < p.c.num_pages) {
+            row = kv_row(p.c, pg, w.h, tok & ((1 << p.c.page_shift) - 1));
+          } else {
+            flag(p.status, QRR_DEV_BAD_INDEX);
+            rows = 0;
+          }
+        }
+        rows = (rows + 3) & ~3;  // whole 16 bytes of scales; within the page
+        const uint32_t bytes = __reduce_add_sync(0xFFFFFFFFu, rows * (D / 2 + D / 16));
+        for (int v = 0; v < 2; ++v, ++n) {
+          if (n >= 3 && !mbar_wait(&sh.raw_empty[slot], (n / 3 - 1) & 1, abort, p.status)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[slot], bytes);
+          __syncwarp();
+          if (rows > 0) {
+            bulk_load(sh.raw[slot] + lane * run * (D / 2), (v ? p.c.vc : p.c.kc) + row * (D / 2), rows * (D / 2), &sh.raw_full[slot]);
+            bulk_load(sh.raw_s[slot] + lane * run * (D / 16), (v ? p.c.vs : p.c.ks) + row * (D / 16), rows * (D / 16), &sh.raw_full[slot]);
+          }
+          if (++slot == 3) slot = 0;
+        }
+      }
+    } while (ok && w.next(p));
+    // every issued copy has landed before the CTA exits
+    volatile int no_abort = 0;
+    for (int i = max(0, n - 3); i < n; ++i) mbar_wait(&sh.raw_full[i % 3], (i / 3) & 1, &no_abort, p.status);
   } else {
     // ---------------- MMA issuer ----------------
     if (elect_one()) {
