@@ -781,6 +781,7 @@ static qrr_status check_kv_nvfp4(const qrr_kv_nvfp4* c, int64_t T, const int32_t
   if ((c->D != 64 && c->D != 128) || c->page < 16 || (c->page & (c->page - 1)) != 0) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (T > kMaxTokens || static_cast<int64_t>(c->max_pages) * c->page > kMaxTokens || c->Hkv > 65536)
     return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (static_cast<int64_t>(c->num_pages) * c->Hkv > static_cast<int64_t>(UINT32_MAX) / c->page) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (T * 2 * c->Hkv * (c->D / 16) > static_cast<int64_t>(INT32_MAX) * 256) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (!cu && T != c->B) return QRR_ERR_INVALID_ARG;
   if (T > 0 && c->Hkv > 0 && !pos && c->B > 0) return QRR_ERR_INVALID_ARG;
@@ -838,7 +839,7 @@ qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t
                                float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
   const qrr_status st = check_kv_nvfp4(cache, T, cu, pos);
   if (st != QRR_OK) return st;
-  if (Hq < 0 || cache->Hkv <= 0 || max_new < 0 || (!cu && max_new != 1)) return QRR_ERR_INVALID_ARG;
+  if (Hq < 0 || cache->Hkv <= 0 || (T > 0 && cache->num_pages == 0) || max_new < 0 || (!cu && max_new != 1)) return QRR_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || scale == INFINITY) return QRR_ERR_INVALID_ARG;
   if (Hq % cache->Hkv != 0 || max_new > kMaxTokens / (Hq > 0 ? Hq : 1)) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (T * Hq > INT32_MAX) return QRR_ERR_UNSUPPORTED_SHAPE;  // rows of out and lse

@@ -7,20 +7,20 @@
 // the G = Hq / Hkv query heads of each of the sequence's new tokens share every
 // key and value that is read.  A row that sees nothing gives zeros, lse -inf.
 //
-// Work is cut stream-K: the 16-token tiles of all (sequence, row tile, KV head)
-// items, one after another, in equal ranges, one a CTA, so ragged lengths
-// balance by themselves.  A CTA whose range holds a whole item writes its
+// Work is cut stream-K: the 16-token tiles of all (sequence, KV head) items, one
+// after another, in equal ranges, one a warp, so ragged lengths balance by
+// themselves (an item counts kItemCost tiles more than it has, about what its
+// start and end cost).  A warp whose range holds a whole item writes its
 // result; the pieces of an item that crosses ranges go to the workspace (at
-// most two a CTA) and a second kernel joins them, in the items' order, so
+// most two a warp) and a second kernel joins them, in the items' order, so
 // results do not depend on timing.
 //
-// Inside a CTA the warps take tiles in turn, each on its own: a tile's codes
-// and scales come from global memory straight into the registers of the lanes
-// that feed them to the tensor core (m16n8k16, f16 operands, fp32 sums), so
-// there is no shared memory and no barrier in the loop.  With K (16 tokens x
-// D) as the A operand the score tile is [16 tokens x 8 rows]; its exponentials,
-// as f16 and transposed by one matrix-move per 8 tokens, are the B operand of
-// O^T += V^T P^T.  The products code x block scale are exact in f16 (at most
+// A tile's codes and scales come by asynchronous copies into the warp's own ring
+// of kStages tiles, three tiles ahead and on into the next item, and from there
+// to the lanes that feed them to the tensor core (m16n8k16, f16 operands, fp32
+// sums); no warp waits for another.  With K (16 tokens x D) as the A operand the
+// score tile is [16 tokens x 8 rows]; its exponentials, as f16 and transposed by
+// one matrix-move per 8 tokens, are the B operand of O^T += V^T P^T.  The products code x block scale are exact in f16 (at most
 // 6 significant bits, 2^-10 .. 2688).  The query enters as f16 after a power
 // of two a row that brings its largest value into [2^14, 2^15), exact for every
 // value within 2^-29 of that; the head's global scales multiply the scores and
@@ -30,6 +30,8 @@
 // and is only moved when some score exceeds it by 15, so p = 2^(s - m) stays
 // within f16, the row's largest p is at least 2^7, and a p keeps f16's full 11
 // bits down to 2^-21 of that (an absolute 2^-32 of it below).
+#include <algorithm>
+
 #include "attention_nvfp4.cuh"
 #include "tc.cuh"
 
@@ -41,8 +43,16 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kCtasPerSm = 4;
-constexpr int kMinTiles = 8;  // tiles of a range: two a warp
+constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 2; }  // by registers
+constexpr int kMinTiles = 8;  // tiles of a range
+constexpr int kItemCost = 2;
+constexpr int kStages = 4;    // tiles of a warp's ring
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t r;
@@ -58,25 +68,31 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// `W` 32-bit words from shared memory.
 template <int W>
 struct Words {
   uint32_t w[W];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (W == 4) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (W == 2) {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      w[0] = x.x, w[1] = x.y;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+  }
 };
 
-template <int W>
-__device__ __forceinline__ Words<W> load_words(const uint8_t* p) {
-  Words<W> r;
-  if constexpr (W == 4) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-    r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
-  } else if constexpr (W == 2) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-    r.w[0] = x.x, r.w[1] = x.y;
-  } else {
-    r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
-  return r;
-}
+// A tile in a warp's ring: 16 rows of key and value codes, key scales, value
+// scales.  Keys' rows 4..7 and 12..15 change places, and (D = 128)
+// values' rows 2, 3, 6, 7, ... have their halves swapped, so that the lanes of
+// a read find their bytes in different banks.
+template <int D>
+struct Raw {
+  uint8_t k[8 * D], v[8 * D], ks[D], vs[D];
+};
 
 // One tile's operands in a lane's registers.  Lane (g, c) = (lane / 4,
 // lane % 4) holds, of tokens tau and tau + 8 with tau = g / 2 + 4 (g % 2), the
@@ -88,56 +104,133 @@ struct Tile {
   Words<D / 32> k[2];
   Words<D / 64> v[4];
   uint32_t ks[2], vs[4];
-  int live;  // tokens of the tile that exist (0..16)
+  __device__ __forceinline__ void load(const Raw<D>& raw, int lane) {
+    const int g = lane >> 2, c = lane & 3, tau = (g >> 1) + 4 * (g & 1), at = tau ^ (D == 128 ? tau >> 2 : 2 * (tau >> 2));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      k[i].load(raw.k + (at + 8 * i) * (D / 2) + c * (D / 8));
+      const uint8_t* s = raw.ks + (tau + 8 * i) * (D / 16) + c * (D / 64);
+      if constexpr (D == 128) ks[i] = *reinterpret_cast<const uint16_t*>(s);
+      else ks[i] = *s;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j].load(raw.v + (c + 4 * j) * (D / 2) + ((g * (D / 16)) ^ (D == 128 ? 16 * (c & 2) : 0)));
+      vs[j] = raw.vs[(c + 4 * j) * (D / 16) + (D == 128 ? g : g >> 1)];
+    }
+  }
 };
 
 struct Item : Seq {
-  int b, rt, h;  // sequence, row tile, KV head
-  int tiles;     // tiles of the item (at least 1)
+  int b, h;   // sequence, KV head
+  int tiles;  // that its last row sees
+  int width;  // that it counts for (none: it has more rows than this kernel takes, or sees nothing)
 };
 
-// Sequence b's row tiles (none if it has more rows than this kernel takes).
-template <int RT>
-__device__ __forceinline__ void seq_item(const Params& p, int b, Item& it, int& rts) {
+// Sequence b's items.  `pad`: whole ranges of kMinTiles each.
+__device__ __forceinline__ void seq_item(const Params& p, int b, bool pad, Item& it) {
   static_cast<Seq&>(it) = seq_of(p, b);
-  it.tiles = max(1, (it.last + 16) >> 4);
+  it.b = b;
+  it.tiles = (it.last + 16) >> 4;
   const int64_t rows = static_cast<int64_t>(it.n) * p.G;
-  rts = rows > kFewRows ? 0 : static_cast<int>((rows + RT - 1) / RT);
+  const bool here = rows > 0 && rows <= kFewRows && it.last >= 0;
+  it.width = !here ? 0 : pad ? (it.tiles + kMinTiles - 1) / kMinTiles * kMinTiles : it.tiles + kItemCost;
 }
 
+// The walk over the items of a range: tiles [t0, stop) of one at a time, and
+// [t0, t1) as they count.
+struct Walk : Item {
+  int t0, t1, stop;
+  int64_t left;  // of the range, from t0 on
+  __device__ __forceinline__ void cut() {
+    t1 = static_cast<int>(min(static_cast<int64_t>(width), t0 + left));
+    stop = min(t1, tiles);
+  }
+  __device__ __forceinline__ void begin(const Params& p, int b_, int64_t off, bool pad, int64_t left_) {
+    seq_item(p, b_, pad, *this);
+    h = static_cast<int>(off / width);
+    t0 = static_cast<int>(off - static_cast<int64_t>(h) * width);
+    left = left_;
+    cut();
+  }
+  __device__ __forceinline__ bool next(const Params& p, bool pad) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    t0 = 0;
+    if (++h == p.c.Hkv) {
+      int at = b;
+      do seq_item(p, ++at, pad, *this);
+      while (width == 0 && at + 1 < p.c.B);
+      h = 0;
+    }
+    cut();
+    return true;
+  }
+};
+
+// The copies of a range's tiles into the warp's ring, kStages - 1 ahead of their
+// use.  The page table is read a tile ahead.
 template <int D>
-__device__ __forceinline__ void load_tile(const Params& p, const int32_t* table, int h, int t, int last, int lane,
-                                          Tile<D>& x) {
-  const int g = lane >> 2, c = lane & 3;
-  const int tok = 16 * t;
-  int pg = __ldg(table + (tok >> p.c.page_shift));
-  x.live = min(16, last + 1 - tok);
-  if (pg < 0 || pg >= p.c.num_pages) {
-    flag(p.status, QRR_DEV_BAD_INDEX);
-    x.live = 0;
+struct Feed {
+  Walk w;
+  const uint8_t *kc, *vc, *sc;  // the lane's bytes of row 0 (scales: keys' in the lower half of the warp)
+  uint32_t to, to_v, to_s;      // its places in the ring's first tile
+  int t, slot, pg;
+  bool more;
+  __device__ __forceinline__ int page_of(const Params& p) const {
+    return __ldg(p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages + (t >> (p.c.page_shift - 4)));
   }
-  if (x.live <= 0) {
-    x = Tile<D>{};
-    return;
+  // the first tile at or after t, over the ends of items
+  __device__ __forceinline__ void settle(const Params& p, bool pad) {
+    while (more && t >= w.stop) {
+      more = w.next(p, pad);
+      t = w.t0;
+    }
+    if (more) pg = page_of(p);
   }
-  const int64_t row = kv_row(p.c, pg, h, tok & ((1 << p.c.page_shift) - 1));
-  const int tau = (g >> 1) + 4 * (g & 1);
-  const uint8_t* kc = p.c.kc + (row + tau) * (D / 2) + c * (D / 8);
-  const uint8_t* ks = p.c.ks + (row + tau) * (D / 16) + c * (D / 64);
-  const uint8_t* vc = p.c.vc + (row + c) * (D / 2) + g * (D / 16);
-  const uint8_t* vs = p.c.vs + (row + c) * (D / 16) + (D == 128 ? g : g >> 1);
+  __device__ __forceinline__ void begin(const Params& p, const Walk& from, const Raw<D>* ring, int lane, bool pad) {
+    constexpr int kChunks = D / 32;  // of 16 bytes a row
+    const int r = lane / kChunks, c = lane % kChunks;
+    kc = p.c.kc + lane * 16;
+    vc = p.c.vc + lane * 16;
+    const int half = lane & 15;
+    sc = (lane < 16 ? p.c.ks : p.c.vs) + half * (D / 16);
+    to = smem_u32(ring) + (r ^ ((D == 128 ? 1 : 2) * (r >> 2 & 1))) * (D / 2) + c * 16;
+    to_v = smem_u32(ring->v) + r * (D / 2) + ((c * 16) ^ (D == 128 ? 16 * (r & 2) : 0));
+    to_s = smem_u32(lane < 16 ? ring->ks : ring->vs) + half * (D / 16);
+    w = from;
+    t = w.t0;
+    slot = 0;
+    more = true;
+    settle(p, pad);
+  }
+  __device__ __forceinline__ void issue(const Params& p, bool pad) {
+    if (more) {
+      uint32_t now = static_cast<uint32_t>(pg);
+      if (now >= static_cast<uint32_t>(p.c.num_pages)) {
+        flag(p.status, QRR_DEV_BAD_INDEX);
+        now = 0u;
+      }
+      const uint32_t page_rows = 1u << p.c.page_shift;
+      const uint32_t row = (now * p.c.Hkv + w.h) * page_rows + (static_cast<uint32_t>(16 * t) & (page_rows - 1));
+      const uint64_t c0 = static_cast<uint64_t>(row) * (D / 2), s0 = static_cast<uint64_t>(row) * (D / 16);
+      const uint32_t at = to + slot * static_cast<uint32_t>(sizeof(Raw<D>));
+      const uint32_t av = to_v + slot * static_cast<uint32_t>(sizeof(Raw<D>));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x.k[i] = load_words<D / 32>(kc + i * 8 * (D / 2));
-    if constexpr (D == 128) x.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(ks + i * 8 * (D / 16)));
-    else x.ks[i] = __ldg(ks + i * 8 * (D / 16));
+      for (int i = 0; i < D / 64; ++i) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 512 * i), "l"(kc + c0 + 512 * i) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(av + 512 * i), "l"(vc + c0 + 512 * i) : "memory");
+      }
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to_s + slot * static_cast<uint32_t>(sizeof(Raw<D>))),
+                   "l"(sc + s0), "n"(D / 16)
+                   : "memory");
+      slot = slot == kStages - 1 ? 0 : slot + 1;
+      ++t;
+      settle(p, pad);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x.v[j] = load_words<D / 64>(vc + j * 4 * (D / 2));
-    x.vs[j] = __ldg(vs + j * 4 * (D / 16));
-  }
-}
+};
 
 // A warp's rows and running state; NT groups of 8 rows.  Lane (g, c) feeds the
 // query of row g of a group to the MMAs and holds the results of rows 2 c and
@@ -157,7 +250,7 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
   const float kg = p.c.kg ? __ldg(p.c.kg + it.h) : 1.0f;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    const int r = it.rt * 8 * NT + 8 * nt + g;
+    const int r = 8 * nt + g;
     const bool in = r < it.n * p.G;
     uint32_t w[D / 8] = {};
     uint32_t mx = 0u;
@@ -195,9 +288,10 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
   }
 }
 
-// One tile of 16 tokens.  `all`: every row sees every token of it.
+// One tile of 16 tokens, of which `live` exist (16 or more: all).  `all`: every
+// row sees every token of it.
 template <int D, int NT>
-__device__ __forceinline__ void step(const Tile<D>& x, int t, bool all, int lane, State<D, NT>& s) {
+__device__ __forceinline__ void step(const Tile<D>& x, int t, int live, bool all, int lane, State<D, NT>& s) {
   const int g = lane >> 2, c = lane & 3;
   float sc[NT][4];
 #pragma unroll
@@ -222,29 +316,41 @@ __device__ __forceinline__ void step(const Tile<D>& x, int t, bool all, int lane
       }
     }
   }
-  // lane's scores: rows 2 c, 2 c + 1 of each group; tokens tau, tau + 8
+  // lane's scores: rows 2 c, 2 c + 1 of each group; tokens tau, tau + 8; against
+  // the reference in log2 units
   const int tok = 16 * t + (g >> 1) + 4 * (g & 1);
-  bool over = false;
+  float e[NT][4], most = -INFINITY;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      sc[nt][i] *= s.f[nt][i & 1];
-      if (!all && (i < 2 ? tok : tok + 8) > s.lim[nt][i & 1]) sc[nt][i] = -INFINITY;
-      over |= sc[nt][i] > s.m[nt][i & 1] + kRoom;
+      e[nt][i] = fmaf(sc[nt][i], s.f[nt][i & 1], -s.m[nt][i & 1]);
     }
-  if (__any_sync(0xFFFFFFFFu, over)) {
+  if (!all)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((i < 2 ? tok : tok + 8) > s.lim[nt][i & 1]) e[nt][i] = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) most = max3(max3(most, e[nt][0], e[nt][1]), e[nt][2], e[nt][3]);
+  if (__any_sync(0xFFFFFFFFu, most > kRoom)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float v = fmaxf(sc[nt][i], sc[nt][i + 2]);
+        // the row's largest score of the tile, itself
+        const bool see0 = all || tok <= s.lim[nt][i], see1 = all || tok + 8 <= s.lim[nt][i];
+        const float s0 = see0 ? sc[nt][i] * s.f[nt][i] : -INFINITY, s1 = see1 ? sc[nt][i + 2] * s.f[nt][i] : -INFINITY;
+        float v = fmaxf(s0, s1);
         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
         const float m = fmaxf(v - kLift, s.m[nt][i]), a = ex2(s.m[nt][i] - m);
         s.m[nt][i] = m;
         s.l[nt][i] *= a;
+        e[nt][i] = s0 - m;
+        e[nt][i + 2] = s1 - m;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) s.o[nt][j][i] *= a, s.o[nt][j][i + 2] *= a;
       }
@@ -252,31 +358,34 @@ __device__ __forceinline__ void step(const Tile<D>& x, int t, bool all, int lane
   uint32_t p[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = ex2(sc[nt][i] - s.m[nt][i & 1]);
-    s.l[nt][0] += e[0] + e[2];
-    s.l[nt][1] += e[1] + e[3];
-    p[nt][0] = movmatrix(f16x2(e[0], e[1]));
-    p[nt][1] = movmatrix(f16x2(e[2], e[3]));
+    for (int i = 0; i < 4; ++i) e[nt][i] = ex2(e[nt][i]);
+    s.l[nt][0] += e[nt][0] + e[nt][2];
+    s.l[nt][1] += e[nt][1] + e[nt][3];
+    p[nt][0] = movmatrix(f16x2(e[nt][0], e[nt][1]));
+    p[nt][1] = movmatrix(f16x2(e[nt][2], e[nt][3]));
   }
-  uint32_t vs[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) vs[j] = c + 4 * j < x.live ? x.vs[j] : 0u;  // what no token wrote may hold a NaN
-  const uint32_t f0 = e4m3x2_to_f16x2(vs[0] | vs[1] << 8), f1 = e4m3x2_to_f16x2(vs[2] | vs[3] << 8);
+  // the two pairs' scales; those of tokens that do not exist count as zero (what
+  // lies there may be anything, a NaN among it)
+  uint32_t v01 = __byte_perm(x.vs[0], x.vs[1], 0x7740), v23 = __byte_perm(x.vs[2], x.vs[3], 0x7740);
+  if (live < 16) {
+    v01 &= (c < live ? 0xFFu : 0u) | (c + 4 < live ? 0xFF00u : 0u);
+    v23 &= (c + 8 < live ? 0xFFu : 0u) | (c + 12 < live ? 0xFF00u : 0u);
+  }
+  const uint32_t f0 = e4m3x2_to_f16x2(v01), f1 = e4m3x2_to_f16x2(v23);
 #pragma unroll
   for (int w = 0; w < D / 64; ++w) {
     // bytes of (first, second) token's codes of one value: even values, odd values
-    uint32_t a[4], b[4], d[4], e[4];
+    uint32_t a[4], b[4], d[4], h[4];
     f16x2x4_from_e2m1x8((x.v[0].w[w] & 0x0F0F0F0Fu) | (x.v[1].w[w] << 4 & 0xF0F0F0F0u), a);
     f16x2x4_from_e2m1x8((x.v[0].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[1].w[w] & 0xF0F0F0F0u), b);
     f16x2x4_from_e2m1x8((x.v[2].w[w] & 0x0F0F0F0Fu) | (x.v[3].w[w] << 4 & 0xF0F0F0F0u), d);
-    f16x2x4_from_e2m1x8((x.v[2].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[3].w[w] & 0xF0F0F0F0u), e);
+    f16x2x4_from_e2m1x8((x.v[2].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[3].w[w] & 0xF0F0F0F0u), h);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), e[i] = hmul2(e[i], f1);
+      a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), h[i] = hmul2(h[i], f1);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma16816(s.o[nt][4 * w + i], a[i], b[i], d[i], e[i], p[nt][0], p[nt][1]);
+      for (int nt = 0; nt < NT; ++nt) mma16816(s.o[nt][4 * w + i], a[i], b[i], d[i], h[i], p[nt][0], p[nt][1]);
     }
   }
 }
@@ -284,37 +393,47 @@ __device__ __forceinline__ void step(const Tile<D>& x, int t, bool all, int lane
 }  // namespace
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(const Params p) {
   constexpr int RT = 8 * NT;
-  __shared__ float so[kWarps][RT][D + 4];
-  __shared__ float sm[kWarps][RT], sl[kWarps][RT];
-  __shared__ int64_t scan[2][kWarps];
-  __shared__ int64_t at_off;
-  __shared__ int at_b;
+  __shared__ __align__(16) Raw<D> ring[kWarps][kStages];
+  __shared__ int64_t sums[2][kWarps], at_off[kWarps];
+  __shared__ int at_b[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_launch_dependents();
 
-  // ---- this CTA's range of the tile sequence
-  const int B = p.c.B, strip = (B + kThreads - 1) / kThreads;
+  // a sequence that sees nothing is no work: one CTA writes its rows
+  const int B = p.c.B;
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    const Seq q = seq_of(p, b);
+    if (q.last >= 0 || static_cast<int64_t>(q.n) * p.G > kFewRows) continue;
+    const int64_t row = static_cast<int64_t>(q.first) * p.Hq;
+    for (int i = tid; i < q.n * p.Hq * (D / 8); i += kThreads) reinterpret_cast<uint4*>(p.out + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (int i = tid; i < q.n * p.Hq; i += kThreads) p.lse[row + i] = -INFINITY;
+  }
+
+  // ---- the warps' ranges of the tile sequence
+  const int ranges = gridDim.x * kWarps, strip = (B + kThreads - 1) / kThreads;
   const int b0 = min(tid * strip, B), b1 = min(b0 + strip, B);
   int64_t sum = 0, padded = 0;
   for (int b = b0; b < b1; ++b) {
     Item it;
-    int rts;
-    seq_item<RT>(p, b, it, rts);
-    const int64_t items = static_cast<int64_t>(rts) * p.c.Hkv;
-    sum += items * it.tiles;
-    padded += items * ((it.tiles + kMinTiles - 1) / kMinTiles * kMinTiles);
+    seq_item(p, b, false, it);
+    sum += it.width;
+    if (it.width > 0) padded += (it.tiles + kMinTiles - 1) / kMinTiles * kMinTiles;
   }
-  int64_t total_padded = padded;
+  sum *= p.c.Hkv;
+  padded *= p.c.Hkv;
+  int64_t total = padded;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) total_padded += __shfl_xor_sync(0xFFFFFFFFu, total_padded, o);
-  if (lane == 0) scan[0][warp] = total_padded;
+  for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
+  if (lane == 0) sums[0][warp] = total;
   __syncthreads();
-  total_padded = 0;
-  for (int w = 0; w < kWarps; ++w) total_padded += scan[0][w];
-  // little work: every item padded to whole ranges of kMinTiles, so that none
-  // is cut where it need not be
-  const bool pad = total_padded <= static_cast<int64_t>(gridDim.x) * kMinTiles;
+  total = 0;
+  for (int w = 0; w < kWarps; ++w) total += sums[0][w];
+  // little work: every item in whole ranges, so that none is cut where it need
+  // not be
+  const bool pad = total <= static_cast<int64_t>(ranges) * kMinTiles;
   const int64_t own = pad ? padded : sum;
   int64_t incl = own;
 #pragma unroll
@@ -322,68 +441,68 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4
     const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) scan[1][warp] = incl;
+  if (lane == 31) sums[1][warp] = incl;
   __syncthreads();
-  int64_t total = 0;
+  total = 0;
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) incl += scan[1][w];
-    total += scan[1][w];
+    if (w < warp) incl += sums[1][w];
+    total += sums[1][w];
   }
-  const int64_t per = pad ? kMinTiles : (total + gridDim.x - 1) / gridDim.x;
-  const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
-  Record rec{};
-  if (begin >= end) {
-    if (tid == 0) p.rec[blockIdx.x] = rec;
+  const int64_t per = pad ? kMinTiles : (total + ranges - 1) / ranges;
+  for (int w = 0; w < kWarps; ++w) {
+    const int64_t begin = (static_cast<int64_t>(blockIdx.x) * kWarps + w) * per;
+    if (begin >= incl - own && begin < incl) {
+      int64_t off = begin - (incl - own);
+      for (int b = b0; b < b1; ++b) {
+        Item it;
+        seq_item(p, b, pad, it);
+        const int64_t all = static_cast<int64_t>(it.width) * p.c.Hkv;
+        if (off < all) {
+          at_b[w] = b;
+          at_off[w] = off;
+          break;
+        }
+        off -= all;
+      }
+    }
+  }
+  __syncthreads();
+  const int range = blockIdx.x * kWarps + warp;
+  const int64_t left = min(per, total - range * per);
+  if (left <= 0) {
+    if (lane == 0) p.rec[range].pieces = 0;
     return;
   }
-  auto width = [&](const Item& it) { return pad ? (it.tiles + kMinTiles - 1) / kMinTiles * kMinTiles : it.tiles; };
-  if (begin >= incl - own && begin < incl) {
-    int64_t off = begin - (incl - own);
-    for (int b = b0; b < b1; ++b) {
-      Item it;
-      int rts;
-      seq_item<RT>(p, b, it, rts);
-      const int64_t w = static_cast<int64_t>(rts) * p.c.Hkv * width(it);
-      if (off < w) {
-        at_b = b;
-        at_off = off;
-        break;
-      }
-      off -= w;
-    }
-  }
-  __syncthreads();
 
-  Item it;
-  it.b = at_b;
-  int rts;
-  seq_item<RT>(p, it.b, it, rts);
-  int64_t idx = at_off / width(it);  // item of the sequence: row tile, head
-  int t0 = static_cast<int>(at_off % width(it));
+  Walk it;
+  it.begin(p, at_b[warp], at_off[warp], pad, left);
+  Feed<D> feed;
+  feed.begin(p, it, ring[warp], lane, pad);
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) feed.issue(p, pad);
+  const int c = lane & 3, g = lane >> 2;
+  Record rec{};
   State<D, NT> s;
-  for (int64_t left = end - begin; left > 0;) {
-    it.rt = static_cast<int>(idx / p.c.Hkv);
-    it.h = static_cast<int>(idx % p.c.Hkv);
-    const int w = width(it), t1 = static_cast<int>(min(static_cast<int64_t>(w), t0 + left));
+  int slot = 0;
+  do {
     load_rows<D, NT>(p, it, lane, s);
-    // what the rows of this tile see at most, and at least (rows behind the
-    // last one are never read again: they need no mask)
-    const int r_end = min((it.rt + 1) * RT, it.n * p.G);
-    const int see = min(it.pos + p.byG.div(r_end - 1), it.last);
-    const int sure = min(it.pos + p.byG.div(it.rt * RT), it.last);
-    const int stop = min(t1, (see + 16) >> 4);
-    const int32_t* table = p.c.table + static_cast<int64_t>(it.b) * p.c.max_pages;
-    Tile<D> x, y;
-    int t = t0 + warp;
-    if (t < stop) load_tile<D>(p, table, it.h, t, see, lane, x);
-    while (t < stop) {
-      if (t + kWarps < stop) load_tile<D>(p, table, it.h, t + kWarps, see, lane, y);
-      step<D, NT>(x, t, x.live == 16 && 16 * t + 15 <= sure, lane, s);
-      x = y;
-      t += kWarps;
+    // tiles before this one are seen whole by every row (rows behind the last one
+    // are never read: no mask for them)
+    const int whole = (min(it.pos, it.last) + 1) >> 4;
+#pragma unroll 1
+    for (int t = it.t0; t < it.stop; ++t) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // the tile is there for all lanes, and the one before it read by all
+      Tile<D> x;
+      x.load(ring[warp][slot], lane);
+      feed.issue(p, pad);
+      slot = slot == kStages - 1 ? 0 : slot + 1;
+      step<D, NT>(x, t, it.last + 1 - 16 * t, t < whole, lane, s);
     }
-    // ---- join the warps
-    const int g = lane >> 2, c = lane & 3;
+    // ---- the rows' results, or a piece of them
+    const bool cut0 = it.t0 > 0, cut1 = it.t1 < it.width;
+    const int64_t piece = static_cast<int64_t>(2 * range + (cut0 ? 0 : 1)) * RT;
+    const float vg = p.c.vg ? __ldg(p.c.vg + it.h) : 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -393,58 +512,35 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? kCtasPerSm : 2) attn_nvfp4
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
         l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-        if (g == 0) {
-          sm[warp][r] = s.m[nt][i];
-          sl[warp][r] = l;
+        if (r >= it.n * p.G) continue;
+        if (!cut0 && !cut1) {
+          const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+          const int64_t orow = out_row(p, it.first, it.h, r);
+          uint32_t w[D / 16];
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(s.o[nt][j][i] * inv, s.o[nt][j][i + 2] * inv);
+            w[j] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j)
+            reinterpret_cast<uint4*>(p.out + orow * D + D / 8 * g)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          if (p.lse && g == 0) p.lse[orow] = l > 0.0f ? (s.m[nt][i] + lg2(l)) * kLn2 : -INFINITY;
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)
+            reinterpret_cast<float4*>(p.po + (piece + r) * D + D / 8 * g)[j] =
+                make_float4(s.o[nt][2 * j][i], s.o[nt][2 * j][i + 2], s.o[nt][2 * j + 1][i], s.o[nt][2 * j + 1][i + 2]);
+          if (g == 0) p.pm[piece + r] = s.m[nt][i], p.pl[piece + r] = l;
         }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-          *reinterpret_cast<float2*>(&so[warp][r][D / 8 * g + 2 * j]) = make_float2(s.o[nt][j][i], s.o[nt][j][i + 2]);
       }
-    __syncthreads();
-    const bool cut0 = t0 > 0, cut1 = t1 < w;
-    const int piece = 2 * blockIdx.x + (cut0 ? 0 : 1);
-    const float vg = p.c.vg ? __ldg(p.c.vg + it.h) : 1.0f;
-    for (int e = tid; e < RT * (D / 4); e += kThreads) {
-      const int r = e / (D / 4), d = 4 * (e % (D / 4));
-      const int row = it.rt * RT + r;
-      if (row >= it.n * p.G) break;
-      float m = kNone;
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) m = fmaxf(m, sm[k][r]);
-      float l = 0.0f, o[4] = {};
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float a = ex2(sm[k][r] - m);
-        l += a * sl[k][r];
-        const float4 v = *reinterpret_cast<const float4*>(&so[k][r][d]);
-        o[0] += a * v.x, o[1] += a * v.y, o[2] += a * v.z, o[3] += a * v.w;
-      }
-      if (!cut0 && !cut1) {
-        const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
-        const int64_t orow = out_row(p, it.first, it.h, row);
-        const __nv_bfloat162 u = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), v = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-        *reinterpret_cast<uint2*>(p.out + orow * D + d) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
-        if (p.lse && d == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
-      } else {
-        const int64_t pr = static_cast<int64_t>(piece) * RT + r;
-        *reinterpret_cast<float4*>(p.po + pr * D + d) = make_float4(o[0], o[1], o[2], o[3]);
-        if (d == 0) p.pm[pr] = m, p.pl[pr] = l;
-      }
+    if (!cut0 && cut1) {
+      rec.pieces = 1 + static_cast<int>((it.width - it.t1 + per - 1) / per);
+      rec.rt = 0, rec.h = it.h, rec.first = it.first, rec.n = it.n;
     }
-    if (cut0) rec.cont = 1, rec.cont_more = cut1;
-    else if (cut1) rec.start = 1, rec.rt = it.rt, rec.h = it.h, rec.first = it.first, rec.n = it.n;
-    __syncthreads();
-    left -= t1 - t0;
-    t0 = 0;
-    if (left > 0 && ++idx == static_cast<int64_t>(rts) * p.c.Hkv) {
-      idx = 0;
-      do seq_item<RT>(p, ++it.b, it, rts);
-      while (rts == 0 && it.b + 1 < B);
-    }
-  }
-  if (tid == 0) p.rec[blockIdx.x] = rec;
+  } while (it.next(p, pad));
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (lane == 0) p.rec[range] = rec;
 }
 
 namespace {
@@ -452,19 +548,21 @@ namespace {
 template <int D, int NT>
 cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   constexpr int RT = 8 * NT;
-  const Params p = make_params(a, a.ws, grid, RT);
+  const int ranges = grid * kWarps;
+  const Params p = make_params(a, a.ws, ranges, RT);
   attn_nvfp4_kernel<D, NT><<<grid, kThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join_kernel<D, RT><<<dim3(grid, NT), 256, 0, stream>>>(p, grid);
-  return cudaGetLastError();
+  return launch_dependent(join_kernel<D, RT>, dim3(ranges, NT), 256, 0, stream, p);
 }
 
 // Whether some sequence may have few rows, or many (see kFewRows).
 bool any_few(int G) { return G <= kFewRows; }
 bool any_many(int64_t max_new, int G) { return max_new * G > kFewRows; }
 
-size_t few_ws_bytes(int D) { return ws_bytes(D, kMaxSms * kCtasPerSm, kFewRows); }
+size_t few_ws_bytes(int D) {
+  return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(1) * kWarps, 8), ws_bytes(D, kMaxSms * ctas_per_sm(2) * kWarps, 16));
+}
 
 }  // namespace
 
@@ -480,7 +578,7 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
   const int G = a.Hq / a.c.Hkv;
   if (any_few(G)) {
     const bool one = static_cast<int64_t>(a.max_new) * G <= 8;
-    const int grid = (sms < kMaxSms ? sms : kMaxSms) * (one ? kCtasPerSm : 2);
+    const int grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(one ? 1 : 2);
     const cudaError_t e = a.c.D == 128 ? (one ? launch<128, 1>(a, grid, stream) : launch<128, 2>(a, grid, stream))
                                        : (one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream));
     if (e != cudaSuccess) return e;

@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "kv_nvfp4.cuh"
+#include "tc.cuh"
 
 namespace qrr {
 
@@ -57,11 +58,9 @@ __device__ __forceinline__ int query_exp(uint32_t mx) {
 
 // Pieces of items that cross ranges.  Piece 2 k is range k's first when it
 // continues an item, piece 2 k + 1 its last when it starts one that the next
-// range continues.
+// ranges continue.
 struct Record {
-  int cont;       // piece 2 k is there
-  int cont_more;  // and the next range continues the same item
-  int start;      // piece 2 k + 1 is there
+  int pieces;           // of the item that starts in the range and goes on (0: none)
   int rt, h, first, n;  // its row tile, KV head, the sequence's rows
 };
 
@@ -118,36 +117,81 @@ __device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, in
 }
 
 // Joins the pieces of the item that starts in range k = blockIdx.x and is
-// continued by the next ones: a warp a row, in the order of the ranges.  RT:
-// rows of a piece.
+// continued by the next ones: a warp a row.  The lanes take the pieces' (m, l),
+// 32 at a time; sums over them are formed in the order of the pieces' lanes,
+// the outputs' in the order of the pieces.  RT: rows of a piece.
 template <int D, int RT>
-__global__ void __launch_bounds__(256) join_kernel(const Params p, int ranges) {
+__global__ void __launch_bounds__(256) join_kernel(const Params p) {
   constexpr int V = D / 32;
+  griddep_wait();
   const int k = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const Record rec = p.rec[k];
-  if (!rec.start) return;
   const int row = rec.rt * RT + r;
-  if (row >= rec.n * p.G) return;
-  int last = k + 1;
-  while (last + 1 < ranges && p.rec[last].cont_more) ++last;
+  if (rec.pieces == 0 || row >= rec.n * p.G) return;
   const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  auto piece = [&](int i) { return static_cast<int64_t>(i == k ? 2 * k + 1 : 2 * i) * RT + r; };
-  float m = kNone;
-  for (int i = k; i <= last; ++i) m = fmaxf(m, p.pm[piece(i)]);
-  float l = 0.0f, o[V] = {};
-  for (int i = k; i <= last; ++i) {
-    const int64_t pr = piece(i);
-    const float a = ex2(p.pm[pr] - m);
-    l += a * p.pl[pr];
+  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * k + 1 : 2 * (k + i)) * RT + r; };
+  float m = kNone, l = 0.0f, o[V] = {};
+  for (int i0 = 0; i0 < rec.pieces; i0 += 32) {
+    const int n = min(32, rec.pieces - i0);
+    float mi = kNone, li = 0.0f;
+    if (lane < n) {
+      mi = p.pm[piece(i0 + lane)];
+      li = p.pl[piece(i0 + lane)];
+    }
+    float top = mi;
 #pragma unroll
-    for (int d = 0; d < V; ++d) o[d] += a * p.po[pr * D + 32 * d + lane];
+    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    top = fmaxf(top, m);
+    const float old = ex2(m - top), a = ex2(mi - top);
+    m = top;
+    float sum = a * li;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    l = l * old + sum;
+#pragma unroll
+    for (int d = 0; d < V; ++d) o[d] *= old;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float ai = __shfl_sync(0xFFFFFFFFu, a, i);
+      const float* src = p.po + piece(i0 + i) * D + V * lane;
+      if constexpr (V == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        o[0] += ai * v.x, o[1] += ai * v.y, o[2] += ai * v.z, o[3] += ai * v.w;
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        o[0] += ai * v.x, o[1] += ai * v.y;
+      }
+    }
   }
   const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
   const int64_t orow = out_row(p, rec.first, rec.h, row);
+  uint32_t y[V / 2];
 #pragma unroll
-  for (int d = 0; d < V; ++d)
-    reinterpret_cast<__nv_bfloat16*>(p.out)[orow * D + 32 * d + lane] = __float2bfloat16_rn(o[d] * inv);
+  for (int d = 0; d < V / 2; ++d) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * d] * inv, o[2 * d + 1] * inv);
+    y[d] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(p.out + orow * D + V * lane) = make_uint2(y[0], y[1]);
+  else *reinterpret_cast<uint32_t*>(p.out + orow * D + V * lane) = y[0];
   if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+}
+
+// Launches a kernel as the programmatic dependent of the one before it in the
+// stream: its CTAs may be placed while that one still runs, and wait for it
+// (griddep_wait) before they touch anything.
+template <class... A>
+cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  la[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Workspace of `ranges` ranges whose pieces have `rt` rows.

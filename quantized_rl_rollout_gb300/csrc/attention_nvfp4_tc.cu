@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   volatile int* abort = &sh.abort;
 
+  griddep_launch_dependents();
   // ---- this CTA's range of the key tiles
   const int B = p.c.B;
   int64_t mine = 0;
@@ -543,8 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         tc_fence_before();
       }
       if (tid == 0) {
-        if (w.t0 > 0) rec.cont = 1, rec.cont_more = w.t1 < w.tiles;
-        else if (w.t1 < w.tiles) rec.start = 1, rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
+        if (w.t0 == 0 && w.t1 < w.tiles) {
+          rec.pieces = 1 + static_cast<int>((w.tiles - w.t1 + per - 1) / per);
+          rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
+        }
       }
     } while (w.next(p));
     if (tid == 0) p.rec[blockIdx.x] = rec;
@@ -702,8 +705,7 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
   attn_nvfp4_tc_kernel<D><<<grid, kThreads, smem, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join_kernel<D, kRows><<<dim3(grid, kRows / 8), 256, 0, stream>>>(p, grid);
-  return cudaGetLastError();
+  return launch_dependent(join_kernel<D, kRows>, dim3(grid, kRows / 8), 256, 0, stream, p);
 }
 
 }  // namespace
