@@ -831,7 +831,7 @@ qrr_status qrr_kv_read_nvfp4(const qrr_kv_nvfp4* cache, int64_t T, const int32_t
 size_t qrr_attention_nvfp4_workspace_bytes(const qrr_kv_nvfp4* cache, int64_t T, int32_t Hq, int32_t max_new) {
   if (!cache || T < 0 || Hq < 0 || max_new < 0 || cache->Hkv <= 0 || (cache->D != 64 && cache->D != 128) || cache->B < 0)
     return 0;
-  return attention_nvfp4_ws_bytes(cache->D, T, cache->B, Hq, cache->Hkv, max_new);
+  return attention_nvfp4_ws_bytes(cache->D, cache->B, Hq, cache->Hkv, max_new);
 }
 
 qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t T, int64_t ld_q, int32_t Hq,
@@ -842,7 +842,7 @@ qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t
   if (Hq < 0 || cache->Hkv <= 0 || (T > 0 && cache->num_pages == 0) || max_new < 0 || (!cu && max_new != 1)) return QRR_ERR_INVALID_ARG;
   if (!(scale > 0.0f) || scale == INFINITY) return QRR_ERR_INVALID_ARG;
   if (Hq % cache->Hkv != 0 || max_new > kMaxTokens / (Hq > 0 ? Hq : 1)) return QRR_ERR_UNSUPPORTED_SHAPE;
-  if (T * Hq > INT32_MAX) return QRR_ERR_UNSUPPORTED_SHAPE;  // rows of out and lse
+  if (T * Hq > INT32_MAX || static_cast<int64_t>(cache->B) * cache->Hkv > INT32_MAX) return QRR_ERR_UNSUPPORTED_SHAPE;  // rows of out and lse
   const int64_t row = static_cast<int64_t>(Hq) * cache->D;
   if (T * row > 0 && (!q || !out)) return QRR_ERR_INVALID_ARG;
   if (T > 1 && ld_q < row) return QRR_ERR_INVALID_ARG;

@@ -7,7 +7,7 @@
 // the G = Hq / Hkv query heads of each of the sequence's new tokens share every
 // key and value that is read.  A row that sees nothing gives zeros, lse -inf.
 //
-// Work is cut stream-K: the 16-token tiles of all (sequence, KV head) items, one
+// Work is cut stream-K: the 32-token tiles of all (sequence, KV head) items, one
 // after another, in equal ranges, one a warp, so ragged lengths balance by
 // themselves (an item counts kItemCost tiles more than it has, about what its
 // start and end cost).  A warp whose range holds a whole item writes its
@@ -16,10 +16,10 @@
 // results do not depend on timing.
 //
 // A tile's codes and scales come by asynchronous copies into the warp's own ring
-// of kStages tiles, three tiles ahead and on into the next item, and from there
+// of kStages tiles, two tiles ahead and on into the next item, and from there
 // to the lanes that feed them to the tensor core (m16n8k16, f16 operands, fp32
-// sums); no warp waits for another.  With K (16 tokens x D) as the A operand the
-// score tile is [16 tokens x 8 rows]; its exponentials, as f16 and transposed by
+// sums); no warp waits for another.  With 16 keys (16 tokens x D) as the A operand
+// a score tile is [16 tokens x 8 rows]; its exponentials, as f16 and transposed by
 // one matrix-move per 8 tokens, are the B operand of O^T += V^T P^T.  The products code x block scale are exact in f16 (at most
 // 6 significant bits, 2^-10 .. 2688).  The query enters as f16 after a power
 // of two a row that brings its largest value into [2^14, 2^15), exact for every
@@ -44,9 +44,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 2; }  // by registers
-constexpr int kMinTiles = 8;  // tiles of a range
-constexpr int kItemCost = 2;
-constexpr int kStages = 4;    // tiles of a warp's ring
+constexpr int kTok = 32;      // tokens of a tile
+constexpr int kMinTiles = 4;  // tiles of a range
+constexpr int kItemCost = 1;
+constexpr int kStages = 3;    // tiles of a warp's ring
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -85,38 +86,46 @@ struct Words {
   }
 };
 
-// A tile in a warp's ring: 16 rows of key and value codes, key scales, value
-// scales.  Keys' rows 4..7 and 12..15 change places, and (D = 128)
-// values' rows 2, 3, 6, 7, ... have their halves swapped, so that the lanes of
-// a read find their bytes in different banks.
+// A tile in a warp's ring: two halves of 16 rows each of key codes, value codes,
+// key scales, value scales.  Keys' rows 4..7 and 12..15 of a half change places,
+// and (D = 128) values' rows 2, 3, 6, 7, ... have their halves swapped, so that
+// the lanes of a read find their bytes in different banks.
 template <int D>
 struct Raw {
-  uint8_t k[8 * D], v[8 * D], ks[D], vs[D];
+  uint8_t k[2][8 * D], v[2][8 * D], ks[2][D], vs[2][D];
 };
 
-// One tile's operands in a lane's registers.  Lane (g, c) = (lane / 4,
+// A half tile's operands in a lane's registers.  Lane (g, c) = (lane / 4,
 // lane % 4) holds, of tokens tau and tau + 8 with tau = g / 2 + 4 (g % 2), the
 // keys' values [D / 4 c, D / 4 (c + 1)), and of tokens c, c + 4, c + 8, c + 12
 // the values' [D / 8 g, D / 8 (g + 1)): the order of tokens and of values that
 // the two MMAs sum over is free, so each lane takes contiguous bytes.
 template <int D>
-struct Tile {
+struct Keys {
   Words<D / 32> k[2];
-  Words<D / 64> v[4];
-  uint32_t ks[2], vs[4];
-  __device__ __forceinline__ void load(const Raw<D>& raw, int lane) {
+  uint32_t s[2];
+  __device__ __forceinline__ void load(const Raw<D>& raw, int half, int lane) {
     const int g = lane >> 2, c = lane & 3, tau = (g >> 1) + 4 * (g & 1), at = tau ^ (D == 128 ? tau >> 2 : 2 * (tau >> 2));
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      k[i].load(raw.k + (at + 8 * i) * (D / 2) + c * (D / 8));
-      const uint8_t* s = raw.ks + (tau + 8 * i) * (D / 16) + c * (D / 64);
-      if constexpr (D == 128) ks[i] = *reinterpret_cast<const uint16_t*>(s);
-      else ks[i] = *s;
+      k[i].load(raw.k[half] + (at + 8 * i) * (D / 2) + c * (D / 8));
+      const uint8_t* x = raw.ks[half] + (tau + 8 * i) * (D / 16) + c * (D / 64);
+      if constexpr (D == 128) s[i] = *reinterpret_cast<const uint16_t*>(x);
+      else s[i] = *x;
     }
+  }
+};
+
+template <int D>
+struct Values {
+  Words<D / 64> v[4];
+  uint32_t s[4];
+  __device__ __forceinline__ void load(const Raw<D>& raw, int half, int lane) {
+    const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j].load(raw.v + (c + 4 * j) * (D / 2) + ((g * (D / 16)) ^ (D == 128 ? 16 * (c & 2) : 0)));
-      vs[j] = raw.vs[(c + 4 * j) * (D / 16) + (D == 128 ? g : g >> 1)];
+      v[j].load(raw.v[half] + (c + 4 * j) * (D / 2) + ((g * (D / 16)) ^ (D == 128 ? 16 * (c & 2) : 0)));
+      s[j] = raw.vs[half][(c + 4 * j) * (D / 16) + (D == 128 ? g : g >> 1)];
     }
   }
 };
@@ -131,7 +140,7 @@ struct Item : Seq {
 __device__ __forceinline__ void seq_item(const Params& p, int b, bool pad, Item& it) {
   static_cast<Seq&>(it) = seq_of(p, b);
   it.b = b;
-  it.tiles = (it.last + 16) >> 4;
+  it.tiles = (it.last + kTok) / kTok;
   const int64_t rows = static_cast<int64_t>(it.n) * p.G;
   const bool here = rows > 0 && rows <= kFewRows && it.last >= 0;
   it.width = !here ? 0 : pad ? (it.tiles + kMinTiles - 1) / kMinTiles * kMinTiles : it.tiles + kItemCost;
@@ -169,16 +178,43 @@ struct Walk : Item {
 };
 
 // The copies of a range's tiles into the warp's ring, kStages - 1 ahead of their
-// use.  The page table is read a tile ahead.
+// use.  Inside a page the addresses only advance; the table's next entry is read
+// a page ahead.  (Pages of 16 tokens: two to a tile.)
 template <int D>
 struct Feed {
   Walk w;
-  const uint8_t *kc, *vc, *sc;  // the lane's bytes of row 0 (scales: keys' in the lower half of the warp)
-  uint32_t to, to_v, to_s;      // its places in the ring's first tile
-  int t, slot, pg;
+  const uint8_t *kp, *vp, *sp;  // the lane's bytes of the next tile (scales: keys' in the lower half of the warp)
+  int64_t rows;                 // from the tile's first half to its second
+  uint32_t to, to_v, to_s;      // places in the ring's first tile
+  uint32_t so;                  // offset of the next tile in the ring
+  int t, next_pg, next_half, lane;
   bool more;
-  __device__ __forceinline__ int page_of(const Params& p) const {
-    return __ldg(p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages + (t >> (p.c.page_shift - 4)));
+  __device__ __forceinline__ void read_page(const Params& p, int tile) {
+    if (tile >= w.stop) return;
+    const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
+    if (p.c.page_shift >= 5) {
+      next_pg = __ldg(table + (tile >> (p.c.page_shift - 5)));
+    } else {
+      next_pg = __ldg(table + 2 * tile);
+      next_half = kTok * tile + 16 <= w.last ? __ldg(table + 2 * tile + 1) : next_pg;
+    }
+  }
+  // addresses of tile t, in the page that `next_pg` names
+  __device__ __forceinline__ void enter_page(const Params& p) {
+    uint32_t now = static_cast<uint32_t>(next_pg), half = static_cast<uint32_t>(next_half);
+    const int tiles = p.c.page_shift >= 5 ? 1 << (p.c.page_shift - 5) : 1;
+    read_page(p, (t & -tiles) + tiles);
+    if (p.c.page_shift >= 5) half = now;
+    const uint32_t pages = static_cast<uint32_t>(p.c.num_pages);
+    if (now >= pages || half >= pages) {
+      flag(p.status, QRR_DEV_BAD_INDEX);
+      now = half = 0u;
+    }
+    const uint32_t row = ((now * p.c.Hkv + w.h) << p.c.page_shift) + static_cast<uint32_t>(t & (tiles - 1)) * kTok;
+    rows = p.c.page_shift >= 5 ? 16 : (static_cast<int64_t>(half) - now) * p.c.Hkv * 16;
+    kp = p.c.kc + static_cast<uint64_t>(row) * (D / 2) + lane * 16;
+    vp = p.c.vc + static_cast<uint64_t>(row) * (D / 2) + lane * 16;
+    sp = (lane < 16 ? p.c.ks : p.c.vs) + (static_cast<uint64_t>(row) + (lane & 15)) * (D / 16);
   }
   // the first tile at or after t, over the ends of items
   __device__ __forceinline__ void settle(const Params& p, bool pad) {
@@ -186,47 +222,49 @@ struct Feed {
       more = w.next(p, pad);
       t = w.t0;
     }
-    if (more) pg = page_of(p);
+    if (more) {
+      read_page(p, t);
+      enter_page(p);
+    }
   }
-  __device__ __forceinline__ void begin(const Params& p, const Walk& from, const Raw<D>* ring, int lane, bool pad) {
+  __device__ __forceinline__ void begin(const Params& p, const Walk& from, const Raw<D>* ring, int lane_, bool pad) {
     constexpr int kChunks = D / 32;  // of 16 bytes a row
+    lane = lane_;
     const int r = lane / kChunks, c = lane % kChunks;
-    kc = p.c.kc + lane * 16;
-    vc = p.c.vc + lane * 16;
-    const int half = lane & 15;
-    sc = (lane < 16 ? p.c.ks : p.c.vs) + half * (D / 16);
     to = smem_u32(ring) + (r ^ ((D == 128 ? 1 : 2) * (r >> 2 & 1))) * (D / 2) + c * 16;
     to_v = smem_u32(ring->v) + r * (D / 2) + ((c * 16) ^ (D == 128 ? 16 * (r & 2) : 0));
-    to_s = smem_u32(lane < 16 ? ring->ks : ring->vs) + half * (D / 16);
+    to_s = smem_u32(lane < 16 ? ring->ks : ring->vs) + (lane & 15) * (D / 16);
+    so = 0;
     w = from;
     t = w.t0;
-    slot = 0;
+    next_half = 0;
     more = true;
     settle(p, pad);
   }
   __device__ __forceinline__ void issue(const Params& p, bool pad) {
     if (more) {
-      uint32_t now = static_cast<uint32_t>(pg);
-      if (now >= static_cast<uint32_t>(p.c.num_pages)) {
-        flag(p.status, QRR_DEV_BAD_INDEX);
-        now = 0u;
-      }
-      const uint32_t page_rows = 1u << p.c.page_shift;
-      const uint32_t row = (now * p.c.Hkv + w.h) * page_rows + (static_cast<uint32_t>(16 * t) & (page_rows - 1));
-      const uint64_t c0 = static_cast<uint64_t>(row) * (D / 2), s0 = static_cast<uint64_t>(row) * (D / 16);
-      const uint32_t at = to + slot * static_cast<uint32_t>(sizeof(Raw<D>));
-      const uint32_t av = to_v + slot * static_cast<uint32_t>(sizeof(Raw<D>));
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + 512 * i), "l"(kc + c0 + 512 * i) : "memory");
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(av + 512 * i), "l"(vc + c0 + 512 * i) : "memory");
+      for (int h = 0; h < 2; ++h) {
+        const int64_t off = h * rows;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + so + 8 * D * h + 512 * i),
+                       "l"(kp + off * (D / 2) + 512 * i)
+                       : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to_v + so + 8 * D * h + 512 * i),
+                       "l"(vp + off * (D / 2) + 512 * i)
+                       : "memory");
+        }
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to_s + so + D * h), "l"(sp + off * (D / 16)), "n"(D / 16)
+                     : "memory");
       }
-      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to_s + slot * static_cast<uint32_t>(sizeof(Raw<D>))),
-                   "l"(sc + s0), "n"(D / 16)
-                   : "memory");
-      slot = slot == kStages - 1 ? 0 : slot + 1;
+      so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
       ++t;
-      settle(p, pad);
+      kp += 16 * D;
+      vp += 16 * D;
+      sp += 2 * D;
+      if (t >= w.stop) settle(p, pad);
+      else if (p.c.page_shift < 5 || (t & ((1 << (p.c.page_shift - 5)) - 1)) == 0) enter_page(p);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
@@ -239,13 +277,13 @@ template <int D, int NT>
 struct State {
   uint32_t q[NT][D / 16][2];
   float f[NT][2];    // score factor of the lane's two rows (log2 units)
-  int lim[NT][2];    // their last visible position
+  int lim[NT][2];    // their last visible position, before the piece's end
   float m[NT][2], l[NT][2];
   float o[NT][D / 16][4];
 };
 
 template <int D, int NT>
-__device__ __forceinline__ void load_rows(const Params& p, const Item& it, int lane, State<D, NT>& s) {
+__device__ __forceinline__ void load_rows(const Params& p, const Item& it, int end, int lane, State<D, NT>& s) {
   const int g = lane >> 2, c = lane & 3;
   const float kg = p.c.kg ? __ldg(p.c.kg + it.h) : 1.0f;
 #pragma unroll
@@ -272,8 +310,9 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) s.q[nt][j][i] = f16x2(sc(bf16_lo(w[2 * j + i])), sc(bf16_hi(w[2 * j + i])));
-    const float f = p.scale * kLog2e * kg * ldexpf(1.0f, e);
-    const int lim = in ? min(it.pos + p.byG.div(r), it.last) : -1;
+    // at least the smallest normal value: a masked score times it stays -inf
+    const float f = fmaxf(p.scale * kLog2e * kg * ldexpf(1.0f, e), 1.17549435e-38f);
+    const int lim = in ? min(min(it.pos + p.byG.div(r), it.last), end - 1) : -1;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       s.f[nt][x] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * c + x));
@@ -288,18 +327,21 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int l
   }
 }
 
-// One tile of 16 tokens, of which `live` exist (16 or more: all).  `all`: every
-// row sees every token of it.
+// One tile, of whose tokens `live` exist (kTok or more: all).  `all`: every row
+// sees every token of it.
 template <int D, int NT>
-__device__ __forceinline__ void step(const Tile<D>& x, int t, int live, bool all, int lane, State<D, NT>& s) {
+__device__ __forceinline__ void step(const Raw<D>& raw, int t, int live, bool all, int lane, State<D, NT>& s) {
   const int g = lane >> 2, c = lane & 3;
-  float sc[NT][4];
+  float e[2][NT][4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int h = 0; h < 2; ++h) {
+    Keys<D> x;
+    x.load(raw, h, lane);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sc[nt][i] = 0.0f;
-  {
-    const uint32_t s0 = e4m3x2_to_f16x2(x.ks[0]), s1 = e4m3x2_to_f16x2(x.ks[1]);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[h][nt][i] = 0.0f;
+    const uint32_t s0 = e4m3x2_to_f16x2(x.s[0]), s1 = e4m3x2_to_f16x2(x.s[1]);
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
       const uint32_t sel = w < 2 ? 0x1010u : 0x3232u;  // D = 64: both words in the lane's one block
@@ -311,81 +353,85 @@ __device__ __forceinline__ void step(const Tile<D>& x, int t, int live, bool all
       for (int i = 0; i < 4; ++i) a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f1);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        mma16816(sc[nt], a[0], b[0], a[1], b[1], s.q[nt][2 * w][0], s.q[nt][2 * w][1]);
-        mma16816(sc[nt], a[2], b[2], a[3], b[3], s.q[nt][2 * w + 1][0], s.q[nt][2 * w + 1][1]);
+        mma16816(e[h][nt], a[0], b[0], a[1], b[1], s.q[nt][2 * w][0], s.q[nt][2 * w][1]);
+        mma16816(e[h][nt], a[2], b[2], a[3], b[3], s.q[nt][2 * w + 1][0], s.q[nt][2 * w + 1][1]);
       }
     }
   }
-  // lane's scores: rows 2 c, 2 c + 1 of each group; tokens tau, tau + 8; against
-  // the reference in log2 units
-  const int tok = 16 * t + (g >> 1) + 4 * (g & 1);
-  float e[NT][4], most = -INFINITY;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e[nt][i] = fmaf(sc[nt][i], s.f[nt][i & 1], -s.m[nt][i & 1]);
-    }
+  // lane's scores: rows 2 c, 2 c + 1 of each group; tokens tau, tau + 8 of each
+  // half
+  const int tok = kTok * t + (g >> 1) + 4 * (g & 1);
   if (!all)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((i < 2 ? tok : tok + 8) > s.lim[nt][i & 1]) e[nt][i] = -INFINITY;
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) most = max3(max3(most, e[nt][0], e[nt][1]), e[nt][2], e[nt][3]);
+        for (int i = 0; i < 4; ++i)
+          if (tok + 16 * h + 8 * (i >> 1) > s.lim[nt][i & 1]) e[h][nt][i] = -INFINITY;
+  float top[NT][2], most = -INFINITY;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      top[nt][i] = fmaxf(max3(e[0][nt][i], e[0][nt][i + 2], e[1][nt][i]), e[1][nt][i + 2]);
+    most = max3(most, fmaf(top[nt][0], s.f[nt][0], -s.m[nt][0]), fmaf(top[nt][1], s.f[nt][1], -s.m[nt][1]));
+  }
   if (__any_sync(0xFFFFFFFFu, most > kRoom)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        // the row's largest score of the tile, itself
-        const bool see0 = all || tok <= s.lim[nt][i], see1 = all || tok + 8 <= s.lim[nt][i];
-        const float s0 = see0 ? sc[nt][i] * s.f[nt][i] : -INFINITY, s1 = see1 ? sc[nt][i + 2] * s.f[nt][i] : -INFINITY;
-        float v = fmaxf(s0, s1);
+        float v = top[nt][i];
         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-        const float m = fmaxf(v - kLift, s.m[nt][i]), a = ex2(s.m[nt][i] - m);
+        const float m = fmaxf(v * s.f[nt][i] - kLift, s.m[nt][i]), a = ex2(s.m[nt][i] - m);
         s.m[nt][i] = m;
         s.l[nt][i] *= a;
-        e[nt][i] = s0 - m;
-        e[nt][i + 2] = s1 - m;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) s.o[nt][j][i] *= a, s.o[nt][j][i + 2] *= a;
       }
   }
-  uint32_t p[NT][2];
+  uint32_t p[2][NT][2];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[nt][i] = ex2(e[nt][i]);
-    s.l[nt][0] += e[nt][0] + e[nt][2];
-    s.l[nt][1] += e[nt][1] + e[nt][3];
-    p[nt][0] = movmatrix(f16x2(e[nt][0], e[nt][1]));
-    p[nt][1] = movmatrix(f16x2(e[nt][2], e[nt][3]));
-  }
-  // the two pairs' scales; those of tokens that do not exist count as zero (what
-  // lies there may be anything, a NaN among it)
-  uint32_t v01 = __byte_perm(x.vs[0], x.vs[1], 0x7740), v23 = __byte_perm(x.vs[2], x.vs[3], 0x7740);
-  if (live < 16) {
-    v01 &= (c < live ? 0xFFu : 0u) | (c + 4 < live ? 0xFF00u : 0u);
-    v23 &= (c + 8 < live ? 0xFFu : 0u) | (c + 12 < live ? 0xFF00u : 0u);
-  }
-  const uint32_t f0 = e4m3x2_to_f16x2(v01), f1 = e4m3x2_to_f16x2(v23);
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-  for (int w = 0; w < D / 64; ++w) {
-    // bytes of (first, second) token's codes of one value: even values, odd values
-    uint32_t a[4], b[4], d[4], h[4];
-    f16x2x4_from_e2m1x8((x.v[0].w[w] & 0x0F0F0F0Fu) | (x.v[1].w[w] << 4 & 0xF0F0F0F0u), a);
-    f16x2x4_from_e2m1x8((x.v[0].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[1].w[w] & 0xF0F0F0F0u), b);
-    f16x2x4_from_e2m1x8((x.v[2].w[w] & 0x0F0F0F0Fu) | (x.v[3].w[w] << 4 & 0xF0F0F0F0u), d);
-    f16x2x4_from_e2m1x8((x.v[2].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[3].w[w] & 0xF0F0F0F0u), h);
+      for (int i = 0; i < 4; ++i) e[h][nt][i] = ex2(fmaf(e[h][nt][i], s.f[nt][i & 1], -s.m[nt][i & 1]));
+      s.l[nt][0] += e[h][nt][0] + e[h][nt][2];
+      s.l[nt][1] += e[h][nt][1] + e[h][nt][3];
+      p[h][nt][0] = movmatrix(f16x2(e[h][nt][0], e[h][nt][1]));
+      p[h][nt][1] = movmatrix(f16x2(e[h][nt][2], e[h][nt][3]));
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), h[i] = hmul2(h[i], f1);
+  for (int h = 0; h < 2; ++h) {
+    Values<D> x;
+    x.load(raw, h, lane);
+    // the two pairs' scales; those of tokens that do not exist count as zero (what
+    // lies there may be anything, a NaN among it)
+    uint32_t v01 = __byte_perm(x.s[0], x.s[1], 0x7740), v23 = __byte_perm(x.s[2], x.s[3], 0x7740);
+    if (live < kTok) {
+      const int n = live - 16 * h - c;
+      v01 &= (n > 0 ? 0xFFu : 0u) | (n > 4 ? 0xFF00u : 0u);
+      v23 &= (n > 8 ? 0xFFu : 0u) | (n > 12 ? 0xFF00u : 0u);
+    }
+    const uint32_t f0 = e4m3x2_to_f16x2(v01), f1 = e4m3x2_to_f16x2(v23);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma16816(s.o[nt][4 * w + i], a[i], b[i], d[i], h[i], p[nt][0], p[nt][1]);
+    for (int w = 0; w < D / 64; ++w) {
+      // bytes of (first, second) token's codes of one value: even values, odd values
+      uint32_t a[4], b[4], d[4], u[4];
+      f16x2x4_from_e2m1x8((x.v[0].w[w] & 0x0F0F0F0Fu) | (x.v[1].w[w] << 4 & 0xF0F0F0F0u), a);
+      f16x2x4_from_e2m1x8((x.v[0].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[1].w[w] & 0xF0F0F0F0u), b);
+      f16x2x4_from_e2m1x8((x.v[2].w[w] & 0x0F0F0F0Fu) | (x.v[3].w[w] << 4 & 0xF0F0F0F0u), d);
+      f16x2x4_from_e2m1x8((x.v[2].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[3].w[w] & 0xF0F0F0F0u), u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), u[i] = hmul2(u[i], f1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s.o[nt][4 * w + i], a[i], b[i], d[i], u[i], p[h][nt][0], p[h][nt][1]);
+      }
     }
   }
 }
@@ -395,17 +441,21 @@ __device__ __forceinline__ void step(const Tile<D>& x, int t, int live, bool all
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(const Params p) {
   constexpr int RT = 8 * NT;
-  __shared__ __align__(16) Raw<D> ring[kWarps][kStages];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Raw<D>* const ring = reinterpret_cast<Raw<D>*>(smem_raw) + kStages * (threadIdx.x >> 5);  // the warp's
   __shared__ int64_t sums[2][kWarps], at_off[kWarps];
   __shared__ int at_b[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_launch_dependents();
 
-  // a sequence that sees nothing is no work: one CTA writes its rows
+  // sequences without work here; of one that sees nothing a CTA writes the rows
   const int B = p.c.B;
   for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    const Seq q = seq_of(p, b);
-    if (q.last >= 0 || static_cast<int64_t>(q.n) * p.G > kFewRows) continue;
+    Item q;
+    seq_item(p, b, false, q);
+    if (q.width > 0) continue;
+    for (int i = tid; i < p.c.Hkv; i += kThreads) p.rec[static_cast<int64_t>(b) * p.c.Hkv + i].pieces = 0;
+    if (static_cast<int64_t>(q.n) * p.G > kFewRows) continue;
     const int64_t row = static_cast<int64_t>(q.first) * p.Hq;
     for (int i = tid; i < q.n * p.Hq * (D / 8); i += kThreads) reinterpret_cast<uint4*>(p.out + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (p.lse)
@@ -469,35 +519,30 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(c
   __syncthreads();
   const int range = blockIdx.x * kWarps + warp;
   const int64_t left = min(per, total - range * per);
-  if (left <= 0) {
-    if (lane == 0) p.rec[range].pieces = 0;
-    return;
-  }
+  if (left <= 0) return;
 
   Walk it;
   it.begin(p, at_b[warp], at_off[warp], pad, left);
   Feed<D> feed;
-  feed.begin(p, it, ring[warp], lane, pad);
+  feed.begin(p, it, ring, lane, pad);
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) feed.issue(p, pad);
   const int c = lane & 3, g = lane >> 2;
-  Record rec{};
   State<D, NT> s;
-  int slot = 0;
+  const uint8_t* const mine = reinterpret_cast<const uint8_t*>(ring);
+  uint32_t so = 0;
   do {
-    load_rows<D, NT>(p, it, lane, s);
+    load_rows<D, NT>(p, it, kTok * it.stop, lane, s);
     // tiles before this one are seen whole by every row (rows behind the last one
     // are never read: no mask for them)
-    const int whole = (min(it.pos, it.last) + 1) >> 4;
+    const int whole = (min(it.pos, it.last) + 1) / kTok;
 #pragma unroll 1
     for (int t = it.t0; t < it.stop; ++t) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // the tile is there for all lanes, and the one before it read by all
-      Tile<D> x;
-      x.load(ring[warp][slot], lane);
       feed.issue(p, pad);
-      slot = slot == kStages - 1 ? 0 : slot + 1;
-      step<D, NT>(x, t, it.last + 1 - 16 * t, t < whole, lane, s);
+      step<D, NT>(*reinterpret_cast<const Raw<D>*>(mine + so), t, it.last + 1 - kTok * t, t < whole, lane, s);
+      so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
     }
     // ---- the rows' results, or a piece of them
     const bool cut0 = it.t0 > 0, cut1 = it.t1 < it.width;
@@ -534,13 +579,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(c
           if (g == 0) p.pm[piece + r] = s.m[nt][i], p.pl[piece + r] = l;
         }
       }
-    if (!cut0 && cut1) {
-      rec.pieces = 1 + static_cast<int>((it.width - it.t1 + per - 1) / per);
-      rec.rt = 0, rec.h = it.h, rec.first = it.first, rec.n = it.n;
-    }
+    if (!cut0 && lane == 0)
+      p.rec[static_cast<int64_t>(it.b) * p.c.Hkv + it.h] =
+          Record{cut1 ? 1 + static_cast<int>((it.width - it.t1 + per - 1) / per) : 0, range, 0, it.h, it.first, it.n};
   } while (it.next(p, pad));
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if (lane == 0) p.rec[range] = rec;
 }
 
 namespace {
@@ -548,27 +591,31 @@ namespace {
 template <int D, int NT>
 cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   constexpr int RT = 8 * NT;
-  const int ranges = grid * kWarps;
-  const Params p = make_params(a, a.ws, ranges, RT);
-  attn_nvfp4_kernel<D, NT><<<grid, kThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const int ranges = grid * kWarps, items = a.c.B * a.c.Hkv;
+  const Params p = make_params(a, a.ws, ranges, RT, items);
+  constexpr int smem = static_cast<int>(sizeof(Raw<D>)) * kStages * kWarps;
+  cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(join_kernel<D, RT>, dim3(ranges, NT), 256, 0, stream, p);
+  attn_nvfp4_kernel<D, NT><<<grid, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent(join_kernel<D, RT>, dim3(items, NT), 256, 0, stream, p);
 }
 
 // Whether some sequence may have few rows, or many (see kFewRows).
 bool any_few(int G) { return G <= kFewRows; }
 bool any_many(int64_t max_new, int G) { return max_new * G > kFewRows; }
 
-size_t few_ws_bytes(int D) {
-  return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(1) * kWarps, 8), ws_bytes(D, kMaxSms * ctas_per_sm(2) * kWarps, 16));
+size_t few_ws_bytes(int D, int64_t items) {
+  return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(1) * kWarps, 8, items),
+                  ws_bytes(D, kMaxSms * ctas_per_sm(2) * kWarps, 16, items));
 }
 
 }  // namespace
 
-size_t attention_nvfp4_ws_bytes(int D, int64_t, int, int Hq, int Hkv, int64_t max_new) {
+size_t attention_nvfp4_ws_bytes(int D, int B, int Hq, int Hkv, int64_t max_new) {
   const int G = Hq / Hkv;
-  return few_ws_bytes(D) + (any_many(max_new, G) ? attention_nvfp4_tc_ws_bytes(D) : 0);
+  return few_ws_bytes(D, static_cast<int64_t>(B) * Hkv) + (any_many(max_new, G) ? attention_nvfp4_tc_ws_bytes(D) : 0);
 }
 
 cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) {
@@ -583,7 +630,7 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
                                        : (one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream));
     if (e != cudaSuccess) return e;
   }
-  return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D), stream) : cudaSuccess;
+  return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D, static_cast<int64_t>(a.c.B) * a.c.Hkv), stream) : cudaSuccess;
 }
 
 }  // namespace qrr

@@ -56,11 +56,12 @@ __device__ __forceinline__ int query_exp(uint32_t mx) {
   return (mx >= 0x80u ? static_cast<int>(mx >> 7) - 127 : 31 - __clz(static_cast<int>(mx)) - 133) - 14;
 }
 
-// Pieces of items that cross ranges.  Piece 2 k is range k's first when it
-// continues an item, piece 2 k + 1 its last when it starts one that the next
-// ranges continue.
+// An item that crosses ranges.  Piece 2 k is range k's first when it continues
+// an item, piece 2 k + 1 its last when it starts one that the next ranges
+// continue.
 struct Record {
-  int pieces;           // of the item that starts in the range and goes on (0: none)
+  int pieces;           // 0: there is nothing to join
+  int range;            // that the item starts in
   int rt, h, first, n;  // its row tile, KV head, the sequence's rows
 };
 
@@ -116,20 +117,19 @@ __device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, in
   return static_cast<int64_t>(first + p.byG.div(row)) * p.Hq + h * p.G + p.byG.mod(row);
 }
 
-// Joins the pieces of the item that starts in range k = blockIdx.x and is
-// continued by the next ones: a warp a row.  The lanes take the pieces' (m, l),
+// Joins the pieces of record blockIdx.x's item: a warp a row.  The lanes take the pieces' (m, l),
 // 32 at a time; sums over them are formed in the order of the pieces' lanes,
 // the outputs' in the order of the pieces.  RT: rows of a piece.
 template <int D, int RT>
 __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   constexpr int V = D / 32;
   griddep_wait();
-  const int k = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const Record rec = p.rec[k];
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Record rec = p.rec[blockIdx.x];
   const int row = rec.rt * RT + r;
   if (rec.pieces == 0 || row >= rec.n * p.G) return;
   const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * k + 1 : 2 * (k + i)) * RT + r; };
+  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)) * RT + r; };
   float m = kNone, l = 0.0f, o[V] = {};
   for (int i0 = 0; i0 < rec.pieces; i0 += 32) {
     const int n = min(32, rec.pieces - i0);
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
     top = fmaxf(top, m);
-    const float old = ex2(m - top), a = ex2(mi - top);
+    const float old = ex2(m - top), a = lane < n ? ex2(mi - top) : 0.0f;
     m = top;
     float sum = a * li;
 #pragma unroll
@@ -150,16 +150,24 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
     l = l * old + sum;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] *= old;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float ai = __shfl_sync(0xFFFFFFFFu, a, i);
-      const float* src = p.po + piece(i0 + i) * D + V * lane;
-      if constexpr (V == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        o[0] += ai * v.x, o[1] += ai * v.y, o[2] += ai * v.z, o[3] += ai * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        o[0] += ai * v.x, o[1] += ai * v.y;
+    for (int i = 0; i < n; i += 8) {  // eight loads under way at a time
+      float v[8][V];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float* src = p.po + piece(i0 + min(i + u, n - 1)) * D + V * lane;
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[u][0] = x.x, v[u][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float ai = __shfl_sync(0xFFFFFFFFu, a, (i + u) & 31);  // 0 behind the last piece
+#pragma unroll
+        for (int d = 0; d < V; ++d) o[d] += ai * v[u][d];
       }
     }
   }
@@ -194,18 +202,18 @@ cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, unsigned threads, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Workspace of `ranges` ranges whose pieces have `rt` rows.
+// Workspace of `ranges` ranges whose pieces have `rt` rows, and their records.
 inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-inline size_t ws_bytes(int D, int ranges, int rt) {
+inline size_t ws_bytes(int D, int ranges, int rt, int64_t records) {
   const size_t rows = static_cast<size_t>(2) * ranges * rt;
-  return align256(sizeof(Record) * ranges) + 2 * align256(rows * 4) + align256(rows * D * 4);
+  return align256(sizeof(Record) * records) + 2 * align256(rows * 4) + align256(rows * D * 4);
 }
-inline Params make_params(const AttnNvfp4Args& a, uint8_t* w, int ranges, int rt) {
+inline Params make_params(const AttnNvfp4Args& a, uint8_t* w, int ranges, int rt, int64_t records) {
   const int G = a.Hq / a.c.Hkv;
   Params p{a.c, a.r, a.q, a.ld_q, a.Hq, G, a.max_new, FastDiv(static_cast<uint32_t>(G)), a.scale, a.out, a.lse};
   const size_t rows = static_cast<size_t>(2) * ranges * rt;
   p.rec = reinterpret_cast<Record*>(w);
-  w += align256(sizeof(Record) * ranges);
+  w += align256(sizeof(Record) * records);
   p.pm = reinterpret_cast<float*>(w);
   w += align256(rows * 4);
   p.pl = reinterpret_cast<float*>(w);

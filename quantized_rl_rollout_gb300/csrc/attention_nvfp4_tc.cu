@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
       if (tid == 0) {
         if (w.t0 == 0 && w.t1 < w.tiles) {
           rec.pieces = 1 + static_cast<int>((w.tiles - w.t1 + per - 1) / per);
-          rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
+          rec.range = blockIdx.x, rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
         }
       }
     } while (w.next(p));
@@ -701,7 +701,7 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
   int dev = 0, sms = kSMs;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = sms < kMaxSms ? sms : kMaxSms;
-  const Params p = make_params(a, ws, grid, kRows);
+  const Params p = make_params(a, ws, grid, kRows, grid);
   attn_nvfp4_tc_kernel<D><<<grid, kThreads, smem, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -710,7 +710,7 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
 
 }  // namespace
 
-size_t attention_nvfp4_tc_ws_bytes(int D) { return ws_bytes(D, kMaxSms, kRows); }
+size_t attention_nvfp4_tc_ws_bytes(int D) { return ws_bytes(D, kMaxSms, kRows, kMaxSms); }
 
 cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
   return a.c.D == 128 ? launch<128>(a, ws, stream) : launch<64>(a, ws, stream);

@@ -70,7 +70,7 @@ struct AttnNvfp4Args {
   int32_t* status;
 };
 
-size_t attention_nvfp4_ws_bytes(int D, int64_t T, int B, int Hq, int Hkv, int64_t max_new);
+size_t attention_nvfp4_ws_bytes(int D, int B, int Hq, int Hkv, int64_t max_new);
 cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream);
 
 }  // namespace qrr
