@@ -782,7 +782,6 @@ static qrr_status check_kv_nvfp4(const qrr_kv_nvfp4* c, int64_t T, const int32_t
   if (T > kMaxTokens || static_cast<int64_t>(c->max_pages) * c->page > kMaxTokens || c->Hkv > 65536)
     return QRR_ERR_UNSUPPORTED_SHAPE;
   if (static_cast<int64_t>(c->num_pages) * c->Hkv > static_cast<int64_t>(UINT32_MAX) / c->page) return QRR_ERR_UNSUPPORTED_SHAPE;
-  if (T * 2 * c->Hkv * (c->D / 16) > static_cast<int64_t>(INT32_MAX) * 256) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (!cu && T != c->B) return QRR_ERR_INVALID_ARG;
   if (T > 0 && c->Hkv > 0 && !pos && c->B > 0) return QRR_ERR_INVALID_ARG;
   if (T > 0 && c->Hkv > 0 && static_cast<int64_t>(c->B) * c->max_pages > 0 && !c->page_table)

@@ -594,11 +594,17 @@ cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   const int ranges = grid * kWarps, items = a.c.B * a.c.Hkv;
   const Params p = make_params(a, a.ws, ranges, RT, items);
   constexpr int smem = static_cast<int>(sizeof(Raw<D>)) * kStages * kWarps;
-  cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  static bool attr = false;
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
   attn_nvfp4_kernel<D, NT><<<grid, kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  const cudaError_t e = cudaGetLastError();
+  // a cache whose longest sequence fits a range, and a range for every item:
+  // nothing is cut
+  if (e != cudaSuccess || (a.c.capacity() <= kMinTiles * kTok && items <= ranges)) return e;
   return launch_dependent(join_kernel<D, RT>, dim3(items, NT), 256, 0, stream, p);
 }
 

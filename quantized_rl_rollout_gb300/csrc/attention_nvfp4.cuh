@@ -65,21 +65,6 @@ struct Record {
   int rt, h, first, n;  // its row tile, KV head, the sequence's rows
 };
 
-// x / d for 0 <= x < 2^31 by a multiplication (T. Granlund, P. Montgomery,
-// "Division by invariant integers using multiplication", PLDI 1994).
-struct FastDiv {
-  uint32_t d, mul, shift;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t d_) : d(d_), mul(0), shift(0) {
-    while ((1ull << shift) < d) ++shift;
-    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
-  }
-  __device__ __forceinline__ int div(int x) const {
-    return static_cast<int>((__umulhi(mul, static_cast<uint32_t>(x)) + static_cast<uint32_t>(x)) >> shift);
-  }
-  __device__ __forceinline__ int mod(int x) const { return x - div(x) * static_cast<int>(d); }
-};
-
 struct Params {
   KvNvfp4 c;
   KvRows r;

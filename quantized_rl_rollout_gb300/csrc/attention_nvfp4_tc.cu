@@ -696,8 +696,12 @@ template <int D>
 cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
   constexpr int smem = static_cast<int>(sizeof(Smem<D>)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  const cudaError_t at = cudaFuncSetAttribute(attn_nvfp4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (at != cudaSuccess) return at;
+  static bool attr = false;
+  if (!attr) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    attr = true;
+  }
   int dev = 0, sms = kSMs;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = sms < kMaxSms ? sms : kMaxSms;

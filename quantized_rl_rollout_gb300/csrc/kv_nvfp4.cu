@@ -7,11 +7,19 @@
 // weight quantizer's rule with g in the place of the tensor scale.
 // Read: bf16_rn(fp32(e2m1(code) e4m3(s)) g).
 //
-// Both are bound by memory: 2 bytes a value on one side, 0.5625 on the other.
-// One thread takes one block of 16 values (two 16-byte accesses of bf16, one
-// 8-byte access of codes, one scale byte).
+// Both are bound by memory: 2 bytes a value on one side, 0.5625 on the other.  A
+// CTA takes some tokens; it finds their places first (a thread a token), then
+// its threads take units of 32 values of them in turn: 64 bytes of bf16, 16 of
+// codes, two scales.
+//
+// The correctly rounded quotients are not formed where they cannot matter: with
+// y near 1 / d, x / d lies between x y (1 - 2^-20) and x y (1 + 2^-20), and where
+// both round to the same code, so does the quotient (rounding is monotonic).
+// Only blocks with a value that near a midpoint of the grid take the division.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <algorithm>
 
 #include "kv_nvfp4.cuh"
 
@@ -20,6 +28,7 @@ namespace qrr {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxTokensCta = 256;
 
 // The sequence that row t belongs to (offsets ascending), -1 for a row behind
 // the last sequence.
@@ -34,107 +43,204 @@ __device__ __forceinline__ int seq_of(const KvRows& r, int B, int t) {
   return lo < B && t >= __ldg(r.cu + lo) ? lo : -1;
 }
 
-// Cache row of call row t and head h; -1: no token (padding, a position below
-// zero), -2: outside the table or its page outside the cache.
-__device__ __forceinline__ int64_t place(const KvNvfp4& c, const KvRows& r, int t, int h) {
+constexpr uint32_t kNoToken = 0xFFFFFFFFu;   // padding, a position below zero
+constexpr uint32_t kBadToken = 0xFFFFFFFEu;  // outside the table, or its page outside the cache
+
+// Cache row of call row t and head 0.
+__device__ __forceinline__ uint32_t place(const KvNvfp4& c, const KvRows& r, int t) {
   const int b = seq_of(r, c.B, t);
-  if (b < 0) return -1;
+  if (b < 0) return kNoToken;
   const int64_t p = static_cast<int64_t>(__ldg(r.pos + b)) + (r.cu ? t - __ldg(r.cu + b) : 0);
-  if (p < 0) return -1;
-  if (p >= c.capacity()) return -2;
+  if (p < 0) return kNoToken;
+  if (p >= c.capacity()) return kBadToken;
   const int pg = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + (p >> c.page_shift));
-  if (pg < 0 || pg >= c.num_pages) return -2;
-  return kv_row(c, pg, h, static_cast<int>(p) & ((1 << c.page_shift) - 1));
+  if (pg < 0 || pg >= c.num_pages) return kBadToken;
+  return static_cast<uint32_t>(kv_row(c, pg, 0, static_cast<int>(p) & ((1 << c.page_shift) - 1)));
 }
 
-}  // namespace
+// How a CTA's units number: `units` of a token, keys' before values'.
+struct Units {
+  int tokens;  // a CTA's
+  FastDiv units;
+};
 
-__global__ void __launch_bounds__(kThreads) kv_append_nvfp4_kernel(const KvNvfp4 c, const KvRows r,
-                                                                   const uint16_t* __restrict__ k,
-                                                                   const uint16_t* __restrict__ v, int64_t ld_k,
-                                                                   int64_t ld_v, int32_t* status) {
-  const int bpr = c.D / 16, per_kind = c.Hkv * bpr;  // blocks of a row of one head, of a token's keys
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t t = idx / (2 * per_kind);
-  if (t >= r.T) return;
-  int rest = static_cast<int>(idx - t * 2 * per_kind);
-  const bool is_v = rest >= per_kind;
-  if (is_v) rest -= per_kind;
-  const int h = rest / bpr, blk = rest % bpr;
-  const int64_t row = place(c, r, static_cast<int>(t), h);
-  if (row < 0) {
-    if (row == -2) flag(status, QRR_DEV_BAD_INDEX);
-    return;
+// One unit of a token: kind, head, chunk of 32 values of the head's row.
+struct Unit {
+  bool value;
+  int h, chunk;
+  __device__ __forceinline__ Unit(const KvNvfp4& c, int u, int units) {
+    value = u >= units / 2;
+    if (value) u -= units / 2;
+    const int shift = c.D == 128 ? 2 : 1;
+    h = u >> shift;
+    chunk = u & ((1 << shift) - 1);
   }
-  const uint16_t* src = (is_v ? v + t * ld_v : k + t * ld_k) + static_cast<int64_t>(rest) * 16;
-  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(src)), b = __ldcs(reinterpret_cast<const uint4*>(src) + 1);
-  uint32_t m = max(absmax_bits8(a), absmax_bits8(b));
+};
+
+// The places of the CTA's tokens t0 .. t0 + n - 1, in shared memory.
+__device__ __forceinline__ int find_places(const KvNvfp4& c, const KvRows& r, const Units& un, int t0, uint32_t* at,
+                                           int32_t* status) {
+  const int n = min(un.tokens, static_cast<int>(r.T) - t0);
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    at[i] = place(c, r, t0 + i);
+    if (at[i] == kBadToken) flag(status, QRR_DEV_BAD_INDEX);
+  }
+  __syncthreads();
+  return n;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+
+// E2M1 codes of 8 values times y.
+__device__ __forceinline__ uint32_t codes_of(const uint64_t (&x)[4], uint64_t y) {
+  const float2 a = unpair(mul2(x[0], y)), b = unpair(mul2(x[1], y)), c = unpair(mul2(x[2], y)), d = unpair(mul2(x[3], y));
+  const float v[8] = {a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+  return cvt_e2m1x8(v);
+}
+
+__device__ __forceinline__ float rcp_near(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr float kUnder = 1.0f - 0x1p-20f, kOver = 1.0f + 0x1p-20f;
+
+// The scale byte and the codes of one block of 16 values.
+__device__ __forceinline__ uint32_t quantize_block(const uint4 (&x)[2], float g, uint2& codes, int32_t* status) {
+  uint32_t m = max(absmax_bits8(x[0]), absmax_bits8(x[1]));
   if (m >= 0x7F80u) {
     flag(status, QRR_DEV_NONFINITE);
     m = 0x7F7Fu;  // the scale written stays finite
   }
-  const float* gp = is_v ? c.vg : c.kg;
-  const float g = gp ? __ldg(gp + h) : 1.0f;
-  const uint32_t s = cvt_e4m3x2(__fdiv_rn(bf16bits_to_f32(m), __fmul_rn(6.0f, g)), 0.0f) & 0xFFu;
-  const float d = __fmul_rn(e4m3_to_f32(s), g);
-  uint2 codes = make_uint2(0u, 0u);
+  const float amax = bf16bits_to_f32(m), g6 = __fmul_rn(6.0f, g);
+  const float near = amax * rcp_near(g6);
+  const uint32_t both = cvt_e4m3x2(near * kUnder, near * kOver);
+  uint32_t s = both & 0xFFu;
+  // (a divisor whose reciprocal leaves the normal range takes the division too)
+  if (s != both >> 8 || !(g6 > 0x1p-100f && g6 < 0x1p100f)) s = cvt_e4m3x2(__fdiv_rn(amax, g6), 0.0f) & 0xFFu;
+  const float d = __fmul_rn(e4m3_to_f32_cvt(s), g);
+  codes = make_uint2(0u, 0u);
   if (d > 0.0f) {
-    const SharedDivisor2 div(d);
-    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    float q[16];
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint64_t lo[4], hi[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) div(bf16_lo(w[i]), bf16_hi(w[i]), q[2 * i], q[2 * i + 1]);
-    const float lo[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
-    const float hi[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
-    codes = make_uint2(cvt_e2m1x8(lo), cvt_e2m1x8(hi));
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
+      hi[i] = pair(bf16_lo(w[i + 4]), bf16_hi(w[i + 4]));
+    }
+    const float y = rcp_near(d);
+    const uint64_t under = pair(y * kUnder, y * kUnder), over = pair(y * kOver, y * kOver);
+    codes = make_uint2(codes_of(lo, under), codes_of(hi, under));
+    if (codes.x != codes_of(lo, over) || codes.y != codes_of(hi, over) || !(d > 0x1p-100f && d < 0x1p100f)) {
+      const SharedDivisor2 div(d);
+      float q[16];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) div(bf16_lo(w[i]), bf16_hi(w[i]), q[2 * i], q[2 * i + 1]);
+      const float a[8] = {q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]};
+      const float b[8] = {q[8], q[9], q[10], q[11], q[12], q[13], q[14], q[15]};
+      codes = make_uint2(cvt_e2m1x8(a), cvt_e2m1x8(b));
+    }
   }
-  reinterpret_cast<uint2*>(is_v ? c.vc : c.kc)[row * bpr + blk] = codes;
-  (is_v ? c.vs : c.ks)[row * bpr + blk] = static_cast<uint8_t>(s);
+  return s;
 }
 
-__global__ void __launch_bounds__(kThreads) kv_read_nvfp4_kernel(const KvNvfp4 c, const KvRows r,
+// The 8 values of a word of codes, as bf16.
+__device__ __forceinline__ uint4 values_of(uint32_t codes, float s, float g) {
+  uint32_t f[4], p[4];
+  f16x2x4_from_e2m1x8(codes, f);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
+    const float2 y = unpair(mul2(mul2(pair(e.x, e.y), pair(s, s)), pair(g, g)));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+    p[j] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(p[0], p[1], p[2], p[3]);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads) kv_append_nvfp4_kernel(const KvNvfp4 c, const KvRows r, const Units un,
+                                                                   const uint16_t* __restrict__ k,
+                                                                   const uint16_t* __restrict__ v, int64_t ld_k,
+                                                                   int64_t ld_v, int32_t* status) {
+  __shared__ uint32_t at[kMaxTokensCta];
+  const int t0 = blockIdx.x * un.tokens, units = static_cast<int>(un.units.d);
+  const int n = find_places(c, r, un, t0, at, status);
+  for (int i = threadIdx.x; i < n * units; i += kThreads) {
+    const int t = un.units.div(i);
+    const Unit u(c, i - t * units, units);
+    const uint32_t row0 = at[t];
+    if (row0 >= kBadToken) continue;
+    const uint16_t* src = (u.value ? v + (t0 + t) * ld_v : k + (t0 + t) * ld_k) + u.h * c.D + u.chunk * 32;
+    uint4 x[2][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j >> 1][j & 1] = __ldcs(reinterpret_cast<const uint4*>(src) + j);
+    const float* gp = u.value ? c.vg : c.kg;
+    const float g = gp ? __ldg(gp + u.h) : 1.0f;
+    uint2 a, b;
+    const uint32_t s0 = quantize_block(x[0], g, a, status), s1 = quantize_block(x[1], g, b, status);
+    const int64_t row = static_cast<int64_t>(row0) + (static_cast<int64_t>(u.h) << c.page_shift);
+    *reinterpret_cast<uint4*>((u.value ? c.vc : c.kc) + row * (c.D / 2) + u.chunk * 16) = make_uint4(a.x, a.y, b.x, b.y);
+    *reinterpret_cast<uint16_t*>((u.value ? c.vs : c.ks) + row * (c.D / 16) + u.chunk * 2) = static_cast<uint16_t>(s0 | s1 << 8);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) kv_read_nvfp4_kernel(const KvNvfp4 c, const KvRows r, const Units un,
                                                                  uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                                  int32_t* status) {
-  const int bpr = c.D / 16, per_kind = c.Hkv * bpr;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t t = idx / (2 * per_kind);
-  if (t >= r.T) return;
-  int rest = static_cast<int>(idx - t * 2 * per_kind);
-  const bool is_v = rest >= per_kind;
-  if (is_v) rest -= per_kind;
-  const int h = rest / bpr, blk = rest % bpr;
-  const int64_t row = place(c, r, static_cast<int>(t), h);
-  uint4 o[2] = {};
-  if (row >= 0) {
-    const uint2 codes = __ldg(reinterpret_cast<const uint2*>(is_v ? c.vc : c.kc) + row * bpr + blk);
-    const float s = e4m3_to_f32(__ldg((is_v ? c.vs : c.ks) + row * bpr + blk));
-    const float* gp = is_v ? c.vg : c.kg;
-    const float g = gp ? __ldg(gp + h) : 1.0f;
-    const uint32_t w[2] = {codes.x, codes.y};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      uint32_t f[4], p[4];
-      f16x2x4_from_e2m1x8(w[i], f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
-        const __nv_bfloat162 y = __floats2bfloat162_rn(__fmul_rn(__fmul_rn(e.x, s), g), __fmul_rn(__fmul_rn(e.y, s), g));
-        p[j] = *reinterpret_cast<const uint32_t*>(&y);
-      }
-      o[i] = make_uint4(p[0], p[1], p[2], p[3]);
+  __shared__ uint32_t at[kMaxTokensCta];
+  const int t0 = blockIdx.x * un.tokens, units = static_cast<int>(un.units.d);
+  const int n = find_places(c, r, un, t0, at, status);
+  for (int i = threadIdx.x; i < n * units; i += kThreads) {
+    const int t = un.units.div(i);
+    const Unit u(c, i - t * units, units);
+    const uint32_t row0 = at[t];
+    uint4* dst = reinterpret_cast<uint4*>((u.value ? v : k) + (static_cast<int64_t>(t0 + t) * c.Hkv + u.h) * c.D + u.chunk * 32);
+    uint4 y[4] = {};
+    if (row0 < kBadToken) {
+      const int64_t row = static_cast<int64_t>(row0) + (static_cast<int64_t>(u.h) << c.page_shift);
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>((u.value ? c.vc : c.kc) + row * (c.D / 2)) + u.chunk);
+      const uint32_t s = __ldg(reinterpret_cast<const uint16_t*>((u.value ? c.vs : c.ks) + row * (c.D / 16)) + u.chunk);
+      const float* gp = u.value ? c.vg : c.kg;
+      const float g = gp ? __ldg(gp + u.h) : 1.0f, s0 = e4m3_to_f32_cvt(s & 0xFFu), s1 = e4m3_to_f32_cvt(s >> 8);
+      y[0] = values_of(w.x, s0, g);
+      y[1] = values_of(w.y, s0, g);
+      y[2] = values_of(w.z, s1, g);
+      y[3] = values_of(w.w, s1, g);
     }
-  } else if (row == -2) {
-    flag(status, QRR_DEV_BAD_INDEX);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) __stcs(dst + j, y[j]);
   }
-  uint4* dst = reinterpret_cast<uint4*>((is_v ? v : k) + (t * per_kind + rest) * 16);
-  __stcs(dst, o[0]);
-  __stcs(dst + 1, o[1]);
 }
 
 namespace {
 
-unsigned blocks_for(const KvNvfp4& c, int64_t T) {
-  return static_cast<unsigned>((T * 2 * c.Hkv * (c.D / 16) + kThreads - 1) / kThreads);
+// Tokens a CTA: enough units for its threads to take several each, but CTAs for
+// every SM.
+Units units_for(const KvNvfp4& c, int64_t T) {
+  int dev = 0, sms = kSMs;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int units = 2 * c.Hkv * (c.D / 32);
+  const int64_t most = std::min<int64_t>(kMaxTokensCta, std::max(1, 8 * kThreads / units)), spread = T / (4 * sms);
+  return Units{static_cast<int>(std::max<int64_t>(1, std::min(most, spread))), FastDiv(static_cast<uint32_t>(units))};
 }
 
 }  // namespace
@@ -142,16 +248,18 @@ unsigned blocks_for(const KvNvfp4& c, int64_t T) {
 cudaError_t launch_kv_append_nvfp4(const KvNvfp4& c, const KvRows& r, const void* k, const void* v, int64_t ld_k,
                                    int64_t ld_v, int32_t* status, cudaStream_t stream) {
   if (r.T == 0 || c.Hkv == 0) return cudaSuccess;
-  kv_append_nvfp4_kernel<<<blocks_for(c, r.T), kThreads, 0, stream>>>(
-      c, r, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_k, ld_v, status);
+  const Units un = units_for(c, r.T);
+  kv_append_nvfp4_kernel<<<static_cast<unsigned>((r.T + un.tokens - 1) / un.tokens), kThreads, 0, stream>>>(
+      c, r, un, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_k, ld_v, status);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read_nvfp4(const KvNvfp4& c, const KvRows& r, void* k, void* v, int32_t* status,
                                  cudaStream_t stream) {
   if (r.T == 0 || c.Hkv == 0) return cudaSuccess;
-  kv_read_nvfp4_kernel<<<blocks_for(c, r.T), kThreads, 0, stream>>>(c, r, static_cast<uint16_t*>(k),
-                                                                   static_cast<uint16_t*>(v), status);
+  const Units un = units_for(c, r.T);
+  kv_read_nvfp4_kernel<<<static_cast<unsigned>((r.T + un.tokens - 1) / un.tokens), kThreads, 0, stream>>>(
+      c, r, un, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), status);
   return cudaGetLastError();
 }
 

@@ -22,6 +22,21 @@ struct KvNvfp4 {
   __host__ __device__ int64_t capacity() const { return static_cast<int64_t>(max_pages) << page_shift; }
 };
 
+// x / d for 0 <= x < 2^31 by a multiplication (T. Granlund, P. Montgomery,
+// "Division by invariant integers using multiplication", PLDI 1994).
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d_) : d(d_), mul(0), shift(0) {
+    while ((1ull << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ int div(int x) const {
+    return static_cast<int>((__umulhi(mul, static_cast<uint32_t>(x)) + static_cast<uint32_t>(x)) >> shift);
+  }
+  __device__ __forceinline__ int mod(int x) const { return x - div(x) * static_cast<int>(d); }
+};
+
 constexpr int kMaxTokens = 1 << 30;  // rows of a call, and positions of a sequence
 
 // A call's rows: sequence b brings rows cu[b] .. cu[b + 1] - 1 (row b alone
@@ -47,7 +62,8 @@ __device__ __forceinline__ bool kv_rows_of(const KvRows& r, int b, int& first, i
   return first == lo && n == hi - lo;
 }
 
-// Row index (token row over all pages) of head h, slot `slot` of page `pg`.
+// Row index (token row over all pages; below 2^32) of head h, slot `slot` of
+// page `pg`.
 __device__ __forceinline__ int64_t kv_row(const KvNvfp4& c, int pg, int h, int slot) {
   return ((static_cast<int64_t>(pg) * c.Hkv + h) << c.page_shift) + slot;
 }

@@ -148,8 +148,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # torch.cuda.current_stream().cuda_stream, without making the Python object (2.9 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -536,6 +536,7 @@ class KvCacheNvfp4:
         self.device = k_codes.device
         self.pages, self.hkv, self.page, self.dim = pages, hkv, page, 2 * half
         self.batch, self.max_pages = page_table.shape
+        self._workspace_bytes = {}  # of attention, by (query heads, max_new)
         self.desc = KvNvfp4Desc(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k_gs), _ptr(v_gs),
                                 _ptr(page_table), pages, hkv, page, 2 * half, self.batch, self.max_pages)
         self._addr = ctypes.addressof(self.desc)
@@ -562,20 +563,33 @@ def _kv_rows(cache, pos, cu, t):
     if cu is None:
         if t != cache.batch:
             raise ValueError(f"without cu there is one row a sequence: {cache.batch}, got {t}")
-    elif cu.dtype is not torch.int32 or not cu.is_cuda or not cu.is_contiguous() or cu.numel() != cache.batch + 1:
+        return None
+    if cu.dtype is not torch.int32 or not cu.is_cuda or not cu.is_contiguous() or cu.numel() != cache.batch + 1:
         raise ValueError(f"cu must be a contiguous CUDA int32 tensor of {cache.batch + 1} values")
+    return cu.data_ptr()
 
 
 def _head_rows(x, heads, dim, name):
     """Row stride of bf16 rows [T, heads, dim] whose heads are contiguous (a slice of a wider projection will do)."""
     if x.dtype is not torch.bfloat16 or not x.is_cuda:
         raise TypeError(f"{name} must be a CUDA bfloat16 tensor")
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
-        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {list(x.shape)}")
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}], got {list(shape)}")
     s = x.stride()
     if s[2] != 1 or (heads > 1 and s[1] != dim):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return s[0] if x.shape[0] > 1 else heads * dim
+    return s[0] if shape[0] > 1 else heads * dim
+
+
+def _result(given, shape, dtype, device, stream, name):
+    """An output: the caller's tensor, checked, or a new one."""
+    if given is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        return out if stream is None else _for_stream(out, stream)
+    if given.dtype is not dtype or not given.is_cuda or not given.is_contiguous() or given.shape != shape:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)}")
+    return given
 
 
 def kv_append_nvfp4(k_new, v_new, cache, pos, cu=None, dev_status=None, stream=None):
@@ -586,9 +600,9 @@ def kv_append_nvfp4(k_new, v_new, cache, pos, cu=None, dev_status=None, stream=N
     t = k_new.shape[0]
     if v_new.shape[0] != t:
         raise ValueError("k_new and v_new must have the same rows")
-    _kv_rows(cache, pos, cu, t)
-    _check(lib().qrr_kv_append_nvfp4(cache._addr, k_new.data_ptr(), v_new.data_ptr(), t, ld_k, ld_v, _ptr(cu),
-                                     pos.data_ptr(), _ptr(dev_status), _stream(stream)), "qrr_kv_append_nvfp4")
+    cu = _kv_rows(cache, pos, cu, t)
+    _check(lib().qrr_kv_append_nvfp4(cache._addr, k_new.data_ptr(), v_new.data_ptr(), t, ld_k, ld_v, cu, pos.data_ptr(),
+                                     _ptr(dev_status), _stream(stream)), "qrr_kv_append_nvfp4")
 
 
 def kv_read_nvfp4(cache, pos, cu=None, rows=None, k=None, v=None, dev_status=None, stream=None):
@@ -598,15 +612,12 @@ def kv_read_nvfp4(cache, pos, cu=None, rows=None, k=None, v=None, dev_status=Non
         if cu is not None and k is None:
             raise ValueError("rows is needed with cu")
         rows = cache.batch if k is None else k.shape[0]
-    _kv_rows(cache, pos, cu, rows)
+    cu = _kv_rows(cache, pos, cu, rows)
     shape = (rows, cache.hkv, cache.dim)
-    k = _for_stream(torch.empty(shape, dtype=torch.bfloat16, device=cache.device), stream) if k is None else k
-    v = _for_stream(torch.empty(shape, dtype=torch.bfloat16, device=cache.device), stream) if v is None else v
-    for x, name in ((k, "k"), (v, "v")):
-        if x.dtype is not torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.shape != shape:
-            raise ValueError(f"{name} must be a contiguous CUDA bfloat16 tensor {list(shape)}")
-    _check(lib().qrr_kv_read_nvfp4(cache._addr, rows, _ptr(cu), pos.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                   _ptr(dev_status), _stream(stream)), "qrr_kv_read_nvfp4")
+    k = _result(k, shape, torch.bfloat16, cache.device, stream, "k")
+    v = _result(v, shape, torch.bfloat16, cache.device, stream, "v")
+    _check(lib().qrr_kv_read_nvfp4(cache._addr, rows, cu, pos.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(dev_status),
+                                   _stream(stream)), "qrr_kv_read_nvfp4")
     return k, v
 
 
@@ -621,27 +632,27 @@ def attention_nvfp4(q, cache, pos, cu=None, max_new=None, scale=None, return_lse
     ``max_new`` bounds the rows of a sequence (needed with ``cu``); ``scale`` is
     1/sqrt(D) unless given.  Returns out bf16 [T, Hq, D], or (out, lse fp32
     [T, Hq]) when ``return_lse`` is set or ``lse`` is given."""
-    if q.dim() != 3:
-        raise ValueError(f"q must be [T, Hq, D], got {list(q.shape)}")
-    t, hq, d = q.shape
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [T, Hq, D], got {list(shape)}")
+    t, hq, d = shape
     ld_q = _head_rows(q, hq, cache.dim, "q")
-    _kv_rows(cache, pos, cu, t)
     if max_new is None:
         if cu is not None:
             raise ValueError("max_new is needed with cu")
         max_new = 1
-    if scale is None:
-        scale = d ** -0.5
-    out = _for_stream(torch.empty(t, hq, d, dtype=torch.bfloat16, device=q.device), stream) if out is None else out
-    if out.dtype is not torch.bfloat16 or not out.is_cuda or not out.is_contiguous() or out.shape != q.shape:
-        raise ValueError(f"out must be a contiguous CUDA bfloat16 tensor {list(q.shape)}")
-    if lse is None:
-        lse = _for_stream(torch.empty(t, hq, dtype=torch.float32, device=q.device), stream) if return_lse else None
-    elif lse.dtype is not torch.float32 or not lse.is_cuda or not lse.is_contiguous() or lse.shape != (t, hq):
-        raise ValueError(f"lse must be a contiguous CUDA float32 tensor {[t, hq]}")
+    cu = _kv_rows(cache, pos, cu, t)
+    device = cache.device
+    out = _result(out, shape, torch.bfloat16, device, stream, "out")
+    if return_lse or lse is not None:
+        lse = _result(lse, (t, hq), torch.float32, device, stream, "lse")
     if workspace is None:
-        workspace = _for_stream(_workspace(attention_nvfp4_workspace_bytes(cache, t, hq, max_new), q.device), stream)
-    _check(lib().qrr_attention_nvfp4(cache._addr, q.data_ptr(), t, ld_q, hq, _ptr(cu), pos.data_ptr(), int(max_new),
-                                     float(scale), out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.numel(),
-                                     _ptr(dev_status), _stream(stream)), "qrr_attention_nvfp4")
+        need = cache._workspace_bytes.get((hq, max_new))
+        if need is None:  # it goes by the cache's shape and these two
+            need = cache._workspace_bytes[hq, max_new] = max(attention_nvfp4_workspace_bytes(cache, t, hq, max_new), 256)
+        workspace = _result(None, (need,), torch.uint8, device, stream, "workspace")
+    _check(lib().qrr_attention_nvfp4(cache._addr, q.data_ptr(), t, ld_q, hq, cu, pos.data_ptr(), max_new,
+                                     d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
+                                     workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream)),
+           "qrr_attention_nvfp4")
     return out if lse is None else (out, lse)
