@@ -8,9 +8,11 @@
 // Read: bf16_rn(fp32(e2m1(code) e4m3(s)) g).
 //
 // Both are bound by memory: 2 bytes a value on one side, 0.5625 on the other.  A
-// CTA takes some tokens; it finds their places first (a thread a token), then
-// its threads take units of 32 values of them in turn: 64 bytes of bf16, 16 of
-// codes, two scales.
+// CTA takes some tokens; it finds their places first (a thread a token).  Then,
+// to write, its threads take units of 32 values of them in turn: 64 bytes of
+// bf16, 16 of codes, two scales.  To read, its warps take kHeads groups of heads
+// of a token at a time, keys and values: a lane a word of 8 codes, so that a
+// store of the warp is one stretch of 512 bytes.
 //
 // The correctly rounded quotients are not formed where they cannot matter: with
 // y near 1 / d, x / d lies between x y (1 - 2^-20) and x y (1 + 2^-20), and where
@@ -29,6 +31,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokensCta = 256;
+constexpr int kHeads = 4;  // rows of keys, and of values, a lane reads at a time
 
 // The sequence that row t belongs to (offsets ascending), -1 for a row behind
 // the last sequence.
@@ -58,9 +61,9 @@ __device__ __forceinline__ uint32_t place(const KvNvfp4& c, const KvRows& r, int
   return static_cast<uint32_t>(kv_row(c, pg, 0, static_cast<int>(p) & ((1 << c.page_shift) - 1)));
 }
 
-// How a CTA's units number: `units` of a token, keys' before values'.
+// A CTA's tokens, and a token's units.
 struct Units {
-  int tokens;  // a CTA's
+  int tokens;
   FastDiv units;
 };
 
@@ -161,14 +164,16 @@ __device__ __forceinline__ uint32_t quantize_block(const uint4 (&x)[2], float g,
   return s;
 }
 
-// The 8 values of a word of codes, as bf16.
-__device__ __forceinline__ uint4 values_of(uint32_t codes, float s, float g) {
-  uint32_t f[4], p[4];
+// The 8 values of a word of codes, as bf16 (code x scale is exact in f16).
+__device__ __forceinline__ uint4 values_of(uint32_t codes, uint32_t scale, float g) {
+  uint32_t f[4], p[4], s2;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(s2) : "r"(scale | scale << 8));
   f16x2x4_from_e2m1x8(codes, f);
+  const uint64_t g2 = pair(g, g);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[j]));
-    const float2 y = unpair(mul2(mul2(pair(e.x, e.y), pair(s, s)), pair(g, g)));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(f[j]) : "r"(s2));
+    const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&f[j])), y = unpair(mul2(pair(e.x, e.y), g2));
     const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
     p[j] = *reinterpret_cast<const uint32_t*>(&b);
   }
@@ -203,43 +208,48 @@ __global__ void __launch_bounds__(kThreads) kv_append_nvfp4_kernel(const KvNvfp4
   }
 }
 
+template <int D>
 __global__ void __launch_bounds__(kThreads) kv_read_nvfp4_kernel(const KvNvfp4 c, const KvRows r, const Units un,
                                                                  uint16_t* __restrict__ k, uint16_t* __restrict__ v,
                                                                  int32_t* status) {
+  constexpr int kWords = D / 8, kRows = 32 / kWords;  // of a row; rows of a warp
   __shared__ uint32_t at[kMaxTokensCta];
-  const int t0 = blockIdx.x * un.tokens, units = static_cast<int>(un.units.d);
+  const int t0 = blockIdx.x * un.tokens, groups = static_cast<int>(un.units.d);
   const int n = find_places(c, r, un, t0, at, status);
-  for (int i = threadIdx.x; i < n * units; i += kThreads) {
-    const int t = un.units.div(i);
-    const Unit u(c, i - t * units, units);
+  const int lane = threadIdx.x & 31, word = lane % kWords, sub = lane / kWords;
+  for (int i = threadIdx.x >> 5; i < n * groups; i += kThreads / 32) {
+    const int t = un.units.div(i), h0 = (i - t * groups) * kHeads * kRows + sub;
     const uint32_t row0 = at[t];
-    uint4* dst = reinterpret_cast<uint4*>((u.value ? v : k) + (static_cast<int64_t>(t0 + t) * c.Hkv + u.h) * c.D + u.chunk * 32);
-    uint4 y[4] = {};
-    if (row0 < kBadToken) {
-      const int64_t row = static_cast<int64_t>(row0) + (static_cast<int64_t>(u.h) << c.page_shift);
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>((u.value ? c.vc : c.kc) + row * (c.D / 2)) + u.chunk);
-      const uint32_t s = __ldg(reinterpret_cast<const uint16_t*>((u.value ? c.vs : c.ks) + row * (c.D / 16)) + u.chunk);
-      const float* gp = u.value ? c.vg : c.kg;
-      const float g = gp ? __ldg(gp + u.h) : 1.0f, s0 = e4m3_to_f32_cvt(s & 0xFFu), s1 = e4m3_to_f32_cvt(s >> 8);
-      y[0] = values_of(w.x, s0, g);
-      y[1] = values_of(w.y, s0, g);
-      y[2] = values_of(w.z, s1, g);
-      y[3] = values_of(w.w, s1, g);
+    uint32_t w[2][kHeads] = {}, s[2][kHeads] = {};
+#pragma unroll
+    for (int u = 0; u < kHeads; ++u) {
+      const int h = h0 + u * kRows;
+      if (row0 >= kBadToken || h >= c.Hkv) continue;
+      const int64_t row = static_cast<int64_t>(row0) + (static_cast<int64_t>(h) << c.page_shift);
+      w[0][u] = __ldg(reinterpret_cast<const uint32_t*>(c.kc) + row * kWords + word);
+      w[1][u] = __ldg(reinterpret_cast<const uint32_t*>(c.vc) + row * kWords + word);
+      s[0][u] = __ldg(c.ks + row * (D / 16) + (word >> 1));
+      s[1][u] = __ldg(c.vs + row * (D / 16) + (word >> 1));
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) __stcs(dst + j, y[j]);
+    for (int u = 0; u < kHeads; ++u) {
+      const int h = h0 + u * kRows;
+      if (h >= c.Hkv) continue;
+      const int64_t to = (static_cast<int64_t>(t0 + t) * c.Hkv + h) * kWords + word;
+      __stcs(reinterpret_cast<uint4*>(k) + to, values_of(w[0][u], s[0][u], c.kg ? __ldg(c.kg + h) : 1.0f));
+      __stcs(reinterpret_cast<uint4*>(v) + to, values_of(w[1][u], s[1][u], c.vg ? __ldg(c.vg + h) : 1.0f));
+    }
   }
 }
 
 namespace {
 
-// Tokens a CTA: enough units for its threads to take several each, but CTAs for
-// every SM.
-Units units_for(const KvNvfp4& c, int64_t T) {
+// Tokens a CTA: enough units for its threads (or warps) to take several each,
+// but CTAs for every SM.
+Units units_for(int64_t T, int units, int want) {
   int dev = 0, sms = kSMs;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int units = 2 * c.Hkv * (c.D / 32);
-  const int64_t most = std::min<int64_t>(kMaxTokensCta, std::max(1, 8 * kThreads / units)), spread = T / (4 * sms);
+  const int64_t most = std::min(kMaxTokensCta, std::max(1, want / units)), spread = (T + 4 * sms - 1) / (4 * sms);
   return Units{static_cast<int>(std::max<int64_t>(1, std::min(most, spread))), FastDiv(static_cast<uint32_t>(units))};
 }
 
@@ -248,7 +258,7 @@ Units units_for(const KvNvfp4& c, int64_t T) {
 cudaError_t launch_kv_append_nvfp4(const KvNvfp4& c, const KvRows& r, const void* k, const void* v, int64_t ld_k,
                                    int64_t ld_v, int32_t* status, cudaStream_t stream) {
   if (r.T == 0 || c.Hkv == 0) return cudaSuccess;
-  const Units un = units_for(c, r.T);
+  const Units un = units_for(r.T, 2 * c.Hkv * (c.D / 32), 8 * kThreads);
   kv_append_nvfp4_kernel<<<static_cast<unsigned>((r.T + un.tokens - 1) / un.tokens), kThreads, 0, stream>>>(
       c, r, un, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), ld_k, ld_v, status);
   return cudaGetLastError();
@@ -257,9 +267,12 @@ cudaError_t launch_kv_append_nvfp4(const KvNvfp4& c, const KvRows& r, const void
 cudaError_t launch_kv_read_nvfp4(const KvNvfp4& c, const KvRows& r, void* k, void* v, int32_t* status,
                                  cudaStream_t stream) {
   if (r.T == 0 || c.Hkv == 0) return cudaSuccess;
-  const Units un = units_for(c, r.T);
-  kv_read_nvfp4_kernel<<<static_cast<unsigned>((r.T + un.tokens - 1) / un.tokens), kThreads, 0, stream>>>(
-      c, r, un, static_cast<uint16_t*>(k), static_cast<uint16_t*>(v), status);
+  const int heads = kHeads * 256 / c.D;  // of a warp's step
+  const Units un = units_for(r.T, (c.Hkv + heads - 1) / heads, 8 * kThreads / 32);
+  const unsigned grid = static_cast<unsigned>((r.T + un.tokens - 1) / un.tokens);
+  uint16_t *kb = static_cast<uint16_t*>(k), *vb = static_cast<uint16_t*>(v);
+  if (c.D == 128) kv_read_nvfp4_kernel<128><<<grid, kThreads, 0, stream>>>(c, r, un, kb, vb, status);
+  else kv_read_nvfp4_kernel<64><<<grid, kThreads, 0, stream>>>(c, r, un, kb, vb, status);
   return cudaGetLastError();
 }
 
