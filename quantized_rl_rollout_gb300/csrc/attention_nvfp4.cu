@@ -155,6 +155,8 @@ struct Walk : Item {
     t1 = static_cast<int>(min(static_cast<int64_t>(width), t0 + left));
     stop = min(t1, tiles);
   }
+  // whether the piece has tiles (an item's end may count for more than it has)
+  __device__ __forceinline__ bool empty() const { return t0 >= tiles; }
   __device__ __forceinline__ void begin(const Params& p, int b_, int64_t off, bool pad, int64_t left_) {
     seq_item(p, b_, pad, *this);
     h = static_cast<int>(off / width);
@@ -545,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(c
       so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
     }
     // ---- the rows' results, or a piece of them
-    const bool cut0 = it.t0 > 0, cut1 = it.t1 < it.width;
+    if (it.empty()) continue;
+    const bool cut0 = it.t0 > 0, cut1 = it.t1 < it.tiles;
     const int64_t piece = static_cast<int64_t>(2 * range + (cut0 ? 0 : 1)) * RT;
     const float vg = p.c.vg ? __ldg(p.c.vg + it.h) : 1.0f;
 #pragma unroll
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(c
       }
     if (!cut0 && lane == 0)
       p.rec[static_cast<int64_t>(it.b) * p.c.Hkv + it.h] =
-          Record{cut1 ? 1 + static_cast<int>((it.width - it.t1 + per - 1) / per) : 0, range, 0, it.h, it.first, it.n};
+          Record{cut1 ? 1 + static_cast<int>((it.tiles - it.t1 + per - 1) / per) : 0, range, 0, it.h, it.first, it.n};
   } while (it.next(p, pad));
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -636,7 +639,7 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
                                        : (one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream));
     if (e != cudaSuccess) return e;
   }
-  return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D, static_cast<int64_t>(a.c.B) * a.c.Hkv), stream) : cudaSuccess;
+  return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D, static_cast<int64_t>(a.c.B) * a.c.Hkv), any_few(G), stream) : cudaSuccess;
 }
 
 }  // namespace qrr

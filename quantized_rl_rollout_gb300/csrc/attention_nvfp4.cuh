@@ -108,6 +108,7 @@ __device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, in
 template <int D, int RT>
 __global__ void __launch_bounds__(256) join_kernel(const Params p) {
   constexpr int V = D / 32;
+  griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
   const Record rec = p.rec[blockIdx.x];
@@ -210,8 +211,9 @@ inline Params make_params(const AttnNvfp4Args& a, uint8_t* w, int ranges, int rt
 
 }  // namespace attn4
 
-// Many rows a sequence (attention_nvfp4_tc.cu); ws: its own part.
+// Many rows a sequence (attention_nvfp4_tc.cu); ws: its own part; beside: the
+// launch before it in the stream is the other kernel's.
 size_t attention_nvfp4_tc_ws_bytes(int D);
-cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream);
+cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_t stream);
 
 }  // namespace qrr

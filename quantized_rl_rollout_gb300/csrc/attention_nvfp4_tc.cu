@@ -42,6 +42,7 @@ constexpr int kThreads = 14 * 32;
 constexpr int kRows = 256;  // rows of an item
 constexpr int kTok = 128;   // tokens of a key tile
 constexpr int kMinTiles = 4;  // key tiles of a range
+constexpr int kItemCost = 2;  // key tiles that an item's start and end cost
 constexpr int kSeqs = 1024;   // sequences whose tile counts are kept in shared memory
 constexpr uint32_t kTmemCols = 512;
 
@@ -57,10 +58,8 @@ struct Smem {
   uint32_t tmem;
   int abort;
   int64_t total;
-  int32_t seq_tiles[kSeqs];
+  int32_t seq_widths[kSeqs];
   int64_t part[kThreads / 32];
-  int64_t start_off;
-  int start_b;
 };
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -94,12 +93,15 @@ __device__ __forceinline__ int key_tiles(const Params& p, const Seq& s, int qt) 
   return max(1, (last_seen(p, s, qt) + kTok) / kTok);
 }
 
-// Key tiles of one KV head of sequence b over all its row tiles, by a warp.
-__device__ __forceinline__ int seq_key_tiles(const Params& p, int b, int lane) {
+// What an item counts for.
+__device__ __forceinline__ int width(const Params& p, const Seq& s, int qt) { return key_tiles(p, s, qt) + kItemCost; }
+
+// What one KV head of sequence b counts for over all its row tiles, by a warp.
+__device__ __forceinline__ int seq_width(const Params& p, int b, int lane) {
   const Seq s = seq_of(p, b);
   const int qts = row_tiles(p, s);
   int sum = 0;
-  for (int qt = lane; qt < qts; qt += 32) sum += key_tiles(p, s, qt);
+  for (int qt = lane; qt < qts; qt += 32) sum += width(p, s, qt);
   return __reduce_add_sync(0xFFFFFFFFu, sum);
 }
 
@@ -108,22 +110,25 @@ struct Walk {
   Seq s;
   int b, h, qt, qts, tiles;  // current item and its key tiles
   int t0, t1;                // the piece's key tiles
-  int64_t left;              // tiles of the range from t0 on
+  int counts;                // what it takes of the range
+  int64_t left;              // of the range, from t0 on
   __device__ __forceinline__ void piece(const Params& p) {
     tiles = key_tiles(p, s, qt);
-    t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + left));
+    counts = static_cast<int>(min(static_cast<int64_t>(tiles + kItemCost - t0), left));
+    t1 = min(t0 + counts, tiles);
   }
-  __device__ __forceinline__ void begin(const Params& p, int b_, int64_t off, int64_t left_) {
+  // false: the range ends with what its only item counts for beyond its tiles
+  __device__ __forceinline__ bool begin(const Params& p, int b_, int64_t off, int64_t left_) {
     b = b_;
     left = left_;
     s = seq_of(p, b);
     qts = row_tiles(p, s);
     const int lane = threadIdx.x & 31;
-    const int64_t per = seq_key_tiles(p, b, lane);  // of one head
+    const int64_t per = seq_width(p, b, lane);  // of one head
     h = static_cast<int>(off / per);
     int rest = static_cast<int>(off - h * per);
     for (qt = 0;; qt += 32) {  // 32 row tiles at a time
-      const int own = qt + lane < qts ? key_tiles(p, s, qt + lane) : 0;
+      const int own = qt + lane < qts ? width(p, s, qt + lane) : 0;
       int incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -146,9 +151,10 @@ struct Walk {
     }
     t0 = rest;
     piece(p);
+    return t0 < tiles || next(p);
   }
   __device__ __forceinline__ bool next(const Params& p) {
-    left -= t1 - t0;
+    left -= counts;
     if (left <= 0) return false;
     t0 = 0;
     if (++qt == qts) {
@@ -276,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
   const int B = p.c.B;
   int64_t mine = 0;
   for (int b = warp; b < B; b += kThreads / 32) {
-    const int n = seq_key_tiles(p, b, lane);
-    if (lane == 0 && b < kSeqs) sh.seq_tiles[b] = n;
+    const int n = seq_width(p, b, lane);
+    if (lane == 0 && b < kSeqs) sh.seq_widths[b] = n;
     mine += n;
   }
   if (lane == 0) sh.part[warp] = mine;
@@ -300,28 +306,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     sh.abort = 0;
     fence_barrier_init();
   }
+  if (warp == 12) tmem_alloc(&sh.tmem, kTmemCols);
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
   int64_t total = 0;
   for (int w = 0; w < kThreads / 32; ++w) total += sh.part[w];
   total *= p.c.Hkv;
   const int64_t per = max(static_cast<int64_t>(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
   const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
-  Record rec{};
-  if (begin >= end) {
-    if (tid == 0) p.rec[blockIdx.x] = rec;
-    return;
-  }
-  if (warp == 12) {
-    tmem_alloc(&sh.tmem, kTmemCols);
-    // the sequence that the range begins in
+  Walk w;
+  bool work = begin < end;
+  if (work) {
+    // the sequence that the range begins in; every warp looks for itself
     int64_t off = begin;
     int found = -1;
     for (int b0 = 0; b0 < B && found < 0; b0 += 32) {
       int n = 0;
-      if (b0 + 32 <= kSeqs) n = b0 + lane < B ? sh.seq_tiles[b0 + lane] : 0;
+      if (b0 + 32 <= kSeqs) n = b0 + lane < B ? sh.seq_widths[b0 + lane] : 0;
       else
         for (int i = 0; i < 32 && b0 + i < B; ++i) {
-          const int x = seq_key_tiles(p, b0 + i, lane);
+          const int x = seq_width(p, b0 + i, lane);
           if (lane == i) n = x;
         }
       const int64_t own = static_cast<int64_t>(n) * p.c.Hkv;
@@ -340,17 +346,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         off -= __shfl_sync(0xFFFFFFFFu, incl, 31);
       }
     }
-    if (lane == 0) {
-      sh.start_b = found;
-      sh.start_off = off;
-    }
+    work = w.begin(p, found, off, end - begin);
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
-  Walk w;
-  w.begin(p, sh.start_b, sh.start_off, end - begin);
+  if (!work) {
+    if (tid == 0) {
+      p.rec[blockIdx.x].pieces = 0;
+      if (blockIdx.x == 0) griddep_wait();
+    }
+    if (warp == 12) tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   if (warp < 8) {
     // ---------------- softmax ----------------
@@ -360,51 +365,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     // the warp's 32 rows of the query tile, by 16-byte pieces: lanes `sub` and
     // `piece` of a copy of kAtOnce rows
     constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
-    const int piece = lane % kLanes, sub = lane / kLanes;
     uint8_t* const stage = sh.q[tile];
     auto at = [&](int rr, int pc) { return stage + (pc >> 3) * (128 * 128) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4); };
+    // The query rows of a piece come in two steps: copied as they are, kLanes
+    // lanes a row (as soon as no MMA reads the ones before), then turned into f16
+    // in place, a thread a row.  (Loops that run once a piece are kept rolled:
+    // straight code would wait for its own instructions.)
+    auto copy_rows = [&](const Walk& x) {
+      const int piece = lane % kLanes, sub = lane / kLanes;
+      const int row = x.qt * kRows + 128 * tile + r, rows = x.s.n * p.G;
+      const bool in = row < rows;
+      const int token = in ? x.s.first + p.byG.div(row) : -1, head = in ? x.h * p.G + p.byG.mod(row) : 0;
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        const int from = i * kAtOnce + sub;  // the copied row's own lane
+        const int tq = __shfl_sync(0xFFFFFFFFu, token, from), hq = __shfl_sync(0xFFFFFFFFu, head, from);
+        const uint16_t* src = p.q + max(tq, 0) * p.ld_q + hq * D + piece * 8;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at(32 * (warp & 3) + from, piece))),
+                     "l"(src), "r"(tq >= 0 ? 16 : 0)
+                     : "memory");
+      }
+    };
+    // returns the factor of the row's scores
+    auto convert_rows = [&](const Walk& x) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      uint32_t mx = 0u;
+#pragma unroll 8
+      for (int i = 0; i < kLanes; ++i) mx = max(mx, absmax_bits8(*reinterpret_cast<const uint4*>(at(r, i))));
+      if (mx >= 0x7F80u) flag(p.status, QRR_DEV_NONFINITE);
+      const int e = max(query_exp(mx), -127);  // one factor 2^-e (a row below 2^-113 comes out smaller)
+      const uint64_t sc = twice(__uint_as_float(static_cast<uint32_t>(127 - e) << 23));
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        uint4* y = reinterpret_cast<uint4*>(at(r, i));
+        const uint4 v = *y;
+        *y = make_uint4(scaled_f16x2(v.x, sc), scaled_f16x2(v.y, sc), scaled_f16x2(v.z, sc), scaled_f16x2(v.w, sc));
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full[tile]);
+      // at least the smallest normal value: a masked score times it stays -inf
+      return fmaxf(p.scale * kLog2e * (p.c.kg ? __ldg(p.c.kg + x.h) : 1.0f) * ldexpf(1.0f, e), 1.17549435e-38f);
+    };
+    auto active = [&](const Walk& x) { return x.qt * kRows + 128 * tile < x.s.n * p.G; };
+    Record rec{};
     uint32_t s_phase = 0, o_phase = 0;
-    bool ok = true;
-    do {
-      const int row0 = w.qt * kRows + 128 * tile, rows = w.s.n * p.G;
-      if (row0 < rows) {
-        const int row = row0 + r;
+    bool ok = true, more = true;
+    float f = 1.0f;
+    if (active(w)) {
+      copy_rows(w);
+      f = convert_rows(w);
+    }
+    while (more) {
+      Walk nx = w;
+      more = nx.next(p);
+      float next_f = 1.0f;
+      if (active(w)) {
+        const int row = w.qt * kRows + 128 * tile + r, rows = w.s.n * p.G;
         const bool in = row < rows;
-        const int token = w.s.first + (in ? p.byG.div(row) : 0), head = w.h * p.G + (in ? p.byG.mod(row) : 0);
-        // ---- the warp's query rows: copied as they are, kLanes lanes a row,
-        // then turned into f16 in place, a thread a row.  (Loops that run once
-        // a piece are kept rolled: straight code would wait for its own
-        // instructions, 9000 cycles in the place of 2500.)
-        {
-#pragma unroll 4
-          for (int i = 0; i < kLanes; ++i) {
-            const int from = i * kAtOnce + sub;  // the copied row's own lane
-            const int tq = __shfl_sync(0xFFFFFFFFu, token, from), hq = __shfl_sync(0xFFFFFFFFu, head, from);
-            const uint16_t* src = p.q + tq * p.ld_q + hq * D + piece * 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at(32 * (warp & 3) + from, piece))),
-                         "l"(src), "r"(row0 + 32 * (warp & 3) + from < rows ? 16 : 0)
-                         : "memory");
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          __syncwarp();
-        }
-        uint32_t mx = 0u;
-#pragma unroll 4
-        for (int i = 0; i < kLanes; ++i) mx = max(mx, absmax_bits8(*reinterpret_cast<const uint4*>(at(r, i))));
-        if (mx >= 0x7F80u) flag(p.status, QRR_DEV_NONFINITE);
-        const int e = max(query_exp(mx), -127);  // one factor 2^-e (a row below 2^-113 comes out smaller)
-        const uint64_t sc = twice(__uint_as_float(static_cast<uint32_t>(127 - e) << 23));
-#pragma unroll 4
-        for (int i = 0; i < kLanes; ++i) {
-          uint4* y = reinterpret_cast<uint4*>(at(r, i));
-          const uint4 x = *y;
-          *y = make_uint4(scaled_f16x2(x.x, sc), scaled_f16x2(x.y, sc), scaled_f16x2(x.z, sc), scaled_f16x2(x.w, sc));
-        }
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.q_full[tile]);
-        // at least the smallest normal value: a masked score times it stays -inf
-        const float f = fmaxf(p.scale * kLog2e * (p.c.kg ? __ldg(p.c.kg + w.h) : 1.0f) * ldexpf(1.0f, e), 1.17549435e-38f);
         const uint64_t f2 = twice(f);
         // rows behind the last one are never read: they need no mask
         const int lim = in ? min(w.s.pos + p.byG.div(row), w.s.last) : 0x7FFFFFFF;
@@ -417,6 +436,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
           }
           s_phase ^= 1;
           tc_fence_after();
+          // the last scores are formed: no MMA reads these query rows any more
+          if (j + 1 == w.t1 && more && active(nx)) copy_rows(nx);
           const int seen = lim - kTok * j + 1;  // of this tile's tokens
           const bool mask = kTok * j + kTok - 1 > lim_warp;
           // 32 columns at a time; weights 32 c .. 32 c + 31 go to the columns
@@ -482,74 +503,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
           if (lane == 0) mbar_arrive(&sh.p_full[tile]);
         }
         if (!ok) break;
+        if (more && active(nx)) next_f = convert_rows(nx);
         // ---- the row's result
         if (!mbar_wait(&sh.o_full[tile], o_phase, abort, p.status)) break;
         o_phase ^= 1;
         tc_fence_after();
-        // through the warp's rows of the query tile, which no MMA reads any
-        // more, so that lanes store neighbouring bytes
-        const bool cut0 = w.t0 > 0, cut1 = w.t1 < w.tiles;
-        if (!cut0 && !cut1) {
-          const float vg = p.c.vg ? __ldg(p.c.vg + w.h) : 1.0f;
-          const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+        const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+        const float vg = p.c.vg ? __ldg(p.c.vg + w.h) : 1.0f;
+        const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+        const int64_t orow = in ? out_row(p, w.s.first, w.h, row) : 0;
+        const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (w.t0 > 0 ? 0 : 1)) * kRows + 128 * tile + r;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tmem_ld32(to + 32 * c, x);
-            tmem_ld_wait32(x);
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(to + 32 * c, x);
+          tmem_ld_wait32(x);
+          if (whole) {
             uint32_t y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               const __nv_bfloat162 v2 = __floats2bfloat162_rn(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
               y[i] = *reinterpret_cast<const uint32_t*>(&v2);
             }
+            if (in)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(at(r, 4 * c + i)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          }
-          const int orow = token * p.Hq + head;
-          if (in && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
-          __syncwarp();
-#pragma unroll 4
-          for (int i = 0; i < kLanes; ++i) {
-            const int from = i * kAtOnce + sub, rr = 32 * (warp & 3) + from;
-            const int64_t to_row = __shfl_sync(0xFFFFFFFFu, orow, from);
-            if (row0 + rr < rows) reinterpret_cast<uint4*>(p.out + to_row * D)[piece] = *reinterpret_cast<const uint4*>(at(rr, piece));
-          }
-        } else {
-          const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (cut0 ? 0 : 1)) * kRows + 128 * tile;
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll 1
-            for (int c = 0; c < D / 64; ++c) {
-              uint32_t x[32];
-              tmem_ld32(to + (D / 2) * half + 32 * c, x);
-              tmem_ld_wait32(x);
+              for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4*>(p.out + orow * D + 32 * c)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else if (in) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(at(r, 8 * c + i)) = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            }
-            __syncwarp();
-#pragma unroll 4
-            for (int i = 0; i < kLanes; ++i) {
-              const int rr = 32 * (warp & 3) + i * kAtOnce + sub;
-              reinterpret_cast<uint4*>(p.po + (pr + rr) * D + (D / 2) * half)[piece] = *reinterpret_cast<const uint4*>(at(rr, piece));
-            }
-            __syncwarp();
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(p.po + pr * D + 32 * c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
-          p.pm[pr + r] = m;
-          p.pl[pr + r] = l;
         }
+        if (in && whole && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+        if (in && !whole) p.pm[pr] = m, p.pl[pr] = l;
         __syncwarp();
         tc_fence_before();
+      } else if (more && active(nx)) {
+        copy_rows(nx);
+        next_f = convert_rows(nx);
       }
-      if (tid == 0) {
-        if (w.t0 == 0 && w.t1 < w.tiles) {
-          rec.pieces = 1 + static_cast<int>((w.tiles - w.t1 + per - 1) / per);
-          rec.range = blockIdx.x, rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
-        }
+      if (tid == 0 && w.t0 == 0 && w.t1 < w.tiles) {
+        rec.pieces = 1 + static_cast<int>((w.tiles - w.t1 + per - 1) / per);
+        rec.range = blockIdx.x, rec.rt = w.qt, rec.h = w.h, rec.first = w.s.first, rec.n = w.s.n;
       }
-    } while (w.next(p));
+      w = nx;
+      f = next_f;
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (tid == 0) p.rec[blockIdx.x] = rec;
   } else if (warp < 12) {
     // ---------------- codes -> key and value tiles ----------------
@@ -688,12 +689,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  // this grid ends after the one that it may run beside (see the launch)
+  if (blockIdx.x == 0 && tid == 0) griddep_wait();
 }
 
 namespace {
 
 template <int D>
-cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
+cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_t stream) {
   constexpr int smem = static_cast<int>(sizeof(Smem<D>)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
   static bool attr = false;
@@ -706,9 +709,16 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int grid = sms < kMaxSms ? sms : kMaxSms;
   const Params p = make_params(a, ws, grid, kRows, grid);
-  attn_nvfp4_tc_kernel<D><<<grid, kThreads, smem, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  // behind the other kernel's launches it may run beside them: what it reads was
+  // there before those, what it writes they do not touch
+  if (beside) {
+    const cudaError_t e = launch_dependent(attn_nvfp4_tc_kernel<D>, dim3(grid), kThreads, smem, stream, p);
+    if (e != cudaSuccess) return e;
+  } else {
+    attn_nvfp4_tc_kernel<D><<<grid, kThreads, smem, stream>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   return launch_dependent(join_kernel<D, kRows>, dim3(grid, kRows / 8), 256, 0, stream, p);
 }
 
@@ -716,8 +726,8 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
 
 size_t attention_nvfp4_tc_ws_bytes(int D) { return ws_bytes(D, kMaxSms, kRows, kMaxSms); }
 
-cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, cudaStream_t stream) {
-  return a.c.D == 128 ? launch<128>(a, ws, stream) : launch<64>(a, ws, stream);
+cudaError_t launch_attention_nvfp4_tc(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_t stream) {
+  return a.c.D == 128 ? launch<128>(a, ws, beside, stream) : launch<64>(a, ws, beside, stream);
 }
 
 }  // namespace qrr
