@@ -43,7 +43,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int ctas_per_sm(int nt) { return nt == 1 ? 4 : 2; }  // by registers
+// CTAs an SM, by registers: with 4 the 128 values of D = 128 are too few (64
+// sequences of 2048..4096 tokens: 46 us with 3, 50 with 4; D = 64: 42 and 41)
+constexpr int ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 128 ? 3 : 4; }
 constexpr int kTok = 32;      // tokens of a tile
 constexpr int kMinTiles = 4;  // tiles of a range
 constexpr int kItemCost = 1;
@@ -69,22 +71,34 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// `W` 32-bit words from shared memory.
+// `W` 32-bit words, a halfword and a byte from shared memory.
 template <int W>
 struct Words {
   uint32_t w[W];
-  __device__ __forceinline__ void load(const uint8_t* p) {
-    if constexpr (W == 4) {
-      const uint4 x = *reinterpret_cast<const uint4*>(p);
-      w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else if constexpr (W == 2) {
-      const uint2 x = *reinterpret_cast<const uint2*>(p);
-      w[0] = x.x, w[1] = x.y;
-    } else {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
+  __device__ __forceinline__ void load(uint32_t at) {
+    if constexpr (W == 4)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    else if constexpr (W == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    else asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
   }
 };
+__device__ __forceinline__ uint32_t load_u16(uint32_t at) {
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t load_u8(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
+// (a & m) | (b & ~m)
+__device__ __forceinline__ uint32_t choose(uint32_t a, uint32_t b, uint32_t m) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xE4;" : "=r"(r) : "r"(a), "r"(b), "r"(m));
+  return r;
+}
 
 // A tile in a warp's ring: two halves of 16 rows each of key codes, value codes,
 // key scales, value scales.  Keys' rows 4..7 and 12..15 of a half change places,
@@ -101,17 +115,27 @@ struct Raw {
 // the values' [D / 8 g, D / 8 (g + 1)): the order of tokens and of values that
 // the two MMAs sum over is free, so each lane takes contiguous bytes.
 template <int D>
+struct Places {  // of a lane's bytes in the ring's first tile
+  uint32_t k, ks, v, vs;
+  __device__ __forceinline__ Places(const Raw<D>* ring, int lane) {
+    const int g = lane >> 2, c = lane & 3, tau = (g >> 1) + 4 * (g & 1), at = tau ^ (D == 128 ? tau >> 2 : 2 * (tau >> 2));
+    k = smem_u32(ring->k) + at * (D / 2) + c * (D / 8);
+    ks = smem_u32(ring->ks) + tau * (D / 16) + c * (D / 64);
+    v = smem_u32(ring->v) + c * (D / 2) + ((g * (D / 16)) ^ (D == 128 ? 16 * (c & 2) : 0));
+    vs = smem_u32(ring->vs) + c * (D / 16) + (D == 128 ? g : g >> 1);
+  }
+};
+
+template <int D>
 struct Keys {
   Words<D / 32> k[2];
   uint32_t s[2];
-  __device__ __forceinline__ void load(const Raw<D>& raw, int half, int lane) {
-    const int g = lane >> 2, c = lane & 3, tau = (g >> 1) + 4 * (g & 1), at = tau ^ (D == 128 ? tau >> 2 : 2 * (tau >> 2));
+  __device__ __forceinline__ void load(uint32_t at, uint32_t at_s, int half) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      k[i].load(raw.k[half] + (at + 8 * i) * (D / 2) + c * (D / 8));
-      const uint8_t* x = raw.ks[half] + (tau + 8 * i) * (D / 16) + c * (D / 64);
-      if constexpr (D == 128) s[i] = *reinterpret_cast<const uint16_t*>(x);
-      else s[i] = *x;
+      k[i].load(at + half * 8 * D + 8 * i * (D / 2));
+      if constexpr (D == 128) s[i] = load_u16(at_s + half * D + 8 * i * (D / 16));
+      else s[i] = load_u8(at_s + half * D + 8 * i * (D / 16));
     }
   }
 };
@@ -120,12 +144,11 @@ template <int D>
 struct Values {
   Words<D / 64> v[4];
   uint32_t s[4];
-  __device__ __forceinline__ void load(const Raw<D>& raw, int half, int lane) {
-    const int g = lane >> 2, c = lane & 3;
+  __device__ __forceinline__ void load(uint32_t at, uint32_t at_s, int half) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j].load(raw.v[half] + (c + 4 * j) * (D / 2) + ((g * (D / 16)) ^ (D == 128 ? 16 * (c & 2) : 0)));
-      s[j] = raw.vs[half][(c + 4 * j) * (D / 16) + (D == 128 ? g : g >> 1)];
+      v[j].load(at + half * 8 * D + 4 * j * (D / 2));
+      s[j] = load_u8(at_s + half * D + 4 * j * (D / 16));
     }
   }
 };
@@ -186,87 +209,84 @@ template <int D>
 struct Feed {
   Walk w;
   const uint8_t *kp, *vp, *sp;  // the lane's bytes of the next tile (scales: keys' in the lower half of the warp)
-  int64_t rows;                 // from the tile's first half to its second
+  int64_t to_half, to_half_s;   // from the codes and scales of the tile's first half to its second's
+  const int32_t* entry;         // the table's entry behind the tile's page
   uint32_t to, to_v, to_s;      // places in the ring's first tile
-  uint32_t so;                  // offset of the next tile in the ring
-  int t, next_pg, next_half, lane;
+  int t, next_pg, next_half;
   bool more;
+  // the page (two pages of 16) of the tile that `entry` belongs to
   __device__ __forceinline__ void read_page(const Params& p, int tile) {
     if (tile >= w.stop) return;
-    const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
-    if (p.c.page_shift >= 5) {
-      next_pg = __ldg(table + (tile >> (p.c.page_shift - 5)));
-    } else {
-      next_pg = __ldg(table + 2 * tile);
-      next_half = kTok * tile + 16 <= w.last ? __ldg(table + 2 * tile + 1) : next_pg;
-    }
+    next_pg = __ldg(entry);
+    if (p.c.page_shift < 5 && kTok * tile + 16 <= w.last) next_half = __ldg(entry + 1);
   }
-  // addresses of tile t, in the page that `next_pg` names
-  __device__ __forceinline__ void enter_page(const Params& p) {
+  // addresses of tile t, in the page that was read
+  __device__ __forceinline__ void enter_page(const Params& p, int lane) {
     uint32_t now = static_cast<uint32_t>(next_pg), half = static_cast<uint32_t>(next_half);
-    const int tiles = p.c.page_shift >= 5 ? 1 << (p.c.page_shift - 5) : 1;
-    read_page(p, (t & -tiles) + tiles);
-    if (p.c.page_shift >= 5) half = now;
+    const int sh = p.c.page_shift, mask = sh >= 5 ? (1 << (sh - 5)) - 1 : 0;
+    entry += sh >= 5 ? 1 : 2;
+    read_page(p, (t | mask) + 1);
     const uint32_t pages = static_cast<uint32_t>(p.c.num_pages);
-    if (now >= pages || half >= pages) {
+    if (now >= pages || (sh < 5 && half >= pages)) {
       flag(p.status, QRR_DEV_BAD_INDEX);
       now = half = 0u;
     }
-    const uint32_t row = ((now * p.c.Hkv + w.h) << p.c.page_shift) + static_cast<uint32_t>(t & (tiles - 1)) * kTok;
-    rows = p.c.page_shift >= 5 ? 16 : (static_cast<int64_t>(half) - now) * p.c.Hkv * 16;
-    kp = p.c.kc + static_cast<uint64_t>(row) * (D / 2) + lane * 16;
-    vp = p.c.vc + static_cast<uint64_t>(row) * (D / 2) + lane * 16;
-    sp = (lane < 16 ? p.c.ks : p.c.vs) + (static_cast<uint64_t>(row) + (lane & 15)) * (D / 16);
+    const uint32_t row = ((now * p.c.Hkv + w.h) << sh) + static_cast<uint32_t>(t & mask) * kTok;
+    if (sh < 5) {
+      const int64_t rows = (static_cast<int64_t>(half) - now) * p.c.Hkv * 16;
+      to_half = rows * (D / 2);
+      to_half_s = rows * (D / 16);
+    }
+    kp = p.c.kc + lane * 16 + static_cast<uint64_t>(row) * (D / 2);
+    vp = p.c.vc + lane * 16 + static_cast<uint64_t>(row) * (D / 2);
+    sp = (lane < 16 ? p.c.ks : p.c.vs) + (lane & 15) * (D / 16) + static_cast<uint64_t>(row) * (D / 16);
   }
   // the first tile at or after t, over the ends of items
-  __device__ __forceinline__ void settle(const Params& p, bool pad) {
+  __device__ __forceinline__ void settle(const Params& p, bool pad, int lane) {
     while (more && t >= w.stop) {
       more = w.next(p, pad);
       t = w.t0;
     }
     if (more) {
+      entry = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages + ((kTok * t) >> p.c.page_shift);
+      next_half = 0;
       read_page(p, t);
-      enter_page(p);
+      enter_page(p, lane);
     }
   }
-  __device__ __forceinline__ void begin(const Params& p, const Walk& from, const Raw<D>* ring, int lane_, bool pad) {
+  __device__ __forceinline__ void begin(const Params& p, const Walk& from, const Raw<D>* ring, int lane, bool pad) {
     constexpr int kChunks = D / 32;  // of 16 bytes a row
-    lane = lane_;
     const int r = lane / kChunks, c = lane % kChunks;
     to = smem_u32(ring) + (r ^ ((D == 128 ? 1 : 2) * (r >> 2 & 1))) * (D / 2) + c * 16;
     to_v = smem_u32(ring->v) + r * (D / 2) + ((c * 16) ^ (D == 128 ? 16 * (r & 2) : 0));
     to_s = smem_u32(lane < 16 ? ring->ks : ring->vs) + (lane & 15) * (D / 16);
-    so = 0;
     w = from;
     t = w.t0;
-    next_half = 0;
+    to_half = 8 * D;
+    to_half_s = D;
     more = true;
-    settle(p, pad);
+    settle(p, pad, lane);
   }
-  __device__ __forceinline__ void issue(const Params& p, bool pad) {
+  // the next tile into the ring's tile `so` bytes from its first
+  __device__ __forceinline__ void issue(const Params& p, bool pad, uint32_t so, int lane) {
     if (more) {
+      const uint32_t a = to + so, b = to_v + so, c = to_s + so;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t off = h * rows;
+        const uint8_t *k = h ? kp + to_half : kp, *v = h ? vp + to_half : vp, *s = h ? sp + to_half_s : sp;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + so + 8 * D * h + 512 * i),
-                       "l"(kp + off * (D / 2) + 512 * i)
-                       : "memory");
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to_v + so + 8 * D * h + 512 * i),
-                       "l"(vp + off * (D / 2) + 512 * i)
-                       : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(a + (8 * D * h + 512 * i)), "l"(k + 512 * i) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(b + (8 * D * h + 512 * i)), "l"(v + 512 * i) : "memory");
         }
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to_s + so + D * h), "l"(sp + off * (D / 16)), "n"(D / 16)
-                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(c + D * h), "l"(s), "n"(D / 16) : "memory");
       }
-      so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
       ++t;
       kp += 16 * D;
       vp += 16 * D;
       sp += 2 * D;
-      if (t >= w.stop) settle(p, pad);
-      else if (p.c.page_shift < 5 || (t & ((1 << (p.c.page_shift - 5)) - 1)) == 0) enter_page(p);
+      if (t >= w.stop) settle(p, pad, lane);
+      else if (((kTok * t) & ((1 << p.c.page_shift) - 1) & -kTok) == 0 || p.c.page_shift < 5) enter_page(p, lane);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
@@ -332,13 +352,13 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int e
 // One tile, of whose tokens `live` exist (kTok or more: all).  `all`: every row
 // sees every token of it.
 template <int D, int NT>
-__device__ __forceinline__ void step(const Raw<D>& raw, int t, int live, bool all, int lane, State<D, NT>& s) {
+__device__ __forceinline__ void step(const Places<D>& at, uint32_t so, int t, int live, bool all, int lane, State<D, NT>& s) {
   const int g = lane >> 2, c = lane & 3;
   float e[2][NT][4];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     Keys<D> x;
-    x.load(raw, h, lane);
+    x.load(at.k + so, at.ks + so, h);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -410,7 +430,7 @@ __device__ __forceinline__ void step(const Raw<D>& raw, int t, int live, bool al
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     Values<D> x;
-    x.load(raw, h, lane);
+    x.load(at.v + so, at.vs + so, h);
     // the two pairs' scales; those of tokens that do not exist count as zero (what
     // lies there may be anything, a NaN among it)
     uint32_t v01 = __byte_perm(x.s[0], x.s[1], 0x7740), v23 = __byte_perm(x.s[2], x.s[3], 0x7740);
@@ -424,10 +444,10 @@ __device__ __forceinline__ void step(const Raw<D>& raw, int t, int live, bool al
     for (int w = 0; w < D / 64; ++w) {
       // bytes of (first, second) token's codes of one value: even values, odd values
       uint32_t a[4], b[4], d[4], u[4];
-      f16x2x4_from_e2m1x8((x.v[0].w[w] & 0x0F0F0F0Fu) | (x.v[1].w[w] << 4 & 0xF0F0F0F0u), a);
-      f16x2x4_from_e2m1x8((x.v[0].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[1].w[w] & 0xF0F0F0F0u), b);
-      f16x2x4_from_e2m1x8((x.v[2].w[w] & 0x0F0F0F0Fu) | (x.v[3].w[w] << 4 & 0xF0F0F0F0u), d);
-      f16x2x4_from_e2m1x8((x.v[2].w[w] >> 4 & 0x0F0F0F0Fu) | (x.v[3].w[w] & 0xF0F0F0F0u), u);
+      f16x2x4_from_e2m1x8(choose(x.v[0].w[w], x.v[1].w[w] << 4, 0x0F0F0F0Fu), a);
+      f16x2x4_from_e2m1x8(choose(x.v[0].w[w] >> 4, x.v[1].w[w], 0x0F0F0F0Fu), b);
+      f16x2x4_from_e2m1x8(choose(x.v[2].w[w], x.v[3].w[w] << 4, 0x0F0F0F0Fu), d);
+      f16x2x4_from_e2m1x8(choose(x.v[2].w[w] >> 4, x.v[3].w[w], 0x0F0F0F0Fu), u);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), u[i] = hmul2(u[i], f1);
@@ -441,7 +461,7 @@ __device__ __forceinline__ void step(const Raw<D>& raw, int t, int live, bool al
 }  // namespace
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_nvfp4_kernel(const Params p) {
   constexpr int RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Raw<D>* const ring = reinterpret_cast<Raw<D>*>(smem_raw) + kStages * (threadIdx.x >> 5);  // the warp's
@@ -528,11 +548,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(c
   Feed<D> feed;
   feed.begin(p, it, ring, lane, pad);
 #pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) feed.issue(p, pad);
+  for (int i = 0; i < kStages - 1; ++i) feed.issue(p, pad, i * static_cast<uint32_t>(sizeof(Raw<D>)), lane);
   const int c = lane & 3, g = lane >> 2;
   State<D, NT> s;
-  const uint8_t* const mine = reinterpret_cast<const uint8_t*>(ring);
-  uint32_t so = 0;
+  const Places<D> at(ring, lane);
+  // the ring's tile in use, and the one before it: that is filled next
+  uint32_t so = 0, free = (kStages - 1) * static_cast<uint32_t>(sizeof(Raw<D>));
   do {
     load_rows<D, NT>(p, it, kTok * it.stop, lane, s);
     // tiles before this one are seen whole by every row (rows behind the last one
@@ -542,8 +563,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NT)) attn_nvfp4_kernel(c
     for (int t = it.t0; t < it.stop; ++t) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
       __syncwarp();  // the tile is there for all lanes, and the one before it read by all
-      feed.issue(p, pad);
-      step<D, NT>(*reinterpret_cast<const Raw<D>*>(mine + so), t, it.last + 1 - kTok * t, t < whole, lane, s);
+      feed.issue(p, pad, free, lane);
+      step<D, NT>(at, so, t, it.last + 1 - kTok * t, t < whole, lane, s);
+      free = so;
       so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
     }
     // ---- the rows' results, or a piece of them
@@ -616,8 +638,8 @@ bool any_few(int G) { return G <= kFewRows; }
 bool any_many(int64_t max_new, int G) { return max_new * G > kFewRows; }
 
 size_t few_ws_bytes(int D, int64_t items) {
-  return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(1) * kWarps, 8, items),
-                  ws_bytes(D, kMaxSms * ctas_per_sm(2) * kWarps, 16, items));
+  return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(D, 1) * kWarps, 8, items),
+                  ws_bytes(D, kMaxSms * ctas_per_sm(D, 2) * kWarps, 16, items));
 }
 
 }  // namespace
@@ -634,7 +656,7 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
   const int G = a.Hq / a.c.Hkv;
   if (any_few(G)) {
     const bool one = static_cast<int64_t>(a.max_new) * G <= 8;
-    const int grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(one ? 1 : 2);
+    const int grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(a.c.D, one ? 1 : 2);
     const cudaError_t e = a.c.D == 128 ? (one ? launch<128, 1>(a, grid, stream) : launch<128, 2>(a, grid, stream))
                                        : (one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream));
     if (e != cudaSuccess) return e;

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kv_nvfp4.cuh"
 #include "tc.cuh"
 
@@ -136,10 +138,13 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
     l = l * old + sum;
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] *= old;
-    for (int i = 0; i < n; i += 8) {  // eight loads under way at a time
-      float v[8][V];
+    // `many` pieces' outputs from the i-th on; eight loads under way at a time
+    // where there are as many
+    auto add = [&](auto many, int i) {
+      constexpr int kMany = decltype(many)::value;
+      float v[kMany][V];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kMany; ++u) {
         const float* src = p.po + piece(i0 + min(i + u, n - 1)) * D + V * lane;
         if constexpr (V == 4) {
           const float4 x = *reinterpret_cast<const float4*>(src);
@@ -150,12 +155,15 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p) {
         }
       }
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kMany; ++u) {
         const float ai = __shfl_sync(0xFFFFFFFFu, a, (i + u) & 31);  // 0 behind the last piece
 #pragma unroll
         for (int d = 0; d < V; ++d) o[d] += ai * v[u][d];
       }
-    }
+    };
+    int i = 0;
+    for (; i + 8 <= n; i += 8) add(std::integral_constant<int, 8>{}, i);
+    for (; i < n; i += 2) add(std::integral_constant<int, 2>{}, i);
   }
   const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
   const int64_t orow = out_row(p, rec.first, rec.h, row);
