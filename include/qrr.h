@@ -347,10 +347,12 @@ qrr_status qrr_attention_decode_fp8(const void* q, int32_t B, int32_t Hq, int32_
  * rows cu[b] .. cu[b + 1] - 1 of the call's T rows (NULL: T = B, one row
  * each); row cu[b] + i stands at position pos[b] + i (pos int32 [B]).  A
  * position below 0 is no token: nothing is written, zeros are read, its
- * attention sees nothing.  Rows outside cu[0] .. cu[B] - 1 are left alone.  A
+ * attention sees nothing.  Rows outside cu[0] .. cu[B] - 1 belong to no
+ * sequence: they are not written, read zeros, and attention leaves them alone.  A
  * position at or above max_pages * page, a page number outside
  * [0, num_pages) or offsets that leave [0, T] raise QRR_DEV_BAD_INDEX; such a
- * row is not written to the cache, and reads zeros.  T <= 2^30,
+ * row is not written to the cache and reads zeros, and the outputs of its
+ * sequence's attention are unspecified.  T <= 2^30,
  * max_pages * page <= 2^30, num_pages * Hkv * page < 2^32.
  *
  * qrr_kv_append_nvfp4: quantizes rows k_new, v_new (bf16, row t at base + t ld

@@ -273,6 +273,95 @@ def test_captured(q):
     assert torch.equal(out, want)
 
 
+def test_captured_rows_of_every_kind(q):
+    """A call whose sequences take every kernel, replayed with other queries."""
+    bed = Bed(q, [600, 33, 300], 2, 128, 32, 20)
+    news = [1, 30, 200]
+    x = torch.randn(sum(news), 8, 128, device=DEV).to(torch.bfloat16)
+    pos, cu = _dev([n - m for n, m in zip(bed.lens, news)]), _dev(np.concatenate([[0], np.cumsum(news)]))
+    ws = torch.empty(q.attention_nvfp4_workspace_bytes(bed.cache, sum(news), 8, 200), dtype=torch.uint8, device=DEV)
+    out = torch.empty_like(x)
+
+    def step():
+        q.attention_nvfp4(x, bed.cache, pos, cu=cu, max_new=200, out=out, workspace=ws)
+
+    step()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        x.copy_(torch.randn(sum(news), 8, 128, device=DEV))
+        step()
+        want = out.clone()
+        out.zero_()
+        g.replay()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("hq,rows", [(4, 1), (4, 2), (20, 1)])
+def test_many_sequences(q, hq, rows):
+    """More sequences than a CTA has threads, and than the many-rows kernel keeps in shared memory; some without tokens."""
+    g = np.random.default_rng(3)
+    lens = [int(x) for x in g.integers(0, 40, 1100)]
+    lens[7], lens[1050] = 300, 260
+    bed = Bed(q, lens, 1, 64, 16, 21)
+    x = torch.randn(1100 * rows, hq, 64, device=DEV).to(torch.bfloat16)
+    pos, st = _dev([n - rows for n in lens]), _dev([0])
+    cu = None if rows == 1 else _dev(np.arange(0, 1101) * rows)
+    out, lse = q.attention_nvfp4(x, bed.cache, pos, cu=cu, max_new=rows, return_lse=True, dev_status=st)
+    assert q.get_last_device_status(st) == 0
+    o, e, xs = to_np(out), to_np(lse), to_np(x)
+    for b in list(range(0, 1100, 37)) + [7, 1050, 1099]:
+        k, v = bed.values(b)
+        want, want_lse, spread = kv.attention(xs[b * rows:(b + 1) * rows], k, v, lens[b] - rows, 0.125)
+        got, got_lse = o[b * rows:(b + 1) * rows], e[b * rows:(b + 1) * rows]
+        none = np.isneginf(want_lse)
+        assert np.array_equal(none, np.isneginf(got_lse)) and not got[none].any()
+        assert (np.abs(got_lse[~none] - want_lse[~none]) <= 2 ** -18 * 64).all()  # |scale q.k| terms sum to well under 63
+        assert (np.abs(got - want) <= 2 ** -8 * np.abs(want) + (2 ** -10 + 2 ** -18 * 64) * spread + 2 ** -31 * np.abs(v).sum(0) + 1e-30).all()
+
+
+def test_rows_of_nobody_stay(q):
+    """Rows in front of cu[0] and behind cu[B] are left alone by every call."""
+    bed = Bed(q, [40, 200], 2, 128, 16, 22)
+    for news in ([1, 2], [9, 150]):
+        cu = _dev([3, 3 + news[0], 3 + sum(news)])
+        t = 3 + sum(news) + 5
+        x = torch.randn(t, 8, 128, device=DEV).to(torch.bfloat16)
+        out, lse = torch.full_like(x, 7), torch.full((t, 8), 7.0, device=DEV)
+        pos = _dev([40 - news[0], 200 - news[1]])
+        q.attention_nvfp4(x, bed.cache, pos, cu=cu, max_new=max(news), out=out, lse=lse)
+        whole = q.attention_nvfp4(x[3:-5], bed.cache, pos, cu=cu - 3, max_new=max(news))
+        assert torch.equal(out[3:-5], whole)
+        for z in (out, lse):
+            assert (z[:3] == 7).all() and (z[-5:] == 7).all()
+        k, v = torch.full((t, 2, 128), 7, dtype=torch.bfloat16, device=DEV), torch.full((t, 2, 128), 7, dtype=torch.bfloat16, device=DEV)
+        q.kv_read_nvfp4(bed.cache, pos, cu=cu, k=k, v=v)
+        assert (k[:3] == 0).all() and (v[-5:] == 0).all()  # no token: reads zeros
+
+
+def test_non_finite_queries_are_told(q):
+    bed = Bed(q, [40, 200], 2, 128, 16, 23)
+    for news in ([1, 1], [40, 60]):
+        x = torch.randn(sum(news), 8, 128, device=DEV).to(torch.bfloat16)
+        x[-1, 3, 17] = float("nan")
+        st = _dev([0])
+        q.attention_nvfp4(x, bed.cache, _dev([40 - news[0], 200 - news[1]]), cu=_dev([0, news[0], sum(news)]), max_new=max(news), dev_status=st)
+        assert q.get_last_device_status(st) == q.DEV_NONFINITE
+
+
+def test_offsets_that_leave_the_rows(q):
+    """Offsets outside [0, T] and descending ones are flagged; what they name stays inside the call's rows."""
+    bed = Bed(q, [40, 200], 2, 128, 16, 24)
+    x = torch.randn(12, 8, 128, device=DEV).to(torch.bfloat16)
+    for cu in ([0, 6, 50], [-3, 6, 12], [0, 9, 4]):
+        st = _dev([0])
+        q.attention_nvfp4(x, bed.cache, _dev([30, 180]), cu=_dev(cu), max_new=12, dev_status=st)
+        assert q.get_last_device_status(st) & q.DEV_BAD_INDEX
+
+
 def test_pages_behind_32_bits(q):
     """Code offsets above 2^32: the last pages of a pool of 4.6 GB."""
     pages, hkv, page, dim = 70000, 8, 128, 128
