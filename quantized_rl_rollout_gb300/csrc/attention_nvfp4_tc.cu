@@ -561,6 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
       if (!mbar_wait(&sh.raw_full[slot], turn & 1, abort, p.status)) return false;
       Codes<D> x;
       x.load(sh.raw[slot], sh.raw_s[slot], live, t);
+      // The next copy into the slot is a write of the asynchronous proxy: only this
+      // fence orders the reads above before it (the arrive alone does not; without
+      // the fence a read can come after the wait below, and finds the next tile).
+      fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.raw_empty[slot]);
       if (use >= 2 && !mbar_wait(empty, ((use >> 1) - 1) & 1, abort, p.status)) return false;

@@ -212,6 +212,38 @@ def test_several_rows(q, dim, hq, hkv, lens, news):
     _attend(Bed(q, lens, hkv, dim, 16, 7), hq, news, strided=True)
 
 
+@pytest.mark.parametrize("dim,page", [(128, 64), (64, 16)])
+def test_many_items_a_range(q, dim, page):
+    """Several whole items in every CTA's range, of one key tile to four."""
+    lens = [17 + 97 * i % 487 for i in range(40)]
+    _attend(Bed(q, lens, 8, dim, page, 37 + dim), 32, lens)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_long_prompt_has_the_same_bits_every_time(q, dim):
+    """A prompt whose items fill the GPU several times over: 60 runs agree bit for bit, and sampled rows with the oracle."""
+    n, hq, hkv = 4096, 32, 8
+    bed = Bed(q, [n], hkv, dim, 64, 39)
+    x = inputs.activations(n * hq, dim, 40, device=DEV).view(n, hq, dim)
+    pos, cu = _dev([0]), _dev([0, n])
+    first = None
+    for i in range(60):
+        out, lse = q.attention_nvfp4(x, bed.cache, pos, cu=cu, max_new=n, return_lse=True)
+        if first is None:
+            first = out, lse
+        else:
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1]), i
+    k, v = bed.values(0)
+    xs, o, e = to_np(x), to_np(first[0]), to_np(first[1])
+    for t in (0, 63, 64, 368, 1000, 2047, 3071, 4095):
+        want, want_lse, spread = kv.attention(xs[t:t + 1], k[:t + 1], v[:t + 1], t, dim ** -0.5)
+        big = np.stack([(np.abs(xs[t, h].astype(np.float64)) @ np.abs(k[:t + 1, h // 4]).T).max() for h in range(hq)]) * dim ** -0.5
+        tol = 2 ** -18 * (big + 1)
+        assert (np.abs(e[t] - want_lse[0]) <= tol).all()
+        bound = 2 ** -8 * np.abs(want[0]) + (2 ** -10 + tol)[:, None] * spread[0] + 2 ** -31 * np.repeat(np.abs(v[:t + 1]).sum(0), 4, 0) + 1e-30
+        assert (np.abs(o[t] - want[0]) <= bound).all()
+
+
 def test_peaked_scores(q):
     """Scores of some hundreds: the running reference moves, weights underflow."""
     _attend(Bed(q, [700, 90], 2, 128, 32, 8, spread=4.0), 8, [1, 1], q_scale=8.0)
