@@ -613,10 +613,138 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_nvfp4_kerne
 
 namespace {
 
+// Joins items of a few pieces each: a warp a row.  The lanes take the pieces'
+// (m, l), 32 at a time; sums over them are formed in the order of the pieces'
+// lanes, the outputs' in the order of the pieces.  RT: rows of a piece.
+template <int D, int RT>
+__global__ void __launch_bounds__(256) join_rows_kernel(const Params p) {
+  constexpr int V = D / 32;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const Record rec = p.rec[blockIdx.x];
+  const int row = rec.rt * RT + r;
+  if (rec.pieces == 0 || row >= rec.n * p.G) return;
+  const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
+  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)) * RT + r; };
+  float m = kNone, l = 0.0f, o[V] = {};
+  for (int i0 = 0; i0 < rec.pieces; i0 += 32) {
+    const int n = min(32, rec.pieces - i0);
+    float mi = kNone, li = 0.0f;
+    if (lane < n) {
+      mi = p.pm[piece(i0 + lane)];
+      li = p.pl[piece(i0 + lane)];
+    }
+    float top = mi;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    top = fmaxf(top, m);
+    const float old = ex2(m - top), a = lane < n ? ex2(mi - top) : 0.0f;
+    m = top;
+    float sum = a * li;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    l = l * old + sum;
+#pragma unroll
+    for (int d = 0; d < V; ++d) o[d] *= old;
+    // `many` pieces' outputs from the i-th on; eight loads under way at a time
+    // where there are as many
+    auto add = [&](auto many, int i) {
+      constexpr int kMany = decltype(many)::value;
+      float v[kMany][V];
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        const float* src = p.po + piece(i0 + min(i + u, n - 1)) * D + V * lane;
+        if constexpr (V == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(src);
+          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(src);
+          v[u][0] = x.x, v[u][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        const float ai = __shfl_sync(0xFFFFFFFFu, a, (i + u) & 31);  // 0 behind the last piece
+#pragma unroll
+        for (int d = 0; d < V; ++d) o[d] += ai * v[u][d];
+      }
+    };
+    int i = 0;
+    for (; i + 8 <= n; i += 8) add(std::integral_constant<int, 8>{}, i);
+    for (; i < n; i += 2) add(std::integral_constant<int, 2>{}, i);
+  }
+  const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+  const int64_t orow = out_row(p, rec.first, rec.h, row);
+  uint32_t y[V / 2];
+#pragma unroll
+  for (int d = 0; d < V / 2; ++d) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * d] * inv, o[2 * d + 1] * inv);
+    y[d] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(p.out + orow * D + V * lane) = make_uint2(y[0], y[1]);
+  else *reinterpret_cast<uint32_t*>(p.out + orow * D + V * lane) = y[0];
+  if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+}
+
+// Joins items of many pieces each (long sequences, few of them): a warp takes a quarter of a row's
+// values (row blockIdx.y of items 2 blockIdx.x and the next); groups of D / 16 lanes
+// take the pieces in turn, so a batch of 32 pieces' loads is under way at once.
+// Every sum has a fixed order.
+template <int D, int RT>
+__global__ void __launch_bounds__(256) join_pieces_kernel(const Params p) {
+  constexpr int kLanes = D / 16, kGroups = 32 / kLanes;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp & 3, grp = lane / kLanes, row = blockIdx.y;
+  const int64_t item = 2 * static_cast<int64_t>(blockIdx.x) + (warp >> 2);
+  if (item >= static_cast<int64_t>(p.c.B) * p.c.Hkv) return;
+  const Record rec = p.rec[item];
+  if (rec.pieces == 0 || row >= rec.n * p.G) return;
+  const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
+  const float* const po = p.po + part * (D / 4) + 4 * (lane % kLanes);
+  float m = kNone, l = 0.0f, o[4] = {};
+  for (int i0 = 0; i0 < rec.pieces; i0 += 32) {
+    const int n = min(32, rec.pieces - i0);
+    float mi = kNone, li = 0.0f, old;
+    if (lane < n) {
+      mi = p.pm[piece_row(rec, i0 + lane, RT) + row];
+      li = p.pl[piece_row(rec, i0 + lane, RT) + row];
+    }
+    // kGroups x `many` pieces
+    auto add = [&](auto many) {
+      constexpr int kMany = decltype(many)::value;
+      float4 x[kMany];
+#pragma unroll
+      for (int u = 0; u < kMany; ++u)
+        x[u] = *reinterpret_cast<const float4*>(po + (piece_row(rec, i0 + min(kGroups * u + grp, n - 1), RT) + row) * D);
+      const float a = piece_weight<32>(mi, li, m, l, old);
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] *= old;
+#pragma unroll
+      for (int u = 0; u < kMany; ++u) {
+        const float ai = __shfl_sync(0xFFFFFFFFu, a, kGroups * u + grp);  // 0 behind the last piece
+        o[0] += ai * x[u].x, o[1] += ai * x[u].y, o[2] += ai * x[u].z, o[3] += ai * x[u].w;
+      }
+    };
+    if (n <= kGroups) add(std::integral_constant<int, 1>{});
+    else add(std::integral_constant<int, kLanes>{});
+  }
+#pragma unroll
+  for (int y = kLanes; y < 32; y <<= 1)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] += __shfl_xor_sync(0xFFFFFFFFu, o[d], y);
+  const int64_t orow = out_row(p, rec.first, rec.h, row);
+  if (grp == 0)
+    *reinterpret_cast<uint2*>(p.out + orow * D + part * (D / 4) + 4 * lane) = bf16x4(o, l > 0.0f ? __fdividef(vg, l) : 0.0f);
+  if (p.lse && part == 0 && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+}
+
 template <int D, int NT>
 cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   constexpr int RT = 8 * NT;
-  const int ranges = grid * kWarps, items = a.c.B * a.c.Hkv;
+  const int ranges = grid * kWarps, rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(a.max_new) * (a.Hq / a.c.Hkv), RT));
+  const int64_t items = static_cast<int64_t>(a.c.B) * a.c.Hkv;
   const Params p = make_params(a, a.ws, ranges, RT, items);
   constexpr int smem = static_cast<int>(sizeof(Raw<D>)) * kStages * kWarps;
   static bool attr = false;
@@ -630,7 +758,11 @@ cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   // a cache whose longest sequence fits a range, and a range for every item:
   // nothing is cut
   if (e != cudaSuccess || (a.c.capacity() <= kMinTiles * kTok && items <= ranges)) return e;
-  return launch_dependent(join_kernel<D, RT>, dim3(items, NT), 256, 0, stream, p);
+  // Eight pieces an item on average, or more: 8 sequences of 20000..33000 tokens
+  // join in 6 us by pieces, in 12 by rows; 64 of 2048..4096 (4 pieces) in 7.7 and 5.8.
+  if (ranges >= 8 * items)
+    return launch_dependent(join_pieces_kernel<D, RT>, dim3(static_cast<unsigned>((items + 1) / 2), rows), 256, 0, stream, p);
+  return launch_dependent(join_rows_kernel<D, RT>, dim3(static_cast<unsigned>(items), NT), 256, 0, stream, p);
 }
 
 // Whether some sequence may have few rows, or many (see kFewRows).

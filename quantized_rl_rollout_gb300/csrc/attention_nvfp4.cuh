@@ -104,78 +104,32 @@ __device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, in
   return static_cast<int64_t>(first + p.byG.div(row)) * p.Hq + h * p.G + p.byG.mod(row);
 }
 
-// Joins the pieces of record blockIdx.x's item: a warp a row.  The lanes take the pieces' (m, l),
-// 32 at a time; sums over them are formed in the order of the pieces' lanes,
-// the outputs' in the order of the pieces.  RT: rows of a piece.
-template <int D, int RT>
-__global__ void __launch_bounds__(256) join_kernel(const Params p) {
-  constexpr int V = D / 32;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const Record rec = p.rec[blockIdx.x];
-  const int row = rec.rt * RT + r;
-  if (rec.pieces == 0 || row >= rec.n * p.G) return;
-  const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)) * RT + r; };
-  float m = kNone, l = 0.0f, o[V] = {};
-  for (int i0 = 0; i0 < rec.pieces; i0 += 32) {
-    const int n = min(32, rec.pieces - i0);
-    float mi = kNone, li = 0.0f;
-    if (lane < n) {
-      mi = p.pm[piece(i0 + lane)];
-      li = p.pl[piece(i0 + lane)];
-    }
-    float top = mi;
+// Weights of up to 32 pieces of a row, piece i in lane i of each `kLanes` lanes
+// (the rest: none), brought to the row's new reference m; `old` brings what the
+// row has so far there.
+template <int kLanes>
+__device__ __forceinline__ float piece_weight(float mi, float li, float& m, float& l, float& old) {
+  float top = mi;
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-    top = fmaxf(top, m);
-    const float old = ex2(m - top), a = lane < n ? ex2(mi - top) : 0.0f;
-    m = top;
-    float sum = a * li;
+  for (int x = kLanes / 2; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+  top = fmaxf(top, m);
+  old = ex2(m - top);
+  m = top;
+  const float a = ex2(mi - top);
+  float sum = a * li;
 #pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-    l = l * old + sum;
-#pragma unroll
-    for (int d = 0; d < V; ++d) o[d] *= old;
-    // `many` pieces' outputs from the i-th on; eight loads under way at a time
-    // where there are as many
-    auto add = [&](auto many, int i) {
-      constexpr int kMany = decltype(many)::value;
-      float v[kMany][V];
-#pragma unroll
-      for (int u = 0; u < kMany; ++u) {
-        const float* src = p.po + piece(i0 + min(i + u, n - 1)) * D + V * lane;
-        if constexpr (V == 4) {
-          const float4 x = *reinterpret_cast<const float4*>(src);
-          v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
-        } else {
-          const float2 x = *reinterpret_cast<const float2*>(src);
-          v[u][0] = x.x, v[u][1] = x.y;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kMany; ++u) {
-        const float ai = __shfl_sync(0xFFFFFFFFu, a, (i + u) & 31);  // 0 behind the last piece
-#pragma unroll
-        for (int d = 0; d < V; ++d) o[d] += ai * v[u][d];
-      }
-    };
-    int i = 0;
-    for (; i + 8 <= n; i += 8) add(std::integral_constant<int, 8>{}, i);
-    for (; i < n; i += 2) add(std::integral_constant<int, 2>{}, i);
-  }
-  const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
-  const int64_t orow = out_row(p, rec.first, rec.h, row);
-  uint32_t y[V / 2];
-#pragma unroll
-  for (int d = 0; d < V / 2; ++d) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * d] * inv, o[2 * d + 1] * inv);
-    y[d] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  if constexpr (V == 4) *reinterpret_cast<uint2*>(p.out + orow * D + V * lane) = make_uint2(y[0], y[1]);
-  else *reinterpret_cast<uint32_t*>(p.out + orow * D + V * lane) = y[0];
-  if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+  for (int x = kLanes / 2; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+  l = l * old + sum;
+  return a;
+}
+
+__device__ __forceinline__ uint2 bf16x4(const float (&o)[4], float f) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(o[0] * f, o[1] * f), b = __floats2bfloat162_rn(o[2] * f, o[3] * f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+__device__ __forceinline__ int64_t piece_row(const Record& rec, int i, int rt) {
+  return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)) * rt;
 }
 
 // Launches a kernel as the programmatic dependent of the one before it in the

@@ -699,6 +699,57 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
 
 namespace {
 
+// Joins this kernel's items: many rows, most often of two pieces.  Eight lanes a
+// row, four rows a warp.
+template <int D>
+__global__ void __launch_bounds__(256) join_many_kernel(const Params p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, sub = lane & 7, first = (blockIdx.x % (kRows / 32)) * 32 + (threadIdx.x >> 5) * 4;
+  const Record rec = p.rec[blockIdx.x / (kRows / 32)];
+  const int r = first + (lane >> 3), row = rec.rt * kRows + r;
+  if (rec.pieces == 0 || rec.rt * kRows + first >= rec.n * p.G) return;  // (the same for the warp)
+  const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
+  float m = kNone, l = 0.0f, o[D / 32][4] = {};
+  for (int i0 = 0; i0 < rec.pieces; i0 += 8) {
+    const int n = min(8, rec.pieces - i0);
+    float mi = kNone, li = 0.0f, old, a = 0.0f;
+    if (sub < n) {
+      mi = p.pm[piece_row(rec, i0 + sub, kRows) + r];
+      li = p.pl[piece_row(rec, i0 + sub, kRows) + r];
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; i += 2) {
+      float4 x[2][D / 32];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          x[u][k] = *reinterpret_cast<const float4*>(p.po + (piece_row(rec, i0 + min(i + u, n - 1), kRows) + r) * D + 32 * k + 4 * sub);
+      if (i == 0) {
+        a = piece_weight<8>(mi, li, m, l, old);
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+          for (int d = 0; d < 4; ++d) o[k][d] *= old;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float ai = i + u < n ? __shfl_sync(0xFFFFFFFFu, a, (lane & 24) + i + u) : 0.0f;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k)
+          o[k][0] += ai * x[u][k].x, o[k][1] += ai * x[u][k].y, o[k][2] += ai * x[u][k].z, o[k][3] += ai * x[u][k].w;
+      }
+    }
+  }
+  if (row >= rec.n * p.G) return;
+  const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+  const int64_t orow = out_row(p, rec.first, rec.h, row);
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) *reinterpret_cast<uint2*>(p.out + orow * D + 32 * k + 4 * sub) = bf16x4(o[k], inv);
+  if (p.lse && sub == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+}
+
 template <int D>
 cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_t stream) {
   constexpr int smem = static_cast<int>(sizeof(Smem<D>)) + 1024;
@@ -723,7 +774,7 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(join_kernel<D, kRows>, dim3(grid, kRows / 8), 256, 0, stream, p);
+  return launch_dependent(join_many_kernel<D>, dim3(grid * (kRows / 32)), 256, 0, stream, p);
 }
 
 }  // namespace
