@@ -43,9 +43,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-// CTAs an SM, by registers: with 4 the 128 values of D = 128 are too few (64
-// sequences of 2048..4096 tokens: 46 us with 3, 50 with 4; D = 64: 42 and 41)
-constexpr int ctas_per_sm(int d, int nt) { return nt == 2 ? 2 : d == 128 ? 3 : 4; }
+// CTAs an SM, by registers: with 4 the 128 of a lane are too few for D = 128 (64
+// sequences of 2048..4096 tokens: 46 us with 3, 50 with 4; D = 64: 42 and 41);
+// 16 rows with 3 spill (32 sequences of 1..9 new tokens: 78 us, 69 with 2)
+constexpr int ctas_per_sm(int d, int nt) { return nt >= 2 ? 2 : d == 128 ? 3 : 4; }
 constexpr int kTok = 32;      // tokens of a tile
 constexpr int kMinTiles = 4;  // tiles of a range
 constexpr int kItemCost = 1;
@@ -294,10 +295,13 @@ struct Feed {
 
 // A warp's rows and running state; NT groups of 8 rows.  Lane (g, c) feeds the
 // query of row g of a group to the MMAs and holds the results of rows 2 c and
-// 2 c + 1.
+// 2 c + 1.  The query is in registers, that of four groups in shared memory.
+template <int NT>
+constexpr bool kQInSmem = NT > 2;
 template <int D, int NT>
 struct State {
-  uint32_t q[NT][D / 16][2];
+  uint4 q[kQInSmem<NT> ? 1 : NT][D / 32];
+  uint32_t qs;  // shared memory: the lane's 16 bytes of [NT][D / 32][32 lanes]
   float f[NT][2];    // score factor of the lane's two rows (log2 units)
   int lim[NT][2];    // their last visible position, before the piece's end
   float m[NT][2], l[NT][2];
@@ -329,9 +333,14 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int e
     const int e = query_exp(mx);
     const Pow2Scaler sc(e);
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
+    for (int j = 0; j < D / 32; ++j) {
+      uint32_t y[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) s.q[nt][j][i] = f16x2(sc(bf16_lo(w[2 * j + i])), sc(bf16_hi(w[2 * j + i])));
+      for (int i = 0; i < 4; ++i) y[i] = f16x2(sc(bf16_lo(w[4 * j + i])), sc(bf16_hi(w[4 * j + i])));
+      if constexpr (kQInSmem<NT>)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(s.qs + 512 * (nt * (D / 32) + j)), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+      else s.q[nt][j] = make_uint4(y[0], y[1], y[2], y[3]);
+    }
     // at least the smallest normal value: a masked score times it stays -inf
     const float f = fmaxf(p.scale * kLog2e * kg * ldexpf(1.0f, e), 1.17549435e-38f);
     const int lim = in ? min(min(it.pos + p.byG.div(r), it.last), end - 1) : -1;
@@ -354,115 +363,185 @@ __device__ __forceinline__ void load_rows(const Params& p, const Item& it, int e
 template <int D, int NT>
 __device__ __forceinline__ void step(const Places<D>& at, uint32_t so, int t, int live, bool all, int lane, State<D, NT>& s) {
   const int g = lane >> 2, c = lane & 3;
-  float e[2][NT][4];
+  // four groups: a half tile at a time, for its registers
+  constexpr int H = NT > 2 ? 1 : 2;
+#pragma unroll 1
+  for (int h0 = 0; h0 < 2; h0 += H) {
+    float e[H][NT][4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    Keys<D> x;
-    x.load(at.k + so, at.ks + so, h);
+    for (int h = 0; h < H; ++h) {
+      Keys<D> x;
+      x.load(at.k + so, at.ks + so, h0 + h);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[h][nt][i] = 0.0f;
-    const uint32_t s0 = e4m3x2_to_f16x2(x.s[0]), s1 = e4m3x2_to_f16x2(x.s[1]);
+        for (int i = 0; i < 4; ++i) e[h][nt][i] = 0.0f;
+      const uint32_t s0 = e4m3x2_to_f16x2(x.s[0]), s1 = e4m3x2_to_f16x2(x.s[1]);
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      const uint32_t sel = w < 2 ? 0x1010u : 0x3232u;  // D = 64: both words in the lane's one block
-      const uint32_t f0 = __byte_perm(s0, s0, sel), f1 = __byte_perm(s1, s1, sel);
-      uint32_t a[4], b[4];
-      f16x2x4_from_e2m1x8(x.k[0].w[w], a);
-      f16x2x4_from_e2m1x8(x.k[1].w[w], b);
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t sel = w < 2 ? 0x1010u : 0x3232u;  // D = 64: both words in the lane's one block
+        const uint32_t f0 = __byte_perm(s0, s0, sel), f1 = __byte_perm(s1, s1, sel);
+        uint32_t a[4], b[4];
+        f16x2x4_from_e2m1x8(x.k[0].w[w], a);
+        f16x2x4_from_e2m1x8(x.k[1].w[w], b);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f1);
+        for (int i = 0; i < 4; ++i) a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f1);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        mma16816(e[h][nt], a[0], b[0], a[1], b[1], s.q[nt][2 * w][0], s.q[nt][2 * w][1]);
-        mma16816(e[h][nt], a[2], b[2], a[3], b[3], s.q[nt][2 * w + 1][0], s.q[nt][2 * w + 1][1]);
+        for (int nt = 0; nt < NT; ++nt) {
+          uint4 y;
+          if constexpr (kQInSmem<NT>)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w) : "r"(s.qs + 512 * (nt * (D / 32) + w)));
+          else y = s.q[nt][w];
+          mma16816(e[h][nt], a[0], b[0], a[1], b[1], y.x, y.y);
+          mma16816(e[h][nt], a[2], b[2], a[3], b[3], y.z, y.w);
+        }
       }
     }
-  }
-  // lane's scores: rows 2 c, 2 c + 1 of each group; tokens tau, tau + 8 of each
-  // half
-  const int tok = kTok * t + (g >> 1) + 4 * (g & 1);
-  if (!all)
+    // lane's scores: rows 2 c, 2 c + 1 of each group; tokens tau, tau + 8 of each
+    // half
+    const int tok = kTok * t + 16 * h0 + (g >> 1) + 4 * (g & 1);
+    if (!all)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (tok + 16 * h + 8 * (i >> 1) > s.lim[nt][i & 1]) e[h][nt][i] = -INFINITY;
-  float top[NT][2], most = -INFINITY;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      top[nt][i] = fmaxf(max3(e[0][nt][i], e[0][nt][i + 2], e[1][nt][i]), e[1][nt][i + 2]);
-    most = max3(most, fmaf(top[nt][0], s.f[nt][0], -s.m[nt][0]), fmaf(top[nt][1], s.f[nt][1], -s.m[nt][1]));
-  }
-  if (__any_sync(0xFFFFFFFFu, most > kRoom)) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float v = top[nt][i];
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
-        const float m = fmaxf(v * s.f[nt][i] - kLift, s.m[nt][i]), a = ex2(s.m[nt][i] - m);
-        s.m[nt][i] = m;
-        s.l[nt][i] *= a;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) s.o[nt][j][i] *= a, s.o[nt][j][i + 2] *= a;
-      }
-  }
-  uint32_t p[2][NT][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
+          for (int i = 0; i < 4; ++i)
+            if (tok + 16 * h + 8 * (i >> 1) > s.lim[nt][i & 1]) e[h][nt][i] = -INFINITY;
+    float top[NT][2], most = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[h][nt][i] = ex2(fmaf(e[h][nt][i], s.f[nt][i & 1], -s.m[nt][i & 1]));
-      s.l[nt][0] += e[h][nt][0] + e[h][nt][2];
-      s.l[nt][1] += e[h][nt][1] + e[h][nt][3];
-      p[h][nt][0] = movmatrix(f16x2(e[h][nt][0], e[h][nt][1]));
-      p[h][nt][1] = movmatrix(f16x2(e[h][nt][2], e[h][nt][3]));
+      for (int i = 0; i < 2; ++i)
+        top[nt][i] = H == 2 ? fmaxf(max3(e[0][nt][i], e[0][nt][i + 2], e[H - 1][nt][i]), e[H - 1][nt][i + 2]) : fmaxf(e[0][nt][i], e[0][nt][i + 2]);
+      most = max3(most, fmaf(top[nt][0], s.f[nt][0], -s.m[nt][0]), fmaf(top[nt][1], s.f[nt][1], -s.m[nt][1]));
     }
+    if (__any_sync(0xFFFFFFFFu, most > kRoom)) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    Values<D> x;
-    x.load(at.v + so, at.vs + so, h);
-    // the two pairs' scales; those of tokens that do not exist count as zero (what
-    // lies there may be anything, a NaN among it)
-    uint32_t v01 = __byte_perm(x.s[0], x.s[1], 0x7740), v23 = __byte_perm(x.s[2], x.s[3], 0x7740);
-    if (live < kTok) {
-      const int n = live - 16 * h - c;
-      v01 &= (n > 0 ? 0xFFu : 0u) | (n > 4 ? 0xFF00u : 0u);
-      v23 &= (n > 8 ? 0xFFu : 0u) | (n > 12 ? 0xFF00u : 0u);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = top[nt][i];
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+          const float m = fmaxf(v * s.f[nt][i] - kLift, s.m[nt][i]), a = ex2(s.m[nt][i] - m);
+          s.m[nt][i] = m;
+          s.l[nt][i] *= a;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) s.o[nt][j][i] *= a, s.o[nt][j][i + 2] *= a;
+        }
     }
-    const uint32_t f0 = e4m3x2_to_f16x2(v01), f1 = e4m3x2_to_f16x2(v23);
+    uint32_t p[H][NT][2];
 #pragma unroll
-    for (int w = 0; w < D / 64; ++w) {
-      // bytes of (first, second) token's codes of one value: even values, odd values
-      uint32_t a[4], b[4], d[4], u[4];
-      f16x2x4_from_e2m1x8(choose(x.v[0].w[w], x.v[1].w[w] << 4, 0x0F0F0F0Fu), a);
-      f16x2x4_from_e2m1x8(choose(x.v[0].w[w] >> 4, x.v[1].w[w], 0x0F0F0F0Fu), b);
-      f16x2x4_from_e2m1x8(choose(x.v[2].w[w], x.v[3].w[w] << 4, 0x0F0F0F0Fu), d);
-      f16x2x4_from_e2m1x8(choose(x.v[2].w[w] >> 4, x.v[3].w[w], 0x0F0F0F0Fu), u);
+    for (int h = 0; h < H; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), u[i] = hmul2(u[i], f1);
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(s.o[nt][4 * w + i], a[i], b[i], d[i], u[i], p[h][nt][0], p[h][nt][1]);
+        for (int i = 0; i < 4; ++i) e[h][nt][i] = ex2(fmaf(e[h][nt][i], s.f[nt][i & 1], -s.m[nt][i & 1]));
+        s.l[nt][0] += e[h][nt][0] + e[h][nt][2];
+        s.l[nt][1] += e[h][nt][1] + e[h][nt][3];
+        p[h][nt][0] = movmatrix(f16x2(e[h][nt][0], e[h][nt][1]));
+        p[h][nt][1] = movmatrix(f16x2(e[h][nt][2], e[h][nt][3]));
+      }
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+      Values<D> x;
+      x.load(at.v + so, at.vs + so, h0 + h);
+      // the two pairs' scales; those of tokens that do not exist count as zero (what
+      // lies there may be anything, a NaN among it)
+      uint32_t v01 = __byte_perm(x.s[0], x.s[1], 0x7740), v23 = __byte_perm(x.s[2], x.s[3], 0x7740);
+      if (live < kTok) {
+        const int n = live - 16 * (h0 + h) - c;
+        v01 &= (n > 0 ? 0xFFu : 0u) | (n > 4 ? 0xFF00u : 0u);
+        v23 &= (n > 8 ? 0xFFu : 0u) | (n > 12 ? 0xFF00u : 0u);
+      }
+      const uint32_t f0 = e4m3x2_to_f16x2(v01), f1 = e4m3x2_to_f16x2(v23);
+#pragma unroll
+      for (int w = 0; w < D / 64; ++w) {
+        // bytes of (first, second) token's codes of one value: even values, odd values
+        uint32_t a[4], b[4], d[4], u[4];
+        f16x2x4_from_e2m1x8(choose(x.v[0].w[w], x.v[1].w[w] << 4, 0x0F0F0F0Fu), a);
+        f16x2x4_from_e2m1x8(choose(x.v[0].w[w] >> 4, x.v[1].w[w], 0x0F0F0F0Fu), b);
+        f16x2x4_from_e2m1x8(choose(x.v[2].w[w], x.v[3].w[w] << 4, 0x0F0F0F0Fu), d);
+        f16x2x4_from_e2m1x8(choose(x.v[2].w[w] >> 4, x.v[3].w[w], 0x0F0F0F0Fu), u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = hmul2(a[i], f0), b[i] = hmul2(b[i], f0), d[i] = hmul2(d[i], f1), u[i] = hmul2(u[i], f1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s.o[nt][4 * w + i], a[i], b[i], d[i], u[i], p[h][nt][0], p[h][nt][1]);
+        }
       }
     }
   }
+}
+
+// A piece of an item: its tiles, and the rows' results or a piece of them.  RT:
+// rows of a piece in the workspace.
+template <int D, int NT, int RT>
+__device__ __forceinline__ void piece(const Params& p, const Walk& it, Feed<D>& feed, const Places<D>& at, bool pad, int range,
+                                      int64_t per, uint32_t qs, uint32_t& so, uint32_t& free, int lane) {
+  const int c = lane & 3, g = lane >> 2;
+  State<D, NT> s;
+  s.qs = qs;
+  load_rows<D, NT>(p, it, kTok * it.stop, lane, s);
+  // tiles before this one are seen whole by every row (rows behind the last one
+  // are never read: no mask for them)
+  const int whole = (min(it.pos, it.last) + 1) / kTok;
+#pragma unroll 1
+  for (int t = it.t0; t < it.stop; ++t) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();  // the tile is there for all lanes, and the one before it read by all
+    feed.issue(p, pad, free, lane);
+    step<D, NT>(at, so, t, it.last + 1 - kTok * t, t < whole, lane, s);
+    free = so;
+    so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
+  }
+  // ---- the rows' results, or a piece of them
+  if (it.empty()) return;
+  const bool cut0 = it.t0 > 0, cut1 = it.t1 < it.tiles;
+  const int64_t piece = static_cast<int64_t>(2 * range + (cut0 ? 0 : 1)) * RT;
+  const float vg = p.c.vg ? __ldg(p.c.vg + it.h) : 1.0f;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = 8 * nt + 2 * c + i;
+      float l = s.l[nt][i];
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+      if (r >= it.n * p.G) continue;
+      if (!cut0 && !cut1) {
+        const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+        const int64_t orow = out_row(p, it.first, it.h, r);
+        uint32_t w[D / 16];
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(s.o[nt][j][i] * inv, s.o[nt][j][i + 2] * inv);
+          w[j] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+          reinterpret_cast<uint4*>(p.out + orow * D + D / 8 * g)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        if (p.lse && g == 0) p.lse[orow] = l > 0.0f ? (s.m[nt][i] + lg2(l)) * kLn2 : -INFINITY;
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+          reinterpret_cast<float4*>(p.po + (piece + r) * D + D / 8 * g)[j] =
+              make_float4(s.o[nt][2 * j][i], s.o[nt][2 * j][i + 2], s.o[nt][2 * j + 1][i], s.o[nt][2 * j + 1][i + 2]);
+        if (g == 0) p.pm[piece + r] = s.m[nt][i], p.pl[piece + r] = l;
+      }
+    }
+  if (!cut0 && lane == 0)
+    p.rec[static_cast<int64_t>(it.b) * p.c.Hkv + it.h] =
+        Record{cut1 ? 1 + static_cast<int>((it.tiles - it.t1 + per - 1) / per) : 0, range, 0, it.h, it.first, it.n};
 }
 
 }  // namespace
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_nvfp4_kernel(const Params p) {
-  constexpr int RT = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Raw<D>* const ring = reinterpret_cast<Raw<D>*>(smem_raw) + kStages * (threadIdx.x >> 5);  // the warp's
   __shared__ int64_t sums[2][kWarps], at_off[kWarps];
@@ -549,64 +628,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attn_nvfp4_kerne
   feed.begin(p, it, ring, lane, pad);
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) feed.issue(p, pad, i * static_cast<uint32_t>(sizeof(Raw<D>)), lane);
-  const int c = lane & 3, g = lane >> 2;
-  State<D, NT> s;
   const Places<D> at(ring, lane);
+  const uint32_t qs = smem_u32(smem_raw) + sizeof(Raw<D>) * kStages * kWarps + (warp * NT * (D / 32) * 32 + lane) * 16;
   // the ring's tile in use, and the one before it: that is filled next
   uint32_t so = 0, free = (kStages - 1) * static_cast<uint32_t>(sizeof(Raw<D>));
   do {
-    load_rows<D, NT>(p, it, kTok * it.stop, lane, s);
-    // tiles before this one are seen whole by every row (rows behind the last one
-    // are never read: no mask for them)
-    const int whole = (min(it.pos, it.last) + 1) / kTok;
-#pragma unroll 1
-    for (int t = it.t0; t < it.stop; ++t) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();  // the tile is there for all lanes, and the one before it read by all
-      feed.issue(p, pad, free, lane);
-      step<D, NT>(at, so, t, it.last + 1 - kTok * t, t < whole, lane, s);
-      free = so;
-      so = so == (kStages - 1) * sizeof(Raw<D>) ? 0 : so + static_cast<uint32_t>(sizeof(Raw<D>));
-    }
-    // ---- the rows' results, or a piece of them
-    if (it.empty()) continue;
-    const bool cut0 = it.t0 > 0, cut1 = it.t1 < it.tiles;
-    const int64_t piece = static_cast<int64_t>(2 * range + (cut0 ? 0 : 1)) * RT;
-    const float vg = p.c.vg ? __ldg(p.c.vg + it.h) : 1.0f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * nt + 2 * c + i;
-        float l = s.l[nt][i];
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-        if (r >= it.n * p.G) continue;
-        if (!cut0 && !cut1) {
-          const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
-          const int64_t orow = out_row(p, it.first, it.h, r);
-          uint32_t w[D / 16];
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(s.o[nt][j][i] * inv, s.o[nt][j][i + 2] * inv);
-            w[j] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-#pragma unroll
-          for (int j = 0; j < D / 64; ++j)
-            reinterpret_cast<uint4*>(p.out + orow * D + D / 8 * g)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          if (p.lse && g == 0) p.lse[orow] = l > 0.0f ? (s.m[nt][i] + lg2(l)) * kLn2 : -INFINITY;
-        } else {
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j)
-            reinterpret_cast<float4*>(p.po + (piece + r) * D + D / 8 * g)[j] =
-                make_float4(s.o[nt][2 * j][i], s.o[nt][2 * j][i + 2], s.o[nt][2 * j + 1][i], s.o[nt][2 * j + 1][i + 2]);
-          if (g == 0) p.pm[piece + r] = s.m[nt][i], p.pl[piece + r] = l;
-        }
-      }
-    if (!cut0 && lane == 0)
-      p.rec[static_cast<int64_t>(it.b) * p.c.Hkv + it.h] =
-          Record{cut1 ? 1 + static_cast<int>((it.tiles - it.t1 + per - 1) / per) : 0, range, 0, it.h, it.first, it.n};
+    if (NT <= 2 || it.n * p.G > 16) piece<D, NT, 8 * NT>(p, it, feed, at, pad, range, per, qs, so, free, lane);
+    else piece<D, 2, 8 * NT>(p, it, feed, at, pad, range, per, qs, so, free, lane);
   } while (it.next(p, pad));
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -746,7 +774,7 @@ cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   const int ranges = grid * kWarps, rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(a.max_new) * (a.Hq / a.c.Hkv), RT));
   const int64_t items = static_cast<int64_t>(a.c.B) * a.c.Hkv;
   const Params p = make_params(a, a.ws, ranges, RT, items);
-  constexpr int smem = static_cast<int>(sizeof(Raw<D>)) * kStages * kWarps;
+  constexpr int smem = (static_cast<int>(sizeof(Raw<D>)) * kStages + (kQInSmem<NT> ? NT * D * 16 : 0)) * kWarps;
   static bool attr = false;
   if (!attr) {
     const cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -771,7 +799,7 @@ bool any_many(int64_t max_new, int G) { return max_new * G > kFewRows; }
 
 size_t few_ws_bytes(int D, int64_t items) {
   return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(D, 1) * kWarps, 8, items),
-                  ws_bytes(D, kMaxSms * ctas_per_sm(D, 2) * kWarps, 16, items));
+                  ws_bytes(D, kMaxSms * ctas_per_sm(D, 4) * kWarps, 32, items));
 }
 
 }  // namespace
@@ -787,10 +815,14 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int G = a.Hq / a.c.Hkv;
   if (any_few(G)) {
-    const bool one = static_cast<int64_t>(a.max_new) * G <= 8;
-    const int grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(a.c.D, one ? 1 : 2);
-    const cudaError_t e = a.c.D == 128 ? (one ? launch<128, 1>(a, grid, stream) : launch<128, 2>(a, grid, stream))
-                                       : (one ? launch<64, 1>(a, grid, stream) : launch<64, 2>(a, grid, stream));
+    const int64_t rows = static_cast<int64_t>(a.max_new) * G;
+    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4, grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(a.c.D, nt);
+    const cudaError_t e = a.c.D == 128 ? (nt == 1   ? launch<128, 1>(a, grid, stream)
+                                          : nt == 2 ? launch<128, 2>(a, grid, stream)
+                                                    : launch<128, 4>(a, grid, stream))
+                                       : (nt == 1   ? launch<64, 1>(a, grid, stream)
+                                          : nt == 2 ? launch<64, 2>(a, grid, stream)
+                                                    : launch<64, 4>(a, grid, stream));
     if (e != cudaSuccess) return e;
   }
   return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D, static_cast<int64_t>(a.c.B) * a.c.Hkv), any_few(G), stream) : cudaSuccess;

@@ -15,7 +15,10 @@ namespace qrr {
 namespace attn4 {
 
 constexpr int kMaxSms = 160;       // of the workspace's size; grids are capped to it
-constexpr int kFewRows = 16;       // a sequence with at most this many rows a KV head takes the first kernel
+// A sequence with at most this many rows a KV head takes the first kernel: four
+// groups of 8 rows are what a lane's registers hold.  16 sequences over 2250
+// tokens, 17..32 rows: 42 us with it, 50 with the other.
+constexpr int kFewRows = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1.0e30f;  // reference of a row that has seen nothing
