@@ -30,6 +30,13 @@
 // and is only moved when some score exceeds it by 15, so p = 2^(s - m) stays
 // within f16, the row's largest p is at least 2^7, and a p keeps f16's full 11
 // bits down to 2^-21 of that (an absolute 2^-32 of it below).
+//
+// Bound by memory, at the ends by latency.  64 sequences of 2048..4096 tokens, 8
+// heads of 128, 4 query heads each: 47 us for 199 MB (4.2 TB/s; 29 us at the copy
+// rate).  Between its ends the kernel streams 6.3 TB/s; 4 us pass before the first
+// loads (the ranges have to be found), the warps' ends lie 8 us apart, and the join
+// and the launches take 8.  Rows share the conversion of codes: per token and head
+// 8 and 16 rows cost about the same, 32 twice that (registers: 8 warps an SM).
 #include <algorithm>
 
 #include "attention_nvfp4.cuh"
