@@ -250,6 +250,21 @@ def test_peaked_scores(q):
     _attend(Bed(q, [700, 90], 2, 64, 32, 8, spread=4.0), 8, [40, 3], q_scale=8.0, scale=0.3)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("hq,news", [(4, [5, 8, 1, 4]), (8, [3, 4, 2, 1]), (16, [2, 1, 2, 1]), (32, [1, 1, 1, 1]), (17, [1, 1, 1, 1])])
+def test_rows_17_to_32(q, dim, hq, news):
+    """More than 16 rows a KV head beside fewer, in one piece and in many, with plain and with peaked scores."""
+    _attend(Bed(q, [900, 33, 16, 2000], 1, dim, 16, 11), hq, news, strided=True)
+    _attend(Bed(q, [300, 70, 5, 31], 1, dim, 32, 12, spread=4.0), hq, news, q_scale=8.0)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_17_to_32_of_many_items(q, dim):
+    """Items of a few pieces each: 40 sequences, 8 KV heads, two to eight new tokens over ragged lengths."""
+    lens = [200 + 53 * i % 700 for i in range(40)]
+    _attend(Bed(q, lens, 8, dim, 64, 13), 32, [2 + i % 7 for i in range(40)])
+
+
 def test_query_magnitudes(q):
     """Queries far from one, zero rows among them."""
     for s in (1e-30, 1e20, 0.0):
@@ -332,7 +347,7 @@ def test_captured_rows_of_every_kind(q):
         assert torch.equal(out, want)
 
 
-@pytest.mark.parametrize("hq,rows", [(4, 1), (4, 2), (20, 1)])
+@pytest.mark.parametrize("hq,rows", [(4, 1), (4, 2), (20, 1), (40, 1)])
 def test_many_sequences(q, hq, rows):
     """More sequences than a CTA has threads, and than the many-rows kernel keeps in shared memory; some without tokens."""
     g = np.random.default_rng(3)
