@@ -268,6 +268,22 @@ __device__ __forceinline__ uint64_t twice(float x) {
   return r;
 }
 
+// 64 bytes of a row.  A store instruction takes a cycle a lane and row here (each
+// lane's row lies elsewhere), so as few as there can be: 32 bytes a lane where the
+// rows are so aligned.
+__device__ __forceinline__ void store16(uint16_t* to, const uint32_t (&y)[16], bool wide) {
+  if (wide) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 2 * i), "r"(y[i]), "r"(y[i + 1]),
+                   "r"(y[i + 2]), "r"(y[i + 3]), "r"(y[i + 4]), "r"(y[i + 5]), "r"(y[i + 6]), "r"(y[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint4*>(to)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+  }
+}
+
 // Two bf16 values times a power of two, as f16.
 __device__ __forceinline__ uint32_t scaled_f16x2(uint32_t w, uint64_t sc) {
   uint64_t x;
@@ -419,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
       return fmaxf(p.scale * kLog2e * (p.c.kg ? __ldg(p.c.kg + x.h) : 1.0f) * ldexpf(1.0f, e), 1.17549435e-38f);
     };
     auto active = [&](const Walk& x) { return x.qt * kRows + 128 * tile < x.s.n * p.G; };
+    const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
     Record rec{};
     uint32_t s_phase = 0, o_phase = 0;
     bool ok = true, more = true;
@@ -522,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         const float vg = p.c.vg ? __ldg(p.c.vg + w.h) : 1.0f;
         const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
         const int64_t orow = in ? out_row(p, w.s.first, w.h, row) : 0;
-        const int64_t pr = static_cast<int64_t>(2 * blockIdx.x + (w.t0 > 0 ? 0 : 1)) * kRows + 128 * tile + r;
+        const int64_t piece = 2 * blockIdx.x + (w.t0 > 0 ? 0 : 1);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t x[32];
@@ -535,18 +552,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
               const __nv_bfloat162 v2 = __floats2bfloat162_rn(__uint_as_float(x[2 * i]) * inv, __uint_as_float(x[2 * i + 1]) * inv);
               y[i] = *reinterpret_cast<const uint32_t*>(&v2);
             }
-            if (in)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4*>(p.out + orow * D + 32 * c)[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            if (in) store16(p.out + orow * D + 32 * c, y, wide);
           } else if (in) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(p.po + pr * D + 32 * c)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+              reinterpret_cast<uint4*>(p.po)[(piece * (D / 4) + 8 * c + i) * kRows + 128 * tile + r] =
+                  make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
         if (in && whole && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
-        if (in && !whole) p.pm[pr] = m, p.pl[pr] = l;
+        if (in && !whole) p.pm[piece * kRows + 128 * tile + r] = m, p.pl[piece * kRows + 128 * tile + r] = l;
         __syncwarp();
         tc_fence_before();
       } else if (more && active(nx)) {
@@ -709,45 +724,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
 
 namespace {
 
-// Joins this kernel's items: many rows, most often of two pieces.  Eight lanes a
-// row, four rows a warp.
+// Joins this kernel's items: many rows, most often of two pieces.  A piece's output
+// is [D / 4][row][4], so that the rows' threads write side by side.  Here eight
+// rows a warp, four lanes a row, a lane every fourth four values; two pieces'
+// loads at a time, sums in the order of the pieces.
 template <int D>
 __global__ void __launch_bounds__(256) join_many_kernel(const Params p) {
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, sub = lane & 7, first = (blockIdx.x % (kRows / 32)) * 32 + (threadIdx.x >> 5) * 4;
-  const Record rec = p.rec[blockIdx.x / (kRows / 32)];
-  const int r = first + (lane >> 3), row = rec.rt * kRows + r;
+  const int lane = threadIdx.x & 31, part = lane >> 3, first = (blockIdx.x % (kRows / 64)) * 64 + (threadIdx.x >> 5) * 8;
+  const Record rec = p.rec[blockIdx.x / (kRows / 64)];
+  const int r = first + (lane & 7), row = rec.rt * kRows + r;
   if (rec.pieces == 0 || rec.rt * kRows + first >= rec.n * p.G) return;  // (the same for the warp)
   const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  float m = kNone, l = 0.0f, o[D / 32][4] = {};
-  for (int i0 = 0; i0 < rec.pieces; i0 += 8) {
-    const int n = min(8, rec.pieces - i0);
-    float mi = kNone, li = 0.0f, old, a = 0.0f;
-    if (sub < n) {
-      mi = p.pm[piece_row(rec, i0 + sub, kRows) + r];
-      li = p.pl[piece_row(rec, i0 + sub, kRows) + r];
+  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)); };
+  float m = kNone, l = 0.0f, o[D / 16][4] = {};
+  for (int i0 = 0; i0 < rec.pieces; i0 += 4) {
+    // the row's lanes take a piece's (m, l) each
+    const int n = min(4, rec.pieces - i0);
+    float mi = kNone, li = 0.0f;
+    if (part < n) {
+      mi = p.pm[piece(i0 + part) * kRows + r];
+      li = p.pl[piece(i0 + part) * kRows + r];
     }
+    float a = 0.0f;
 #pragma unroll 1
     for (int i = 0; i < n; i += 2) {
-      float4 x[2][D / 32];
+      float4 x[2][D / 16];
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          x[u][k] = *reinterpret_cast<const float4*>(p.po + (piece_row(rec, i0 + min(i + u, n - 1), kRows) + r) * D + 32 * k + 4 * sub);
+        for (int k = 0; k < D / 16; ++k)
+          x[u][k] = reinterpret_cast<const float4*>(p.po)[(piece(i0 + min(i + u, n - 1)) * (D / 4) + 4 * k + part) * kRows + r];
       if (i == 0) {
-        a = piece_weight<8>(mi, li, m, l, old);
+        float top = fmaxf(mi, __shfl_xor_sync(0xFFFFFFFFu, mi, 8));
+        top = fmaxf(m, fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16)));
+        const float old = ex2(m - top);
+        m = top;
+        a = ex2(mi - top);
+        float sum = a * li;
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 8);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
+        l = l * old + sum;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
+        for (int k = 0; k < D / 16; ++k)
 #pragma unroll
           for (int d = 0; d < 4; ++d) o[k][d] *= old;
       }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const float ai = i + u < n ? __shfl_sync(0xFFFFFFFFu, a, (lane & 24) + i + u) : 0.0f;
+        const float ai = i + u < n ? __shfl_sync(0xFFFFFFFFu, a, 8 * (i + u) + (lane & 7)) : 0.0f;
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k)
+        for (int k = 0; k < D / 16; ++k)
           o[k][0] += ai * x[u][k].x, o[k][1] += ai * x[u][k].y, o[k][2] += ai * x[u][k].z, o[k][3] += ai * x[u][k].w;
       }
     }
@@ -756,8 +784,8 @@ __global__ void __launch_bounds__(256) join_many_kernel(const Params p) {
   const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
   const int64_t orow = out_row(p, rec.first, rec.h, row);
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) *reinterpret_cast<uint2*>(p.out + orow * D + 32 * k + 4 * sub) = bf16x4(o[k], inv);
-  if (p.lse && sub == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+  for (int k = 0; k < D / 16; ++k) *reinterpret_cast<uint2*>(p.out + orow * D + 16 * k + 4 * part) = bf16x4(o[k], inv);
+  if (p.lse && part == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
 }
 
 template <int D>
@@ -784,7 +812,7 @@ cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  return launch_dependent(join_many_kernel<D>, dim3(grid * (kRows / 32)), 256, 0, stream, p);
+  return launch_dependent(join_many_kernel<D>, dim3(grid * (kRows / 64)), 256, 0, stream, p);
 }
 
 }  // namespace
