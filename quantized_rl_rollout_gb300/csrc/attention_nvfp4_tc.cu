@@ -33,12 +33,15 @@
 // A key tile of 256 rows takes 3800 cycles, of which the MMAs are 2048 (64 an
 // M128 N128 K16): a group's chain of scores (480 to reach the softmax), softmax (2000),
 // weights to the issuer (300) and its two MMAs (1024) is what bounds, the other
-// group's runs beside it.  19 x 64 tokens over 8128, 4 query heads a head of 128: 1090
-// TFLOP/s; a prompt of 4096 tokens (171 us) 805, with 8 us of start and 13 of join;
-// 4 x 300..700 tokens over 6000..10000 (5 query heads) 1030..1150.  Measured and
-// not taken: scores in two 64-column buffers (as fast: the MMAs read the queries
-// twice as often), the first half of a tile's weights handed over early (prompt
-// 183 us), the next codes in registers while one tile is converted (178).
+// group's runs beside it.  An item's start and end take 10000 more: query rows 5000,
+// output 4500.  19 x 64 tokens over 8128, 4 query heads a head of 128: 1085 TFLOP/s; a
+// prompt of 4096 tokens 880 (156 us, 8 of start and 13 of join among them), of 16384
+// 1230; 4 x 300..700 tokens over 6000..10000 (5 query heads) 1050..1150.  Measured
+// and not taken: scores in two 64-column buffers (as fast: the MMAs read the
+// queries twice as often); the first half of a tile's weights handed over early,
+// the next codes in registers while one tile is converted, query rows copied by
+// two warps of their own (prompt 4 to 9 % longer); 16 softmax warps, two a row
+// (24 %); a tile's maximum before its weights (20 %: the scores are read twice).
 #include "attention_nvfp4.cuh"
 #include "tc.cuh"
 
