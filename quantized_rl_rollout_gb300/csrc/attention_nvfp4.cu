@@ -804,16 +804,19 @@ cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
 bool any_few(int G) { return G <= kFewRows; }
 bool any_many(int64_t max_new, int G) { return max_new * G > kFewRows; }
 
-size_t few_ws_bytes(int D, int64_t items) {
-  return std::max(ws_bytes(D, kMaxSms * ctas_per_sm(D, 1) * kWarps, 8, items),
-                  ws_bytes(D, kMaxSms * ctas_per_sm(D, 4) * kWarps, 32, items));
+// Groups of 8 rows that this kernel is launched for.
+int row_groups(int64_t max_new, int G) { return max_new * G <= 8 ? 1 : max_new * G <= 16 ? 2 : 4; }
+
+size_t few_ws_bytes(int D, int64_t items, int64_t max_new, int G) {
+  const int nt = row_groups(max_new, G);
+  return any_few(G) ? ws_bytes(D, kMaxSms * ctas_per_sm(D, nt) * kWarps, 8 * nt, items) : 0;
 }
 
 }  // namespace
 
 size_t attention_nvfp4_ws_bytes(int D, int B, int Hq, int Hkv, int64_t max_new) {
   const int G = Hq / Hkv;
-  return few_ws_bytes(D, static_cast<int64_t>(B) * Hkv) + (any_many(max_new, G) ? attention_nvfp4_tc_ws_bytes(D) : 0);
+  return few_ws_bytes(D, static_cast<int64_t>(B) * Hkv, max_new, G) + (any_many(max_new, G) ? attention_nvfp4_tc_ws_bytes(D) : 0);
 }
 
 cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) {
@@ -822,8 +825,7 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int G = a.Hq / a.c.Hkv;
   if (any_few(G)) {
-    const int64_t rows = static_cast<int64_t>(a.max_new) * G;
-    const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4, grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(a.c.D, nt);
+    const int nt = row_groups(a.max_new, G), grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(a.c.D, nt);
     const cudaError_t e = a.c.D == 128 ? (nt == 1   ? launch<128, 1>(a, grid, stream)
                                           : nt == 2 ? launch<128, 2>(a, grid, stream)
                                                     : launch<128, 4>(a, grid, stream))
@@ -832,7 +834,9 @@ cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) 
                                                     : launch<64, 4>(a, grid, stream));
     if (e != cudaSuccess) return e;
   }
-  return any_many(a.max_new, G) ? launch_attention_nvfp4_tc(a, a.ws + few_ws_bytes(a.c.D, static_cast<int64_t>(a.c.B) * a.c.Hkv), any_few(G), stream) : cudaSuccess;
+  if (!any_many(a.max_new, G)) return cudaSuccess;
+  uint8_t* const ws = a.ws + few_ws_bytes(a.c.D, static_cast<int64_t>(a.c.B) * a.c.Hkv, a.max_new, G);
+  return launch_attention_nvfp4_tc(a, ws, any_few(G), stream);
 }
 
 }  // namespace qrr
