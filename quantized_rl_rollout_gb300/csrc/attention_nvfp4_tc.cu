@@ -486,6 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
               weights(x, f2, twice(-m), top, sum, y);
               const bool move = top * f > m + kRoom;
               if (!__any_sync(0xFFFFFFFFu, move)) break;
+              // the weights of the chunks before are read back below: a load of tensor
+              // memory is not ordered behind a store but by this wait
+              tmem_st_wait();
               // a new reference: scale what the row has so far, and form the
               // chunk's weights again
               const float m1 = move ? top * f - kLift : m, a = ex2(m - m1);
