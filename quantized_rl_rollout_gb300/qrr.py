@@ -550,10 +550,16 @@ class KvCacheNvfp4:
         return cls(codes[0], scales[0], codes[1], scales[1], page_table, k_gs, v_gs)
 
 
-def _for_stream(t, stream):
-    """``t``, allocated here, kept from being reused before ``stream`` (another than the current one, if given) is done."""
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
+def _on_stream(shape, dtype, device, stream, returned=True):
+    """A new tensor for a call on ``stream`` (None: the current one), from that stream's memory: a block of the current
+    stream's may still be in use by work queued there.  ``returned``: the caller may go on with it on the current stream."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
     return t
 
 
@@ -585,8 +591,7 @@ def _head_rows(x, heads, dim, name):
 def _result(given, shape, dtype, device, stream, name):
     """An output: the caller's tensor, checked, or a new one."""
     if given is None:
-        out = torch.empty(shape, dtype=dtype, device=device)
-        return out if stream is None else _for_stream(out, stream)
+        return _on_stream(shape, dtype, device, stream)
     if given.dtype is not dtype or not given.is_cuda or not given.is_contiguous() or given.shape != shape:
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {list(shape)}")
     return given
@@ -650,7 +655,7 @@ def attention_nvfp4(q, cache, pos, cu=None, max_new=None, scale=None, return_lse
         need = cache._workspace_bytes.get((hq, max_new))
         if need is None:  # it goes by the cache's shape and these two
             need = cache._workspace_bytes[hq, max_new] = max(attention_nvfp4_workspace_bytes(cache, t, hq, max_new), 256)
-        workspace = _result(None, (need,), torch.uint8, device, stream, "workspace")
+        workspace = _on_stream((need,), torch.uint8, device, stream, returned=False)
     _check(lib().qrr_attention_nvfp4(cache._addr, q.data_ptr(), t, ld_q, hq, cu, pos.data_ptr(), max_new,
                                      d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
                                      workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream)),

@@ -1,0 +1,101 @@
+"""Buffers that the binding makes for a call on another stream come from that stream's memory: a block of the current
+stream's could still be in use there.  Host only: the stream, the allocator and the library are stand-ins."""
+
+import contextlib
+
+import pytest
+import torch
+
+from quantized_rl_rollout_gb300 import qrr
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+class Tensor:
+    """What the binding looks at, of a CUDA tensor with one head of 64 values a row."""
+
+    is_cuda, device = True, "cuda:0"
+
+    def __init__(self, shape, dtype, under=None):
+        self.shape, self.dtype, self.under, self.recorded = torch.Size(shape), dtype, under, []
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return tuple(int(torch.Size(self.shape[i + 1:]).numel()) for i in range(len(self.shape)))
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return 0x10000
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+CURRENT, SIDE = Stream(11), Stream(22)
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """Every tensor that is allocated, with the stream that was current then."""
+    now, made = [CURRENT], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        now.append(s)
+        yield
+        now.pop()
+
+    def empty(*shape, dtype=None, device=None):
+        made.append(Tensor(shape[0] if len(shape) == 1 and not isinstance(shape[0], int) else shape, dtype, now[-1].cuda_stream))
+        return made[-1]
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 1000 if name.endswith("_bytes") else 0
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: now[-1].cuda_stream, raising=False)
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(qrr, "lib", lambda: Lib())
+    return made
+
+
+@pytest.fixture
+def cache(made):
+    u8 = [Tensor((4, 1, 16, n), torch.uint8) for n in (32, 4, 32, 4)]
+    return qrr.KvCacheNvfp4(*u8, Tensor((2, 2), torch.int32))
+
+
+POS, X = Tensor((2,), torch.int32), Tensor((2, 1, 64), torch.bfloat16)
+
+
+@pytest.mark.parametrize("stream", [SIDE, 22])
+def test_nvfp4_cache_calls(cache, made, stream):
+    got = qrr.attention_nvfp4(X, cache, POS, return_lse=True, stream=stream)
+    assert len(made) == 3 and [t.under for t in made] == [22] * 3  # out, lse, workspace
+    # what the caller gets may be used on their own stream as well
+    assert [t.recorded for t in got] == [[11]] * 2
+    del made[:]
+    got = qrr.kv_read_nvfp4(cache, POS, stream=stream)
+    assert [t.under for t in made] == [22] * 2 and [t.recorded for t in got] == [[11]] * 2
+
+
+@pytest.mark.parametrize("stream", [None, CURRENT, 11])
+def test_nvfp4_cache_calls_on_the_current_stream(cache, made, stream):
+    qrr.attention_nvfp4(X, cache, POS, return_lse=True, stream=stream)
+    qrr.kv_read_nvfp4(cache, POS, stream=stream)
+    assert len(made) == 5 and all(t.under == 11 and not t.recorded for t in made)

@@ -1,0 +1,46 @@
+"""Calls on a side stream beside work that is queued on the current one: each call's own buffers are its own."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def q():
+    from quantized_rl_rollout_gb300 import build, qrr
+
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    build.build()
+    qrr.lib()
+    return qrr
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_nvfp4_attention_and_read(q, handle):
+    """No synchronization between the calls; a prompt's attention takes long enough for the next to be queued behind it."""
+    n, page = 2048, 64
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    cache = q.KvCacheNvfp4.empty(n // page, 2, page, 128, torch.arange(n // page, dtype=torch.int32, device=DEV)[None])
+    kv = [torch.randn(n, 2, 128, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    x = [torch.randn(n, 16, 128, device=DEV).to(torch.bfloat16) for _ in range(2)]
+    pos, cu = i32([0]), i32([0, n])
+    q.kv_append_nvfp4(*kv, cache, pos, cu=cu)
+
+    def call(i, stream=None):
+        return q.attention_nvfp4(x[i], cache, pos, cu=cu, max_new=n, return_lse=True, stream=stream) + q.kv_read_nvfp4(
+            cache, pos, cu=cu, rows=n, stream=stream)
+
+    want = [call(0), call(1)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if handle else side
+    for _ in range(20):
+        a = [call(0) for _ in range(3)]
+        b = call(1, given)
+        c = call(0)
+        torch.cuda.synchronize()
+        for got, i in [(g, 0) for g in a] + [(b, 1), (c, 0)]:
+            assert all(torch.equal(y, z) for y, z in zip(got, want[i]))
+        del a, b, c, got
