@@ -162,8 +162,21 @@ def _need(t, dtype, name):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _workspace(nbytes: int, device):
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+def _on_stream(shape, dtype, device, stream, returned=True):
+    """A new tensor for a call on ``stream`` (None: the current one), from that stream's memory: a block of the current
+    stream's may still be in use by work queued there.  ``returned``: the caller may go on with it on the current stream."""
+    if stream is None or _stream(stream) == _stream(None):
+        return torch.empty(shape, dtype=dtype, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    with torch.cuda.stream(s):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _workspace(nbytes: int, device, stream):
+    return _on_stream((max(int(nbytes), 256),), torch.uint8, device, stream, returned=False)
 
 
 # ---------------------------------------------------------------------------
@@ -173,11 +186,11 @@ def quantize_nvfp4(W, codes=None, scales=None, tensor_scale=None, workspace=None
     _need(W, torch.bfloat16, "W")
     n, k = W.shape
     dev = W.device
-    codes = torch.empty(n, k // 2, dtype=torch.uint8, device=dev) if codes is None else codes
-    scales = torch.empty(n, k // 16, dtype=torch.uint8, device=dev) if scales is None else scales
-    tensor_scale = torch.empty(1, dtype=torch.float32, device=dev) if tensor_scale is None else tensor_scale
+    codes = _on_stream((n, k // 2), torch.uint8, dev, stream) if codes is None else codes
+    scales = _on_stream((n, k // 16), torch.uint8, dev, stream) if scales is None else scales
+    tensor_scale = _on_stream((1,), torch.float32, dev, stream) if tensor_scale is None else tensor_scale
     ws_bytes = lib().qrr_quantize_nvfp4_workspace_bytes()
-    workspace = _workspace(ws_bytes, dev) if workspace is None else workspace
+    workspace = _workspace(ws_bytes, dev, stream) if workspace is None else workspace
     _check(lib().qrr_quantize_nvfp4(_ptr(W), n, k, _ptr(codes), _ptr(scales), _ptr(tensor_scale), _ptr(workspace),
                                     workspace.numel(), _ptr(dev_status), _stream(stream)), "qrr_quantize_nvfp4")
     return codes, scales, tensor_scale
@@ -194,9 +207,9 @@ def linear_nvfp4_lora(x, codes, scales, tensor_scale, lora_A=None, lora_B=None, 
     m, k = x.shape
     n = codes.shape[0]
     r = 0 if lora_A is None or lora_B is None else int(lora_A.shape[0])
-    y = torch.empty(m, n, dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = _on_stream((m, n), torch.bfloat16, x.device, stream) if y is None else y
     if workspace is None:
-        workspace = _workspace(linear_nvfp4_lora_workspace_bytes(m, n, k, r), x.device)
+        workspace = _workspace(linear_nvfp4_lora_workspace_bytes(m, n, k, r), x.device, stream)
     _check(lib().qrr_linear_nvfp4_lora(_ptr(x), m, k, _ptr(codes), _ptr(scales), _ptr(tensor_scale), n,
                                        _ptr(lora_A), _ptr(lora_B), r, float(alpha), _ptr(y), _ptr(workspace),
                                        workspace.numel(), _ptr(dev_status), _stream(stream)),
@@ -211,14 +224,14 @@ def linear_nvfp4_lora_noalloc(x, codes, scales, tensor_scale, lora_A=None, lora_
     m, k = x.shape
     n = codes.shape[0]
     r = 0 if lora_A is None or lora_B is None else int(lora_A.shape[0])
-    y = torch.empty(m, n, dtype=torch.bfloat16, device=x.device) if y is None else y
+    y = _on_stream((m, n), torch.bfloat16, x.device, stream) if y is None else y
     _check(lib().qrr_linear_nvfp4_lora_noalloc(_ptr(x), m, k, _ptr(codes), _ptr(scales), _ptr(tensor_scale), n,
                                                _ptr(lora_A), _ptr(lora_B), r, float(alpha), _ptr(y),
                                                _ptr(dev_status), _stream(stream)), "qrr_linear_nvfp4_lora_noalloc")
     return y
 
 
-def _linear_descs(layers):
+def _linear_descs(layers, stream=None):
     descs = (LinearDesc * len(layers))()
     m = None
     for i, d in enumerate(layers):
@@ -231,7 +244,7 @@ def _linear_descs(layers):
         elif x.shape[0] != m:
             raise ValueError("every layer of a grouped call has the same token count")
         if d.get("y") is None:
-            d["y"] = torch.empty(m, codes.shape[0], dtype=torch.bfloat16, device=x.device)
+            d["y"] = _on_stream((m, codes.shape[0]), torch.bfloat16, x.device, stream)
         descs[i] = LinearDesc(_ptr(x), codes.shape[0], x.shape[1], _ptr(codes), _ptr(scales), _ptr(ts), _ptr(a),
                               _ptr(b), r, float(d.get("alpha", 0.0)), _ptr(d["y"]))
     return descs, (m or 0)
@@ -249,10 +262,10 @@ def linear_nvfp4_lora_grouped(layers, workspace=None, dev_status=None, stream=No
     optionally lora_A, lora_B, alpha, y (allocated when absent).  Returns the
     list of outputs.
     """
-    descs, m = _linear_descs(layers)
+    descs, m = _linear_descs(layers, stream)
     if workspace is None:
         nbytes = lib().qrr_linear_nvfp4_lora_grouped_workspace_bytes(descs, len(layers), m)
-        workspace = _workspace(nbytes, layers[0]["x"].device)
+        workspace = _workspace(nbytes, layers[0]["x"].device, stream)
     _check(lib().qrr_linear_nvfp4_lora_grouped(descs, len(layers), m, _ptr(workspace), workspace.numel(),
                                                _ptr(dev_status), _stream(stream)), "qrr_linear_nvfp4_lora_grouped")
     return [d["y"] for d in layers]
@@ -271,7 +284,7 @@ class GroupedLinear:
         self.descs, self.m = _linear_descs(layers)
         nbytes = int(lib().qrr_linear_nvfp4_lora_grouped_workspace_bytes(self.descs, len(layers), self.m))
         if workspace is None:
-            workspace = _workspace(nbytes, layers[0]["x"].device)
+            workspace = _workspace(nbytes, layers[0]["x"].device, None)
         elif workspace.numel() < nbytes:
             raise ValueError(f"workspace of {workspace.numel()} bytes, the call needs {nbytes}")
         self.workspace = workspace
@@ -287,8 +300,8 @@ class GroupedLinear:
 def quantize_fp8_w128x128(W, mode=SCALE_FP32, q=None, scales=None, dev_status=None, stream=None):
     _need(W, torch.bfloat16, "W")
     n, k = W.shape
-    q = torch.empty(n, k, dtype=torch.uint8, device=W.device) if q is None else q
-    scales = torch.empty((n + 127) // 128, k // 128, dtype=torch.float32, device=W.device) if scales is None else scales
+    q = _on_stream((n, k), torch.uint8, W.device, stream) if q is None else q
+    scales = _on_stream(((n + 127) // 128, k // 128), torch.float32, W.device, stream) if scales is None else scales
     _check(lib().qrr_quantize_fp8_w128x128(_ptr(W), n, k, _ptr(q), _ptr(scales), int(mode), _ptr(dev_status),
                                            _stream(stream)), "qrr_quantize_fp8_w128x128")
     return q, scales
@@ -297,8 +310,8 @@ def quantize_fp8_w128x128(W, mode=SCALE_FP32, q=None, scales=None, dev_status=No
 def quantize_fp8_a1x128(x, mode=SCALE_FP32, q=None, scales=None, dev_status=None, stream=None):
     _need(x, torch.bfloat16, "x")
     m, k = x.shape
-    q = torch.empty(m, k, dtype=torch.uint8, device=x.device) if q is None else q
-    scales = torch.empty(m, k // 128, dtype=torch.float32, device=x.device) if scales is None else scales
+    q = _on_stream((m, k), torch.uint8, x.device, stream) if q is None else q
+    scales = _on_stream((m, k // 128), torch.float32, x.device, stream) if scales is None else scales
     _check(lib().qrr_quantize_fp8_a1x128(_ptr(x), m, k, _ptr(q), _ptr(scales), int(mode), _ptr(dev_status),
                                          _stream(stream)), "qrr_quantize_fp8_a1x128")
     return q, scales
@@ -307,7 +320,7 @@ def quantize_fp8_a1x128(x, mode=SCALE_FP32, q=None, scales=None, dev_status=None
 def gemm_fp8_blockwise(qa, sa, qw, sw, mode=SCALE_FP32, y=None, dev_status=None, stream=None):
     m, k = qa.shape
     n = qw.shape[0]
-    y = torch.empty(m, n, dtype=torch.bfloat16, device=qa.device) if y is None else y
+    y = _on_stream((m, n), torch.bfloat16, qa.device, stream) if y is None else y
     _check(lib().qrr_gemm_fp8_blockwise(_ptr(qa), _ptr(sa), _ptr(qw), _ptr(sw), m, n, k, _ptr(y), int(mode),
                                         _ptr(dev_status), _stream(stream)), "qrr_gemm_fp8_blockwise")
     return y
@@ -333,7 +346,7 @@ def requantize_weights(weights, outputs, fmt=FORMAT_NVFP4, mode=SCALE_FP32, work
     descs, count = _weight_descs(weights, outputs, fmt)
     dev = weights[0].device if count else torch.device("cuda")
     if workspace is None:
-        workspace = _workspace(lib().qrr_requantize_workspace_bytes(count), dev)
+        workspace = _workspace(lib().qrr_requantize_workspace_bytes(count), dev, stream)
     _check(lib().qrr_requantize_weights(descs, count, int(fmt), int(mode), _ptr(workspace), workspace.numel(),
                                         _ptr(dev_status), _stream(stream)), "qrr_requantize_weights")
     return outputs
@@ -345,7 +358,7 @@ def requantize_weights_aqn(weights, outputs, sigma, seed, step, fmt=FORMAT_NVFP4
     descs, count = _weight_descs(weights, outputs, fmt)
     dev = weights[0].device if count else torch.device("cuda")
     if workspace is None:
-        workspace = _workspace(lib().qrr_requantize_workspace_bytes(count), dev)
+        workspace = _workspace(lib().qrr_requantize_workspace_bytes(count), dev, stream)
     _check(lib().qrr_requantize_weights_aqn(descs, count, int(fmt), int(mode), float(sigma), int(seed), int(step),
                                             _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)),
            "qrr_requantize_weights_aqn")
@@ -357,7 +370,7 @@ def aqn_sigma(step, steps, sigma_start, sigma_end) -> float:
 
 
 def aqn_noise_probe(n, seed, tensor, step, start=0, out=None, stream=None):
-    out = torch.empty(n, dtype=torch.float32, device="cuda") if out is None else out
+    out = _on_stream((n,), torch.float32, "cuda", stream) if out is None else out
     _check(lib().qrr_aqn_noise_probe(_ptr(out), int(n), int(start), int(seed), int(tensor), int(step),
                                      _stream(stream)), "qrr_aqn_noise_probe")
     return out
@@ -365,7 +378,7 @@ def aqn_noise_probe(n, seed, tensor, step, start=0, out=None, stream=None):
 
 def round_probe(values, fmt, out=None, stream=None):
     _need(values, torch.float32, "values")
-    out = torch.empty(values.numel(), dtype=torch.uint8, device=values.device) if out is None else out
+    out = _on_stream((values.numel(),), torch.uint8, values.device, stream) if out is None else out
     _check(lib().qrr_round_probe(_ptr(values), values.numel(), int(fmt), _ptr(out), _stream(stream)),
            "qrr_round_probe")
     return out
@@ -438,10 +451,10 @@ def token_logprobs_is(logits, tokens, rollout_logp=None, cap=0.0, logp=None, w=N
     _need(logits, torch.bfloat16, "logits")
     _need(tokens, torch.int32, "tokens")
     t, v = logits.shape
-    logp = torch.empty(t, dtype=torch.float32, device=logits.device) if logp is None else logp
+    logp = _on_stream((t,), torch.float32, logits.device, stream) if logp is None else logp
     if rollout_logp is not None:
         _need(rollout_logp, torch.float32, "rollout_logp")
-        w = torch.empty(t, dtype=torch.float32, device=logits.device) if w is None else w
+        w = _on_stream((t,), torch.float32, logits.device, stream) if w is None else w
     _check(lib().qrr_token_logprobs_is(_ptr(logits), t, v, _ptr(tokens), _ptr(rollout_logp), float(cap), _ptr(logp),
                                        _ptr(w) if rollout_logp is not None else None, _ptr(dev_status),
                                        _stream(stream)), "qrr_token_logprobs_is")
@@ -461,13 +474,13 @@ def lora_backward_nvfp4(dy, x, codes, scales, tensor_scale, lora_A=None, lora_B=
     k = codes.shape[1] * 2
     r = 0 if lora_A is None or lora_B is None else int(lora_A.shape[0])
     dev = dy.device
-    dx = torch.empty(m, k, dtype=torch.bfloat16, device=dev) if dx is None else dx
+    dx = _on_stream((m, k), torch.bfloat16, dev, stream) if dx is None else dx
     if r:
         _need(x, torch.bfloat16, "x")
-        dA = torch.empty(r, k, dtype=torch.float32, device=dev) if dA is None else dA
-        dB = torch.empty(n, r, dtype=torch.float32, device=dev) if dB is None else dB
+        dA = _on_stream((r, k), torch.float32, dev, stream) if dA is None else dA
+        dB = _on_stream((n, r), torch.float32, dev, stream) if dB is None else dB
     if workspace is None:
-        workspace = _workspace(lora_backward_workspace_bytes(m, n, k, r), dev)
+        workspace = _workspace(lora_backward_workspace_bytes(m, n, k, r), dev, stream)
     _check(lib().qrr_lora_backward_nvfp4(_ptr(dy), m, n, _ptr(x), k, _ptr(codes), _ptr(scales), _ptr(tensor_scale),
                                          _ptr(lora_A), _ptr(lora_B), r, float(alpha), _ptr(dx),
                                          _ptr(dA) if r else None, _ptr(dB) if r else None, _ptr(workspace),
@@ -496,9 +509,9 @@ def attention_decode_fp8(q, k_cache, k_scales, v_cache, v_scales, lens, out=None
     _need(lens, torch.int32, "lens")
     b, hq, _ = q.shape
     hkv, lmax = k_cache.shape[1], k_cache.shape[2]
-    out = torch.empty_like(q) if out is None else out
+    out = _on_stream(q.shape, q.dtype, q.device, stream) if out is None else out
     if workspace is None:
-        workspace = _workspace(lib().qrr_attention_decode_fp8_workspace_bytes(b, hq, lmax), q.device)
+        workspace = _workspace(lib().qrr_attention_decode_fp8_workspace_bytes(b, hq, lmax), q.device, stream)
     _check(lib().qrr_attention_decode_fp8(_ptr(q), b, hq, hkv, _ptr(k_cache), _ptr(k_scales), _ptr(v_cache),
                                           _ptr(v_scales), _ptr(lens), lmax, _ptr(out), _ptr(workspace),
                                           workspace.numel(), _ptr(dev_status), _stream(stream)),
@@ -548,19 +561,6 @@ class KvCacheNvfp4:
         codes = [torch.zeros(pages, hkv, page, dim // 2, dtype=torch.uint8, device=dev) for _ in range(2)]
         scales = [torch.zeros(pages, hkv, page, dim // 16, dtype=torch.uint8, device=dev) for _ in range(2)]
         return cls(codes[0], scales[0], codes[1], scales[1], page_table, k_gs, v_gs)
-
-
-def _on_stream(shape, dtype, device, stream, returned=True):
-    """A new tensor for a call on ``stream`` (None: the current one), from that stream's memory: a block of the current
-    stream's may still be in use by work queued there.  ``returned``: the caller may go on with it on the current stream."""
-    if stream is None or _stream(stream) == _stream(None):
-        return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    with torch.cuda.stream(s):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        t.record_stream(torch.cuda.current_stream())
-    return t
 
 
 def _kv_rows(cache, pos, cu, t):

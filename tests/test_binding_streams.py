@@ -99,3 +99,38 @@ def test_nvfp4_cache_calls_on_the_current_stream(cache, made, stream):
     qrr.attention_nvfp4(X, cache, POS, return_lse=True, stream=stream)
     qrr.kv_read_nvfp4(cache, POS, stream=stream)
     assert len(made) == 5 and all(t.under == 11 and not t.recorded for t in made)
+
+
+def _bf16(*shape):
+    return Tensor(shape, torch.bfloat16)
+
+
+W = [Tensor((128, 32), torch.uint8), Tensor((128, 4), torch.uint8), Tensor((1,), torch.float32)]
+CALLS = {
+    "quantize_nvfp4": (4, lambda s: qrr.quantize_nvfp4(_bf16(128, 64), stream=s)),
+    "linear": (2, lambda s: qrr.linear_nvfp4_lora(_bf16(2, 64), *W, stream=s)),
+    "linear_noalloc": (1, lambda s: qrr.linear_nvfp4_lora_noalloc(_bf16(2, 64), *W, stream=s)),
+    "grouped": (2, lambda s: qrr.linear_nvfp4_lora_grouped([dict(x=_bf16(2, 64), codes=W[0], scales=W[1], tensor_scale=W[2])], stream=s)),
+    "fp8 weight": (2, lambda s: qrr.quantize_fp8_w128x128(_bf16(128, 128), stream=s)),
+    "fp8 activation": (2, lambda s: qrr.quantize_fp8_a1x128(_bf16(2, 128), stream=s)),
+    "fp8 gemm": (1, lambda s: qrr.gemm_fp8_blockwise(Tensor((2, 128), torch.uint8), Tensor((2, 1), torch.float32), Tensor((128, 128), torch.uint8),
+                                                    Tensor((1, 1), torch.float32), stream=s)),
+    "requantize": (1, lambda s: qrr.requantize_weights([_bf16(128, 64)], [W], stream=s)),
+    "requantize aqn": (1, lambda s: qrr.requantize_weights_aqn([_bf16(128, 64)], [W], 0.1, 1, 2, stream=s)),
+    "aqn probe": (1, lambda s: qrr.aqn_noise_probe(8, 1, 0, 0, stream=s)),
+    "round probe": (1, lambda s: qrr.round_probe(Tensor((8,), torch.float32), 0, stream=s)),
+    "logprobs": (2, lambda s: qrr.token_logprobs_is(_bf16(2, 64), Tensor((2,), torch.int32), Tensor((2,), torch.float32), stream=s)),
+    "lora backward": (4, lambda s: qrr.lora_backward_nvfp4(_bf16(2, 128), _bf16(2, 64), *W, _bf16(8, 64), _bf16(128, 8), stream=s)),
+    "fp8 attention": (2, lambda s: qrr.attention_decode_fp8(_bf16(2, 4, 128), Tensor((2, 4, 16, 128), torch.uint8), W[2], W[0], W[2],
+                                                            Tensor((2,), torch.int32), stream=s)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_other_calls(made, monkeypatch, name):
+    monkeypatch.setattr(torch, "empty_like", lambda t: torch.empty(*t.shape, dtype=t.dtype))
+    count, call = CALLS[name]
+    for stream, under in ((SIDE, 22), (22, 22), (None, 11), (CURRENT, 11)):
+        del made[:]
+        call(stream)
+        assert [t.under for t in made] == [under] * count

@@ -44,3 +44,30 @@ def test_nvfp4_attention_and_read(q, handle):
         for got, i in [(g, 0) for g in a] + [(b, 1), (c, 0)]:
             assert all(torch.equal(y, z) for y, z in zip(got, want[i]))
         del a, b, c, got
+
+
+def test_linear_and_fp8_attention(q):
+    """The linear (prefill and decode) and the FP8 cache's attention."""
+    from quantized_rl_rollout_gb300 import inputs
+
+    codes, scales, ts = q.quantize_nvfp4(inputs.weight(2048, 2048, 1, device=DEV))
+    xs = [[inputs.activations(m, 2048, 2 + i, device=DEV) for i in range(2)] for m in (4, 1024)]
+    b, lmax = 64, 2048
+    kq, ks = q.quantize_fp8_a1x128(inputs.activations(b * 2 * lmax, 128, 5, device=DEV))
+    kv = (kq.view(b, 2, lmax, 128), ks.view(b, 2, lmax)) * 2
+    qs = [inputs.activations(b * 8, 128, 6 + i, device=DEV).view(b, 8, 128) for i in range(2)]
+    lens = torch.full((b,), lmax, dtype=torch.int32, device=DEV)
+
+    def call(i, stream=None):
+        return [q.linear_nvfp4_lora(x[i], codes, scales, ts, stream=stream) for x in xs] + [
+            q.attention_decode_fp8(qs[i], *kv, lens, stream=stream)]
+
+    want = [call(0), call(1)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        got = [(call(0), 0), (call(0), 0), (call(1, side), 1), (call(0), 0)]
+        torch.cuda.synchronize()
+        for g, i in got:
+            assert all(torch.equal(y, z) for y, z in zip(g, want[i]))
+        del got, g
