@@ -22,7 +22,9 @@ constexpr int kFewRows = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1.0e30f;  // reference of a row that has seen nothing
-constexpr float kLift = 7.0f, kRoom = 15.0f;  // the reference lies kLift under the largest score and moves above kRoom
+// a new reference lies kLift under the largest score (many rows: kLift to kLift + 1,
+// a whole number) and moves when a score exceeds it by kRoom
+constexpr float kLift = 7.0f, kRoom = 15.0f;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -28,7 +28,8 @@
 //
 // A row's weights are formed with the running reference in one pass over its
 // scores; only when a score exceeds it by kRoom (and on a row's first tile) the
-// pass is repeated with a new one and the row's output so far is scaled.
+// pass is repeated with a new one (a whole number) and what the row has so far
+// is scaled.
 //
 // A key tile of 256 rows takes 3800 cycles, of which the MMAs are 2048 (64 an
 // M128 N128 K16): a group's chain of scores (480 to reach the softmax), softmax (2000),
@@ -489,19 +490,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
               // the weights of the chunks before are read back below: a load of tensor
               // memory is not ordered behind a store but by this wait
               tmem_st_wait();
-              // a new reference: scale what the row has so far, and form the
-              // chunk's weights again
-              const float m1 = move ? top * f - kLift : m, a = ex2(m - m1);
+              // A new reference: scale what the row has so far, and form the chunk's weights
+              // again.  References are whole numbers, so the factor is a power of two and
+              // a stored weight is rounded again only below f16's normal range (by little
+              // more than 2^-25, 2^-32 of the row's largest weight).  f16 has powers of
+              // two down to 2^-24: smaller factors come as a product.
+              const float m1 = move ? floorf(top * f) - kLift : m, by = m - m1;
+              const float a = by > -127.0f ? __uint_as_float(static_cast<uint32_t>(127 + static_cast<int>(by)) << 23) : 0.0f;
               m = m1;
               l *= a;
-              const uint32_t a2 = f16x2(a, a);
+              const float a_hi = fmaxf(a, 0x1p-24f), a_lo = a < 0x1p-24f ? a * 0x1p24f : 1.0f;
+              const uint32_t hi2 = f16x2(a_hi, a_hi), lo2 = f16x2(a_lo, a_lo);
 #pragma unroll 1
               for (int k = 0; k < c; ++k) {
                 uint32_t z[16];
                 tmem_ld16(ts + 16 * k, z);
                 tmem_ld_wait16(z);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = hmul2(z[i], a2);
+                for (int i = 0; i < 16; ++i) z[i] = hmul2(hmul2(z[i], hi2), lo2);
                 tmem_st16(ts + 16 * k, z);
               }
               if (j > w.t0)
