@@ -15,10 +15,6 @@ namespace qrr {
 namespace attn4 {
 
 constexpr int kMaxSms = 160;       // of the workspace's size; grids are capped to it
-// A sequence with at most this many rows a KV head takes the first kernel: four
-// groups of 8 rows are what a lane's registers hold.  16 sequences over 2250
-// tokens, 17..32 rows: 42 us with it, 50 with the other.
-constexpr int kFewRows = 32;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNone = -1.0e30f;  // reference of a row that has seen nothing
@@ -85,12 +81,6 @@ struct Params {
   Record* rec;
   float *pm, *pl, *po;  // [piece][row], [piece][row], [piece][row][D]
   int32_t* status;
-};
-
-// A sequence as the kernels see it: its rows, the position of the first, the
-// last visible position of the last (-1: none).
-struct Seq {
-  int first, n, pos, last;
 };
 
 __device__ __forceinline__ Seq seq_of(const Params& p, int b) {

@@ -49,18 +49,13 @@
 namespace qrr {
 
 using namespace attn4;
+using namespace attn4::many;
 
 namespace {
 
 constexpr int kThreads = 14 * 32;
-constexpr int kRows = 256;  // rows of an item
-constexpr int kTok = 128;   // tokens of a key tile
 constexpr int kMinTiles = 4;  // key tiles of a range
-// Key tiles that an item's start and end cost (about 10000 cycles beside 3800 a
-// tile).  A prompt of 4096 tokens with 2, 3, 4: 158, 156, 161 us; of 64 tokens,
-// whose items then fit a range of kMinTiles: 23, 17, 17.
-constexpr int kItemCost = 3;
-constexpr int kSeqs = 1024;   // sequences whose tile counts are kept in shared memory
+constexpr int kSeqs = 1024;   // sequences whose counts are kept in shared memory
 constexpr uint32_t kTmemCols = 512;
 
 template <int D>
@@ -75,7 +70,7 @@ struct Smem {
   uint32_t tmem;
   int abort;
   int64_t total;
-  int32_t seq_widths[kSeqs];
+  int32_t seq_widths[kSeqs];  // -1: above 32 bits
   int64_t part[kThreads / 32];
 };
 
@@ -97,29 +92,13 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-// Items of a sequence: row tiles of 256 (none if it has few rows), and the key
-// tiles of one (at least 1).
-__device__ __forceinline__ int row_tiles(const Params& p, const Seq& s) {
-  const int64_t rows = static_cast<int64_t>(s.n) * p.G;
-  return rows <= kFewRows ? 0 : static_cast<int>((rows + kRows - 1) / kRows);
-}
-__device__ __forceinline__ int last_seen(const Params& p, const Seq& s, int qt) {
-  return min(s.pos + p.byG.div(min((qt + 1) * kRows, s.n * p.G) - 1), s.last);
-}
-__device__ __forceinline__ int key_tiles(const Params& p, const Seq& s, int qt) {
-  return max(1, (last_seen(p, s, qt) + kTok) / kTok);
-}
-
-// What an item counts for.
-__device__ __forceinline__ int width(const Params& p, const Seq& s, int qt) { return key_tiles(p, s, qt) + kItemCost; }
-
 // What one KV head of sequence b counts for over all its row tiles, by a warp.
-__device__ __forceinline__ int seq_width(const Params& p, int b, int lane) {
-  const Seq s = seq_of(p, b);
-  const int qts = row_tiles(p, s);
-  int sum = 0;
-  for (int qt = lane; qt < qts; qt += 32) sum += width(p, s, qt);
-  return __reduce_add_sync(0xFFFFFFFFu, sum);
+__device__ __forceinline__ int64_t seq_width(const Params& p, int b, int lane) {
+  const int64_t sum = lane_width(p.byG, seq_of(p, b), lane);
+  // a lane's sum is below 2^41 (2^17 row tiles of 2^23 key tiles): 26 bits and the rest
+  const uint32_t lo = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(sum) & 0x3FFFFFFu);
+  const uint32_t hi = __reduce_add_sync(0xFFFFFFFFu, static_cast<uint32_t>(sum >> 26));
+  return (static_cast<int64_t>(hi) << 26) + lo;
 }
 
 // The walk over a range's pieces of items; every thread of the CTA makes it.
@@ -130,7 +109,7 @@ struct Walk {
   int counts;                // what it takes of the range
   int64_t left;              // of the range, from t0 on
   __device__ __forceinline__ void piece(const Params& p) {
-    tiles = key_tiles(p, s, qt);
+    tiles = key_tiles(p.byG, s, qt);
     counts = static_cast<int>(min(static_cast<int64_t>(tiles + kItemCost - t0), left));
     t1 = min(t0 + counts, tiles);
   }
@@ -139,13 +118,13 @@ struct Walk {
     b = b_;
     left = left_;
     s = seq_of(p, b);
-    qts = row_tiles(p, s);
+    qts = row_tiles(p.byG, s);
     const int lane = threadIdx.x & 31;
     const int64_t per = seq_width(p, b, lane);  // of one head
     h = static_cast<int>(off / per);
-    int rest = static_cast<int>(off - h * per);
+    int64_t rest = off - h * per;
     for (qt = 0;; qt += 32) {  // 32 row tiles at a time
-      const int own = qt + lane < qts ? width(p, s, qt + lane) : 0;
+      const int own = qt + lane < qts ? width(p.byG, s, qt + lane) : 0;
       int incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -166,7 +145,7 @@ struct Walk {
         break;
       }
     }
-    t0 = rest;
+    t0 = static_cast<int>(rest);
     piece(p);
     return t0 < tiles || next(p);
   }
@@ -181,7 +160,7 @@ struct Walk {
         do {
           if (++b >= p.c.B) return false;
           s = seq_of(p, b);
-          qts = row_tiles(p, s);
+          qts = row_tiles(p.byG, s);
         } while (qts == 0);
       }
     }
@@ -315,8 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
   const int B = p.c.B;
   int64_t mine = 0;
   for (int b = warp; b < B; b += kThreads / 32) {
-    const int n = seq_width(p, b, lane);
-    if (lane == 0 && b < kSeqs) sh.seq_widths[b] = n;
+    const int64_t n = seq_width(p, b, lane);
+    if (lane == 0 && b < kSeqs) sh.seq_widths[b] = n <= INT32_MAX ? static_cast<int>(n) : -1;
     mine += n;
   }
   if (lane == 0) sh.part[warp] = mine;
@@ -356,14 +335,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     int64_t off = begin;
     int found = -1;
     for (int b0 = 0; b0 < B && found < 0; b0 += 32) {
-      int n = 0;
-      if (b0 + 32 <= kSeqs) n = b0 + lane < B ? sh.seq_widths[b0 + lane] : 0;
-      else
-        for (int i = 0; i < 32 && b0 + i < B; ++i) {
-          const int x = seq_width(p, b0 + i, lane);
-          if (lane == i) n = x;
-        }
-      const int64_t own = static_cast<int64_t>(n) * p.c.Hkv;
+      const bool in_b = b0 + lane < B, kept = b0 + 32 <= kSeqs;
+      int64_t n = kept && in_b ? sh.seq_widths[b0 + lane] : 0;
+      for (uint32_t todo = __ballot_sync(0xFFFFFFFFu, kept ? n < 0 : in_b); todo; todo &= todo - 1) {
+        const int i = __ffs(static_cast<int>(todo)) - 1;
+        const int64_t x = seq_width(p, b0 + i, lane);
+        if (lane == i) n = x;
+      }
+      const int64_t own = n * p.c.Hkv;
       int64_t incl = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -616,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
       return true;
     };
     do {
-      const int last = last_seen(p, w.s, w.qt);
+      const int last = last_seen(p.byG, w.s, w.qt);
       for (int j = w.t0; j < w.t1 && ok; ++j, ++use) {
         const int st = use & 1, live = last + 1 - kTok * j;
         ok = half(sh.k[st], &sh.k_empty[st], &sh.k_full[st], live) && half(sh.v[st], &sh.v_empty[st], &sh.v_full[st], live);
@@ -628,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     int slot = 0, n = 0;
     bool ok = true;
     do {
-      const int last = last_seen(p, w.s, w.qt);
+      const int last = last_seen(p.byG, w.s, w.qt);
       const int32_t* table = p.c.table + static_cast<int64_t>(w.b) * p.c.max_pages;
       for (int j = w.t0; j < w.t1 && ok; ++j) {
         const int tok = kTok * j + lane * run;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "attention_nvfp4_items.cuh"
 #include "common.cuh"
 
 namespace qrr {
@@ -21,23 +22,6 @@ struct KvNvfp4 {
   int num_pages, Hkv, page_shift, D, B, max_pages;
   __host__ __device__ int64_t capacity() const { return static_cast<int64_t>(max_pages) << page_shift; }
 };
-
-// x / d for 0 <= x < 2^31 by a multiplication (T. Granlund, P. Montgomery,
-// "Division by invariant integers using multiplication", PLDI 1994).
-struct FastDiv {
-  uint32_t d, mul, shift;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t d_) : d(d_), mul(0), shift(0) {
-    while ((1ull << shift) < d) ++shift;
-    mul = static_cast<uint32_t>((((1ull << shift) - d) << 32) / d + 1);
-  }
-  __device__ __forceinline__ int div(int x) const {
-    return static_cast<int>((__umulhi(mul, static_cast<uint32_t>(x)) + static_cast<uint32_t>(x)) >> shift);
-  }
-  __device__ __forceinline__ int mod(int x) const { return x - div(x) * static_cast<int>(d); }
-};
-
-constexpr int kMaxTokens = 1 << 30;  // rows of a call, and positions of a sequence
 
 // A call's rows: sequence b brings rows cu[b] .. cu[b + 1] - 1 (row b alone
 // where cu is null), row cu[b] + i at position pos[b] + i.
