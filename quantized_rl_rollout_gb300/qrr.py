@@ -564,6 +564,8 @@ class KvCacheNvfp4:
 
 
 def _kv_rows(cache, pos, cu, t):
+    """Address of ``cu`` (None without).  The caller keeps the tensor to the end of its call: it may be a temporary, whose
+    memory a buffer of the call would take."""
     if pos.dtype is not torch.int32 or not pos.is_cuda or not pos.is_contiguous() or pos.numel() != cache.batch:
         raise ValueError(f"pos must be a contiguous CUDA int32 tensor of {cache.batch} values")
     if cu is None:
@@ -605,8 +607,8 @@ def kv_append_nvfp4(k_new, v_new, cache, pos, cu=None, dev_status=None, stream=N
     t = k_new.shape[0]
     if v_new.shape[0] != t:
         raise ValueError("k_new and v_new must have the same rows")
-    cu = _kv_rows(cache, pos, cu, t)
-    _check(lib().qrr_kv_append_nvfp4(cache._addr, k_new.data_ptr(), v_new.data_ptr(), t, ld_k, ld_v, cu, pos.data_ptr(),
+    cu_ptr = _kv_rows(cache, pos, cu, t)
+    _check(lib().qrr_kv_append_nvfp4(cache._addr, k_new.data_ptr(), v_new.data_ptr(), t, ld_k, ld_v, cu_ptr, pos.data_ptr(),
                                      _ptr(dev_status), _stream(stream)), "qrr_kv_append_nvfp4")
 
 
@@ -617,11 +619,11 @@ def kv_read_nvfp4(cache, pos, cu=None, rows=None, k=None, v=None, dev_status=Non
         if cu is not None and k is None:
             raise ValueError("rows is needed with cu")
         rows = cache.batch if k is None else k.shape[0]
-    cu = _kv_rows(cache, pos, cu, rows)
+    cu_ptr = _kv_rows(cache, pos, cu, rows)
     shape = (rows, cache.hkv, cache.dim)
     k = _result(k, shape, torch.bfloat16, cache.device, stream, "k")
     v = _result(v, shape, torch.bfloat16, cache.device, stream, "v")
-    _check(lib().qrr_kv_read_nvfp4(cache._addr, rows, cu, pos.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(dev_status),
+    _check(lib().qrr_kv_read_nvfp4(cache._addr, rows, cu_ptr, pos.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(dev_status),
                                    _stream(stream)), "qrr_kv_read_nvfp4")
     return k, v
 
@@ -646,7 +648,7 @@ def attention_nvfp4(q, cache, pos, cu=None, max_new=None, scale=None, return_lse
         if cu is not None:
             raise ValueError("max_new is needed with cu")
         max_new = 1
-    cu = _kv_rows(cache, pos, cu, t)
+    cu_ptr = _kv_rows(cache, pos, cu, t)
     device = cache.device
     out = _result(out, shape, torch.bfloat16, device, stream, "out")
     if return_lse or lse is not None:
@@ -656,7 +658,7 @@ def attention_nvfp4(q, cache, pos, cu=None, max_new=None, scale=None, return_lse
         if need is None:  # it goes by the cache's shape and these two
             need = cache._workspace_bytes[hq, max_new] = max(attention_nvfp4_workspace_bytes(cache, t, hq, max_new), 256)
         workspace = _on_stream((need,), torch.uint8, device, stream, returned=False)
-    _check(lib().qrr_attention_nvfp4(cache._addr, q.data_ptr(), t, ld_q, hq, cu, pos.data_ptr(), max_new,
+    _check(lib().qrr_attention_nvfp4(cache._addr, q.data_ptr(), t, ld_q, hq, cu_ptr, pos.data_ptr(), max_new,
                                      d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
                                      workspace.data_ptr(), workspace.numel(), _ptr(dev_status), _stream(stream)),
            "qrr_attention_nvfp4")

@@ -2,6 +2,7 @@
 stream's could still be in use there.  Host only: the stream, the allocator and the library are stand-ins."""
 
 import contextlib
+import weakref
 
 import pytest
 import torch
@@ -134,3 +135,38 @@ def test_other_calls(made, monkeypatch, name):
         del made[:]
         call(stream)
         assert [t.under for t in made] == [under] * count
+
+
+NVFP4_CALLS = {
+    "qrr_kv_append_nvfp4": lambda cache, make: qrr.kv_append_nvfp4(make(X), make(X), cache, make(POS), cu=make(CU), dev_status=make(ST)),
+    "qrr_kv_read_nvfp4": lambda cache, make: qrr.kv_read_nvfp4(cache, make(POS), cu=make(CU), rows=2, dev_status=make(ST)),
+    "qrr_attention_nvfp4": lambda cache, make: qrr.attention_nvfp4(make(X), cache, make(POS), cu=make(CU), max_new=2, return_lse=True,
+                                                                   dev_status=make(ST)),
+}
+CU, ST = Tensor((3,), torch.int32), Tensor((1,), torch.int32)
+
+
+@pytest.mark.parametrize("name", NVFP4_CALLS)
+def test_arguments_live_until_the_launch(cache, made, monkeypatch, name):
+    """Tensors that only the call holds (made in its argument list) keep their memory until it has launched: the call's
+    own buffers would be put there otherwise, and written while the offsets are read."""
+    refs, seen = [], []
+
+    def make(like):
+        t = Tensor(like.shape, like.dtype)
+        refs.append(weakref.ref(t))
+        return t
+
+    def alive(*a, **k):
+        seen.append([r() is not None for r in refs])
+
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: (alive(), empty(*a, **k))[1])
+
+    class Lib:
+        def __getattr__(self, entry):
+            return lambda *a: 1000 if entry.endswith("_bytes") else (alive() if entry == name else None, 0)[1]
+
+    monkeypatch.setattr(qrr, "lib", lambda: Lib())
+    NVFP4_CALLS[name](cache, make)
+    assert seen and all(all(s) for s in seen), seen

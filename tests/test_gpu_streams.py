@@ -71,3 +71,25 @@ def test_linear_and_fp8_attention(q):
         for g, i in got:
             assert all(torch.equal(y, z) for y, z in zip(g, want[i]))
         del got, g
+
+
+@pytest.mark.parametrize("news", [[1, 3, 2], [4, 1, 1], [40, 300, 60]])
+def test_arguments_made_in_the_call(q, news):
+    """Every tensor of the calls a temporary: results are those with the tensors held, a sequence that sees nothing first."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    n = 400
+    cache = q.KvCacheNvfp4.empty(3 * 25, 2, 16, 64, torch.arange(75, dtype=torch.int32, device=DEV).view(3, 25))
+    kv = torch.randn(3 * n, 2, 64, device=DEV).to(torch.bfloat16)
+    ends = [0, n, 2 * n, 3 * n]
+    q.kv_append_nvfp4(kv.clone(), kv.clone(), cache, i32([0, 0, 0]), cu=i32(ends))
+    whole = torch.cat(q.kv_read_nvfp4(cache, i32([0, 0, 0]), cu=i32(ends), rows=3 * n))
+    t = sum(news)
+    x, pos, cu = torch.randn(t, 8, 64, device=DEV).to(torch.bfloat16), i32([-news[0], n - news[1], 5]), i32([0, news[0], news[0] + news[1], t])
+    held = i32(ends)
+    assert torch.equal(whole, torch.cat(q.kv_read_nvfp4(cache, i32([0, 0, 0]), cu=held, rows=3 * n)))
+    want = q.attention_nvfp4(x, cache, pos, cu=cu, max_new=max(news), return_lse=True)
+    assert torch.isneginf(want[1][:news[0]]).all() and torch.isfinite(want[1][news[0]:]).all() and want[1][news[0]:].max() < 20
+    for _ in range(30):
+        got = q.attention_nvfp4(x.clone(), cache, pos.clone(), cu=cu.clone(), max_new=max(news), return_lse=True)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        del got
