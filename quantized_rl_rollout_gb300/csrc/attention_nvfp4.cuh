@@ -84,13 +84,11 @@ struct Params {
 };
 
 __device__ __forceinline__ Seq seq_of(const Params& p, int b) {
-  Seq s;
-  if (!kv_rows_of(p.r, b, s.first, s.n) || s.n > p.max_new) flag(p.status, QRR_DEV_BAD_INDEX);
-  s.n = min(s.n, p.max_new);
-  s.pos = min(__ldg(p.r.pos + b), kMaxTokens);  // with at most kMaxTokens rows: sums stay in 32 bits
-  const int last = s.pos + s.n - 1, cap = static_cast<int>(p.c.capacity());
-  if (s.n > 0 && last >= cap) flag(p.status, QRR_DEV_BAD_INDEX);
-  s.last = min(max(last, -1), cap - 1);
+  int first, n;
+  if (!kv_rows_of(p.r, b, first, n) || n > p.max_new) flag(p.status, QRR_DEV_BAD_INDEX);
+  const int cap = static_cast<int>(p.c.capacity());
+  const Seq s = seq_at(first, min(n, p.max_new), __ldg(p.r.pos + b), cap);
+  if (s.n > 0 && s.pos + (s.n - 1) >= cap) flag(p.status, QRR_DEV_BAD_INDEX);
   return s;
 }
 

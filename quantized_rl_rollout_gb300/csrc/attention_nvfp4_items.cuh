@@ -48,6 +48,15 @@ struct Seq {
   int first, n, pos, last;
 };
 
+// Of n <= kMaxTokens rows from position pos on, in a table for `cap` <= kMaxTokens
+// tokens.  Positions beyond kMaxTokens either way come nearer, which leaves them
+// outside; sums with rows and tokens of a tile then stay in 32 bits.
+QRR_HD Seq seq_at(int first, int n, int pos, int cap) {
+  pos = pos < -kMaxTokens ? -kMaxTokens : pos > kMaxTokens ? kMaxTokens : pos;
+  const int last = pos + (n - 1);
+  return Seq{first, n, pos, last < 0 ? -1 : last < cap ? last : cap - 1};
+}
+
 namespace many {
 
 constexpr int kRows = 256;  // rows of an item
@@ -84,6 +93,10 @@ QRR_HD int64_t lane_width(const FastDiv& byG, const Seq& s, int lane) {
   for (int qt = lane; qt < qts; qt += 32) sum += width(byG, s, qt);
   return sum;
 }
+
+// Of key tile j's tokens, how many a row sees whose last visible position is
+// `lim` (any value outside 0 .. kTok: none or all).
+QRR_HD int seen_of(int lim, int j) { return lim - kTok * j + 1; }
 
 }  // namespace many
 

@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
           tc_fence_after();
           // the last scores are formed: no MMA reads these query rows any more
           if (j + 1 == w.t1 && more && active(nx)) copy_rows(nx);
-          const int seen = lim - kTok * j + 1;  // of this tile's tokens
+          const int seen = seen_of(lim, j);  // of this tile's tokens
           const bool mask = kTok * j + kTok - 1 > lim_warp;
           // 32 columns at a time; weights 32 c .. 32 c + 31 go to the columns
           // 16 c .. 16 c + 15, whose scores have been loaded by then
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
     do {
       const int last = last_seen(p.byG, w.s, w.qt);
       for (int j = w.t0; j < w.t1 && ok; ++j, ++use) {
-        const int st = use & 1, live = last + 1 - kTok * j;
+        const int st = use & 1, live = seen_of(last, j);
         ok = half(sh.k[st], &sh.k_empty[st], &sh.k_full[st], live) && half(sh.v[st], &sh.v_empty[st], &sh.v_full[st], live);
       }
     } while (ok && w.next(p));

@@ -9,6 +9,7 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_rl_rollout_gb300", "csrc")
 
+# row tiles, what they count for, the most of a lane, the last row tile's key tiles
 PROGRAM = r"""
 #include <cstdio>
 #include <cstdlib>
@@ -34,14 +35,14 @@ int main(int argc, char** argv) {
 """
 
 
-@pytest.fixture(scope="module")
-def counts(tmp_path_factory):
+def _compiled(tmp_path_factory, program):
+    """A function from cases (four whole numbers each) to the program's lines of whole numbers."""
     gxx = shutil.which("g++")
     if gxx is None:
         pytest.skip("no host compiler")
     d = tmp_path_factory.mktemp("items")
     src, exe = d / "items.cpp", d / "items"
-    src.write_text(PROGRAM)
+    src.write_text(program)
     subprocess.run([gxx, "-std=c++17", "-O2", "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error",
                     "-I" + CSRC, str(src), "-o", str(exe)], check=True)
 
@@ -51,6 +52,11 @@ def counts(tmp_path_factory):
         return [tuple(map(int, line.split())) for line in out.splitlines()]
 
     return run
+
+
+@pytest.fixture(scope="module")
+def counts(tmp_path_factory):
+    return _compiled(tmp_path_factory, PROGRAM)
 
 
 def _want(n, g, pos, last):
@@ -89,3 +95,37 @@ def test_prompts_whose_count_passes_32_bits(counts, n, g, pos):
     total = sum((pos + (min(256 * (qt + 1), n * g) - 1) // g + 128) // 128 for qt in range(qts)) + 3 * qts
     assert got[0] == qts and got[1] == total > 2 ** 31
     assert got[2] < 2 ** 41  # what the warp's two-part sum rests on
+
+
+# of rows, rows a token, first position and the table's tokens: the last visible position, the first row tile's key tiles,
+# and how many of the first tile's tokens its last row, the loads and the last 32 columns' mask see
+POSITIONS = r"""
+#include <cstdio>
+#include "attention_nvfp4_items.cuh"
+using namespace qrr;
+using namespace qrr::attn4;
+int main() {
+  long v[4];
+  while (std::scanf("%ld %ld %ld %ld", v, v + 1, v + 2, v + 3) == 4) {
+    const FastDiv byG(static_cast<uint32_t>(v[1]));
+    const Seq s = seq_at(0, static_cast<int>(v[0]), static_cast<int>(v[2]), static_cast<int>(v[3]));
+    const int last = many::last_seen(byG, s, 0), seen = many::seen_of(last, 0);
+    std::printf("%d %d %d %d %d\n", s.last, many::key_tiles(byG, s, 0), seen, seen - 112, seen - 96);
+  }
+}
+"""
+
+
+def test_positions_at_the_ends_of_32_bits(tmp_path_factory):
+    """A first position of any value: no sum overflows, and rows before the first token see nothing."""
+    lowest, most = -2 ** 31, 2 ** 31 - 1
+    cases = [(n, g, pos, cap) for n in (1, 40, 300, 1 << 20, 1 << 30) for g in (1, 5, 64) if n * g <= 1 << 30
+             for pos in (lowest, lowest + 5, -2 ** 30 - 1, -2 ** 30, -n, -n + 1, -1, 0, 2 ** 30, most) for cap in (16, 1 << 30)]
+    for (n, g, pos, cap), got in zip(cases, _compiled(tmp_path_factory, POSITIONS)(cases)):
+        last = max(min(pos + n - 1, cap - 1), -1)
+        assert got[0] == last
+        tile = min(pos + (min(256, n * g) - 1) // g, last)  # of the first row tile
+        if pos + n - 1 < 0 or tile < 0:
+            assert got[1] == 1 and all(x <= 0 for x in got[2:]), (n, g, pos, cap)
+        elif pos <= 2 ** 30:
+            assert got[1] == (tile + 128) // 128 and got[2] == tile + 1
