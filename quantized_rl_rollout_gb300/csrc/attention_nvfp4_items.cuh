@@ -95,7 +95,9 @@ QRR_HD int64_t lane_width(const FastDiv& byG, const Seq& s, int lane) {
 }
 
 // Of key tile j's tokens, how many a row sees whose last visible position is
-// `lim` (any value outside 0 .. kTok: none or all).
+// `lim` (any value outside 0 .. kTok: none or all).  A row that needs no mask has
+// kAllSeen in its place: behind every position, and seen_of stays in 32 bits.
+constexpr int kAllSeen = kMaxTokens;
 QRR_HD int seen_of(int lim, int j) { return lim - kTok * j + 1; }
 
 }  // namespace many

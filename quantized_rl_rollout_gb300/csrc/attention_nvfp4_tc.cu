@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         const bool in = row < rows;
         const uint64_t f2 = twice(f);
         // rows behind the last one are never read: they need no mask
-        const int lim = in ? min(w.s.pos + p.byG.div(row), w.s.last) : 0x7FFFFFFF;
+        const int lim = in ? min(w.s.pos + p.byG.div(row), w.s.last) : kAllSeen;
         const int lim_warp = __reduce_min_sync(0xFFFFFFFFu, lim);
         float m = kNone, l = 0.0f;
         for (int j = w.t0; j < w.t1 && ok; ++j) {

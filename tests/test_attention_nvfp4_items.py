@@ -129,3 +129,29 @@ def test_positions_at_the_ends_of_32_bits(tmp_path_factory):
             assert got[1] == 1 and all(x <= 0 for x in got[2:]), (n, g, pos, cap)
         elif pos <= 2 ** 30:
             assert got[1] == (tile + 128) // 128 and got[2] == tile + 1
+
+
+# of rows that need no mask, from key tile v[0] on in steps of v[1] to v[2]: the fewest tokens seen, less the last column's place
+UNMASKED = r"""
+#include <cstdio>
+#include "attention_nvfp4_items.cuh"
+using namespace qrr::attn4;
+int main() {
+  long v[4];
+  while (std::scanf("%ld %ld %ld %ld", v, v + 1, v + 2, v + 3) == 4) {
+    int least = 2147483647;
+    for (int j = static_cast<int>(v[0]); j <= v[2]; j += static_cast<int>(v[1])) {
+      const int x = many::seen_of(many::kAllSeen, j) - 96;
+      if (x < least) least = x;
+    }
+    std::printf("%d\n", least);
+  }
+}
+"""
+
+
+def test_rows_without_a_mask(tmp_path_factory):
+    """A row behind the last one sees every column (32 at a time) of every key tile of a table for 2^30 tokens."""
+    tiles = 2 ** 30 // 128
+    for (least,) in _compiled(tmp_path_factory, UNMASKED)([(0, 1, 1000, 0), (0, 997, tiles - 1, 0), (tiles - 3, 1, tiles - 1, 0)]):
+        assert least >= 32
