@@ -351,8 +351,10 @@ qrr_status qrr_attention_decode_fp8(const void* q, int32_t B, int32_t Hq, int32_
  * sequence: they are not written, read zeros, and attention leaves them alone.  A
  * position at or above max_pages * page, a page number outside
  * [0, num_pages) or offsets that leave [0, T] raise QRR_DEV_BAD_INDEX; such a
- * row is not written to the cache and reads zeros, and the outputs of its
- * sequence's attention are unspecified.  T <= 2^30,
+ * row (with offsets: each row of that sequence) is not written to the cache and
+ * reads zeros, and the outputs of its sequence's attention are unspecified.
+ * Offsets that descend raise it too; which rows they name is unspecified, but
+ * nothing outside the call's rows is touched.  T <= 2^30,
  * max_pages * page <= 2^30, num_pages * Hkv * page < 2^32.
  *
  * qrr_kv_append_nvfp4: quantizes rows k_new, v_new (bf16, row t at base + t ld

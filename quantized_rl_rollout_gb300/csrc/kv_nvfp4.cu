@@ -38,26 +38,31 @@ constexpr int kMaxTokensCta = 256;
 constexpr int kHeads = 4;  // rows of keys, and of values, a lane reads at a time
 
 // The sequence that row t belongs to (offsets ascending), -1 for a row behind
-// the last sequence.
-__device__ __forceinline__ int seq_of(const KvRows& r, int B, int t) {
+// the last sequence; its first row and the one behind its last.
+__device__ __forceinline__ int seq_of(const KvRows& r, int B, int t, int& first, int& end) {
+  first = t, end = t + 1;
   if (!r.cu) return t;
   int lo = 0, hi = B;  // the first b with cu[b + 1] > t is in [lo, hi]
+  first = __ldg(r.cu);
   while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(r.cu + mid + 1) > t) hi = mid;
-    else lo = mid + 1;
+    const int mid = (lo + hi) >> 1, x = __ldg(r.cu + mid + 1);
+    if (x > t) hi = mid, end = x;
+    else lo = mid + 1, first = x;
   }
-  return lo < B && t >= __ldg(r.cu + lo) ? lo : -1;
+  return lo < B && t >= first ? lo : -1;
 }
 
 constexpr uint32_t kNoToken = 0xFFFFFFFFu;   // padding, a position below zero
-constexpr uint32_t kBadToken = 0xFFFFFFFEu;  // outside the table, or its page outside the cache
+// outside the table, its page outside the cache, or of a sequence whose offsets leave the call's rows
+constexpr uint32_t kBadToken = 0xFFFFFFFEu;
 
 // Cache row of call row t and head 0.
 __device__ __forceinline__ uint32_t place(const KvNvfp4& c, const KvRows& r, int t) {
-  const int b = seq_of(r, c.B, t);
+  int first, end;
+  const int b = seq_of(r, c.B, t, first, end);
   if (b < 0) return kNoToken;
-  const int64_t p = static_cast<int64_t>(__ldg(r.pos + b)) + (r.cu ? t - __ldg(r.cu + b) : 0);
+  if (first < 0 || end > r.T) return kBadToken;
+  const int64_t p = static_cast<int64_t>(__ldg(r.pos + b)) + (t - first);
   if (p < 0) return kNoToken;
   if (p >= c.capacity()) return kBadToken;
   const int pg = __ldg(c.table + static_cast<int64_t>(b) * c.max_pages + (p >> c.page_shift));
@@ -84,10 +89,16 @@ struct Unit {
   }
 };
 
-// The places of the CTA's tokens t0 .. t0 + n - 1, in shared memory.
+// The places of the CTA's tokens t0 .. t0 + n - 1, in shared memory.  Offsets that
+// leave the call's rows or descend are told whether they name a row or not.
 __device__ __forceinline__ int find_places(const KvNvfp4& c, const KvRows& r, const Units& un, int t0, uint32_t* at,
                                            int32_t* status) {
   const int n = min(un.tokens, static_cast<int>(r.T) - t0);
+  if (r.cu && blockIdx.x == 0)
+    for (int b = threadIdx.x; b < c.B; b += kThreads) {
+      int first, rows;
+      if (!kv_rows_of(r, b, first, rows)) flag(status, QRR_DEV_BAD_INDEX);
+    }
   for (int i = threadIdx.x; i < n; i += kThreads) {
     at[i] = place(c, r, t0 + i);
     if (at[i] == kBadToken) flag(status, QRR_DEV_BAD_INDEX);

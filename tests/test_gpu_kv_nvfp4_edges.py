@@ -37,3 +37,65 @@ def test_positions_far_below_zero(q, dim, news, low):  # noqa: F811
     assert torch.isfinite(lse[mid]).all() and (lse[mid] - alone[1]).abs().max() < 1e-4
     assert (out[mid] - alone[0]).float().abs().max() <= 2 ** -6 * alone[0].float().abs().max()
     assert all(torch.equal(a, b) for a, b in zip(before, bed.cache.tensors[:4]))
+
+
+T = 12
+OFFSETS = [  # offsets of two sequences, and the rows that belong to a sequence with sound ones
+    ([0, 6, 50], range(0, 6)), ([-3, 6, 12], range(6, 12)), ([0, 12, 13], range(0, 12)), ([-1, 0, 12], range(0, 12)), ([5, 40, 60], []),
+    ([0, 6, 12], range(0, 12)), ([2, 2, 9], range(2, 9))]
+
+
+def _guarded(shape, dtype):
+    """A tensor of sevens inside a larger one, and a check that what lies around it stays."""
+    n = int(np.prod(shape))
+    whole = torch.full((n + 4096,), 7, dtype=dtype, device=DEV)
+    return whole[2048:2048 + n].view(shape), lambda: bool((whole[:2048] == 7).all() and (whole[2048 + n:] == 7).all())
+
+
+@pytest.mark.parametrize("cu,sound", OFFSETS)
+def test_append_and_read_tell_offsets_that_leave_the_rows(q, cu, sound):  # noqa: F811
+    """Such a sequence's rows are not written and read zeros; the others are as ever."""
+    bad = not 0 <= cu[0] <= cu[1] <= cu[2] <= T
+    cache = q.KvCacheNvfp4.empty(8, 2, 16, 64, _dev([[0, 1, 2, 3], [4, 5, 6, 7]]))
+    x = torch.randn(T, 2, 64, device=DEV).to(torch.bfloat16)
+    st, pos = _dev([0]), _dev([1, 20])
+    q.kv_append_nvfp4(x, x, cache, pos, cu=_dev(cu), dev_status=st)
+    assert q.get_last_device_status(st) == (q.DEV_BAD_INDEX if bad else 0)
+    places = {(int(t >= cu[1]), [1, 20][t >= cu[1]] + t - cu[t >= cu[1]]): t for t in sound}  # (sequence, position): row
+    for s in (0, 1):
+        for p in range(64):
+            there = bool(cache.tensors[1][4 * s + p // 16, :, p % 16].any())
+            assert there == ((s, p) in places), (s, p)
+    full = torch.randn(128, 2, 64, device=DEV).to(torch.bfloat16)
+    q.kv_append_nvfp4(full, full, cache, _dev([0, 0]), cu=_dev([0, 64, 128]))
+    (k, k_ok), (v, v_ok) = _guarded((T, 2, 64), torch.bfloat16), _guarded((T, 2, 64), torch.bfloat16)
+    st.zero_()
+    q.kv_read_nvfp4(cache, pos, cu=_dev(cu), k=k, v=v, dev_status=st)
+    assert q.get_last_device_status(st) == (q.DEV_BAD_INDEX if bad else 0) and k_ok() and v_ok()
+    want = torch.cat(q.kv_read_nvfp4(cache, _dev([0, 0]), cu=_dev([0, 64, 128]), rows=128)[:1])
+    rows = {t: 64 * s + p for (s, p), t in places.items()}
+    for t in range(T):
+        assert torch.equal(k[t], want[rows[t]]) if t in rows else not k[t].any()
+
+
+@pytest.mark.parametrize("cu", [[0, 9, 4], [0, 13, 4], [7, 3, 12]])
+def test_descending_offsets_are_told(q, cu):  # noqa: F811
+    """What rows such offsets name is not said; nothing outside the call's rows is touched."""
+    cache = q.KvCacheNvfp4.empty(8, 2, 16, 64, _dev([[0, 1, 2, 3], [4, 5, 6, 7]]))
+    x = torch.randn(T, 2, 64, device=DEV).to(torch.bfloat16)
+    for call in (lambda st: q.kv_append_nvfp4(x, x, cache, _dev([1, 20]), cu=_dev(cu), dev_status=st),
+                 lambda st: q.kv_read_nvfp4(cache, _dev([1, 20]), cu=_dev(cu), k=k, v=v, dev_status=st)):
+        (k, k_ok), (v, v_ok), st = _guarded((T, 2, 64), torch.bfloat16), _guarded((T, 2, 64), torch.bfloat16), _dev([0])
+        call(st)
+        assert q.get_last_device_status(st) == q.DEV_BAD_INDEX and k_ok() and v_ok()
+
+
+@pytest.mark.parametrize("cu", [[0, 6, 50], [-3, 6, 12], [0, 9, 4], [5, 40, 60]])
+@pytest.mark.parametrize("hq,hkv", [(8, 2), (80, 1)])
+def test_attention_stays_inside_the_rows(q, cu, hq, hkv):  # noqa: F811
+    """Offsets that leave the rows or descend: flagged, and nothing around out and lse is written (both kernels)."""
+    bed = Bed(q, [40, 200], hkv, 64, 16, 24)
+    x = torch.randn(T, hq, 64, device=DEV).to(torch.bfloat16)
+    (out, out_ok), (lse, lse_ok), st = _guarded((T, hq, 64), torch.bfloat16), _guarded((T, hq), torch.float32), _dev([0])
+    q.attention_nvfp4(x, bed.cache, _dev([30, 180]), cu=_dev(cu), max_new=12, out=out, lse=lse, dev_status=st)
+    assert q.get_last_device_status(st) & q.DEV_BAD_INDEX and out_ok() and lse_ok()
