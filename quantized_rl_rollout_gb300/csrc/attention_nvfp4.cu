@@ -790,9 +790,9 @@ cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
   }
   attn_nvfp4_kernel<D, NT><<<grid, kThreads, smem, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
-  // a cache whose longest sequence fits a range, and a range for every item:
-  // nothing is cut
-  if (e != cudaSuccess || (a.c.capacity() <= kMinTiles * kTok && items <= ranges)) return e;
+  // no sequence may have rows (the kernel has told those that do), or a cache whose
+  // longest sequence fits a range, and a range for every item: nothing is cut
+  if (e != cudaSuccess || rows == 0 || (a.c.capacity() <= kMinTiles * kTok && items <= ranges)) return e;
   // Eight pieces an item on average, or more: 8 sequences of 20000..33000 tokens
   // join in 6 us by pieces, in 12 by rows; 64 of 2048..4096 (4 pieces) in 7.7 and 5.8.
   if (ranges >= 8 * items)

@@ -99,3 +99,17 @@ def test_attention_stays_inside_the_rows(q, cu, hq, hkv):  # noqa: F811
     (out, out_ok), (lse, lse_ok), st = _guarded((T, hq, 64), torch.bfloat16), _guarded((T, hq), torch.float32), _dev([0])
     q.attention_nvfp4(x, bed.cache, _dev([30, 180]), cu=_dev(cu), max_new=12, out=out, lse=lse, dev_status=st)
     assert q.get_last_device_status(st) & q.DEV_BAD_INDEX and out_ok() and lse_ok()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("b,hkv", [(2, 2), (600, 8)])
+def test_no_rows_a_sequence_beside_rows_of_nobody(q, dim, b, hkv):  # noqa: F811
+    """max_new = 0 over a cache of more than a range's tokens, with few items and with many: the rows are left alone, and
+    a sequence that does bring one is told."""
+    cache = q.KvCacheNvfp4.empty(20, hkv, 16, dim, torch.zeros(b, 20, dtype=torch.int32, device=DEV))
+    x = torch.randn(5, 2 * hkv, dim, device=DEV).to(torch.bfloat16)
+    for at, cu in ((0, [3] * (b + 1)), (q.DEV_BAD_INDEX, [0] * b + [1])):
+        (out, out_ok), (lse, lse_ok), st = _guarded(tuple(x.shape), torch.bfloat16), _guarded((5, 2 * hkv), torch.float32), _dev([0])
+        q.attention_nvfp4(x, cache, _dev([40] * b), cu=_dev(cu), max_new=0, out=out, lse=lse, dev_status=st)
+        assert q.get_last_device_status(st) == at and out_ok() and lse_ok()
+        assert (out == 7).all() and (lse == 7).all()
