@@ -776,20 +776,17 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(const Params p) {
 }
 
 template <int D, int NT>
-cudaError_t launch(const AttnNvfp4Args& a, int grid, cudaStream_t stream) {
+cudaError_t launch(const AttnNvfp4Args& a, int dev, int grid, cudaStream_t stream) {
   constexpr int RT = 8 * NT;
   const int ranges = grid * kWarps, rows = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(a.max_new) * (a.Hq / a.c.Hkv), RT));
   const int64_t items = static_cast<int64_t>(a.c.B) * a.c.Hkv;
   const Params p = make_params(a, a.ws, ranges, RT, items);
   constexpr int smem = (static_cast<int>(sizeof(Raw<D>)) * kStages + (kQInSmem<NT> ? NT * D * 16 : 0)) * kWarps;
-  static bool attr = false;
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
+  static OncePerDevice limit;
+  cudaError_t e = limit(dev, [] { return cudaFuncSetAttribute(attn_nvfp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
   attn_nvfp4_kernel<D, NT><<<grid, kThreads, smem, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   // no sequence may have rows (the kernel has told those that do), or a cache whose
   // longest sequence fits a range, and a range for every item: nothing is cut
   if (e != cudaSuccess || rows == 0 || (a.c.capacity() <= kMinTiles * kTok && items <= ranges)) return e;
@@ -822,16 +819,17 @@ size_t attention_nvfp4_ws_bytes(int D, int B, int Hq, int Hkv, int64_t max_new) 
 cudaError_t launch_attention_nvfp4(const AttnNvfp4Args& a, cudaStream_t stream) {
   if (a.r.T == 0 || a.Hq == 0 || a.c.B == 0) return cudaSuccess;
   int dev = 0, sms = kSMs;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_of(dev, sms);
+  if (e != cudaSuccess) return e;
   const int G = a.Hq / a.c.Hkv;
   if (any_few(G)) {
     const int nt = row_groups(a.max_new, G), grid = (sms < kMaxSms ? sms : kMaxSms) * ctas_per_sm(a.c.D, nt);
-    const cudaError_t e = a.c.D == 128 ? (nt == 1   ? launch<128, 1>(a, grid, stream)
-                                          : nt == 2 ? launch<128, 2>(a, grid, stream)
-                                                    : launch<128, 4>(a, grid, stream))
-                                       : (nt == 1   ? launch<64, 1>(a, grid, stream)
-                                          : nt == 2 ? launch<64, 2>(a, grid, stream)
-                                                    : launch<64, 4>(a, grid, stream));
+    e = a.c.D == 128 ? (nt == 1   ? launch<128, 1>(a, dev, grid, stream)
+                        : nt == 2 ? launch<128, 2>(a, dev, grid, stream)
+                                  : launch<128, 4>(a, dev, grid, stream))
+                     : (nt == 1   ? launch<64, 1>(a, dev, grid, stream)
+                        : nt == 2 ? launch<64, 2>(a, dev, grid, stream)
+                                  : launch<64, 4>(a, dev, grid, stream));
     if (e != cudaSuccess) return e;
   }
   if (!any_many(a.max_new, G)) return cudaSuccess;

@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "kv_nvfp4.cuh"
+#include "once_per_device.cuh"
 #include "tc.cuh"
 
 namespace qrr {
@@ -141,6 +142,12 @@ cudaError_t launch_dependent(void (*kernel)(A...), dim3 grid, unsigned threads, 
   cfg.attrs = la;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The current device and its SMs.
+inline cudaError_t device_of(int& dev, int& sms) {
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
 // Workspace of `ranges` ranges whose pieces have `rt` rows, and their records.

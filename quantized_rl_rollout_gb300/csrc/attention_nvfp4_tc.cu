@@ -786,24 +786,22 @@ template <int D>
 cudaError_t launch(const AttnNvfp4Args& a, uint8_t* ws, bool beside, cudaStream_t stream) {
   constexpr int smem = static_cast<int>(sizeof(Smem<D>)) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  static bool attr = false;
-  if (!attr) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_nvfp4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    attr = true;
-  }
   int dev = 0, sms = kSMs;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device_of(dev, sms);
+  if (e != cudaSuccess) return e;
+  static OncePerDevice limit;
+  e = limit(dev, [] { return cudaFuncSetAttribute(attn_nvfp4_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); });
+  if (e != cudaSuccess) return e;
   const int grid = sms < kMaxSms ? sms : kMaxSms;
   const Params p = make_params(a, ws, grid, kRows, grid);
   // behind the other kernel's launches it may run beside them: what it reads was
   // there before those, what it writes they do not touch
   if (beside) {
-    const cudaError_t e = launch_dependent(attn_nvfp4_tc_kernel<D>, dim3(grid), kThreads, smem, stream, p);
+    e = launch_dependent(attn_nvfp4_tc_kernel<D>, dim3(grid), kThreads, smem, stream, p);
     if (e != cudaSuccess) return e;
   } else {
     attn_nvfp4_tc_kernel<D><<<grid, kThreads, smem, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(join_many_kernel<D>, dim3(grid * (kRows / 64)), 256, 0, stream, p);
