@@ -386,6 +386,8 @@ qrr_status qrr_kv_read_nvfp4(const qrr_kv_nvfp4* cache, int64_t T, const int32_t
  *   lse = log(sum_j p_j)
  * over the cached positions j <= pos[b] + i (the row's own token included:
  * append first).  A row that sees nothing gives zeros and lse -inf.
+ * A query row with a value that is not finite raises QRR_DEV_NONFINITE; a NaN
+ * comes through to its out and lse.
  *   q    bf16, row t at q + t ld_q elements, Hq heads of D; ld_q % 8 == 0
  *   scale > 0 and finite (1 / sqrt(D), usually)
  *   max_new  host bound on cu[b + 1] - cu[b] (1 where cu is NULL); a sequence

@@ -520,7 +520,7 @@ __device__ __forceinline__ void piece(const Params& p, const Walk& it, Feed<D>& 
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
       if (r >= it.n * p.G) continue;
       if (!cut0 && !cut1) {
-        const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+        const float inv = row_factor(vg, l);
         const int64_t orow = out_row(p, it.first, it.h, r);
         uint32_t w[D / 16];
 #pragma unroll
@@ -531,7 +531,7 @@ __device__ __forceinline__ void piece(const Params& p, const Walk& it, Feed<D>& 
 #pragma unroll
         for (int j = 0; j < D / 64; ++j)
           reinterpret_cast<uint4*>(p.out + orow * D + D / 8 * g)[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-        if (p.lse && g == 0) p.lse[orow] = l > 0.0f ? (s.m[nt][i] + lg2(l)) * kLn2 : -INFINITY;
+        if (p.lse && g == 0) p.lse[orow] = row_lse(s.m[nt][i], l);
       } else {
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
@@ -709,7 +709,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const Params p) {
     for (; i + 8 <= n; i += 8) add(std::integral_constant<int, 8>{}, i);
     for (; i < n; i += 2) add(std::integral_constant<int, 2>{}, i);
   }
-  const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+  const float inv = row_factor(vg, l);
   const int64_t orow = out_row(p, rec.first, rec.h, row);
   uint32_t y[V / 2];
 #pragma unroll
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const Params p) {
   }
   if constexpr (V == 4) *reinterpret_cast<uint2*>(p.out + orow * D + V * lane) = make_uint2(y[0], y[1]);
   else *reinterpret_cast<uint32_t*>(p.out + orow * D + V * lane) = y[0];
-  if (p.lse && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+  if (p.lse && lane == 0) p.lse[orow] = row_lse(m, l);
 }
 
 // Joins items of many pieces each (long sequences, few of them): a warp takes a quarter of a row's
@@ -771,8 +771,8 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(const Params p) {
     for (int d = 0; d < 4; ++d) o[d] += __shfl_xor_sync(0xFFFFFFFFu, o[d], y);
   const int64_t orow = out_row(p, rec.first, rec.h, row);
   if (grp == 0)
-    *reinterpret_cast<uint2*>(p.out + orow * D + part * (D / 4) + 4 * lane) = bf16x4(o, l > 0.0f ? __fdividef(vg, l) : 0.0f);
-  if (p.lse && part == 0 && lane == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+    *reinterpret_cast<uint2*>(p.out + orow * D + part * (D / 4) + 4 * lane) = bf16x4(o, row_factor(vg, l));
+  if (p.lse && part == 0 && lane == 0) p.lse[orow] = row_lse(m, l);
 }
 
 template <int D, int NT>

@@ -35,6 +35,11 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+// A row's factor of its weighted sum, and its log-sum-exp, from its reference and its
+// sum of weights: 0 and -inf where it has seen nothing (a NaN comes through).
+__device__ __forceinline__ float row_factor(float vg, float l) { return l == 0.0f ? 0.0f : __fdividef(vg, l); }
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + lg2(l)) * kLn2; }
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
         tc_fence_after();
         const bool whole = w.t0 == 0 && w.t1 == w.tiles;
         const float vg = p.c.vg ? __ldg(p.c.vg + w.h) : 1.0f;
-        const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+        const float inv = row_factor(vg, l);
         const int64_t orow = in ? out_row(p, w.s.first, w.h, row) : 0;
         const int64_t piece = 2 * blockIdx.x + (w.t0 > 0 ? 0 : 1);
 #pragma unroll 1
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_nvfp4_tc_kernel(const Params
                   make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         }
-        if (in && whole && p.lse) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+        if (in && whole && p.lse) p.lse[orow] = row_lse(m, l);
         if (in && !whole) p.pm[piece * kRows + 128 * tile + r] = m, p.pl[piece * kRows + 128 * tile + r] = l;
         __syncwarp();
         tc_fence_before();
@@ -775,11 +775,11 @@ __global__ void __launch_bounds__(256) join_many_kernel(const Params p) {
     }
   }
   if (row >= rec.n * p.G) return;
-  const float inv = l > 0.0f ? __fdividef(vg, l) : 0.0f;
+  const float inv = row_factor(vg, l);
   const int64_t orow = out_row(p, rec.first, rec.h, row);
 #pragma unroll
   for (int k = 0; k < D / 16; ++k) *reinterpret_cast<uint2*>(p.out + orow * D + 16 * k + 4 * part) = bf16x4(o[k], inv);
-  if (p.lse && part == 0) p.lse[orow] = l > 0.0f ? (m + lg2(l)) * kLn2 : -INFINITY;
+  if (p.lse && part == 0) p.lse[orow] = row_lse(m, l);
 }
 
 template <int D>

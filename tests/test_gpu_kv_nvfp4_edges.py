@@ -113,3 +113,25 @@ def test_no_rows_a_sequence_beside_rows_of_nobody(q, dim, b, hkv):  # noqa: F811
         q.attention_nvfp4(x, cache, _dev([40] * b), cu=_dev(cu), max_new=0, out=out, lse=lse, dev_status=st)
         assert q.get_last_device_status(st) == at and out_ok() and lse_ok()
         assert (out == 7).all() and (lse == 7).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lens,news", [([60, 30], [1, 1]), ([3000, 30], [1, 2]), ([9000, 20], [1, 4]), ([700, 90], [40, 60]), ([5000, 40], [300, 1])])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_queries_that_are_not_finite(q, dim, lens, news, value):  # noqa: F811
+    """Such a row comes out as NaN, its log-sum-exp too (not as a row that sees nothing); every other row is as without it.
+    Items in one piece, in a few and in many, both kernels."""
+    bed = Bed(q, lens, 2, dim, 16, 31)
+    t = sum(news)
+    x = torch.randn(t, 8, dim, device=DEV).to(torch.bfloat16)
+    pos, cu = _dev([n - m for n, m in zip(lens, news)]), _dev([0, news[0], t])
+    want = q.attention_nvfp4(x, bed.cache, pos, cu=cu, max_new=max(news), return_lse=True)
+    hit = torch.zeros(t, 8, dtype=torch.bool, device=DEV)
+    for row, head in ((0, 3), (t - 1, 6)):
+        x[row, head, 17] = value
+        hit[row, head] = True
+    st = _dev([0])
+    out, lse = q.attention_nvfp4(x, bed.cache, pos, cu=cu, max_new=max(news), return_lse=True, dev_status=st)
+    assert q.get_last_device_status(st) == q.DEV_NONFINITE
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    assert torch.equal(out[~hit], want[0][~hit]) and torch.equal(lse[~hit], want[1][~hit])
