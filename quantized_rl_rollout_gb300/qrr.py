@@ -165,10 +165,14 @@ def _need(t, dtype, name):
 def _on_stream(shape, dtype, device, stream, returned=True):
     """A new tensor for a call on ``stream`` (None: the current one), from that stream's memory: a block of the current
     stream's may still be in use by work queued there.  ``returned``: the caller may go on with it on the current stream."""
-    if stream is None or _stream(stream) == _stream(None):
+    handle = None if stream is None else _stream(stream)
+    if handle in (0, 1, 2):  # the default stream, and a thread's own, which is ordered with it both ways
+        handle = 0
+    if handle is None or handle == _stream(None):
         return torch.empty(shape, dtype=dtype, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    with torch.cuda.stream(s):
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if returned:
         t.record_stream(torch.cuda.current_stream())

@@ -64,8 +64,14 @@ def made(monkeypatch):
         def __getattr__(self, name):
             return lambda *a: 1000 if name.endswith("_bytes") else 0
 
+    def external(handle):
+        """As the real one: 0 makes a stream of its own, and the other two default handles cannot be used."""
+        assert handle not in (1, 2), "invalid StreamId"
+        return Stream(handle or 99)
+
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", external)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: Stream(0))
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: now[-1])
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
@@ -93,6 +99,20 @@ def test_nvfp4_cache_calls(cache, made, stream):
     del made[:]
     got = qrr.kv_read_nvfp4(cache, POS, stream=stream)
     assert [t.under for t in made] == [22] * 2 and [t.recorded for t in got] == [[11]] * 2
+
+
+@pytest.mark.parametrize("stream", [0, 1, 2])
+def test_default_streams_by_their_handles(cache, made, monkeypatch, stream):
+    """The default stream (0, or by its name 1) and a thread's (2), which waits for it and is waited for by it, take the
+    default stream's memory; where that is the current one, the call is as without a stream."""
+    got = qrr.attention_nvfp4(X, cache, POS, return_lse=True, stream=stream)
+    qrr.linear_nvfp4_lora(_bf16(2, 64), *W, stream=stream)
+    assert len(made) == 5 and [t.under for t in made] == [0] * 5 and [t.recorded for t in got] == [[11]] * 2
+    del made[:]
+    monkeypatch.setattr(CURRENT, "cuda_stream", 0)
+    qrr.attention_nvfp4(X, cache, POS, return_lse=True, stream=stream)
+    qrr.linear_nvfp4_lora(_bf16(2, 64), *W, stream=stream)
+    assert len(made) == 5 and all(t.under == 0 and not t.recorded for t in made)
 
 
 @pytest.mark.parametrize("stream", [None, CURRENT, 11])

@@ -93,3 +93,21 @@ def test_arguments_made_in_the_call(q, news):
         got = q.attention_nvfp4(x.clone(), cache, pos.clone(), cu=cu.clone(), max_new=max(news), return_lse=True)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         del got
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])
+def test_default_streams_by_their_handles(q, handle):
+    """A call on the default stream, or a thread's own, while another stream is current."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    cache = q.KvCacheNvfp4.empty(8, 2, 64, 128, i32([list(range(8))]))
+    kv = torch.randn(512, 2, 128, device=DEV).to(torch.bfloat16)
+    x = torch.randn(512, 8, 128, device=DEV).to(torch.bfloat16)
+    pos, cu = i32([0]), i32([0, 512])
+    q.kv_append_nvfp4(kv, kv, cache, pos, cu=cu)
+    want = q.attention_nvfp4(x, cache, pos, cu=cu, max_new=512, return_lse=True)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = [q.attention_nvfp4(x, cache, pos, cu=cu, max_new=512, return_lse=True, stream=s) for s in (handle, None, handle)]
+        torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
