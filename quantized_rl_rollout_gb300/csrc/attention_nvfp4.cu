@@ -59,12 +59,6 @@ constexpr int kMinTiles = 4;  // tiles of a range
 constexpr int kItemCost = 1;
 constexpr int kStages = 3;    // tiles of a warp's ring
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -661,25 +655,15 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const Params p) {
   const int row = rec.rt * RT + r;
   if (rec.pieces == 0 || row >= rec.n * p.G) return;
   const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)) * RT + r; };
   float m = kNone, l = 0.0f, o[V] = {};
   for (int i0 = 0; i0 < rec.pieces; i0 += 32) {
     const int n = min(32, rec.pieces - i0);
-    float mi = kNone, li = 0.0f;
+    float mi = kNone, li = 0.0f, old;
     if (lane < n) {
-      mi = p.pm[piece(i0 + lane)];
-      li = p.pl[piece(i0 + lane)];
+      mi = p.pm[piece_row(rec, i0 + lane, RT) + r];
+      li = p.pl[piece_row(rec, i0 + lane, RT) + r];
     }
-    float top = mi;
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-    top = fmaxf(top, m);
-    const float old = ex2(m - top), a = lane < n ? ex2(mi - top) : 0.0f;
-    m = top;
-    float sum = a * li;
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-    l = l * old + sum;
+    const float a = piece_weight(mi, li, m, l, old);
 #pragma unroll
     for (int d = 0; d < V; ++d) o[d] *= old;
     // `many` pieces' outputs from the i-th on; eight loads under way at a time
@@ -689,7 +673,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const Params p) {
       float v[kMany][V];
 #pragma unroll
       for (int u = 0; u < kMany; ++u) {
-        const float* src = p.po + piece(i0 + min(i + u, n - 1)) * D + V * lane;
+        const float* src = p.po + (piece_row(rec, i0 + min(i + u, n - 1), RT) + r) * D + V * lane;
         if constexpr (V == 4) {
           const float4 x = *reinterpret_cast<const float4*>(src);
           v[u][0] = x.x, v[u][1] = x.y, v[u][2] = x.z, v[u][3] = x.w;
@@ -753,7 +737,7 @@ __global__ void __launch_bounds__(256) join_pieces_kernel(const Params p) {
 #pragma unroll
       for (int u = 0; u < kMany; ++u)
         x[u] = *reinterpret_cast<const float4*>(po + (piece_row(rec, i0 + min(kGroups * u + grp, n - 1), RT) + row) * D);
-      const float a = piece_weight<32>(mi, li, m, l, old);
+      const float a = piece_weight(mi, li, m, l, old);
 #pragma unroll
       for (int d = 0; d < 4; ++d) o[d] *= old;
 #pragma unroll

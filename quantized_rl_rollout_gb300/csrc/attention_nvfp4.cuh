@@ -40,6 +40,12 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ float row_factor(float vg, float l) { return l == 0.0f ? 0.0f : __fdividef(vg, l); }
 __device__ __forceinline__ float row_lse(float m, float l) { return l == 0.0f ? -INFINITY : (m + lg2(l)) * kLn2; }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -103,21 +109,19 @@ __device__ __forceinline__ int64_t out_row(const Params& p, int first, int h, in
   return static_cast<int64_t>(first + p.byG.div(row)) * p.Hq + h * p.G + p.byG.mod(row);
 }
 
-// Weights of up to 32 pieces of a row, piece i in lane i of each `kLanes` lanes
-// (the rest: none), brought to the row's new reference m; `old` brings what the
-// row has so far there.
-template <int kLanes>
+// Weights of up to 32 pieces of a row, piece i in lane i (the rest: none), brought to
+// the row's new reference m; `old` brings what the row has so far there.
 __device__ __forceinline__ float piece_weight(float mi, float li, float& m, float& l, float& old) {
   float top = mi;
 #pragma unroll
-  for (int x = kLanes / 2; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+  for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
   top = fmaxf(top, m);
   old = ex2(m - top);
   m = top;
   const float a = ex2(mi - top);
   float sum = a * li;
 #pragma unroll
-  for (int x = kLanes / 2; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+  for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
   l = l * old + sum;
   return a;
 }

@@ -69,7 +69,6 @@ struct Smem {
   uint64_t q_full[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], done;
   uint32_t tmem;
   int abort;
-  int64_t total;
   int32_t seq_widths[kSeqs];  // -1: above 32 bits
   int64_t part[kThreads / 32];
 };
@@ -217,12 +216,6 @@ struct Codes {
 };
 
 // ---- softmax -------------------------------------------------------------------
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 // 32 scores of a row -> weights 2^(s f - m): f16 pairs, their fp32 sums, the
 // largest score.
@@ -731,7 +724,7 @@ __global__ void __launch_bounds__(256) join_many_kernel(const Params p) {
   const int r = first + (lane & 7), row = rec.rt * kRows + r;
   if (rec.pieces == 0 || rec.rt * kRows + first >= rec.n * p.G) return;  // (the same for the warp)
   const float vg = p.c.vg ? __ldg(p.c.vg + rec.h) : 1.0f;
-  auto piece = [&](int i) { return static_cast<int64_t>(i == 0 ? 2 * rec.range + 1 : 2 * (rec.range + i)); };
+  auto piece = [&](int i) { return piece_row(rec, i, 1); };
   float m = kNone, l = 0.0f, o[D / 16][4] = {};
   for (int i0 = 0; i0 < rec.pieces; i0 += 4) {
     // the row's lanes take a piece's (m, l) each
