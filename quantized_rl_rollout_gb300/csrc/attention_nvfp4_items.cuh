@@ -66,11 +66,11 @@ constexpr int kTok = 128;   // tokens of a key tile
 // whose items then fit a range of kMinTiles: 23, 17, 17.
 constexpr int kItemCost = 3;
 
-// Items of a sequence with G rows a token: row tiles of 256 (none if it has few
-// rows), and the key tiles of one (at least 1).
+// Items of a sequence with G rows a token (2^30 rows at most): row tiles of 256
+// (none if it has few rows), and the key tiles of one (at least 1).
 QRR_HD int row_tiles(const FastDiv& byG, const Seq& s) {
-  const int64_t rows = static_cast<int64_t>(s.n) * byG.d;
-  return rows <= kFewRows ? 0 : static_cast<int>((rows + kRows - 1) / kRows);
+  const int rows = s.n * static_cast<int>(byG.d);
+  return rows <= kFewRows ? 0 : (rows + kRows - 1) / kRows;
 }
 QRR_HD int last_seen(const FastDiv& byG, const Seq& s, int qt) {
   const int rows = s.n * static_cast<int>(byG.d), end = (qt + 1) * kRows;
