@@ -387,18 +387,20 @@ qrr_status qrr_kv_read_nvfp4(const qrr_kv_nvfp4* cache, int64_t T, const int32_t
  * over the cached positions j <= pos[b] + i (the row's own token included:
  * append first).  A row that sees nothing gives zeros and lse -inf.
  * A query row with a value that is not finite raises QRR_DEV_NONFINITE; a NaN
- * comes through to its out and lse.
+ * comes through to its out and lse.  What lies behind a sequence's last visible
+ * position does not count, whatever it is; a NaN block scale at a position that
+ * only a later row sees (append writes none) reaches the earlier rows' out.
  *   q    bf16, row t at q + t ld_q elements, Hq heads of D; ld_q % 8 == 0
  *   scale > 0 and finite (1 / sqrt(D), usually)
  *   max_new  host bound on cu[b + 1] - cu[b] (1 where cu is NULL); a sequence
  *            with more rows raises QRR_DEV_BAD_INDEX, its outputs unspecified
  *   out  bf16 [T][Hq][D];  lse fp32 [T][Hq] or NULL
  *   workspace  qrr_attention_nvfp4_workspace_bytes(cache, T, Hq, max_new)
- * Hq a multiple of Hkv, T * Hq < 2^31.  Cached values convert exactly; the query is carried
- * in f16 after a power of two a row (exact for values within 2^-29 of the
- * row's largest); p is rounded to f16, all sums are fp32.  Work is cut over
- * the cached tokens and joined in a fixed order: results do not depend on
- * timing. */
+ * Hq a multiple of Hkv, T * Hq < 2^31.  Cached values convert exactly; the
+ * query is carried in f16 after a power of two a row (exact for values within
+ * 2^-29 of the row's largest); p is rounded to f16 (2^-11 of itself, or 2^-32 of
+ * the row's largest p); all sums are fp32.  Work is cut over the cached tokens
+ * and joined in a fixed order: results do not depend on timing. */
 size_t qrr_attention_nvfp4_workspace_bytes(const qrr_kv_nvfp4* cache, int64_t T, int32_t Hq, int32_t max_new);
 qrr_status qrr_attention_nvfp4(const qrr_kv_nvfp4* cache, const void* q, int64_t T, int64_t ld_q, int32_t Hq,
                                const int32_t* cu, const int32_t* pos, int32_t max_new, float scale, void* out,

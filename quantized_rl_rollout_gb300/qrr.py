@@ -280,6 +280,8 @@ class GroupedLinear:
     fixed buffers: the layers' tensors (x, weights, adapters, y) and the
     workspace are bound at construction, checked once, and ``run()`` only
     launches.  Refill x in place between runs; y is rewritten by each run.
+    (Buffers made here belong to the stream that is current now: a ``run`` on
+    another stream has to be ordered behind its work.)
     The numbers are those of ``linear_nvfp4_lora_grouped`` on the same
     tensors, bit for bit (it is the same C call)."""
 
