@@ -429,6 +429,112 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
                                  void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Losses over rows of logits with their gradients, for the training step that
+ * follows a rollout: distillation from a teacher's top logits, and the policy
+ * gradient of the tokens that were taken ("NVIDIA NeMo RL behaalt 48% ...",
+ * the paragraph on importance sampling: the shift between the two engines is
+ * corrected token by token; the sources give no formula for either loss).
+ *
+ * Rows.  logits: bf16 or fp32 (qrr_dtype), row t at logits + t ld elements,
+ * V values; ld >= V, any alignment of the element type.  The gradient dlogits
+ * has the logits' type, row t at dlogits + t ldd; it may be logits itself
+ * (with ldd == ld), but must not overlap it in any other way.  V * the
+ * element's size <= QRR_MAX_LOSS_ROW_BYTES, T <= 2^27.  Logits of -inf are
+ * masked out (q = 0); a row of nothing but -inf has q = 0 everywhere.  A row
+ * with a NaN or +inf raises QRR_DEV_NONFINITE, its outputs unspecified.
+ * Sums are fp32 with the hardware's base-2 exponential (about 2^-22 relative);
+ * results do not depend on timing.
+ *
+ * Teacher.  top_ids int32 [T][k], top_logits fp32 [T][k], 0 <= k <= 1024: the
+ * teacher's logits at k tokens of each row, in any order; a slot with a
+ * negative id is unused, an id >= V is unused and raises QRR_DEV_BAD_INDEX, slots
+ * that name one id add up.  With temperature t (1e-6 .. 1e6):
+ *   q = softmax(logits / t)
+ *   top_lse NULL:      p_j = e^{y_j / t} / sum_i e^{y_i / t}
+ *   top_lse fp32 [T]:  p_j = e^{y_j / t - top_lse}, top_lse the log-sum-exp of the
+ *                      teacher's whole row / t; what is missing, p_r =
+ *                      max(0, 1 - sum_j p_j), is one outcome more, beside q_r,
+ *                      the student's probability outside the ids
+ *   loss = sum_j p_j (ln p_j - ln q_j) [+ p_r (ln p_r - ln q_r)]
+ * (where a row has nothing but -inf outside the ids, q_r = 0, a p_r of up to
+ * 2^-16 counts as rounding: 0).
+ * A row without a used slot has no teacher: loss 0, gradient 0, not read.
+ *
+ * qrr_distill_topk: loss fp32 [T]; stats fp32 [T][2] = (log-sum-exp of the row
+ * / t, that of the logits outside the ids; without top_lse the first again).
+ * qrr_distill_topk_backward: dlogits = grad[t] dloss/dlogits, from the stats
+ * of the forward call with the same arguments.  (q is taken from the fp32
+ * log-sum-exp: its rounding is a relative error of q.)
+ * qrr_distill_topk_grad: loss and dlogits at once, where grad [T] (a weight a
+ * row) is known before the loss: each logit is read once. */
+#define QRR_MAX_LOSS_ROW_BYTES (3u << 19)
+typedef enum qrr_dtype { QRR_DTYPE_BF16 = 0, QRR_DTYPE_FP32 = 1 } qrr_dtype;
+
+qrr_status qrr_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
+                            const float* top_logits, int32_t k, const float* top_lse, float temperature, float* loss,
+                            float* stats, int32_t* dev_status, void* stream);
+qrr_status qrr_distill_topk_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                     const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
+                                     float temperature, const float* stats, const float* grad, void* dlogits,
+                                     int64_t ldd, int32_t* dev_status, void* stream);
+qrr_status qrr_distill_topk_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                 const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
+                                 float temperature, const float* grad, float* loss, void* dlogits, int64_t ldd,
+                                 int32_t* dev_status, void* stream);
+
+/* qrr_token_logprobs_is_grad: qrr_token_logprobs_is and the gradient of
+ * -sum_t A_t w_t logp_t at once, w held fixed:
+ *   dlogits[t][v] = A_t w_t (softmax(logits[t])[v] - [v == tokens[t]])
+ * advantages fp32 [T]; w = min(exp(logp - rollout_logp), cap) (cap <= 0: no
+ * cap), 1 where rollout_logp is NULL (w is then not written and may be NULL).
+ * A negative token is padding: logp = w = 0, gradient 0, not read; a token
+ * >= V likewise, and raises QRR_DEV_BAD_INDEX.  Rows as above. */
+qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                      const int32_t* tokens, const float* advantages, const float* rollout_logp,
+                                      float cap, float* logp, float* w, void* dlogits, int64_t ldd,
+                                      int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Verification of drafted tokens against the target's probabilities, from
+ * given random numbers, with the log-probabilities that the importance-sampling
+ * weights of the training step want.
+ * Sequence b brings the drafts cu[b] .. cu[b + 1] - 1 of the call's T (cu int32
+ * [B + 1], ascending; NULL: T / B each) and one row of target logits more than
+ * drafts: rows cu[b] + b .. cu[b + 1] + b, the last behind its last draft.
+ *   p_i = softmax(target row / t), q_i = softmax(draft row / t)
+ * Drafts d_0, d_1, .. are taken in order while u_i q_i(d_i) < p_i(d_i).  At the
+ * first refusal the next token is argmax_v max(p_i(v) - q_i(v), 0) / e_v (p_i in
+ * the place of the difference where nothing is left of it), behind the last
+ * draft argmax_v p_n(v) / e_v: the lowest index of equals.  With u uniform in
+ * [0, 1) and e exponential the tokens are distributed as drawn from p.
+ *   target        logits [T + B][V], bf16 or fp32 (dtype), rows ld_target apart
+ *   draft         logits [T][V] of the same type, rows ld_draft apart; NULL: the
+ *                 drafts have no probabilities, q_i = [v == d_i]
+ *   drafts        int32 [T]; a negative one ends its sequence's drafts (the next
+ *                 token is drawn from p there), one >= V as well, and raises
+ *                 QRR_DEV_BAD_INDEX
+ *   uniforms      fp32 [T];  noise fp32 [B], rows of V values ld_noise apart, > 0
+ *   temperature   1e-6 .. 1e6, or 0: a draft is taken if it is the target's
+ *                 likeliest token (the lowest index of equals), which is the
+ *                 next token; draft, uniforms and noise are not used
+ *   tokens        int32 [T + B] (out): in the places of b's target rows the
+ *                 drafts taken, the next token, then -1
+ *   accepted      int32 [B] (out): drafts taken
+ *   logp          fp32 [T + B] (out): ln p of each token (softmax(target) where
+ *                 the temperature is 0), 0 beside -1
+ * Logits of -inf are masked out.  A row without a finite logit, or with a NaN or
+ * +inf, raises QRR_DEV_NONFINITE; the token from it is then -1 or unspecified,
+ * in [0, V).  Rows behind a refusal may go unread.  Offsets that descend or
+ * leave [0, T] raise QRR_DEV_BAD_INDEX; nothing is written for that sequence.
+ * Places outside cu[0] .. cu[B] are left as they were.  B <= 2^26, V <= 2^30, T
+ * <= 2^30.  Sums are fp32 with the hardware's base-2 exponential, probabilities
+ * that decide take expf; results do not depend on timing. */
+qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
+                             int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,
+                             const float* uniforms, const float* noise, int64_t ld_noise, float temperature,
+                             int32_t* tokens, int32_t* accepted, float* logp, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* The explicit sync point for device-detected conditions: copies the status
  * word `dev_status` (device int32, as passed to the calls above) into
  * `*host_out` once every call queued on `stream` before it has finished, then

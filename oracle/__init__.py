@@ -28,7 +28,11 @@ written in numpy:
 * ``attention`` -- decode attention over an E4M3 key/value cache with 1x128
   row scales;
 * ``kv_nvfp4`` -- the paged NVFP4 key/value cache (write, read back) and attention
-  over it.
+  over it;
+* ``distill`` -- distillation from a teacher's top logits and the policy gradient
+  of a rollout's tokens, with their gradients in the logits;
+* ``verify``   -- verification of drafted tokens against the target's
+  probabilities.
 
 Sources.  The pages describe QeRL ("QeRL: Beyond Efficiency -- Quantization-
 enhanced Reinforcement Learning for LLMs", abstract; "NVIDIA and MIT Collaborate
@@ -45,4 +49,4 @@ float32 arithmetic (correctly rounded, subnormals kept) produces it; sums of
 products are formed in float64.
 """
 
-from . import formats, nvfp4, fp8, linear, requant, rollout_is, aqn, lora_backward, attention, kv_nvfp4  # noqa: F401
+from . import formats, nvfp4, fp8, linear, requant, rollout_is, aqn, lora_backward, attention, kv_nvfp4, distill, verify  # noqa: F401

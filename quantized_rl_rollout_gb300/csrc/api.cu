@@ -12,6 +12,7 @@
 
 #include "kv_nvfp4.cuh"
 #include "linear.cuh"
+#include "logits.cuh"
 #include "quant.cuh"
 #include "tc.cuh"
 
@@ -866,6 +867,190 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
   if (injected_cuda_fault()) return QRR_ERR_CUDA;
   return from_cuda(
       launch_token_logprob_is(logits, T, V, tokens, rollout_logp, cap, logp, w, dev_status, as_stream(stream)));
+}
+
+namespace {
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+inline bool is_dtype(int32_t d) { return d == QRR_DTYPE_BF16 || d == QRR_DTYPE_FP32; }
+inline size_t dtype_bytes(int32_t d) { return d == QRR_DTYPE_FP32 ? 4 : 2; }
+inline bool is_temperature(float t) { return t >= kMinTemperature && t <= kMaxTemperature; }
+
+// Rows of logits [T][V] with `ld` between them.
+qrr_status check_rows(const void* p, int32_t dtype, int64_t T, int64_t V, int64_t ld) {
+  if (T > 0 && !p) return QRR_ERR_INVALID_ARG;
+  if (T > 1 && ld < V) return QRR_ERR_INVALID_ARG;
+  if (ld < 0 || ld > (int64_t{1} << 40)) return QRR_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % dtype_bytes(dtype) ? QRR_ERR_MISALIGNED : QRR_OK;
+}
+
+qrr_status check_loss_rows(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld) {
+  if (!is_dtype(dtype) || T < 0 || V < 1) return QRR_ERR_INVALID_ARG;
+  if (T > (int64_t{1} << 27) || V > static_cast<int64_t>(QRR_MAX_LOSS_ROW_BYTES / dtype_bytes(dtype)))
+    return QRR_ERR_UNSUPPORTED_SHAPE;
+  return check_rows(logits, dtype, T, V, ld);
+}
+
+// The gradient's rows: the logits' own, or beside them.
+qrr_status check_dlogits(const LogitsLossArgs& a, int32_t dtype) {
+  const qrr_status st = check_rows(a.dlogits, dtype, a.T, a.V, a.ldd);
+  if (st != QRR_OK || a.T == 0) return st;
+  const uintptr_t e = dtype_bytes(dtype), x = reinterpret_cast<uintptr_t>(a.logits), y = reinterpret_cast<uintptr_t>(a.dlogits);
+  if (x == y) return a.T > 1 && a.ld != a.ldd ? QRR_ERR_INVALID_ARG : QRR_OK;
+  return QRR_OK;
+}
+
+qrr_status check_teacher(const LogitsLossArgs& a) {
+  if (a.k < 0 || !is_temperature(a.temperature)) return QRR_ERR_INVALID_ARG;
+  if (a.k > kMaxTop) return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (a.T > 0 && a.k > 0 && (!a.ids || !a.top)) return QRR_ERR_INVALID_ARG;
+  return aligned4(a.ids) && aligned4(a.top) && aligned4(a.top_lse) ? QRR_OK : QRR_ERR_MISALIGNED;
+}
+
+LogitsLossArgs distill_args(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
+                            const float* top_logits, int32_t k, const float* top_lse, float temperature, int32_t* dev_status) {
+  LogitsLossArgs a{};
+  a.logits = logits;
+  a.fp32 = dtype == QRR_DTYPE_FP32;
+  a.T = T;
+  a.V = static_cast<int>(V);
+  a.ld = ld;
+  a.ids = top_ids;
+  a.top = top_logits;
+  a.k = k;
+  a.top_lse = top_lse;
+  a.temperature = temperature;
+  a.status = dev_status;
+  return a;
+}
+
+}  // namespace
+
+qrr_status qrr_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
+                            const float* top_logits, int32_t k, const float* top_lse, float temperature, float* loss,
+                            float* stats, int32_t* dev_status, void* stream) {
+  qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
+  if (st != QRR_OK) return st;
+  LogitsLossArgs a = distill_args(logits, dtype, T, V, ld, top_ids, top_logits, k, top_lse, temperature, dev_status);
+  st = check_teacher(a);
+  if (st != QRR_OK) return st;
+  if (T > 0 && (!loss || !stats)) return QRR_ERR_INVALID_ARG;
+  if (!aligned4(loss) || !aligned4(stats)) return QRR_ERR_MISALIGNED;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  a.loss = loss;
+  a.stats = stats;
+  return from_cuda(launch_logits_loss(a, LossMode::kLoss, as_stream(stream)));
+}
+
+qrr_status qrr_distill_topk_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                     const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
+                                     float temperature, const float* stats, const float* grad, void* dlogits,
+                                     int64_t ldd, int32_t* dev_status, void* stream) {
+  qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
+  if (st != QRR_OK) return st;
+  LogitsLossArgs a = distill_args(logits, dtype, T, V, ld, top_ids, top_logits, k, top_lse, temperature, dev_status);
+  st = check_teacher(a);
+  if (st != QRR_OK) return st;
+  if (T > 0 && (!stats || !grad)) return QRR_ERR_INVALID_ARG;
+  if (!aligned4(stats) || !aligned4(grad)) return QRR_ERR_MISALIGNED;
+  a.stats_in = stats;
+  a.grad = grad;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  st = check_dlogits(a, dtype);
+  if (st != QRR_OK) return st;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  return from_cuda(launch_logits_loss(a, LossMode::kBackward, as_stream(stream)));
+}
+
+qrr_status qrr_distill_topk_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                 const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
+                                 float temperature, const float* grad, float* loss, void* dlogits, int64_t ldd,
+                                 int32_t* dev_status, void* stream) {
+  qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
+  if (st != QRR_OK) return st;
+  LogitsLossArgs a = distill_args(logits, dtype, T, V, ld, top_ids, top_logits, k, top_lse, temperature, dev_status);
+  st = check_teacher(a);
+  if (st != QRR_OK) return st;
+  if (T > 0 && (!loss || !grad)) return QRR_ERR_INVALID_ARG;
+  if (!aligned4(loss) || !aligned4(grad)) return QRR_ERR_MISALIGNED;
+  a.loss = loss;
+  a.grad = grad;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  st = check_dlogits(a, dtype);
+  if (st != QRR_OK) return st;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  return from_cuda(launch_logits_loss(a, LossMode::kGrad, as_stream(stream)));
+}
+
+qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
+                                      const int32_t* tokens, const float* advantages, const float* rollout_logp,
+                                      float cap, float* logp, float* w, void* dlogits, int64_t ldd,
+                                      int32_t* dev_status, void* stream) {
+  qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
+  if (st != QRR_OK) return st;
+  if (T > 0 && (!tokens || !advantages || !logp || (rollout_logp && !w))) return QRR_ERR_INVALID_ARG;
+  if (!aligned4(tokens) || !aligned4(advantages) || !aligned4(rollout_logp) || !aligned4(logp) || !aligned4(w))
+    return QRR_ERR_MISALIGNED;
+  LogitsLossArgs a = distill_args(logits, dtype, T, V, ld, nullptr, nullptr, 1, nullptr, 1.0f, dev_status);
+  a.tokens = tokens;
+  a.advantages = advantages;
+  a.rollout_logp = rollout_logp;
+  a.cap = cap;
+  a.logp = logp;
+  a.w = rollout_logp ? w : nullptr;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  st = check_dlogits(a, dtype);
+  if (st != QRR_OK) return st;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  return from_cuda(launch_logits_loss(a, LossMode::kPolicy, as_stream(stream)));
+}
+
+qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
+                             int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,
+                             const float* uniforms, const float* noise, int64_t ld_noise, float temperature,
+                             int32_t* tokens, int32_t* accepted, float* logp, int32_t* dev_status, void* stream) {
+  if (!is_dtype(dtype) || T < 0 || B < 0 || V < 1) return QRR_ERR_INVALID_ARG;
+  if (!cu && (B == 0 ? T > 0 : T % B != 0)) return QRR_ERR_INVALID_ARG;
+  if (temperature != 0.0f && !is_temperature(temperature)) return QRR_ERR_INVALID_ARG;
+  const bool greedy = temperature == 0.0f;
+  if (T > (int64_t{1} << 30) || B > (1 << 26) || V > (int64_t{1} << 30)) return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (B > 0 && (!target || !tokens || !accepted || !logp)) return QRR_ERR_INVALID_ARG;
+  if (B > 0 && T > 0 && (!drafts || (!greedy && !uniforms))) return QRR_ERR_INVALID_ARG;
+  if (B > 0 && !greedy && (!noise || ld_noise < 0 || (B > 1 && ld_noise < V))) return QRR_ERR_INVALID_ARG;
+  qrr_status st = check_rows(target, dtype, T + B, V, ld_target);
+  if (st != QRR_OK) return st;
+  if (draft && !greedy) {
+    st = check_rows(draft, dtype, T, V, ld_draft);
+    if (st != QRR_OK) return st;
+  }
+  if (!aligned4(drafts) || !aligned4(cu) || !aligned4(uniforms) || !aligned4(noise) || !aligned4(tokens) ||
+      !aligned4(accepted) || !aligned4(logp))
+    return QRR_ERR_MISALIGNED;
+  if (injected_cuda_fault()) return QRR_ERR_CUDA;
+  VerifyArgs a{};
+  a.target = target;
+  a.ld_target = ld_target;
+  a.draft = draft;
+  a.ld_draft = ld_draft;
+  a.T = T;
+  a.B = B;
+  a.V = static_cast<int>(V);
+  a.fp32 = dtype == QRR_DTYPE_FP32;
+  a.drafts = drafts;
+  a.cu = cu;
+  a.uniforms = uniforms;
+  a.noise = noise;
+  a.ld_noise = ld_noise;
+  a.temperature = temperature;
+  a.tokens = tokens;
+  a.accepted = accepted;
+  a.logp = logp;
+  a.status = dev_status;
+  return from_cuda(launch_verify_drafts(a, as_stream(stream)));
 }
 
 qrr_status qrr_get_last_device_status(int32_t* host_out, const int32_t* dev_status, void* stream) {

@@ -1,0 +1,216 @@
+// Rows of logits: what the losses (logits_loss.cu) and the verification of drafts (verify_drafts.cu) share.
+//
+// A row starts anywhere its element type allows (an odd vocabulary, a slice of padded rows), so it is read in granules of
+// 16 aligned bytes: granule i holds the elements i kN - lead .. i kN - lead + kN - 1, lead being the elements between the
+// 16-byte boundary at or before the row's start and that start. The first and the last granule may be cut; what they hold
+// beside the row reads -inf.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "linear.cuh"
+#include "tc.cuh"
+
+namespace qrr {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Element types: Bf16 keeps its bits as uint16_t.
+using Bf16 = uint16_t;
+template <class E>
+constexpr int kPer = 16 / static_cast<int>(sizeof(E));  // elements of a granule
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float to_f32(Bf16 x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ Bf16 from_f32(float x, Bf16) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float from_f32(float x, float) { return x; }
+
+template <class E>
+__device__ __forceinline__ E minus_inf() {
+  if constexpr (sizeof(E) == 2) return 0xFF80u;
+  else return -INFINITY;
+}
+
+__device__ __forceinline__ void unpack(uint4 g, float (&x)[8]) {
+  x[0] = bf16_lo(g.x), x[1] = bf16_hi(g.x), x[2] = bf16_lo(g.y), x[3] = bf16_hi(g.y);
+  x[4] = bf16_lo(g.z), x[5] = bf16_hi(g.z), x[6] = bf16_lo(g.w), x[7] = bf16_hi(g.w);
+}
+__device__ __forceinline__ void unpack(uint4 g, float (&x)[4]) {
+  x[0] = __uint_as_float(g.x), x[1] = __uint_as_float(g.y), x[2] = __uint_as_float(g.z), x[3] = __uint_as_float(g.w);
+}
+
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, x[i]);
+  return m;
+}
+
+// Elements between the 16-byte boundary at or before `row` and it, and the granules of a row of V.
+template <class E>
+__device__ __forceinline__ int lead_of(const E* row) {
+  return static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u) / static_cast<int>(sizeof(E));
+}
+template <class E>
+__host__ __device__ __forceinline__ int granules_of(int lead, int V) {
+  return (lead + V + kPer<E> - 1) / kPer<E>;
+}
+
+// A cut granule: first element e0 (below 0, or with its end behind the row), -inf outside the row.
+template <class E>
+__device__ __noinline__ uint4 load_cut(const E* row, int e0, int V) {
+  float x[kPer<E>];
+#pragma unroll
+  for (int u = 0; u < kPer<E>; ++u) x[u] = e0 + u >= 0 && e0 + u < V ? to_f32(row[e0 + u]) : -INFINITY;
+  return pack(x);
+}
+
+// Running maximum m and sum s of e^{(x - m) / t} of a thread's values, c = log2(e) / t. The difference is taken before the
+// factor: a row at its type's lowest value would overflow with it first. m is -inf while every value is.
+struct Sum {
+  float m = -INFINITY, s = 0.0f;
+
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N], float bmax, float c) {
+    if (bmax > m) {
+      s *= ex2_approx((m - bmax) * c);
+      m = bmax;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;  // nothing but -inf (or NaN, which comes through)
+    float a[4] = {};
+#pragma unroll
+    for (int u = 0; u < N; ++u) a[u & 3] += ex2_approx((x[u] - ref) * c);
+    s += (a[0] + a[1]) + (a[2] + a[3]);
+  }
+  // A sum of no values has s = 0 and m = -inf; a NaN in s stays.
+  __device__ __forceinline__ void merge(float m2, float s2, float c) {
+    const float mx = fmaxf(m, m2), ref = mx == -INFINITY ? 0.0f : mx;
+    s = s * ex2_approx((m - ref) * c) + s2 * ex2_approx((m2 - ref) * c);
+    m = mx;
+  }
+  __device__ __forceinline__ void merge_warp(float c) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
+      merge(m2, s2, c);
+    }
+  }
+};
+
+// ---- clusters ---------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_cluster(const uint64_t* p, uint32_t rank) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// ---- host -------------------------------------------------------------------
+
+constexpr float kMinTemperature = 1e-6f, kMaxTemperature = 1e6f;
+
+// Launch on clusters of `cluster` CTAs along x.
+template <class... K, class... A>
+cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, int cluster, int threads, size_t smem, cudaStream_t stream,
+                            A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A&&>(args)...);
+}
+
+// ---- arguments ----------------------------------------------------------------
+
+// A call of logits_loss.cu: the rows, the teacher or the tokens, and the outputs.
+struct LogitsLossArgs {
+  const void* logits;
+  int64_t ld, T;
+  int V, fp32;
+  // distillation
+  const int32_t* ids;  // [T][k]
+  const float* top;    // [T][k]
+  const float* top_lse;
+  int k;
+  float temperature;
+  const float* grad;
+  const float* stats_in;
+  float* loss;
+  float* stats;
+  // policy gradient
+  const int32_t* tokens;
+  const float* advantages;
+  const float* rollout_logp;
+  float cap;
+  float* logp;
+  float* w;
+  void* dlogits;
+  int64_t ldd;
+  int32_t* status;
+};
+enum class LossMode { kLoss, kGrad, kBackward, kPolicy };
+constexpr int kMaxTop = 1024;
+// Bytes of a row that the largest cluster holds on chip.
+constexpr int64_t kMaxLossRowBytes = 3 << 19;
+cudaError_t launch_logits_loss(const LogitsLossArgs& a, LossMode mode, cudaStream_t stream);
+
+struct VerifyArgs {
+  const void* target;  // [T + B][V]
+  int64_t ld_target;
+  const void* draft;  // [T][V] or null
+  int64_t ld_draft;
+  int64_t T;
+  int B, V, fp32;
+  const int32_t* drafts;  // [T]
+  const int32_t* cu;      // [B + 1] or null
+  const float* uniforms;  // [T]
+  const float* noise;     // [B][V]
+  int64_t ld_noise;
+  float temperature;  // 0: the likeliest token
+  int32_t* tokens;    // [T + B]
+  int32_t* accepted;  // [B]
+  float* logp;        // [T + B]
+  int32_t* status;
+};
+cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t stream);
+
+}  // namespace qrr

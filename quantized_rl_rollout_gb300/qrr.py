@@ -24,6 +24,8 @@ DEV_NONFINITE = 0x1
 DEV_TIMEOUT = 0x2
 DEV_SCALE_RANGE = 0x4
 DEV_BAD_INDEX = 0x8
+DTYPE_BF16 = 0
+DTYPE_FP32 = 1
 OP_QUANTIZE_NVFP4 = 0
 OP_LINEAR_NVFP4_LORA = 1
 OP_REQUANTIZE_WEIGHTS = 2
@@ -103,6 +105,16 @@ SIGNATURES = {
     "qrr_aqn_noise_probe": (ctypes.c_int, [_c_p, _c_i64, _c_i64, ctypes.c_uint64, _c_i32, _c_i32, _c_p]),
     "qrr_token_logprobs_is": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, ctypes.c_float, _c_p, _c_p, _c_p,
                                              _c_p]),
+    "qrr_distill_topk": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, ctypes.c_float, _c_p,
+                                        _c_p, _c_p, _c_p]),
+    "qrr_distill_topk_backward": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p,
+                                                 ctypes.c_float, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
+    "qrr_distill_topk_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, ctypes.c_float,
+                                             _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
+    "qrr_token_logprobs_is_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, ctypes.c_float,
+                                                  _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
+    "qrr_verify_drafts": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p,
+                                         _c_i64, ctypes.c_float, _c_p, _c_p, _c_p, _c_p, _c_p]),
     "qrr_workspace_bytes": (_c_sz, [_c_i32, _c_i64, _c_i64, _c_i64, _c_i32]),
     "qrr_wait_probe": (ctypes.c_int, [_c_i64, _c_i32, _c_p, _c_p, _c_p]),
     "qrr_stream_probe": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
@@ -465,6 +477,169 @@ def token_logprobs_is(logits, tokens, rollout_logp=None, cap=0.0, logp=None, w=N
                                        _ptr(w) if rollout_logp is not None else None, _ptr(dev_status),
                                        _stream(stream)), "qrr_token_logprobs_is")
     return logp if rollout_logp is None else (logp, w)
+
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+def _logit_rows(x, rows, v, name, dtype=None):
+    """(dtype number, row stride) of logits [rows, v] whose rows are contiguous (a slice of wider rows will do)."""
+    if x.dtype not in _DTYPES or not x.is_cuda or (dtype is not None and x.dtype != dtype):
+        raise TypeError(f"{name} must be a CUDA {'bfloat16 or float32' if dtype is None else dtype} tensor, got {x.dtype}")
+    if tuple(x.shape) != (rows, v):
+        raise ValueError(f"{name} must be {[rows, v]}, got {list(x.shape)}")
+    s = x.stride()
+    if (v > 1 and s[1] != 1) or (rows > 1 and s[0] < v):
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return _DTYPES[x.dtype], s[0] if rows > 1 else v
+
+
+def _vector(x, n, dtype, name, device):
+    """Address of a contiguous vector of n values (None stays)."""
+    if x is None:
+        return None
+    if x.dtype != dtype or not x.is_cuda or not x.is_contiguous() or x.numel() != n:
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} values")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, the logits on {device}")
+    return x.data_ptr()
+
+
+def _same_device(device, *tensors):
+    if device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"the logits are on {device}, which is not the current device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"every tensor must be on {device}, got one on {t.device}")
+
+
+def _loss_rows(logits, dlogits, stream, grad=True):
+    """Of a call on rows of logits: (T, V, dtype number, row stride) and the gradient's tensor with its row stride."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [T, V], got {list(logits.shape)}")
+    t, v = logits.shape
+    dtype, ld = _logit_rows(logits, t, v, "logits")
+    _same_device(logits.device, dlogits)
+    if not grad:
+        return (dtype, t, v, ld), None, 0
+    if dlogits is None:
+        return (dtype, t, v, ld), _on_stream((t, v), logits.dtype, logits.device, stream), v
+    return (dtype, t, v, ld), dlogits, _logit_rows(dlogits, t, v, "dlogits", logits.dtype)[1]
+
+
+def _teacher(top_ids, top_logits, top_lse, temperature, t, device):
+    if top_ids.dim() != 2 or top_ids.shape[0] != t or top_logits.shape != top_ids.shape:
+        raise ValueError(f"top_ids and top_logits must both be [{t}, k], got {list(top_ids.shape)} and {list(top_logits.shape)}")
+    n = top_ids.numel()
+    return (_vector(top_ids, n, torch.int32, "top_ids", device), _vector(top_logits, n, torch.float32, "top_logits", device),
+            top_ids.shape[1], _vector(top_lse, t, torch.float32, "top_lse", device), float(temperature))
+
+
+def distill_topk(logits, top_ids, top_logits, top_lse=None, temperature=1.0, loss=None, stats=None, dev_status=None,
+                 stream=None):
+    """Distillation from a teacher's top logits: (loss fp32 [T], stats fp32 [T, 2] for ``distill_topk_backward``).
+
+    ``logits`` bf16 or fp32 [T, V]; ``top_ids`` int32 and ``top_logits`` fp32 [T, k], a negative id an unused slot;
+    ``top_lse`` fp32 [T]: the log-sum-exp of the teacher's whole row over the temperature, for a tail (see
+    ``qrr_distill_topk``)."""
+    rows, _, _ = _loss_rows(logits, None, stream, grad=False)
+    t, dev = rows[1], logits.device
+    teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
+    loss = _on_stream((t,), torch.float32, dev, stream) if loss is None else loss
+    stats = _on_stream((t, 2), torch.float32, dev, stream) if stats is None else stats
+    _check(lib().qrr_distill_topk(logits.data_ptr(), *rows, *teacher, _vector(loss, t, torch.float32, "loss", dev),
+                                  _vector(stats, 2 * t, torch.float32, "stats", dev), _ptr(dev_status), _stream(stream)),
+           "qrr_distill_topk")
+    return loss, stats
+
+
+def distill_topk_backward(logits, top_ids, top_logits, stats, grad, top_lse=None, temperature=1.0, dlogits=None,
+                          dev_status=None, stream=None):
+    """dlogits [T, V] = grad[t] dloss[t]/dlogits in the logits' type, from the ``stats`` of ``distill_topk`` with the same
+    arguments; ``dlogits`` may be ``logits`` itself."""
+    rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
+    t, dev = rows[1], logits.device
+    teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
+    _check(lib().qrr_distill_topk_backward(logits.data_ptr(), *rows, *teacher, _vector(stats, 2 * t, torch.float32, "stats", dev),
+                                           _vector(grad, t, torch.float32, "grad", dev), dlogits.data_ptr(), ldd,
+                                           _ptr(dev_status), _stream(stream)), "qrr_distill_topk_backward")
+    return dlogits
+
+
+def distill_topk_grad(logits, top_ids, top_logits, grad, top_lse=None, temperature=1.0, loss=None, dlogits=None,
+                      dev_status=None, stream=None):
+    """(loss, dlogits) of ``distill_topk`` and ``distill_topk_backward`` at once, where the rows' weights ``grad`` are known
+    beforehand: the logits are read once."""
+    rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
+    t, dev = rows[1], logits.device
+    teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
+    loss = _on_stream((t,), torch.float32, dev, stream) if loss is None else loss
+    _check(lib().qrr_distill_topk_grad(logits.data_ptr(), *rows, *teacher, _vector(grad, t, torch.float32, "grad", dev),
+                                       _vector(loss, t, torch.float32, "loss", dev), dlogits.data_ptr(), ldd, _ptr(dev_status),
+                                       _stream(stream)), "qrr_distill_topk_grad")
+    return loss, dlogits
+
+
+def token_logprobs_is_grad(logits, tokens, advantages, rollout_logp=None, cap=0.0, logp=None, w=None, dlogits=None,
+                           dev_status=None, stream=None):
+    """(logp, w, dlogits): ``token_logprobs_is`` and the gradient of -sum A w logp in the logits (bf16 or fp32) at once, w
+    held fixed (None, for 1, without ``rollout_logp``); ``dlogits`` may be ``logits`` itself."""
+    rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
+    t, dev = rows[1], logits.device
+    logp = _on_stream((t,), torch.float32, dev, stream) if logp is None else logp
+    if rollout_logp is None:
+        w = None
+    elif w is None:
+        w = _on_stream((t,), torch.float32, dev, stream)
+    _check(lib().qrr_token_logprobs_is_grad(logits.data_ptr(), *rows, _vector(tokens, t, torch.int32, "tokens", dev),
+                                            _vector(advantages, t, torch.float32, "advantages", dev),
+                                            _vector(rollout_logp, t, torch.float32, "rollout_logp", dev), float(cap),
+                                            _vector(logp, t, torch.float32, "logp", dev), _vector(w, t, torch.float32, "w", dev),
+                                            dlogits.data_ptr(), ldd, _ptr(dev_status), _stream(stream)),
+           "qrr_token_logprobs_is_grad")
+    return logp, w, dlogits
+
+
+def verify_drafts(target, drafts, uniforms=None, noise=None, draft_logits=None, cu=None, temperature=1.0, tokens=None,
+                  accepted=None, logp=None, dev_status=None, stream=None):
+    """Test drafted tokens against the target's probabilities and draw the token that follows (see ``qrr_verify_drafts``).
+
+    ``target`` logits [T + B, V] (bf16 or fp32), ``drafts`` int32 [T]: sequence b has the drafts cu[b] .. cu[b + 1] - 1 (as
+    many as any other without ``cu``) and one row more, from cu[b] + b on.  ``draft_logits`` [T, V] is None for drafts
+    without probabilities; ``uniforms`` fp32 [T] in [0, 1) and ``noise`` fp32 [B, V], exponential, are not needed at
+    temperature 0.  Returns (tokens int32 [T + B], -1 behind the last of a sequence; accepted int32 [B]; logp fp32
+    [T + B])."""
+    if target.dim() != 2:
+        raise ValueError(f"target must be [T + B, V], got {list(target.shape)}")
+    rows, v = target.shape
+    t = drafts.numel()
+    b, dev = rows - t, target.device
+    if b < 0:
+        raise ValueError(f"target must have a row more than drafts for every sequence: {rows} rows, {t} drafts")
+    dtype, ld_target = _logit_rows(target, rows, v, "target")
+    ld_draft = ld_noise = 0
+    if temperature == 0:
+        draft_logits = uniforms = noise = None
+    else:
+        if (t and uniforms is None) or (b and noise is None):
+            raise ValueError("uniforms and noise are needed but at temperature 0")
+        if draft_logits is not None:
+            ld_draft = _logit_rows(draft_logits, t, v, "draft_logits", target.dtype)[1]
+        if noise is not None:
+            ld_noise = _logit_rows(noise, b, v, "noise", torch.float32)[1]
+    _same_device(dev, draft_logits, noise)
+    cu_ptr = _vector(cu, b + 1, torch.int32, "cu", dev)
+    tokens = _on_stream((rows,), torch.int32, dev, stream) if tokens is None else tokens
+    accepted = _on_stream((b,), torch.int32, dev, stream) if accepted is None else accepted
+    logp = _on_stream((rows,), torch.float32, dev, stream) if logp is None else logp
+    _check(lib().qrr_verify_drafts(target.data_ptr(), ld_target, _ptr(draft_logits), ld_draft, dtype, t, b, v,
+                                   _vector(drafts, t, torch.int32, "drafts", dev), cu_ptr,
+                                   _vector(uniforms, t, torch.float32, "uniforms", dev), _ptr(noise), ld_noise,
+                                   float(temperature), _vector(tokens, rows, torch.int32, "tokens", dev),
+                                   _vector(accepted, b, torch.int32, "accepted", dev),
+                                   _vector(logp, rows, torch.float32, "logp", dev), _ptr(dev_status), _stream(stream)),
+           "qrr_verify_drafts")
+    return tokens, accepted, logp
 
 
 def lora_backward_workspace_bytes(M, N, K, r) -> int:
