@@ -85,37 +85,134 @@ __device__ __noinline__ uint4 load_cut(const E* row, int e0, int V) {
   return pack(x);
 }
 
-// Running maximum m and sum s of e^{(x - m) / t} of a thread's values, c = log2(e) / t. The difference is taken before the
-// factor: a row at its type's lowest value would overflow with it first. m is -inf while every value is.
+// ---- sums of e^{x / t} ----------------------------------------------------------
+//
+// With c = log2(e) / t, a sum is kept as s = sum 2^{c x - r} for a reference r = rint(c m), m one of the logits. fp32's
+// exponents reach far enough that m need not be the largest: it is the largest of the first values that a thread sees, and
+// the values behind them cost a multiply-add, an exponential and an addition each, no comparison. A sum that gets near
+// the end of the range is taken again with the largest of all (add_largest). References are whole numbers so that a sum
+// moves to another by a power of two, and c x - r is rounded once.
+// A reference of more than 2^20 (rows at their type's lowest value, say, where c m itself may overflow) takes the
+// difference of the logits first: r = c m in effect, 2^{c (x - m)}.
+
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f32x2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The reference that a logit m makes (m = -inf: 0, for sums without a value).
+struct Ref {
+  float m, r;
+  bool far;
+  __device__ __forceinline__ Ref(float m_, float c) : m(m_ == -INFINITY ? 0.0f : m_) {
+    r = rintf(m * c);
+    far = !(fabsf(r) <= 0x1p20f);
+  }
+  __device__ __forceinline__ float operator()(float x, float c) const {
+    return ex2_approx(far ? (x - m) * c : fmaf(x, c, -r));
+  }
+};
+
+// The largest of a warp's values (NaN aside).
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 struct Sum {
   float m = -INFINITY, s = 0.0f;
 
-  template <int N>
-  __device__ __forceinline__ void add(const float (&x)[N], float bmax, float c) {
-    if (bmax > m) {
-      s *= ex2_approx((m - bmax) * c);
-      m = bmax;
-    }
-    const float ref = m == -INFINITY ? 0.0f : m;  // nothing but -inf (or NaN, which comes through)
-    float a[4] = {};
-#pragma unroll
-    for (int u = 0; u < N; ++u) a[u & 3] += ex2_approx((x[u] - ref) * c);
-    s += (a[0] + a[1]) + (a[2] + a[3]);
+  // What a sum at m is worth at another reference, not below it.
+  __device__ __forceinline__ static float moved(float m, const Ref& to, float c) {
+    const Ref from(m, c);
+    return m == -INFINITY ? 0.0f : ex2_approx(from.far || to.far ? (m - to.m) * c : from.r - to.r);
   }
-  // A sum of no values has s = 0 and m = -inf; a NaN in s stays.
+  // A sum without values has s = 0 and m = -inf; a NaN in s stays.
   __device__ __forceinline__ void merge(float m2, float s2, float c) {
-    const float mx = fmaxf(m, m2), ref = mx == -INFINITY ? 0.0f : mx;
-    s = s * ex2_approx((m - ref) * c) + s2 * ex2_approx((m2 - ref) * c);
-    m = mx;
+    const Ref to(fmaxf(m, m2), c);
+    s = s * moved(m, to, c) + s2 * moved(m2, to, c);
+    m = fmaxf(m, m2);
   }
+  // Of a warp's sums, the same in every lane: one move each, to the largest reference.
   __device__ __forceinline__ void merge_warp(float c) {
+    const float to = warp_max(m);
+    s *= moved(m, Ref(to, c), c);
+    m = to;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const float m2 = __shfl_xor_sync(0xFFFFFFFFu, m, o), s2 = __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      merge(m2, s2, c);
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  }
+  // Values with their largest: the reference follows it.
+  template <int N>
+  __device__ __forceinline__ void add_largest(const float (&x)[N], float largest, float c) {
+    if (largest > m) {
+      s *= moved(m, Ref(largest, c), c);
+      m = largest;
     }
+    const Ref ref(m, c);
+#pragma unroll
+    for (int u = 0; u < N; ++u) s += ref(x[u], c);
+  }
+  // Whether the reference that is kept served.
+  __device__ __forceinline__ bool served() const { return m > -INFINITY && s < 0x1p64f; }
+};
+
+// A thread's sum at a reference that stays, in two accumulators of two values.
+template <class E>
+struct FixedSum {
+  uint64_t c2, nr2, a0, a1;
+  __device__ __forceinline__ void start(const Ref& ref, float c) {
+    c2 = f32x2(c, c);
+    nr2 = f32x2(-ref.r, -ref.r);
+    a0 = a1 = 0;
+  }
+  __device__ __forceinline__ void add(uint4 g) {
+    float x[kPer<E>];
+    unpack(g, x);
+#pragma unroll
+    for (int u = 0; u < kPer<E>; u += 4) {
+      float e0, e1, e2, e3;
+      f32x2(fma2(f32x2(x[u], x[u + 1]), c2, nr2), e0, e1);
+      f32x2(fma2(f32x2(x[u + 2], x[u + 3]), c2, nr2), e2, e3);
+      a0 = add2(a0, f32x2(ex2_approx(e0), ex2_approx(e1)));
+      a1 = add2(a1, f32x2(ex2_approx(e2), ex2_approx(e3)));
+    }
+  }
+  __device__ __forceinline__ float total() const {
+    float x, y;
+    f32x2(add2(a0, a1), x, y);
+    return x + y;
   }
 };
+
+// The sum of n granules load(0) .. load(n - 1), once more with the largest of them.
+template <class E, class Load>
+__device__ __noinline__ Sum sum_largest(int n, Load load, float c) {
+  Sum sum;
+  for (int i = 0; i < n; ++i) {
+    float x[kPer<E>];
+    unpack(load(i), x);
+    sum.add_largest(x, max_of(x), c);
+  }
+  return sum;
+}
 
 // ---- clusters ---------------------------------------------------------------
 
@@ -133,6 +230,11 @@ __device__ __forceinline__ uint64_t ld_cluster(const uint64_t* p, uint32_t rank)
   uint64_t v;
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
   return v;
+}
+// 16 bytes to the same variable of CTA `rank`.
+__device__ __forceinline__ void st_cluster(const float4* p, uint32_t rank, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }

@@ -27,26 +27,11 @@ namespace {
 
 constexpr int kMaxThreads = 256;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
+constexpr float kLn2 = 0.6931471805599453f;
 // A rest of the teacher's that is no more than the rounding of its log-sum-exp and of the sum of p_j: beside a student
 // without any, it is none.
 constexpr float kDust = 1.0f / 65536;
 
-// What a CTA tells the others of its part of the row.
-struct Part {
-  float m_out, s_out;  // logits outside the ids
-  float m_top, s_top;  // at the ids
-};
-
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
@@ -71,6 +56,11 @@ __device__ __forceinline__ void store_range(E* out, int e0, int e1, Block block,
 
 // A CTA takes part rank of `parts` of row blockIdx.x / parts: `per` granules. In every mode but kBackward, whose sums are
 // known, the parts of a row are a cluster.
+//
+// A part's life is a chain of short steps (ids, row, sum, exchange, gradient), and several parts an SM hide one
+// another's: what does not need the row (the teacher, the logits at its ids, read beside the row by every part) is done
+// while the row is on its way, and the exchange writes a part's sum into the other CTAs ahead of the barrier, so that
+// behind it everything is at hand.
 template <class E, LossMode M>
 __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLossArgs a, const int parts, const int per) {
   constexpr int N = kPer<E>;
@@ -85,29 +75,35 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
   uint4* const tile = reinterpret_cast<uint4*>(smem);
   E* const held = reinterpret_cast<E*>(smem);
   int* const sid = reinterpret_cast<int*>(tile + per);  // id of a slot, -1: unused
-  float* const sx = reinterpret_cast<float*>(sid + k);  // its logit, where it lies in this part or this is the first
-  float* const sp = sx + k;                             // the teacher's probability
-  int* const sown = reinterpret_cast<int*>(sp + k);     // of the slots with one id, the one that speaks for them
-  __shared__ float2 sums[kMaxThreads / 32];
-  __shared__ Part part, whole;
+  float* const sy = reinterpret_cast<float*>(sid + k);  // the teacher's logit
+  float* const sp = sy + k;                             // its probability
+  float* const sx = sp + k;                             // the row's logit
+  __shared__ uint64_t loaded;
+  __shared__ float4 shares[8 * kMaxThreads / 32];  // of every part's warps: reference and sum outside the ids, whether slots share one
+  __shared__ int abort, twice_here;
 
   const int lead = lead_of(row), granules = granules_of<E>(lead, V);
   const int g0 = min(rank * per, granules), g1 = min(g0 + per, granules), base = g0 * N - lead;
   const int e0 = max(base, 0), e1 = min(g1 * N - lead, V);  // this part's elements
 
+  if (tid == 0) {
+    mbar_init(&loaded, 1);
+    fence_barrier_init();
+    abort = twice_here = 0;
+  }
   bool any = false;
   for (int j = tid; j < k; j += threads) {
     int id = __ldg(kPolicy ? a.tokens + t : a.ids + t * k + j);
+    if constexpr (!kPolicy) sy[j] = __ldg(a.top + t * k + j);
     if (id >= V) {
       flag(a.status, QRR_DEV_BAD_INDEX);
       id = -1;
     }
     sid[j] = id;
     any |= id >= 0;
-    // the first part takes the loss, so it wants the logits of all ids (before another part writes over its own)
-    if (kSums && (rank == 0 || kPolicy) && id >= 0) sx[j] = to_f32(row[id]);
   }
-  if (!__syncthreads_or(any)) {  // nothing to learn: the whole cluster ends here
+  if (kSums && parts > 1) cluster_arrive();  // this CTA runs
+  if (!__syncthreads_or(any)) {              // nothing to learn: the whole cluster ends here
     if constexpr (kWrites)
       if (e0 < e1)
         store_range(out, e0, e1, [](int) { return make_uint4(0, 0, 0, 0); }, [](int) { return from_f32(0.0f, E{}); });
@@ -119,14 +115,30 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
         if (a.w) a.w[t] = 0.0f;
       }
     }
+    if (kSums && parts > 1) cluster_wait();
     return;
   }
 
-  for (int g = g0 + tid; g < g1; g += threads) {
-    const int e = g * N - lead;
-    if (e >= 0 && e + N <= V) cp_async16(tile + (g - g0), row + e);
-    else tile[g - g0] = load_cut(row, e, V);
+  // The part's whole granules by bulk copies, the row's cut ones by a thread each.
+  const int whole0 = base < 0 ? g0 + 1 : g0, whole1 = g1 > g0 && g1 * N - lead > V ? g1 - 1 : g1;
+  if (tid == 0) {
+    const uint32_t bytes = whole1 > whole0 ? 16u * static_cast<uint32_t>(whole1 - whole0) : 0u;
+    mbar_arrive_expect_tx(&loaded, bytes);
+    constexpr uint32_t kChunk = 16 << 10;
+    const uint8_t* const src = reinterpret_cast<const uint8_t*>(row + (whole0 * N - lead));
+    for (uint32_t at = 0; at < bytes; at += kChunk)
+      bulk_load(reinterpret_cast<uint8_t*>(tile + (whole0 - g0)) + at, src + at, min(kChunk, bytes - at), &loaded);
   }
+  if (tid == threads - 1 && g0 < g1) {
+    if (whole0 > g0) tile[0] = load_cut(row, base, V);
+    if (whole1 < g1 && (whole1 > g0 || whole0 == g0)) tile[whole1 - g0] = load_cut(row, whole1 * N - lead, V);
+  }
+  // The logits at the ids: of every id (no part writes a gradient over them before the exchange); without an exchange, of
+  // this part's alone. Each thread's first is on its way until it is wanted.
+  auto wanted = [&](int j) { return j < k && (kSums ? sid[j] >= 0 : sid[j] >= e0 && sid[j] < e1); };
+  const E x_first = wanted(tid) ? row[sid[tid]] : E{};
+  for (int j = tid + threads; j < k; j += threads)
+    if (wanted(j)) sx[j] = to_f32(row[sid[j]]);
 
   // The teacher, by every warp on its own: mass = sum_j p_j, and the log-sum-exp that its logits are measured from as
   // y_max / t + ln y_sum (without a tail) or lse_teacher.
@@ -136,25 +148,24 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
   if constexpr (kPolicy) {
     if (tid == 0) sp[0] = 1.0f;
   } else {
-    const float* const top = a.top + t * k;
     if (tail) {
       lse_teacher = __ldg(a.top_lse + t);
     } else {
       y_max = -INFINITY;
       for (int j = lane; j < k; j += 32)
-        if (sid[j] >= 0) y_max = fmaxf(y_max, __ldg(top + j));
+        if (sid[j] >= 0) y_max = fmaxf(y_max, sy[j]);
       y_max = warp_max(y_max);
       if (y_max == -INFINITY) y_max = 0.0f;
       y_sum = 0.0f;
       for (int j = lane; j < k; j += 32)
-        if (sid[j] >= 0) y_sum += expf((__ldg(top + j) - y_max) * inv_t);
+        if (sid[j] >= 0) y_sum += expf((sy[j] - y_max) * inv_t);
       y_sum = warp_sum(y_sum);
     }
     mass = 0.0f;
     const float norm = 1.0f / y_sum;
     for (int j = lane; j < k; j += 32) {
       float p = 0.0f;
-      if (sid[j] >= 0) p = tail ? expf(fmaf(__ldg(top + j), inv_t, -lse_teacher)) : expf((__ldg(top + j) - y_max) * inv_t) * norm;
+      if (sid[j] >= 0) p = tail ? expf(fmaf(sy[j], inv_t, -lse_teacher)) : expf((sy[j] - y_max) * inv_t) * norm;
       mass += p;
       if (warp == 0) sp[j] = p;
     }
@@ -162,109 +173,119 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
   }
   const float rest = tail ? fmaxf(1.0f - mass, 0.0f) : 0.0f;  // p_r
 
-  cp_async_wait_all();
+  // The ids' logits are taken out of the part. Slots that name one id find out by writing their numbers to its place.
+  mbar_wait(&loaded, 0, &abort, a.status);
+  auto number = [](int j) {
+    if constexpr (sizeof(E) == 2) return static_cast<E>(j);
+    else return __int_as_float(j);
+  };
+  auto bits = [](E x) {
+    if constexpr (sizeof(E) == 2) return static_cast<int>(x);
+    else return __float_as_int(x);
+  };
+  if (wanted(tid)) sx[tid] = to_f32(x_first);
+  __syncthreads();  // the cut granules
+  for (int j = tid; j < k; j += threads)
+    if (sid[j] >= e0 && sid[j] < e1) held[sid[j] - base] = number(j);
   __syncthreads();
-  // Warp 0 takes the ids' logits out of the part. Slots that name one id find out by writing their numbers to its place:
-  // the one that stays there speaks for all.
-  bool twice = false;
-  if (warp == 0) {
-    auto each = [&](auto f) {
-      for (int j = lane; j < k; j += 32) {
-        const int id = sid[j];
-        if (id >= e0 && id < e1) f(j, id - base);
-      }
-      __syncwarp();
-    };
-    auto number = [](int j) {
-      if constexpr (sizeof(E) == 2) return static_cast<E>(j);
-      else return __int_as_float(j);
-    };
-    each([&](int j, int at) { sx[j] = to_f32(held[at]); });
-    each([&](int j, int at) { held[at] = number(j); });
-    each([&](int j, int at) {
-      int o;
-      if constexpr (sizeof(E) == 2) o = held[at];
-      else o = __float_as_int(held[at]);
-      sown[j] = o;
-      twice |= o != j;
-    });
-    each([&](int, int at) { held[at] = minus_inf<E>(); });
-    twice = __any_sync(kAll, twice);
-    if constexpr (kSums) {
-      Sum top;
-      for (int j = lane; j < k; j += 32) {
-        const int id = sid[j];
-        if (id < e0 || id >= e1 || sown[j] != j) continue;
-        const float x[1] = {sx[j]};
-        top.add(x, x[0], c);
-      }
-      top.merge_warp(c);
-      if (lane == 0) {
-        part.m_top = top.m;
-        part.s_top = top.s;
-      }
+  for (int j = tid; j < k; j += threads)
+    if (sid[j] >= e0 && sid[j] < e1) {
+      if (bits(held[sid[j] - base]) != j) twice_here = 1;
+      held[sid[j] - base] = minus_inf<E>();
     }
-  }
   __syncthreads();
 
   // Of the whole row: references and sums outside the ids and at them.
-  float m_out, s_out, m, s;
+  float m_out, s_out, m, s, known = 0.0f, known_out = 0.0f;
+  bool twice = twice_here;
+  // the first slot of its id, where some share one
+  auto first = [&](int j) {
+    for (int i = 0; i < j; ++i)
+      if (sid[i] == sid[j]) return false;
+    return true;
+  };
   if constexpr (kSums) {
     Sum mine;
-    for (int g = tid; g < g1 - g0; g += threads) {
+    const int n = (g1 - g0 - tid + threads - 1) / threads;  // granules of this thread (0 or below: none)
+    if (n > 0) {
+      auto load = [&](int i) { return tile[tid + i * threads]; };
       float x[N];
-      unpack(tile[g], x);
-      mine.add(x, max_of(x), c);
+      unpack(load(0), x);
+      mine.m = max_of(x);
+      const Ref ref(mine.m, c);
+      FixedSum<E> sum;
+      sum.start(ref, c);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) sum.add(load(i));
+      mine.s = sum.total();
+      if (ref.far || !mine.served()) mine = sum_largest<E>(n, load, c);
     }
     mine.merge_warp(c);
-    if (lane == 0) sums[warp] = make_float2(mine.m, mine.s);
-    __syncthreads();
-    if (warp == 0) {
-      mine = Sum{};
-      if (lane < threads / 32) mine = Sum{sums[lane].x, sums[lane].y};
-      mine.merge_warp(c);
-      if (lane == 0) {
-        part.m_out = mine.m;
-        part.s_out = mine.s;
-      }
-      __syncwarp();
-    }
+    const int warps = threads / 32;
+    const float4 share = make_float4(mine.m, mine.s, twice ? 1.0f : 0.0f, 0.0f);
     if (parts > 1) {
+      cluster_wait();  // every CTA runs
+      if (lane < parts) st_cluster(shares + rank * warps + warp, lane, share);
       cluster_arrive();
-      cluster_wait();
+    } else if (lane == 0) {
+      shares[warp] = share;
     }
-    if (warp == 0) {
-      Sum outside, top;
-      if (lane < parts) {
-        outside.m = ld_cluster(&part.m_out, lane);
-        outside.s = ld_cluster(&part.s_out, lane);
-        top.m = ld_cluster(&part.m_top, lane);
-        top.s = ld_cluster(&part.s_top, lane);
-      }
-      outside.merge_warp(c);
-      top.merge_warp(c);
-      if (lane == 0) whole = Part{outside.m, outside.s, top.m, top.s};
+    // meanwhile the sum at the ids, by every warp on its own
+    auto at_ids = [&](bool once) {
+      Sum top;
+      for (int j = lane; j < k; j += 32)
+        if (sid[j] >= 0) top.m = fmaxf(top.m, sx[j]);
+      top.m = warp_max(top.m);
+      const Ref ref(top.m, c);
+      for (int j = lane; j < k; j += 32)
+        if (sid[j] >= 0 && (!once || first(j))) top.s += ref(sx[j], c);
+      top.s = warp_sum(top.s);
+      return top;
+    };
+    Sum top = at_ids(false);
+    if (parts > 1) cluster_wait();
+    else __syncthreads();
+    Sum outside;
+    for (int i = lane; i < parts * warps; i += 32) {
+      const float4 of = shares[i];
+      outside.merge(of.x, of.y, c);
+      twice |= of.z != 0.0f;
     }
-    if (parts > 1) cluster_arrive();  // nobody ends while another reads its part
-    __syncthreads();
-    m_out = whole.m_out, s_out = whole.s_out;
-    Sum all;
-    all.m = m_out, all.s = s_out;
-    all.merge(whole.m_top, whole.s_top, c);
+    outside.merge_warp(c);
+    twice = __any_sync(kAll, twice);
+    m_out = outside.m, s_out = outside.s;
+    if (twice) top = at_ids(true);
+    Sum all{m_out, s_out};
+    all.merge(top.m, top.s, c);
     m = all.m, s = all.s;
   } else {
-    m = __ldg(a.stats_in + 2 * t) * a.temperature;
-    m_out = __ldg(a.stats_in + 2 * t + 1) * a.temperature;
+    known = __ldg(a.stats_in + 2 * t);
+    known_out = __ldg(a.stats_in + 2 * t + 1);
+    m = known * a.temperature;
+    m_out = known_out * a.temperature;
     s = s_out = 1.0f;
   }
   const bool empty = m == -INFINITY;  // a row of -inf alone has no probabilities: q = 0
   if (empty) m = 0.0f, s = 1.0f;
   const bool none = m_out == -INFINITY;
   if (none) m_out = 0.0f, s_out = 1.0f;
+  // of the whole row and of its logits outside the ids; known log-sum-exps are references themselves
+  Ref ref(m, c), ref_out(m_out, c);
+  if constexpr (!kSums) {
+    ref.r = empty ? 0.0f : known * kLog2e;
+    ref_out.r = none ? 0.0f : known_out * kLog2e;
+  }
 
   float factor;
   if constexpr (kPolicy) {
-    const float lp = (sx[0] - m) - logf(s);
+    float lp;
+    if (ref.far) {
+      lp = (sx[0] - m) - logf(s);
+    } else {  // s = 2^e f: r + e is exact, and what is left is rounded as the small number that it is
+      int e;
+      const float f = frexpf(s, &e);
+      lp = (fmaf(sx[0], c, -(ref.r + static_cast<float>(e))) - log2f(f)) * kLn2;
+    }
     float w = 1.0f;
     if (a.rollout_logp) {
       w = expf(lp - __ldg(a.rollout_logp + t));
@@ -283,17 +304,18 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
 
   if constexpr (kWrites) {
     const float inv_s = 1.0f / s;
-    // outside the ids: e^{(x - ref) / t} times `scale`
-    const float ref = tail ? m_out : m;
+    // outside the ids: e^{x / t} over that at `at` times `scale`
+    const Ref at = tail ? ref_out : ref;
     float scale = factor * inv_s;
     if (tail) {
-      const float q_rest = s_out * ex2_approx((m_out - m) * c) * inv_s;
+      const float up = !kSums ? (known_out - known) * kLog2e : ref.far || ref_out.far ? (m_out - m) * c : ref_out.r - ref.r;
+      const float q_rest = s_out * ex2_approx(up) * inv_s;
       scale = none ? 0.0f : factor * (q_rest - rest) / s_out;
     }
-    auto value = [&](float x) { return ex2_approx((x - ref) * c) * scale; };
     if (e0 < e1) {
       const int shift = -base;  // of an element in `held`
       const bool same = lead_of(out) == lead;
+      const uint64_t c2 = f32x2(c, c), nr2 = f32x2(-at.r, -at.r), scale2 = f32x2(scale, scale);
       store_range(
           out, e0, e1,
           [&](int e) {
@@ -304,32 +326,40 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
 #pragma unroll
               for (int u = 0; u < N; ++u) x[u] = to_f32(held[e + shift + u]);
             }
+            if (!at.far) {
 #pragma unroll
-            for (int u = 0; u < N; ++u) x[u] = value(x[u]);
+              for (int u = 0; u < N; u += 2) {
+                float y, z;
+                f32x2(fma2(f32x2(x[u], x[u + 1]), c2, nr2), y, z);
+                f32x2(mul2(f32x2(ex2_approx(y), ex2_approx(z)), scale2), x[u], x[u + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int u = 0; u < N; ++u) x[u] = at(x[u], c) * scale;
+            }
             return pack(x);
           },
-          [&](int e) { return from_f32(value(to_f32(held[e + shift])), E{}); });
+          [&](int e) { return from_f32(at(to_f32(held[e + shift]), c) * scale, E{}); });
     }
     __syncthreads();
-    if (warp == 0) {
-      for (int j = lane; j < k; j += 32) {
-        const int id = sid[j];
-        if (id < e0 || id >= e1 || sown[j] != j) continue;
-        float p = sp[j];
-        if (twice) {
-          p = 0.0f;
-          for (int i = 0; i < k; ++i) p += sid[i] == id ? sp[i] : 0.0f;
-        }
-        out[id] = from_f32(factor * (ex2_approx((sx[j] - m) * c) * inv_s - p), E{});
+    for (int j = tid; j < k; j += threads) {
+      const int id = sid[j];
+      if (id < e0 || id >= e1) continue;
+      float p = sp[j];
+      if (twice) {
+        if (!first(j)) continue;
+        p = 0.0f;
+        for (int i = j; i < k; ++i) p += sid[i] == id ? sp[i] : 0.0f;
       }
+      out[id] = from_f32(factor * (ref(sx[j], c) * inv_s - p), E{});
     }
   }
-  // The loss, by the last warp: sum_j p_j ((y_j - (x_j - m)) / t - (lse_teacher - ln s)), its few terms in 64 bits.
+  // The loss, by the last warp: sum_j p_j ((y_j - (x_j - m)) / t - (lse_teacher - (lse - m / t))), its few terms in 64 bits.
   if (kSums && !kPolicy && rank == 0 && warp == threads / 32 - 1) {
     double cross = 0.0, sum_p = 0.0;
     for (int j = lane; j < k; j += 32)
       if (sid[j] >= 0 && sp[j] > 0.0f) {
-        const double p = sp[j], y = __ldg(a.top + t * k + j), x = sx[j];
+        const double p = sp[j], y = sy[j], x = sx[j];
         cross += p * (y - (x - static_cast<double>(m)));
         sum_p += p;
       }
@@ -339,11 +369,19 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
       sum_p += __shfl_xor_sync(kAll, sum_p, o);
     }
     if (lane == 0) {
-      const double inv = 1.0 / static_cast<double>(a.temperature), ln_s = log(static_cast<double>(s));
+      const double inv = 1.0 / static_cast<double>(a.temperature);
+      // of a sum's log-sum-exp, what it is above m / t
+      auto above = [&](const Ref& r, float sum) {
+        const double ln = log(static_cast<double>(sum));
+        if (r.far) return ln;
+        const double back = inv / static_cast<double>(c);  // from powers of 2 at this c
+        return (static_cast<double>(r.r) - static_cast<double>(r.m) * static_cast<double>(c) + ln * 1.4426950408889634) * back;
+      };
+      const double ln_s = above(ref, s);
       const double lse_y = tail ? static_cast<double>(lse_teacher) : static_cast<double>(y_max) * inv + log(static_cast<double>(y_sum));
       double loss = cross * inv - sum_p * (lse_y - ln_s), lse = static_cast<double>(m) * inv + ln_s, lse_out = lse;
       if (tail) {
-        const double ln_out = none ? -INFINITY : log(static_cast<double>(s_out));
+        const double ln_out = none ? -INFINITY : above(ref_out, s_out);
         lse_out = static_cast<double>(m_out) * inv + ln_out;
         if (rest > (none ? kDust : 0.0f))
           loss += static_cast<double>(rest) * (log(static_cast<double>(rest)) -
@@ -356,8 +394,6 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
       }
     }
   }
-  if constexpr (kSums)
-    if (parts > 1) cluster_wait();
 }
 
 // Bytes of a row that a CTA holds, at most, where fewer parts would do.

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const Verify
         const float top = max_of(x);
         if constexpr (kGreedy)
           if (top > sum.m) where = rank * per + (here * kInFlight + u) * kThreads + tid;
-        sum.add(x, top, c);
+        sum.add_largest(x, top, c);
       }
       if (!last) continue;
       const float m = sum.m;
@@ -217,6 +217,8 @@ __global__ void __launch_bounds__(kThreads, 3) verify_drafts_kernel(const Verify
         if (rank == 0) flag(a.status, QRR_DEV_NONFINITE);
         if (x.m == -INFINITY) x.m = 0.0f, x.s = 1.0f;  // a row of -inf alone: no probabilities
       }
+      const Ref ref(x.m, c);  // from here on a sum of e^{(x - m) / t}
+      if (!ref.far) x.s *= ex2_approx(fmaf(-x.m, c, ref.r));
       whole[tid] = x;
     }
     if (tid == 0) s_refused = kGroup;
