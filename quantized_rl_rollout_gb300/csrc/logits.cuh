@@ -214,6 +214,16 @@ __device__ __noinline__ Sum sum_largest(int n, Load load, float c) {
   return sum;
 }
 
+// Whether the phase with the given parity is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
 // ---- clusters ---------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -231,10 +241,9 @@ __device__ __forceinline__ uint64_t ld_cluster(const uint64_t* p, uint32_t rank)
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
   return v;
 }
-// 16 bytes to the same variable of CTA `rank`.
-__device__ __forceinline__ void st_cluster(const float4* p, uint32_t rank, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
+// To the same variable of CTA `rank`.
+__device__ __forceinline__ void st_cluster(const float2* p, uint32_t rank, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }

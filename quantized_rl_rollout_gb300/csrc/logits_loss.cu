@@ -10,14 +10,18 @@
 // Policy gradient of token a with advantage A: logp = x_a - lse, w = min(e^{logp - logp_rollout}, cap),
 //   d(-A w logp)/dx_v = A w (q_v - [v = a]), w held fixed: the same form with p_a = 1 and the factor A w.
 //
-// Bound by memory: a logit is read once and its gradient written once (the loss alone only reads). The two sums of a row are
-// known when all of it has been read, so it stays on chip until then: a cluster of CTAs holds it in shared memory, a
-// contiguous part each, and joins maxima and sums over distributed shared memory.
+// Bound by memory: a logit is read from it once and its gradient written once (the loss alone only reads). The sums of a row
+// are known when all of it has been read, so the gradient reads it again, from L2: a CTA takes a whole row, two CTAs an SM
+// (78 MB of rows of 128256 bf16, of which half is still wanted, in 129 MB), and a row is read again before others push it
+// out. Where there are few rows, a cluster of CTAs takes one, a contiguous part each, and joins sums over distributed
+// shared memory.
 //
-// The logits at the teacher's ids are taken out of the held row (-inf in their place), so that the sum outside them is one
-// of positive terms, not a difference. Sums are fp32; e^x is the hardware's base-2 approximation (about 2^-22 relative)
-// where it is taken a logit and expf where it is taken an id; a loss is a small difference of large logarithms, and its k
-// terms are added in 64 bits.
+// With a tail, the logits at the teacher's ids are left out of the sum (marked in shared memory, a byte a granule), so that
+// the sum outside them is one of positive terms, not a difference. Sums are fp32; e^x is the hardware's base-2 approximation (about 2^-22 relative)
+// where it is taken a logit and expf where it is taken an id. A loss is a small difference of large logarithms: each is
+// taken from a whole power of two, so that it is rounded as a small number.
+#include <algorithm>
+
 #include "logits.cuh"
 #include "once_per_device.cuh"
 
@@ -25,12 +29,32 @@ namespace qrr {
 
 namespace {
 
-constexpr int kMaxThreads = 256;
+constexpr int kMaxThreads = 512, kMaxParts = 8;
+constexpr int kBackwardThreads = 256;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kLn2 = 0.6931471805599453f;
 // A rest of the teacher's that is no more than the rounding of its log-sum-exp and of the sum of p_j: beside a student
 // without any, it is none.
 constexpr float kDust = 1.0f / 65536;
+
+// L2's treatment of what is read: once, or again soon.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t read_again() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy));
+  return v;
+}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -38,13 +62,128 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// out[e0 .. e1) of a row = value(e), whole granules at once: block(e) gives those of kPer elements from e on.
+// Part `rank` of a row: `per` granules, elements e0 .. e1 - 1; element e stands at e - base of the CTA's tile.
+template <class E>
+struct Part {
+  const E* row;
+  int V, lead, g0, g1, base, e0, e1;
+
+  __device__ __forceinline__ Part(const E* row_, int V_, int rank, int per) : row(row_), V(V_), lead(lead_of(row_)) {
+    const int granules = granules_of<E>(lead, V);
+    g0 = min(rank * per, granules);
+    g1 = min(g0 + per, granules);
+    base = g0 * kPer<E> - lead;
+    e0 = max(base, 0);
+    e1 = min(g1 * kPer<E> - lead, V);
+  }
+  __device__ __forceinline__ bool has(int id) const { return id >= e0 && id < e1; }
+  // the granules that lie in the row as a whole
+  __device__ __forceinline__ int whole0() const { return base < 0 ? g0 + 1 : g0; }
+  __device__ __forceinline__ int whole1() const { return g1 > g0 && g1 * kPer<E> - lead > V ? g1 - 1 : g1; }
+  // f(granule number) for the cut ones, by a thread each.
+  template <class F>
+  __device__ __forceinline__ void cut(int tid, int threads, F f) const {
+    const int w0 = whole0(), w1 = whole1();
+    if (g0 == g1) return;
+    if (tid == 0 && w0 > g0) f(g0);
+    if (tid == threads - 1 && w1 < g1 && (w1 > g0 || w0 == g0)) f(w1);
+  }
+  // Bulk copies of the whole granules to a tile, counted on `bar` with its one arrival (by one thread).
+  __device__ __forceinline__ void copy(uint4* tile, uint64_t* bar) const {
+    const int w0 = whole0(), w1 = whole1();
+    const uint32_t bytes = w1 > w0 ? 16u * static_cast<uint32_t>(w1 - w0) : 0u;
+    mbar_arrive_expect_tx(bar, bytes);
+    constexpr uint32_t kChunk = 16 << 10;
+    const uint8_t* const src = reinterpret_cast<const uint8_t*>(granules() + w0);
+    for (uint32_t at = 0; at < bytes; at += kChunk)
+      bulk_load(reinterpret_cast<uint8_t*>(tile + (w0 - g0)) + at, src + at, min(kChunk, bytes - at), bar);
+  }
+  __device__ __forceinline__ const uint4* granules() const { return reinterpret_cast<const uint4*>(row - lead); }
+  __device__ __forceinline__ uint4 load_cut(int i) const { return qrr::load_cut(row, i * kPer<E> - lead, V); }
+};
+
+// The teacher's slots of a row, in shared memory.
+struct Slots {
+  int* id;   // -1: unused
+  float* y;  // the teacher's logit
+  float* p;  // its probability
+  float* x;  // the row's logit
+  int k;
+  __device__ __forceinline__ Slots(uint8_t* at, int k_) : k(k_) {
+    id = reinterpret_cast<int*>(at);
+    y = reinterpret_cast<float*>(id + k);
+    p = y + k;
+    x = p + k;
+  }
+  // False: unused.
+  __device__ __forceinline__ bool set(int j, int given, float logit, int V, int32_t* status) const {
+    if (given >= V) flag(status, QRR_DEV_BAD_INDEX);
+    const bool used = given >= 0 && given < V;
+    id[j] = used ? given : -1;
+    y[j] = logit;
+    return used;
+  }
+  // Whether slot j is the first of its id.
+  __device__ __forceinline__ bool first(int j) const {
+    for (int i = 0; i < j; ++i)
+      if (id[i] == id[j]) return false;
+    return true;
+  }
+  // What the teacher gives the id of slot j, its first.
+  __device__ __forceinline__ float all(int j) const {
+    float sum = 0.0f;
+    for (int i = j; i < k; ++i) sum += id[i] == id[j] ? p[i] : 0.0f;
+    return sum;
+  }
+};
+
+// mass = sum_j p_j, rest = p_r, and the log-sum-exp that the teacher's logits are measured from: y_sum = sum 2^{c y - r} at
+// the reference of y_max (without a tail) or lse.
+struct Teacher {
+  float mass, rest, y_max, y_sum, lse;
+};
+
+// By a warp; the slots' p_j are written.
+__device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse, const Slots& s, float c, int lane) {
+  Teacher r{0.0f, 0.0f, 0.0f, 1.0f, 0.0f};
+  const float inv_t = 1.0f / a.temperature;
+  if (a.top_lse) {
+    r.lse = top_lse;
+  } else {
+    r.y_max = -INFINITY;
+    for (int j = lane; j < s.k; j += 32)
+      if (s.id[j] >= 0) r.y_max = fmaxf(r.y_max, s.y[j]);
+    r.y_max = warp_max(r.y_max);
+    if (r.y_max == -INFINITY) r.y_max = 0.0f;
+    const Ref ref(r.y_max, c);
+    r.y_sum = 0.0f;
+    for (int j = lane; j < s.k; j += 32) {
+      const float p = s.id[j] >= 0 ? ref.far ? expf((s.y[j] - ref.m) * inv_t) : exp2f(fmaf(s.y[j], c, -ref.r)) : 0.0f;
+      s.p[j] = p;
+      r.y_sum += p;
+    }
+    r.y_sum = warp_sum(r.y_sum);
+  }
+  const float norm = 1.0f / r.y_sum;
+  for (int j = lane; j < s.k; j += 32) {
+    float p = 0.0f;
+    if (s.id[j] >= 0) p = a.top_lse ? expf(fmaf(s.y[j], inv_t, -r.lse)) : s.p[j] * norm;
+    r.mass += p;
+    s.p[j] = p;
+  }
+  r.mass = warp_sum(r.mass);
+  r.rest = a.top_lse ? fmaxf(1.0f - r.mass, 0.0f) : 0.0f;
+  return r;
+}
+
+// out[e0 .. e1) of a row, whole granules at once: block(e) gives kPer elements from e on, one(e) a single one.
 template <class E, class Block, class One>
-__device__ __forceinline__ void store_range(E* out, int e0, int e1, Block block, One one) {
+__device__ __forceinline__ void store_range(E* out, int e0, int e1, int tid, int threads, Block block, One one) {
   constexpr int N = kPer<E>;
+  if (e0 >= e1) return;
   const int lead = lead_of(out);
   const int first = (e0 + lead) / N, last = (e1 + lead + N - 1) / N;
-  for (int g = first + threadIdx.x; g < last; g += blockDim.x) {
+  for (int g = first + tid; g < last; g += threads) {
     const int f = g * N - lead;
     if (f >= e0 && f + N <= e1) {
       __stcs(reinterpret_cast<uint4*>(out + f), block(f));
@@ -54,59 +193,310 @@ __device__ __forceinline__ void store_range(E* out, int e0, int e1, Block block,
   }
 }
 
-// A CTA takes part rank of `parts` of row blockIdx.x / parts: `per` granules. In every mode but kBackward, whose sums are
-// known, the parts of a row are a cluster.
-//
-// A part's life is a chain of short steps (ids, row, sum, exchange, gradient), and several parts an SM hide one
-// another's: what does not need the row (the teacher, the logits at its ids, read beside the row by every part) is done
-// while the row is on its way, and the exchange writes a part's sum into the other CTAs ahead of the barrier, so that
-// behind it everything is at hand.
-template <class E, LossMode M>
-__global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLossArgs a, const int parts, const int per) {
+template <class E>
+__device__ __forceinline__ void store_zeros(E* out, const Part<E>& part, int tid, int threads) {
+  store_range(out, part.e0, part.e1, tid, threads, [](int) { return make_uint4(0, 0, 0, 0); },
+              [](int) { return from_f32(0.0f, E{}); });
+}
+
+// The gradient outside the ids: e^{x / t} over that at `at`, times `scale`.
+struct Gradient {
+  Ref at;
+  float c, scale;
+  __device__ __forceinline__ float operator()(float x) const { return at(x, c) * scale; }
+  template <int N>
+  __device__ __forceinline__ uint4 block(float (&x)[N]) const {
+    if (!at.far) {
+      const uint64_t c2 = f32x2(c, c), nr2 = f32x2(-at.r, -at.r), scale2 = f32x2(scale, scale);
+#pragma unroll
+      for (int u = 0; u < N; u += 2) {
+        float y, z;
+        f32x2(fma2(f32x2(x[u], x[u + 1]), c2, nr2), y, z);
+        f32x2(mul2(f32x2(ex2_approx(y), ex2_approx(z)), scale2), x[u], x[u + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) x[u] = (*this)(x[u]);
+    }
+    return pack(x);
+  }
+};
+
+// use(i, load(i)) for i = first, first + step, .. below end, kInFlight loads at a time.
+template <int kInFlight, class Load, class Use>
+__device__ __forceinline__ void stream(int first, int end, int step, Load load, Use use) {
+  int i = first;
+  for (; i + (kInFlight - 1) * step < end; i += kInFlight * step) {
+    uint4 g[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) g[u] = load(i + u * step);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) use(i + u * step, g[u]);
+  }
+  uint4 g[kInFlight];
+#pragma unroll
+  for (int u = 0; u < kInFlight; ++u)
+    if (i + u * step < end) g[u] = load(i + u * step);
+#pragma unroll
+  for (int u = 0; u < kInFlight; ++u)
+    if (i + u * step < end) use(i + u * step, g[u]);
+}
+
+// The gradient of a part to its row of it, from `row` (element e's place in memory or in a tile) by load(granule).
+template <int kInFlight, class E, class Load>
+__device__ __forceinline__ void store_gradient(E* out, const Part<E>& part, const E* row, const Gradient& of, int tid, int threads, Load load) {
   constexpr int N = kPer<E>;
-  constexpr bool kPolicy = M == LossMode::kPolicy, kWrites = M != LossMode::kLoss, kSums = M != LossMode::kBackward;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  auto one = [&](int e) { return from_f32(of(to_f32(row[e])), E{}); };
+  if (lead_of(out) == part.lead) {
+    uint4* const to = reinterpret_cast<uint4*>(out - part.lead);
+    stream<kInFlight>(part.whole0() + tid, part.whole1(), threads, load, [&](int i, uint4 g) {
+      float x[N];
+      unpack(g, x);
+      __stcs(to + i, of.block(x));
+    });
+    part.cut(tid, threads, [&](int i) {
+      for (int e = max(i * N - part.lead, 0); e < min((i + 1) * N - part.lead, part.V); ++e) out[e] = one(e);
+    });
+  } else {
+    store_range(
+        out, part.e0, part.e1, tid, threads,
+        [&](int e) {
+          float x[N];
+#pragma unroll
+          for (int u = 0; u < N; ++u) x[u] = to_f32(row[e + u]);
+          return of.block(x);
+        },
+        one);
+  }
+}
+
+// And at the ids of this part, behind it: factor (q_j - p_j).
+template <class E>
+__device__ __forceinline__ void store_ids(E* out, const Part<E>& part, const Slots& s, bool twice, const Ref& ref, float c, float inv_s,
+                                          float factor, int tid, int threads) {
+  for (int j = tid; j < s.k; j += threads) {
+    if (!part.has(s.id[j]) || (twice && !s.first(j))) continue;
+    const float p = twice ? s.all(j) : s.p[j];
+    out[s.id[j]] = from_f32(factor * (ref(s.x[j], c) * inv_s - p), E{});
+  }
+}
+
+// A sum s = sum 2^{c x - r} as a power of two and a small logarithm: log2 of it and its reference = whole + part.
+struct Log2 {
+  float whole, part;
+  __device__ __forceinline__ Log2(const Ref& ref, float s) {
+    int e;
+    part = log2f(frexpf(s, &e));
+    whole = ref.r + static_cast<float>(e);  // exact
+  }
+};
+
+// ln of e^{x / t} / s: what is left of c x behind the whole powers of two is rounded as the small number that it is.
+__device__ __forceinline__ float ln_share(float x, const Ref& ref, float s, const Log2& log2, float c, float inv_t) {
+  // c x may overflow where x / t does not, and beside such numbers the sum's own power of two is nothing
+  if (ref.far || !(fabsf(x) < 1e30f)) return (x - ref.m) * inv_t - logf(s);
+  return (fmaf(x, c, -log2.whole) - log2.part) * kLn2;
+}
+
+// What a CTA's threads tell one another about a row.
+struct RowInfo {
+  Teacher teacher;
+  float m_top;               // the largest logit at the ids, the reference of the row's sums
+  float weight, rollout;     // the gradient's, or the advantage; the token's log-probability in the rollout
+  int again;                 // whether the sums are to be taken once more
+  int twice;                 // whether slots share an id
+  float m, s, m_out, s_out;  // references and sums of the whole row, and of its logits outside the ids (with a tail)
+  float m_at, scale;         // the gradient outside the ids
+  float inv_s, factor;       // and at them
+  float lse, lse_at;         // kBackward: known, of m and m_at
+};
+
+// The loss of a row, by a warp.
+template <LossMode M>
+__device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, const Slots& s, const RowInfo& info, float c, int lane) {
+  const bool empty = info.m == -INFINITY, none = info.m_out == -INFINITY;
+  const float sum = empty ? 1.0f : info.s, inv_t = 1.0f / a.temperature;
+  const Ref ref(info.m, c), ref_out(info.m_out, c), ref_y(info.teacher.y_max, c);
+  const Log2 log2(ref, sum), log2_y(ref_y, info.teacher.y_sum);
+  const Teacher& y = info.teacher;
+  float loss = 0.0f;
+  for (int j = lane; j < s.k; j += 32)
+    if (s.id[j] >= 0 && s.p[j] > 0.0f) {
+      const float ln_p = a.top_lse ? fmaf(s.y[j], inv_t, -y.lse) : ln_share(s.y[j], ref_y, y.y_sum, log2_y, c, inv_t);
+      loss += s.p[j] * (ln_p - ln_share(s.x[j], ref, sum, log2, c, inv_t));
+    }
+  loss = warp_sum(loss);
+  if (lane != 0) return;
+  float lse = ref.far ? ref.m * inv_t + logf(sum) : fmaf(log2.whole, kLn2, log2.part * kLn2), lse_out = lse;
+  if (empty) lse = lse_out = -INFINITY;
+  if (a.top_lse) {
+    const Log2 log2_out(ref_out, none ? 1.0f : info.s_out);
+    lse_out = none ? -INFINITY : ref_out.far ? ref_out.m * inv_t + logf(info.s_out) : fmaf(log2_out.whole, kLn2, log2_out.part * kLn2);
+    if (y.rest > (none ? kDust : 0.0f)) {
+      const float ln_q = none ? -INFINITY : ref.far || ref_out.far ? (ref_out.m - ref.m) * inv_t + logf(info.s_out) - logf(sum)
+                                                                   : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
+      loss += y.rest * (logf(y.rest) - ln_q);
+    }
+  }
+  a.loss[t] = loss;
+  if constexpr (M == LossMode::kLoss) {
+    a.stats[2 * t] = lse;
+    a.stats[2 * t + 1] = lse_out;
+  }
+  if (!(fabsf(ref.m) < INFINITY) || !(sum < INFINITY) || !(y.mass < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
+}
+
+// The sum at the ids, each once, by a warp.
+__device__ __forceinline__ Sum sum_at_ids(const Slots& slots, const RowInfo& info, float c, int lane) {
+  Sum top{info.m_top, 0.0f};
+  const Ref ref(top.m, c);
+  for (int j = lane; j < slots.k; j += 32)
+    if (slots.id[j] >= 0 && (!info.twice || slots.first(j))) top.s += ref(slots.x[j], c);
+  top.s = warp_sum(top.s);
+  return top;
+}
+
+// What follows from the references and sums of the row and (with a tail) outside the ids, whose sum at the row's reference
+// is q_rest. By a warp; `writes`: of the row's parts, this one writes what is the row's.
+template <bool kPolicy>
+__device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& all,
+                                         const Sum& outside, float q_rest, bool tail, float c, int lane, bool writes) {
+  const float inv_t = kPolicy ? 1.0f : 1.0f / a.temperature;
+  const Ref ref(all.m, c);
+  const bool bare = all.m == -INFINITY, none = outside.m == -INFINITY;
+  const float sum = bare ? 1.0f : all.s;  // a row of -inf alone has no probabilities: q = 0
+  float factor = info.weight * inv_t;
+  if constexpr (kPolicy) {
+    const float lp = ln_share(slots.x[0], ref, sum, Log2(ref, sum), c, inv_t);
+    float w = 1.0f;
+    if (a.rollout_logp) {
+      w = expf(lp - info.rollout);
+      if (a.cap > 0.0f) w = fminf(w, a.cap);
+    }
+    factor *= w;
+    if (writes && lane == 0) {
+      a.logp[t] = lp;
+      if (a.w) a.w[t] = w;
+      if (!(fabsf(ref.m) < INFINITY) || !(sum < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
+    }
+  }
+  if (lane == 0) {
+    const float inv_s = 1.0f / sum;
+    info.m = all.m, info.s = all.s, info.m_out = outside.m, info.s_out = outside.s;
+    info.m_at = tail ? outside.m : all.m;
+    info.scale = !tail ? factor * inv_s : none ? 0.0f : factor * (q_rest * inv_s - info.teacher.rest) / outside.s;
+    info.inv_s = inv_s;
+    info.factor = factor;
+  }
+}
+
+// From sums at the reference of the ids. False if that served badly: the sums that are divided by have to be there, far
+// from the ends of fp32's range.
+template <bool kPolicy>
+__device__ __forceinline__ bool conclude_first(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& top,
+                                               float total, bool tail, float c, int lane, bool writes) {
+  auto served = [](float x) { return x > 0x1p-60f && x < 0x1p64f; };
+  const Sum outside{top.m, total}, all{top.m, tail ? total + top.s : total};
+  if (!served(all.s) || (tail && !served(total)) || top.m == -INFINITY) return false;
+  conclude<kPolicy>(a, t, slots, info, all, outside, total, tail, c, lane, writes);
+  return true;
+}
+
+// From sums at the largest logits.
+template <bool kPolicy>
+__device__ __forceinline__ void conclude_largest(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& top,
+                                                 const Sum& outside, bool tail, float c, int lane, bool writes) {
+  Sum all = outside;
+  if (tail) all.merge(top.m, top.s, c);
+  conclude<kPolicy>(a, t, slots, info, all, outside, outside.s * Sum::moved(outside.m, Ref(all.m, c), c), tail, c, lane, writes);
+}
+
+// From known log-sum-exps, which are references themselves, not rounded to whole numbers. By one thread.
+__device__ __forceinline__ void conclude_known(const LogitsLossArgs& a, int64_t t, RowInfo& info) {
+  const bool tail = a.top_lse;
+  const float lse = __ldg(a.stats_in + 2 * t), lse_out = __ldg(a.stats_in + 2 * t + 1);
+  info.lse = lse;
+  info.lse_at = tail ? lse_out : lse;
+  info.inv_s = 1.0f;
+  info.factor = info.weight / a.temperature;
+  info.scale = !tail ? info.factor : lse_out == -INFINITY ? 0.0f : info.factor * (ex2_approx((lse_out - lse) * kLog2e) - info.teacher.rest);
+  if (!(info.teacher.mass < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
+}
+__device__ __forceinline__ Ref known_ref(float lse, float temperature, float c) {
+  Ref ref(lse * temperature, c);
+  if (lse > -INFINITY) ref.r = lse * kLog2e;
+  return ref;
+}
+
+// Granule g without the marked elements.
+template <class E>
+__device__ __forceinline__ uint4 without(uint4 g, uint32_t marked) {
+  if (marked == 0) return g;
+  float x[kPer<E>];
+  unpack(g, x);
+#pragma unroll
+  for (int u = 0; u < kPer<E>; ++u)
+    if (marked >> u & 1u) x[u] = -INFINITY;
+  return pack(x);
+}
+
+// Marks an id of a part (a byte a granule, a bit an element). True if it was marked before, which is another slot's doing.
+template <class E>
+__device__ __forceinline__ bool mark(uint32_t* marks, int id, int base) {
+  const int at = id - base, bit = 8 * (at / kPer<E> % 4) + at % kPer<E>;
+  return atomicOr(&marks[at / kPer<E> / 4], 1u << bit) >> bit & 1u;
+}
+
+// ---- losses -------------------------------------------------------------------------
+//
+// A CTA takes part blockIdx.x % parts of row blockIdx.x / parts: `per` granules. The parts of a row are a cluster.
+//
+// A gradient reads its row again, so what counts is that it is still in L2: two CTAs of 512 threads an SM with eight
+// granules a thread under way (step batch below: 375 us; three and four CTAs of 256: 400 and 419). A loss alone reads once:
+// six CTAs of 256 threads hide one another's ends (2048 rows of 128256 bf16: 74 us; two of 512: 89).
+template <LossMode M>
+struct Shape {
+  static constexpr bool kTwice = M != LossMode::kLoss;
+  static constexpr int kThreads = kTwice ? 512 : 256, kCtas = kTwice ? 2 : 6, kInFlight = kTwice ? 8 : 4;
+};
+
+template <class E, LossMode M>
+__global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_loss_kernel(const LogitsLossArgs a, const int parts, const int per) {
+  constexpr int N = kPer<E>;
+  constexpr bool kPolicy = M == LossMode::kPolicy, kWrites = M != LossMode::kLoss;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads / 32;
   const int64_t t = blockIdx.x / parts;
-  const int rank = blockIdx.x % parts, k = kPolicy ? 1 : a.k, V = a.V;
-  const E* const row = static_cast<const E*>(a.logits) + t * a.ld;
+  const int rank = blockIdx.x % parts, k = kPolicy ? 1 : a.k;
+  const Part<E> part(static_cast<const E*>(a.logits) + t * a.ld, a.V, rank, per);
   E* const out = kWrites ? static_cast<E*>(a.dlogits) + t * a.ldd : nullptr;
+  const float inv_t = kPolicy ? 1.0f : 1.0f / a.temperature, c = kLog2e * inv_t;
+  const bool tail = !kPolicy && a.top_lse;
 
   extern __shared__ __align__(16) uint8_t smem[];
-  uint4* const tile = reinterpret_cast<uint4*>(smem);
-  E* const held = reinterpret_cast<E*>(smem);
-  int* const sid = reinterpret_cast<int*>(tile + per);  // id of a slot, -1: unused
-  float* const sy = reinterpret_cast<float*>(sid + k);  // the teacher's logit
-  float* const sp = sy + k;                             // its probability
-  float* const sx = sp + k;                             // the row's logit
-  __shared__ uint64_t loaded;
-  __shared__ float4 shares[8 * kMaxThreads / 32];  // of every part's warps: reference and sum outside the ids, whether slots share one
-  __shared__ int abort, twice_here;
+  const Slots slots(smem, k);
+  uint32_t* const marks = reinterpret_cast<uint32_t*>(smem + 16 * k);
+  __shared__ RowInfo info;
+  __shared__ float2 sums[kMaxThreads / 32];
+  __shared__ float2 shares[2][kMaxParts];  // of every part: sum and whether slots share an id; the second time reference and sum
 
-  const int lead = lead_of(row), granules = granules_of<E>(lead, V);
-  const int g0 = min(rank * per, granules), g1 = min(g0 + per, granules), base = g0 * N - lead;
-  const int e0 = max(base, 0), e1 = min(g1 * N - lead, V);  // this part's elements
-
-  if (tid == 0) {
-    mbar_init(&loaded, 1);
-    fence_barrier_init();
-    abort = twice_here = 0;
-  }
+  float weight = 0.0f, rollout = 0.0f;
+  if (kWrites) weight = __ldg((kPolicy ? a.advantages : a.grad) + t);
+  if (kPolicy && a.rollout_logp) rollout = __ldg(a.rollout_logp + t);
+  const float top_lse = tail ? __ldg(a.top_lse + t) : 0.0f;
   bool any = false;
-  for (int j = tid; j < k; j += threads) {
-    int id = __ldg(kPolicy ? a.tokens + t : a.ids + t * k + j);
-    if constexpr (!kPolicy) sy[j] = __ldg(a.top + t * k + j);
-    if (id >= V) {
-      flag(a.status, QRR_DEV_BAD_INDEX);
-      id = -1;
-    }
-    sid[j] = id;
-    any |= id >= 0;
+  for (int j = tid; j < k; j += threads)
+    any |= slots.set(j, __ldg(kPolicy ? a.tokens + t : a.ids + t * k + j), kPolicy ? 0.0f : __ldg(a.top + t * k + j), a.V, a.status);
+  if constexpr (!kPolicy)
+    for (int i = tid; i < (per + 15) / 16; i += threads) reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
+  if (tid == 0) {
+    info.weight = weight;
+    info.rollout = rollout;
+    info.twice = 0;
+    if constexpr (kPolicy) slots.p[0] = 1.0f;
   }
-  if (kSums && parts > 1) cluster_arrive();  // this CTA runs
-  if (!__syncthreads_or(any)) {              // nothing to learn: the whole cluster ends here
-    if constexpr (kWrites)
-      if (e0 < e1)
-        store_range(out, e0, e1, [](int) { return make_uint4(0, 0, 0, 0); }, [](int) { return from_f32(0.0f, E{}); });
+  if (parts > 1) cluster_arrive();  // this CTA runs
+  if (!__syncthreads_or(any)) {     // nothing to learn: the whole cluster ends here
+    if constexpr (kWrites) store_zeros(out, part, tid, threads);
     if (rank == 0 && tid == 0) {
       if constexpr (M == LossMode::kLoss || M == LossMode::kGrad) a.loss[t] = 0.0f;
       if constexpr (M == LossMode::kLoss) a.stats[2 * t] = a.stats[2 * t + 1] = 0.0f;
@@ -115,310 +505,212 @@ __global__ void __launch_bounds__(kMaxThreads) logits_loss_kernel(const LogitsLo
         if (a.w) a.w[t] = 0.0f;
       }
     }
-    if (kSums && parts > 1) cluster_wait();
+    if (parts > 1) cluster_wait();
     return;
   }
 
-  // The part's whole granules by bulk copies, the row's cut ones by a thread each.
-  const int whole0 = base < 0 ? g0 + 1 : g0, whole1 = g1 > g0 && g1 * N - lead > V ? g1 - 1 : g1;
-  if (tid == 0) {
-    const uint32_t bytes = whole1 > whole0 ? 16u * static_cast<uint32_t>(whole1 - whole0) : 0u;
-    mbar_arrive_expect_tx(&loaded, bytes);
-    constexpr uint32_t kChunk = 16 << 10;
-    const uint8_t* const src = reinterpret_cast<const uint8_t*>(row + (whole0 * N - lead));
-    for (uint32_t at = 0; at < bytes; at += kChunk)
-      bulk_load(reinterpret_cast<uint8_t*>(tile + (whole0 - g0)) + at, src + at, min(kChunk, bytes - at), &loaded);
+  // The logits at the ids, and marks of those here. No part writes a gradient before all have been here, as sums are joined
+  // in between.
+  for (int j = tid; j < k; j += threads) {
+    const int id = slots.id[j];
+    if (id < 0) continue;
+    const bool here = part.has(id);
+    slots.x[j] = to_f32(part.row[id]);
+    if (!kPolicy && here && mark<E>(marks, id, part.base)) info.twice = 1;
   }
-  if (tid == threads - 1 && g0 < g1) {
-    if (whole0 > g0) tile[0] = load_cut(row, base, V);
-    if (whole1 < g1 && (whole1 > g0 || whole0 == g0)) tile[whole1 - g0] = load_cut(row, whole1 * N - lead, V);
-  }
-  // The logits at the ids: of every id (no part writes a gradient over them before the exchange); without an exchange, of
-  // this part's alone. Each thread's first is on its way until it is wanted.
-  auto wanted = [&](int j) { return j < k && (kSums ? sid[j] >= 0 : sid[j] >= e0 && sid[j] < e1); };
-  const E x_first = wanted(tid) ? row[sid[tid]] : E{};
-  for (int j = tid + threads; j < k; j += threads)
-    if (wanted(j)) sx[j] = to_f32(row[sid[j]]);
-
-  // The teacher, by every warp on its own: mass = sum_j p_j, and the log-sum-exp that its logits are measured from as
-  // y_max / t + ln y_sum (without a tail) or lse_teacher.
-  const float inv_t = kPolicy ? 1.0f : 1.0f / a.temperature, c = kLog2e * inv_t;
-  const bool tail = !kPolicy && a.top_lse;
-  float mass = 1.0f, y_max = 0.0f, y_sum = 1.0f, lse_teacher = 0.0f;
-  if constexpr (kPolicy) {
-    if (tid == 0) sp[0] = 1.0f;
-  } else {
-    if (tail) {
-      lse_teacher = __ldg(a.top_lse + t);
-    } else {
-      y_max = -INFINITY;
-      for (int j = lane; j < k; j += 32)
-        if (sid[j] >= 0) y_max = fmaxf(y_max, sy[j]);
-      y_max = warp_max(y_max);
-      if (y_max == -INFINITY) y_max = 0.0f;
-      y_sum = 0.0f;
-      for (int j = lane; j < k; j += 32)
-        if (sid[j] >= 0) y_sum += expf((sy[j] - y_max) * inv_t);
-      y_sum = warp_sum(y_sum);
-    }
-    mass = 0.0f;
-    const float norm = 1.0f / y_sum;
-    for (int j = lane; j < k; j += 32) {
-      float p = 0.0f;
-      if (sid[j] >= 0) p = tail ? expf(fmaf(sy[j], inv_t, -lse_teacher)) : expf((sy[j] - y_max) * inv_t) * norm;
-      mass += p;
-      if (warp == 0) sp[j] = p;
-    }
-    mass = warp_sum(mass);
-  }
-  const float rest = tail ? fmaxf(1.0f - mass, 0.0f) : 0.0f;  // p_r
-
-  // The ids' logits are taken out of the part. Slots that name one id find out by writing their numbers to its place.
-  mbar_wait(&loaded, 0, &abort, a.status);
-  auto number = [](int j) {
-    if constexpr (sizeof(E) == 2) return static_cast<E>(j);
-    else return __int_as_float(j);
-  };
-  auto bits = [](E x) {
-    if constexpr (sizeof(E) == 2) return static_cast<int>(x);
-    else return __float_as_int(x);
-  };
-  if (wanted(tid)) sx[tid] = to_f32(x_first);
-  __syncthreads();  // the cut granules
-  for (int j = tid; j < k; j += threads)
-    if (sid[j] >= e0 && sid[j] < e1) held[sid[j] - base] = number(j);
   __syncthreads();
-  for (int j = tid; j < k; j += threads)
-    if (sid[j] >= e0 && sid[j] < e1) {
-      if (bits(held[sid[j] - base]) != j) twice_here = 1;
-      held[sid[j] - base] = minus_inf<E>();
+  float m_top = -INFINITY;
+  for (int j = lane; j < k; j += 32)
+    if (slots.id[j] >= 0) m_top = fmaxf(m_top, slots.x[j]);
+  m_top = warp_max(m_top);
+  if (tid == 0) info.m_top = m_top;
+  {
+    const Ref ref(m_top, c);
+    const uint4* const granules = part.granules();
+    const uint64_t hint = kWrites ? read_again() : read_once();
+    auto load = [&](int i) { return load_hint(granules + i, hint); };
+    const uint8_t* const marked = reinterpret_cast<const uint8_t*>(marks) - part.g0;
+    auto left = [&](int i, uint4 g) { return !kPolicy && tail ? without<E>(g, marked[i]) : g; };
+    const int w0 = part.whole0() + tid, w1 = part.whole1();
+    FixedSum<E> fixed;
+    fixed.start(ref, c);
+    stream<Shape<M>::kInFlight>(w0, w1, threads, load, [&](int i, uint4 g) { fixed.add(left(i, g)); });
+    part.cut(tid, threads, [&](int i) { fixed.add(left(i, part.load_cut(i))); });
+    const float mine = warp_sum(ref.far ? INFINITY : fixed.total());
+    if (lane == 0) sums[warp] = make_float2(mine, 0.0f);
+    if (!kPolicy && warp == warps - 1) {
+      const Teacher y = teach(a, top_lse, slots, c, lane);
+      if (lane == 0) info.teacher = y;
     }
-  __syncthreads();
+    __syncthreads();
 
-  // Of the whole row: references and sums outside the ids and at them.
-  float m_out, s_out, m, s, known = 0.0f, known_out = 0.0f;
-  bool twice = twice_here;
-  // the first slot of its id, where some share one
-  auto first = [&](int j) {
-    for (int i = 0; i < j; ++i)
-      if (sid[i] == sid[j]) return false;
-    return true;
-  };
-  if constexpr (kSums) {
-    Sum mine;
-    const int n = (g1 - g0 - tid + threads - 1) / threads;  // granules of this thread (0 or below: none)
-    if (n > 0) {
-      auto load = [&](int i) { return tile[tid + i * threads]; };
-      float x[N];
-      unpack(load(0), x);
-      mine.m = max_of(x);
-      const Ref ref(mine.m, c);
-      FixedSum<E> sum;
-      sum.start(ref, c);
-#pragma unroll 4
-      for (int i = 0; i < n; ++i) sum.add(load(i));
-      mine.s = sum.total();
-      if (ref.far || !mine.served()) mine = sum_largest<E>(n, load, c);
-    }
-    mine.merge_warp(c);
-    const int warps = threads / 32;
-    const float4 share = make_float4(mine.m, mine.s, twice ? 1.0f : 0.0f, 0.0f);
-    if (parts > 1) {
-      cluster_wait();  // every CTA runs
-      if (lane < parts) st_cluster(shares + rank * warps + warp, lane, share);
+    // What warp 0 has of all parts: each one's `of` in the lane of its number.
+    auto exchange = [&](int round, float2 of) {
+      if (parts == 1) return lane == 0 ? of : make_float2(round ? -INFINITY : 0.0f, 0.0f);
+      if (round == 0) cluster_wait();  // every CTA runs
+      if (warp == 0 && lane < parts) st_cluster(&shares[round][rank], lane, of);
       cluster_arrive();
-    } else if (lane == 0) {
-      shares[warp] = share;
-    }
-    // meanwhile the sum at the ids, by every warp on its own
-    auto at_ids = [&](bool once) {
-      Sum top;
-      for (int j = lane; j < k; j += 32)
-        if (sid[j] >= 0) top.m = fmaxf(top.m, sx[j]);
-      top.m = warp_max(top.m);
-      const Ref ref(top.m, c);
-      for (int j = lane; j < k; j += 32)
-        if (sid[j] >= 0 && (!once || first(j))) top.s += ref(sx[j], c);
-      top.s = warp_sum(top.s);
-      return top;
+      cluster_wait();
+      return lane < parts ? shares[round][lane] : make_float2(round ? -INFINITY : 0.0f, 0.0f);
     };
-    Sum top = at_ids(false);
-    if (parts > 1) cluster_wait();
-    else __syncthreads();
-    Sum outside;
-    for (int i = lane; i < parts * warps; i += 32) {
-      const float4 of = shares[i];
-      outside.merge(of.x, of.y, c);
-      twice |= of.z != 0.0f;
+    float2 of = make_float2(0.0f, 0.0f);
+    if (warp == 0) of = make_float2(warp_sum(lane < warps ? sums[lane].x : 0.0f), info.twice ? 1.0f : 0.0f);
+    of = exchange(0, of);
+    Sum top;
+    if (warp == 0) {
+      const float total = warp_sum(of.x);
+      const bool twice = __any_sync(kAll, of.y != 0.0f);
+      if (lane == 0) info.twice = twice;
+      __syncwarp();
+      top = Sum{info.m_top, 0.0f};
+      if (tail) top = sum_at_ids(slots, info, c, lane);
+      const bool served = conclude_first<kPolicy>(a, t, slots, info, top, total, tail, c, lane, rank == 0);
+      if (lane == 0) info.again = !served;
     }
-    outside.merge_warp(c);
-    twice = __any_sync(kAll, twice);
-    m_out = outside.m, s_out = outside.s;
-    if (twice) top = at_ids(true);
-    Sum all{m_out, s_out};
-    all.merge(top.m, top.s, c);
-    m = all.m, s = all.s;
-  } else {
-    known = __ldg(a.stats_in + 2 * t);
-    known_out = __ldg(a.stats_in + 2 * t + 1);
-    m = known * a.temperature;
-    m_out = known_out * a.temperature;
-    s = s_out = 1.0f;
-  }
-  const bool empty = m == -INFINITY;  // a row of -inf alone has no probabilities: q = 0
-  if (empty) m = 0.0f, s = 1.0f;
-  const bool none = m_out == -INFINITY;
-  if (none) m_out = 0.0f, s_out = 1.0f;
-  // of the whole row and of its logits outside the ids; known log-sum-exps are references themselves
-  Ref ref(m, c), ref_out(m_out, c);
-  if constexpr (!kSums) {
-    ref.r = empty ? 0.0f : known * kLog2e;
-    ref_out.r = none ? 0.0f : known_out * kLog2e;
-  }
-
-  float factor;
-  if constexpr (kPolicy) {
-    float lp;
-    if (ref.far) {
-      lp = (sx[0] - m) - logf(s);
-    } else {  // s = 2^e f: r + e is exact, and what is left is rounded as the small number that it is
-      int e;
-      const float f = frexpf(s, &e);
-      lp = (fmaf(sx[0], c, -(ref.r + static_cast<float>(e))) - log2f(f)) * kLn2;
+    __syncthreads();
+    if (info.again) {
+      Sum largest = sum_largest<E>((w1 - w0 + threads - 1) / threads,
+                                   [&](int n) { return left(w0 + n * threads, load(w0 + n * threads)); }, c);
+      part.cut(tid, threads, [&](int i) {
+        float x[N];
+        unpack(left(i, part.load_cut(i)), x);
+        largest.add_largest(x, max_of(x), c);
+      });
+      largest.merge_warp(c);
+      if (lane == 0) sums[warp] = make_float2(largest.m, largest.s);
+      __syncthreads();
+      Sum outside;
+      if (warp == 0) {
+        if (lane < warps) outside = Sum{sums[lane].x, sums[lane].y};
+        outside.merge_warp(c);
+      }
+      of = exchange(1, make_float2(outside.m, outside.s));
+      if (warp == 0) {
+        outside = Sum{of.x, of.y};
+        outside.merge_warp(c);
+        conclude_largest<kPolicy>(a, t, slots, info, top, outside, tail, c, lane, rank == 0);
+      }
+      __syncthreads();
     }
-    float w = 1.0f;
-    if (a.rollout_logp) {
-      w = expf(lp - __ldg(a.rollout_logp + t));
-      if (a.cap > 0.0f) w = fminf(w, a.cap);
-    }
-    if (rank == 0 && tid == 0) {
-      a.logp[t] = lp;
-      if (a.w) a.w[t] = w;
-      if (!(s < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
-    }
-    factor = w * __ldg(a.advantages + t);
-  } else {
-    if (rank == 0 && tid == 0 && (!(fabsf(m) < INFINITY) || !(s < INFINITY) || !(mass < INFINITY))) flag(a.status, QRR_DEV_NONFINITE);
-    factor = kWrites ? __ldg(a.grad + t) * inv_t : 0.0f;
   }
 
   if constexpr (kWrites) {
-    const float inv_s = 1.0f / s;
-    // outside the ids: e^{x / t} over that at `at` times `scale`
-    const Ref at = tail ? ref_out : ref;
-    float scale = factor * inv_s;
-    if (tail) {
-      const float up = !kSums ? (known_out - known) * kLog2e : ref.far || ref_out.far ? (m_out - m) * c : ref_out.r - ref.r;
-      const float q_rest = s_out * ex2_approx(up) * inv_s;
-      scale = none ? 0.0f : factor * (q_rest - rest) / s_out;
-    }
-    if (e0 < e1) {
-      const int shift = -base;  // of an element in `held`
-      const bool same = lead_of(out) == lead;
-      const uint64_t c2 = f32x2(c, c), nr2 = f32x2(-at.r, -at.r), scale2 = f32x2(scale, scale);
-      store_range(
-          out, e0, e1,
-          [&](int e) {
-            float x[N];
-            if (same) {
-              unpack(*reinterpret_cast<const uint4*>(held + e + shift), x);
-            } else {
-#pragma unroll
-              for (int u = 0; u < N; ++u) x[u] = to_f32(held[e + shift + u]);
-            }
-            if (!at.far) {
-#pragma unroll
-              for (int u = 0; u < N; u += 2) {
-                float y, z;
-                f32x2(fma2(f32x2(x[u], x[u + 1]), c2, nr2), y, z);
-                f32x2(mul2(f32x2(ex2_approx(y), ex2_approx(z)), scale2), x[u], x[u + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int u = 0; u < N; ++u) x[u] = at(x[u], c) * scale;
-            }
-            return pack(x);
-          },
-          [&](int e) { return from_f32(at(to_f32(held[e + shift]), c) * scale, E{}); });
-    }
+    const uint4* const granules = part.granules();
+    const uint64_t hint = read_once();
+    store_gradient<Shape<M>::kInFlight>(out, part, part.row, Gradient{Ref(info.m_at, c), c, info.scale}, tid, threads,
+                                        [&](int i) { return load_hint(granules + i, hint); });
     __syncthreads();
-    for (int j = tid; j < k; j += threads) {
-      const int id = sid[j];
-      if (id < e0 || id >= e1) continue;
-      float p = sp[j];
-      if (twice) {
-        if (!first(j)) continue;
-        p = 0.0f;
-        for (int i = j; i < k; ++i) p += sid[i] == id ? sp[i] : 0.0f;
-      }
-      out[id] = from_f32(factor * (ref(sx[j], c) * inv_s - p), E{});
-    }
+    store_ids(out, part, slots, info.twice, Ref(info.m, c), c, info.inv_s, info.factor, tid, threads);
   }
-  // The loss, by the last warp: sum_j p_j ((y_j - (x_j - m)) / t - (lse_teacher - (lse - m / t))), its few terms in 64 bits.
-  if (kSums && !kPolicy && rank == 0 && warp == threads / 32 - 1) {
-    double cross = 0.0, sum_p = 0.0;
-    for (int j = lane; j < k; j += 32)
-      if (sid[j] >= 0 && sp[j] > 0.0f) {
-        const double p = sp[j], y = sy[j], x = sx[j];
-        cross += p * (y - (x - static_cast<double>(m)));
-        sum_p += p;
-      }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      cross += __shfl_xor_sync(kAll, cross, o);
-      sum_p += __shfl_xor_sync(kAll, sum_p, o);
-    }
-    if (lane == 0) {
-      const double inv = 1.0 / static_cast<double>(a.temperature);
-      // of a sum's log-sum-exp, what it is above m / t
-      auto above = [&](const Ref& r, float sum) {
-        const double ln = log(static_cast<double>(sum));
-        if (r.far) return ln;
-        const double back = inv / static_cast<double>(c);  // from powers of 2 at this c
-        return (static_cast<double>(r.r) - static_cast<double>(r.m) * static_cast<double>(c) + ln * 1.4426950408889634) * back;
-      };
-      const double ln_s = above(ref, s);
-      const double lse_y = tail ? static_cast<double>(lse_teacher) : static_cast<double>(y_max) * inv + log(static_cast<double>(y_sum));
-      double loss = cross * inv - sum_p * (lse_y - ln_s), lse = static_cast<double>(m) * inv + ln_s, lse_out = lse;
-      if (tail) {
-        const double ln_out = none ? -INFINITY : above(ref_out, s_out);
-        lse_out = static_cast<double>(m_out) * inv + ln_out;
-        if (rest > (none ? kDust : 0.0f))
-          loss += static_cast<double>(rest) * (log(static_cast<double>(rest)) -
-                                               ((static_cast<double>(m_out) - static_cast<double>(m)) * inv + ln_out - ln_s));
-      }
-      a.loss[t] = static_cast<float>(loss);
-      if constexpr (M == LossMode::kLoss) {
-        a.stats[2 * t] = empty ? -INFINITY : static_cast<float>(lse);
-        a.stats[2 * t + 1] = empty ? -INFINITY : static_cast<float>(lse_out);
-      }
-    }
-  }
+  if ((M == LossMode::kLoss || M == LossMode::kGrad) && rank == 0 && warp == warps - 1) write_loss<M>(a, t, slots, info, c, lane);
 }
 
-// Bytes of a row that a CTA holds, at most, where fewer parts would do.
-constexpr int kPartBytes = 64 << 10;
+// ---- the gradient from known log-sum-exps ------------------------------------------
+//
+// Part blockIdx.x % parts of row blockIdx.x / parts, with nothing to exchange: a tile by bulk copies, three CTAs an SM.
+template <class E>
+__global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const LogitsLossArgs a, const int parts, const int per) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, k = a.k;
+  const int64_t t = blockIdx.x / parts;
+  E* const out = static_cast<E*>(a.dlogits) + t * a.ldd;
+  const Part<E> part(static_cast<const E*>(a.logits) + t * a.ld, a.V, blockIdx.x % parts, per);
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* const tile = reinterpret_cast<uint4*>(smem);
+  E* const held = reinterpret_cast<E*>(smem);
+  const Slots slots(smem + 16 * per, k);
+  __shared__ uint64_t loaded;
+  __shared__ int abort;
+  __shared__ RowInfo info;
+  const float c = kLog2e / a.temperature, top_lse = a.top_lse ? __ldg(a.top_lse + t) : 0.0f;
+  if (tid == 0) {
+    mbar_init(&loaded, 1);
+    fence_barrier_init();
+    abort = 0;
+  }
+  bool any = false;
+  for (int j = tid; j < k; j += threads) {
+    any |= slots.set(j, __ldg(a.ids + t * k + j), __ldg(a.top + t * k + j), a.V, a.status);
+  }
+  if (!__syncthreads_or(any)) {
+    store_zeros(out, part, tid, threads);
+    return;
+  }
+  if (tid == 0) part.copy(tile, &loaded);
+  part.cut(tid, threads, [&](int i) { tile[i - part.g0] = part.load_cut(i); });
+  for (int j = tid; j < k; j += threads)
+    if (part.has(slots.id[j])) slots.x[j] = to_f32(part.row[slots.id[j]]);
+  if (warp == 0) {
+    const Teacher y = teach(a, top_lse, slots, c, lane);
+    if (lane == 0) {
+      info.teacher = y;
+      info.weight = __ldg(a.grad + t);
+      conclude_known(a, t, info);
+    }
+  }
+  mbar_wait(&loaded, 0, &abort, a.status);
+  __syncthreads();
+  // Slots that name one id find out by writing their numbers to its place, which store_ids fills in the end.
+  bool twice = false;
+  for (int j = tid; j < k; j += threads)
+    if (part.has(slots.id[j])) {
+      if constexpr (sizeof(E) == 2) held[slots.id[j] - part.base] = static_cast<E>(j);
+      else held[slots.id[j] - part.base] = __int_as_float(j);
+    }
+  __syncthreads();
+  for (int j = tid; j < k; j += threads)
+    if (part.has(slots.id[j])) {
+      if constexpr (sizeof(E) == 2) twice |= held[slots.id[j] - part.base] != j;
+      else twice |= __float_as_int(held[slots.id[j] - part.base]) != j;
+    }
+  twice = __syncthreads_or(twice);
+
+  const Ref ref = known_ref(info.lse, a.temperature, c);
+  const Gradient of{known_ref(info.lse_at, a.temperature, c), c, info.scale};
+  store_gradient<1>(out, part, held - part.base, of, tid, threads, [&](int i) { return tile[i - part.g0]; });
+  __syncthreads();
+  store_ids(out, part, slots, twice, ref, c, 1.0f, info.factor, tid, threads);
+}
+
+constexpr int kMaxSmem = 220 << 10;  // of a CTA, beside what is declared
+
+cudaError_t device(int& dev, int& sms) {
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+}
 
 template <class E, LossMode M>
 cudaError_t launch(const LogitsLossArgs& a, cudaStream_t stream) {
   int dev = 0, sms = kSMs;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = device(dev, sms);
   if (e != cudaSuccess) return e;
   const int granules = granules_of<E>(kPer<E> - 1, a.V);
+  int parts = 1;  // more where rows do not fill the SMs
+  while (parts < kMaxParts && a.T * parts < sms && granules > parts * 256) parts *= 2;
+  const int per = (granules + parts - 1) / parts;
+  const int threads = std::min(Shape<M>::kThreads, per >= 2048 ? 512 : per >= 1024 ? 256 : per >= 256 ? 128 : 64);
+  const size_t smem = M == LossMode::kPolicy ? 16 : 16 * static_cast<size_t>(a.k) + (per + 15) / 16 * 16;
+  static OncePerDevice limit;
+  e = limit(dev, [] { return cudaFuncSetAttribute(logits_loss_kernel<E, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
+  if (e != cudaSuccess) return e;
+  return launch_clusters(logits_loss_kernel<E, M>, static_cast<unsigned>(a.T * parts), parts, threads, smem, stream, a, parts, per);
+}
+
+template <class E>
+cudaError_t launch_backward(const LogitsLossArgs& a, cudaStream_t stream) {
+  int dev = 0, sms = kSMs;
+  cudaError_t e = device(dev, sms);
+  if (e != cudaSuccess) return e;
+  constexpr int kPartBytes = 64 << 10;
+  const int granules = granules_of<E>(kPer<E> - 1, a.V);
   int parts = 1;
-  while (parts < 8 && (granules * 16 > parts * kPartBytes || (a.T * parts < sms && granules > parts * 256))) parts *= 2;
+  while (parts < 32 && (granules * 16 > parts * kPartBytes || (a.T * parts < sms && granules > parts * 256))) parts *= 2;
   const int per = (granules + parts - 1) / parts;
   const int threads = per >= 1024 ? 256 : per >= 256 ? 128 : 64;
-  const size_t smem = static_cast<size_t>(per) * 16 + static_cast<size_t>(M == LossMode::kPolicy ? 1 : a.k) * 16;
   static OncePerDevice limit;
-  e = limit(dev, [] {
-    return cudaFuncSetAttribute(logits_loss_kernel<E, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(kMaxLossRowBytes / 8 + 32 + 16 * kMaxTop));
-  });
+  e = limit(dev, [] { return cudaFuncSetAttribute(logits_backward_kernel<E>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(a.T * parts);
-  return launch_clusters(logits_loss_kernel<E, M>, grid, M == LossMode::kBackward ? 1 : parts, threads, smem, stream, a, parts, per);
+  logits_backward_kernel<E><<<static_cast<unsigned>(a.T * parts), threads, 16 * static_cast<size_t>(per + a.k), stream>>>(a, parts, per);
+  return cudaGetLastError();
 }
 
 template <class E>
@@ -426,7 +718,7 @@ cudaError_t launch(const LogitsLossArgs& a, LossMode mode, cudaStream_t stream) 
   switch (mode) {
     case LossMode::kLoss: return launch<E, LossMode::kLoss>(a, stream);
     case LossMode::kGrad: return launch<E, LossMode::kGrad>(a, stream);
-    case LossMode::kBackward: return launch<E, LossMode::kBackward>(a, stream);
+    case LossMode::kBackward: return launch_backward<E>(a, stream);
     default: return launch<E, LossMode::kPolicy>(a, stream);
   }
 }
