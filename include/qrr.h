@@ -522,17 +522,21 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
  *   accepted      int32 [B] (out): drafts taken
  *   logp          fp32 [T + B] (out): ln p of each token (softmax(target) where
  *                 the temperature is 0), 0 beside -1
+ *   workspace     qrr_verify_drafts_workspace_bytes(T, B, V, dtype)
  * Logits of -inf are masked out.  A row without a finite logit, or with a NaN or
  * +inf, raises QRR_DEV_NONFINITE; the token from it is then -1 or unspecified,
  * in [0, V).  Rows behind a refusal may go unread.  Offsets that descend or
- * leave [0, T] raise QRR_DEV_BAD_INDEX; nothing is written for that sequence.
+ * leave [0, T] raise QRR_DEV_BAD_INDEX; nothing is written for that sequence,
+ * and what is for sequences that share its places is unspecified.
  * Places outside cu[0] .. cu[B] are left as they were.  B <= 2^26, V <= 2^30, T
  * <= 2^30.  Sums are fp32 with the hardware's base-2 exponential, probabilities
  * that decide take expf; results do not depend on timing. */
+size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_t dtype);
 qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
                              int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,
                              const float* uniforms, const float* noise, int64_t ld_noise, float temperature,
-                             int32_t* tokens, int32_t* accepted, float* logp, int32_t* dev_status, void* stream);
+                             int32_t* tokens, int32_t* accepted, float* logp, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* The explicit sync point for device-detected conditions: copies the status

@@ -1009,10 +1009,16 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
   return from_cuda(launch_logits_loss(a, LossMode::kPolicy, as_stream(stream)));
 }
 
+size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_t dtype) {
+  if (!is_dtype(dtype) || T < 0 || B < 0 || V < 1 || T > (int64_t{1} << 30) || B > (1 << 26) || V > (int64_t{1} << 30)) return 0;
+  return verify_drafts_ws_bytes(T, B, V, dtype == QRR_DTYPE_FP32);
+}
+
 qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
                              int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,
                              const float* uniforms, const float* noise, int64_t ld_noise, float temperature,
-                             int32_t* tokens, int32_t* accepted, float* logp, int32_t* dev_status, void* stream) {
+                             int32_t* tokens, int32_t* accepted, float* logp, void* workspace, size_t workspace_bytes,
+                             int32_t* dev_status, void* stream) {
   if (!is_dtype(dtype) || T < 0 || B < 0 || V < 1) return QRR_ERR_INVALID_ARG;
   if (!cu && (B == 0 ? T > 0 : T % B != 0)) return QRR_ERR_INVALID_ARG;
   if (temperature != 0.0f && !is_temperature(temperature)) return QRR_ERR_INVALID_ARG;
@@ -1030,6 +1036,8 @@ qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* 
   if (!aligned4(drafts) || !aligned4(cu) || !aligned4(uniforms) || !aligned4(noise) || !aligned4(tokens) ||
       !aligned4(accepted) || !aligned4(logp))
     return QRR_ERR_MISALIGNED;
+  if (B > 0 && (!workspace || workspace_bytes < qrr_verify_drafts_workspace_bytes(T, B, V, dtype))) return QRR_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QRR_ERR_MISALIGNED;
   if (injected_cuda_fault()) return QRR_ERR_CUDA;
   VerifyArgs a{};
   a.target = target;
@@ -1049,6 +1057,7 @@ qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* 
   a.tokens = tokens;
   a.accepted = accepted;
   a.logp = logp;
+  a.workspace = workspace;
   a.status = dev_status;
   return from_cuda(launch_verify_drafts(a, as_stream(stream)));
 }

@@ -14,6 +14,8 @@
 namespace qrr {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 // Element types: Bf16 keeps its bits as uint16_t.
 using Bf16 = uint16_t;
@@ -130,6 +132,11 @@ struct Ref {
   }
 };
 
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
 // The largest of a warp's values (NaN aside).
 __device__ __forceinline__ float warp_max(float v) {
   float r;
@@ -214,14 +221,60 @@ __device__ __noinline__ Sum sum_largest(int n, Load load, float c) {
   return sum;
 }
 
-// Whether the phase with the given parity is complete, without waiting for it.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok)
-               : "r"(smem_u32(bar)), "r"(parity)
-               : "memory");
-  return ok != 0;
+// A sum s = sum 2^{c x - r} as a power of two and a small logarithm: log2 of it and its reference = whole + part.
+struct Log2 {
+  float whole, part;
+  __device__ __forceinline__ Log2(const Ref& ref, float s) {
+    int e;
+    part = log2f(frexpf(s, &e));
+    whole = ref.r + static_cast<float>(e);  // exact
+  }
+};
+
+// ln of e^{x / t} / s: what is left of c x behind the whole powers of two is rounded as the small number that it is.
+__device__ __forceinline__ float ln_share(float x, const Ref& ref, float s, const Log2& log2, float c, float inv_t) {
+  // c x may overflow where x / t does not, and beside such numbers the sum's own power of two is nothing
+  if (ref.far || !(fabsf(x) < 1e30f)) return (x - ref.m) * inv_t - logf(s);
+  return (fmaf(x, c, -log2.whole) - log2.part) * kLn2;
+}
+
+// L2's treatment of what is read: once, or again soon.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t read_again() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t policy) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(policy));
+  return v;
+}
+
+// use(i, load(i)) for i = first, first + step, .. below end, kInFlight loads at a time.
+template <int kInFlight, class Load, class Use>
+__device__ __forceinline__ void stream(int first, int end, int step, Load load, Use use) {
+  int i = first;
+  for (; i + (kInFlight - 1) * step < end; i += kInFlight * step) {
+    uint4 g[kInFlight];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) g[u] = load(i + u * step);
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u) use(i + u * step, g[u]);
+  }
+  uint4 g[kInFlight];
+#pragma unroll
+  for (int u = 0; u < kInFlight; ++u)
+    if (i + u * step < end) g[u] = load(i + u * step);
+#pragma unroll
+  for (int u = 0; u < kInFlight; ++u)
+    if (i + u * step < end) use(i + u * step, g[u]);
 }
 
 // ---- clusters ---------------------------------------------------------------
@@ -231,19 +284,16 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint64_t ld_cluster(const uint64_t* p, uint32_t rank) {
-  uint64_t v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
-  return v;
-}
 // To the same variable of CTA `rank`.
 __device__ __forceinline__ void st_cluster(const float2* p, uint32_t rank, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_cluster(const float4* p, uint32_t rank, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster(const uint64_t* p, uint32_t rank, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(p, rank)), "l"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -320,8 +370,10 @@ struct VerifyArgs {
   int32_t* tokens;    // [T + B]
   int32_t* accepted;  // [B]
   float* logp;        // [T + B]
+  void* workspace;    // verify_drafts_ws_bytes
   int32_t* status;
 };
+size_t verify_drafts_ws_bytes(int64_t T, int64_t B, int64_t V, int fp32);
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t stream);
 
 }  // namespace qrr

@@ -31,36 +31,9 @@ namespace {
 
 constexpr int kMaxThreads = 512, kMaxParts = 8;
 constexpr int kBackwardThreads = 256;
-constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr float kLn2 = 0.6931471805599453f;
 // A rest of the teacher's that is no more than the rounding of its log-sum-exp and of the sum of p_j: beside a student
 // without any, it is none.
 constexpr float kDust = 1.0f / 65536;
-
-// L2's treatment of what is read: once, or again soon.
-__device__ __forceinline__ uint64_t read_once() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ uint64_t read_again() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t policy) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p), "l"(policy));
-  return v;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
-  return v;
-}
 
 // Part `rank` of a row: `per` granules, elements e0 .. e1 - 1; element e stands at e - base of the CTA's tile.
 template <class E>
@@ -222,26 +195,6 @@ struct Gradient {
   }
 };
 
-// use(i, load(i)) for i = first, first + step, .. below end, kInFlight loads at a time.
-template <int kInFlight, class Load, class Use>
-__device__ __forceinline__ void stream(int first, int end, int step, Load load, Use use) {
-  int i = first;
-  for (; i + (kInFlight - 1) * step < end; i += kInFlight * step) {
-    uint4 g[kInFlight];
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) g[u] = load(i + u * step);
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u) use(i + u * step, g[u]);
-  }
-  uint4 g[kInFlight];
-#pragma unroll
-  for (int u = 0; u < kInFlight; ++u)
-    if (i + u * step < end) g[u] = load(i + u * step);
-#pragma unroll
-  for (int u = 0; u < kInFlight; ++u)
-    if (i + u * step < end) use(i + u * step, g[u]);
-}
-
 // The gradient of a part to its row of it, from `row` (element e's place in memory or in a tile) by load(granule).
 template <int kInFlight, class E, class Load>
 __device__ __forceinline__ void store_gradient(E* out, const Part<E>& part, const E* row, const Gradient& of, int tid, int threads, Load load) {
@@ -279,23 +232,6 @@ __device__ __forceinline__ void store_ids(E* out, const Part<E>& part, const Slo
     const float p = twice ? s.all(j) : s.p[j];
     out[s.id[j]] = from_f32(factor * (ref(s.x[j], c) * inv_s - p), E{});
   }
-}
-
-// A sum s = sum 2^{c x - r} as a power of two and a small logarithm: log2 of it and its reference = whole + part.
-struct Log2 {
-  float whole, part;
-  __device__ __forceinline__ Log2(const Ref& ref, float s) {
-    int e;
-    part = log2f(frexpf(s, &e));
-    whole = ref.r + static_cast<float>(e);  // exact
-  }
-};
-
-// ln of e^{x / t} / s: what is left of c x behind the whole powers of two is rounded as the small number that it is.
-__device__ __forceinline__ float ln_share(float x, const Ref& ref, float s, const Log2& log2, float c, float inv_t) {
-  // c x may overflow where x / t does not, and beside such numbers the sum's own power of two is nothing
-  if (ref.far || !(fabsf(x) < 1e30f)) return (x - ref.m) * inv_t - logf(s);
-  return (fmaf(x, c, -log2.whole) - log2.part) * kLn2;
 }
 
 // What a CTA's threads tell one another about a row.

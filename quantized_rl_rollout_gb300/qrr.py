@@ -113,8 +113,9 @@ SIGNATURES = {
                                              _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
     "qrr_token_logprobs_is_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, ctypes.c_float,
                                                   _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
+    "qrr_verify_drafts_workspace_bytes": (_c_sz, [_c_i64, _c_i32, _c_i64, _c_i32]),
     "qrr_verify_drafts": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p,
-                                         _c_i64, ctypes.c_float, _c_p, _c_p, _c_p, _c_p, _c_p]),
+                                         _c_i64, ctypes.c_float, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
     "qrr_workspace_bytes": (_c_sz, [_c_i32, _c_i64, _c_i64, _c_i64, _c_i32]),
     "qrr_wait_probe": (ctypes.c_int, [_c_i64, _c_i32, _c_p, _c_p, _c_p]),
     "qrr_stream_probe": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
@@ -601,7 +602,7 @@ def token_logprobs_is_grad(logits, tokens, advantages, rollout_logp=None, cap=0.
 
 
 def verify_drafts(target, drafts, uniforms=None, noise=None, draft_logits=None, cu=None, temperature=1.0, tokens=None,
-                  accepted=None, logp=None, dev_status=None, stream=None):
+                  accepted=None, logp=None, workspace=None, dev_status=None, stream=None):
     """Test drafted tokens against the target's probabilities and draw the token that follows (see ``qrr_verify_drafts``).
 
     ``target`` logits [T + B, V] (bf16 or fp32), ``drafts`` int32 [T]: sequence b has the drafts cu[b] .. cu[b + 1] - 1 (as
@@ -632,13 +633,15 @@ def verify_drafts(target, drafts, uniforms=None, noise=None, draft_logits=None, 
     tokens = _on_stream((rows,), torch.int32, dev, stream) if tokens is None else tokens
     accepted = _on_stream((b,), torch.int32, dev, stream) if accepted is None else accepted
     logp = _on_stream((rows,), torch.float32, dev, stream) if logp is None else logp
+    if workspace is None:
+        workspace = _workspace(lib().qrr_verify_drafts_workspace_bytes(t, b, v, dtype), dev, stream)
     _check(lib().qrr_verify_drafts(target.data_ptr(), ld_target, _ptr(draft_logits), ld_draft, dtype, t, b, v,
                                    _vector(drafts, t, torch.int32, "drafts", dev), cu_ptr,
                                    _vector(uniforms, t, torch.float32, "uniforms", dev), _ptr(noise), ld_noise,
                                    float(temperature), _vector(tokens, rows, torch.int32, "tokens", dev),
                                    _vector(accepted, b, torch.int32, "accepted", dev),
-                                   _vector(logp, rows, torch.float32, "logp", dev), _ptr(dev_status), _stream(stream)),
-           "qrr_verify_drafts")
+                                   _vector(logp, rows, torch.float32, "logp", dev), workspace.data_ptr(), workspace.numel(),
+                                   _ptr(dev_status), _stream(stream)), "qrr_verify_drafts")
     return tokens, accepted, logp
 
 

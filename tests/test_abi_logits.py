@@ -60,9 +60,9 @@ def test_policy(qrr, change, status):
 
 
 def _verify(qrr, target=FAKE, ld=100, draft=FAKE, ld_draft=100, dtype=0, T=6, B=3, V=100, drafts=FAKE, cu=None, u=FAKE, noise=FAKE,
-            ld_noise=100, temp=1.0, tokens=FAKE, accepted=FAKE, logp=FAKE):
+            ld_noise=100, temp=1.0, tokens=FAKE, accepted=FAKE, logp=FAKE, ws=FAKE, ws_bytes=1 << 50):
     return qrr.lib().qrr_verify_drafts(target, ld, draft, ld_draft, dtype, T, B, V, drafts, cu, u, noise, ld_noise, temp, tokens,
-                                       accepted, logp, None, None)
+                                       accepted, logp, ws, ws_bytes, None, None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -71,7 +71,8 @@ def _verify(qrr, target=FAKE, ld=100, draft=FAKE, ld_draft=100, dtype=0, T=6, B=
     (dict(u=None), 1), (dict(noise=None), 1), (dict(temp=-0.5), 1), (dict(temp=1e-8), 1), (dict(temp=float("nan")), 1),
     (dict(tokens=None), 1), (dict(accepted=None), 1), (dict(logp=None), 1), (dict(B=(1 << 26) + 1, cu=FAKE), 2),
     (dict(V=(1 << 30) + 1), 2), (dict(T=3 << 29, cu=FAKE), 2), (dict(target=FAKE + 1), 3), (dict(draft=FAKE + 2, dtype=1), 3),
-    (dict(cu=FAKE + 2), 3), (dict(u=FAKE + 2), 3), (dict(noise=FAKE + 2), 3), (dict(tokens=FAKE + 2), 3), (dict(logp=FAKE + 1), 3)])
+    (dict(cu=FAKE + 2), 3), (dict(u=FAKE + 2), 3), (dict(noise=FAKE + 2), 3), (dict(tokens=FAKE + 2), 3), (dict(logp=FAKE + 1), 3),
+    (dict(ws=None), 4), (dict(ws_bytes=64), 4), (dict(ws=FAKE + 8), 3)])
 def test_verify(qrr, change, status):
     assert _verify(qrr, **change) == status
 
@@ -80,7 +81,9 @@ def test_nothing_to_do(qrr):
     """No rows: nothing is needed and nothing is launched."""
     assert _losses(qrr, T=0, logits=None, ids=None, top=None, grad=None, loss=None, stats=None, dlogits=None) == (0, 0, 0)
     assert _policy(qrr, T=0, logits=None, tokens=None, adv=None, rollout=None, logp=None, w=None, dlogits=None) == 0
-    assert _verify(qrr, T=0, B=0, target=None, draft=None, drafts=None, u=None, noise=None, tokens=None, accepted=None, logp=None) == 0
+    assert _verify(qrr, T=0, B=0, target=None, draft=None, drafts=None, u=None, noise=None, tokens=None, accepted=None, logp=None,
+                   ws=None, ws_bytes=0) == 0
+    assert qrr.lib().qrr_verify_drafts_workspace_bytes(6, 3, 100, 2) == 0 and qrr.lib().qrr_verify_drafts_workspace_bytes(-1, 3, 100, 0) == 0
 
 
 def test_injected_fault(qrr, monkeypatch):
@@ -134,7 +137,7 @@ def binding(monkeypatch):
 
     class Lib:
         def __getattr__(self, name):
-            return lambda *a: calls.append((name, a)) or 0
+            return lambda *a: 4096 if name.endswith("_bytes") else calls.append((name, a)) or 0
 
     monkeypatch.setattr(qrr, "lib", lambda: Lib())
     monkeypatch.setattr(qrr, "_stream", lambda s: 0)
