@@ -94,6 +94,9 @@ __device__ __noinline__ uint4 load_cut(const E* row, int e0, int V) {
 // the values behind them cost a multiply-add, an exponential and an addition each, no comparison. A sum that gets near
 // the end of the range is taken again with the largest of all (add_largest). References are whole numbers so that a sum
 // moves to another by a power of two, and c x - r is rounded once.
+// c is held in two parts: rounded to one, the exponents of a row would be off by up to 2^-24 of themselves, which is 1e-6 of a
+// probability where logits reach 20. The second part costs half an instruction an element, beside an exponential's
+// eight cycles.
 // A reference of more than 2^20 (rows at their type's lowest value, say, where c m itself may overflow) takes the
 // difference of the logits first: r = c m in effect, 2^{c (x - m)}.
 
@@ -119,16 +122,64 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// 1 / t, and log2(e) / t in two parts, c rounded down and lo > 0: of a logit of -inf both products are -inf.
+struct Scale {
+  float inv_t, c, lo;
+  __device__ __forceinline__ operator float() const { return c; }
+  __device__ __forceinline__ float exponent(float x, float r) const { return fmaf(x, lo, fmaf(x, c, -r)); }
+};
+inline Scale scale_of(float t) {
+  const double k = 1.4426950408889634 / t;
+  float c = static_cast<float>(k);
+  if (c >= k) c = nextafterf(c, 0.0f);
+  return Scale{1.0f / t, c, static_cast<float>(k - c)};
+}
+
+// A number in two parts, and sums of such.
+struct Two {
+  float high = 0.0f, low = 0.0f;
+  __device__ __forceinline__ void add(Two x) {
+    const float sum = high + x.high, part = sum - high;
+    low = (low + x.low) + ((high - (sum - part)) + (x.high - part));
+    high = sum;
+  }
+  __device__ __forceinline__ void add_warp() {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) add(Two{__shfl_xor_sync(kAll, high, o), __shfl_xor_sync(kAll, low, o)});
+  }
+};
+
+// 2^(x + lo) for a small lo, in two parts: the hardware's is 2 ulps off, which is seen where few values make up a sum. 2^f by
+// its series, |f| <= 1/2.
+__device__ __forceinline__ Two pow2(float x, float lo) {
+  const float n = rintf(fminf(fmaxf(x, -200.0f), 200.0f)), f = (x - n) + lo;
+  float p = 1.52527338e-5f;  // ln(2)^7 / 7!
+  p = fmaf(p, f, 1.54035304e-4f);
+  p = fmaf(p, f, 1.33335581e-3f);
+  p = fmaf(p, f, 9.61812911e-3f);
+  p = fmaf(p, f, 5.55041087e-2f);
+  p = fmaf(p, f, 2.40226507e-1f);
+  p = fmaf(p, f, 6.93147181e-1f);
+  const float high = fmaf(p, f, 1.0f), low = fmaf(p, f, 1.0f - high);
+  const int e = static_cast<int>(n);
+  return x < -200.0f ? Two{} : Two{ldexpf(high, e), ldexpf(low, e)};
+}
+
 // The reference that a logit m makes (m = -inf: 0, for sums without a value).
 struct Ref {
   float m, r;
   bool far;
-  __device__ __forceinline__ Ref(float m_, float c) : m(m_ == -INFINITY ? 0.0f : m_) {
+  __device__ __forceinline__ Ref(float m_, Scale c) : m(m_ == -INFINITY ? 0.0f : m_) {
     r = rintf(m * c);
     far = !(fabsf(r) <= 0x1p20f);
   }
-  __device__ __forceinline__ float operator()(float x, float c) const {
-    return ex2_approx(far ? (x - m) * c : fmaf(x, c, -r));
+  __device__ __forceinline__ float operator()(float x, Scale c) const {
+    return ex2_approx(far ? (x - m) * c : c.exponent(x, r));
+  }
+  __device__ __forceinline__ Two exactly(float x, Scale c) const {
+    if (far || !(fabsf(x) < 1e30f)) return Two{(*this)(x, c), 0.0f};
+    const float high = __fmul_rn(x, c);  // (not contracted: what it is off by is added)
+    return pow2(high - r, fmaf(x, c, -high) + x * c.lo);
   }
 };
 
@@ -148,18 +199,18 @@ struct Sum {
   float m = -INFINITY, s = 0.0f;
 
   // What a sum at m is worth at another reference, not below it.
-  __device__ __forceinline__ static float moved(float m, const Ref& to, float c) {
+  __device__ __forceinline__ static float moved(float m, const Ref& to, Scale c) {
     const Ref from(m, c);
     return m == -INFINITY ? 0.0f : ex2_approx(from.far || to.far ? (m - to.m) * c : from.r - to.r);
   }
   // A sum without values has s = 0 and m = -inf; a NaN in s stays.
-  __device__ __forceinline__ void merge(float m2, float s2, float c) {
+  __device__ __forceinline__ void merge(float m2, float s2, Scale c) {
     const Ref to(fmaxf(m, m2), c);
     s = s * moved(m, to, c) + s2 * moved(m2, to, c);
     m = fmaxf(m, m2);
   }
   // Of a warp's sums, the same in every lane: one move each, to the largest reference.
-  __device__ __forceinline__ void merge_warp(float c) {
+  __device__ __forceinline__ void merge_warp(Scale c) {
     const float to = warp_max(m);
     s *= moved(m, Ref(to, c), c);
     m = to;
@@ -168,7 +219,7 @@ struct Sum {
   }
   // Values with their largest: the reference follows it.
   template <int N>
-  __device__ __forceinline__ void add_largest(const float (&x)[N], float largest, float c) {
+  __device__ __forceinline__ void add_largest(const float (&x)[N], float largest, Scale c) {
     if (largest > m) {
       s *= moved(m, Ref(largest, c), c);
       m = largest;
@@ -184,9 +235,10 @@ struct Sum {
 // A thread's sum at a reference that stays, in two accumulators of two values.
 template <class E>
 struct FixedSum {
-  uint64_t c2, nr2, a0, a1;
-  __device__ __forceinline__ void start(const Ref& ref, float c) {
+  uint64_t c2, lo2, nr2, a0, a1;
+  __device__ __forceinline__ void start(const Ref& ref, Scale c) {
     c2 = f32x2(c, c);
+    lo2 = f32x2(c.lo, c.lo);
     nr2 = f32x2(-ref.r, -ref.r);
     a0 = a1 = 0;
   }
@@ -196,8 +248,9 @@ struct FixedSum {
 #pragma unroll
     for (int u = 0; u < kPer<E>; u += 4) {
       float e0, e1, e2, e3;
-      f32x2(fma2(f32x2(x[u], x[u + 1]), c2, nr2), e0, e1);
-      f32x2(fma2(f32x2(x[u + 2], x[u + 3]), c2, nr2), e2, e3);
+      const uint64_t x0 = f32x2(x[u], x[u + 1]), x1 = f32x2(x[u + 2], x[u + 3]);
+      f32x2(fma2(x0, lo2, fma2(x0, c2, nr2)), e0, e1);
+      f32x2(fma2(x1, lo2, fma2(x1, c2, nr2)), e2, e3);
       a0 = add2(a0, f32x2(ex2_approx(e0), ex2_approx(e1)));
       a1 = add2(a1, f32x2(ex2_approx(e2), ex2_approx(e3)));
     }
@@ -211,7 +264,7 @@ struct FixedSum {
 
 // The sum of n granules load(0) .. load(n - 1), once more with the largest of them.
 template <class E, class Load>
-__device__ __noinline__ Sum sum_largest(int n, Load load, float c) {
+__device__ __noinline__ Sum sum_largest(int n, Load load, Scale c) {
   Sum sum;
   for (int i = 0; i < n; ++i) {
     float x[kPer<E>];
@@ -221,21 +274,25 @@ __device__ __noinline__ Sum sum_largest(int n, Load load, float c) {
   return sum;
 }
 
-// A sum s = sum 2^{c x - r} as a power of two and a small logarithm: log2 of it and its reference = whole + part.
+// A sum s = sum 2^{c x - r} (and a low part of it) as a power of two and a small logarithm: log2 of it and its reference =
+// whole + part, |part| <= 1/2.
 struct Log2 {
   float whole, part;
-  __device__ __forceinline__ Log2(const Ref& ref, float s) {
+  __device__ __forceinline__ Log2(const Ref& ref, float s, float low = 0.0f) {
     int e;
-    part = log2f(frexpf(s, &e));
+    float f = frexpf(s, &e);
+    if (f < 0.70710678f) f += f, --e;
+    part = log2f(f);
+    if (low != 0.0f) part = fmaf(low / s, kLog2e, part);
     whole = ref.r + static_cast<float>(e);  // exact
   }
 };
 
 // ln of e^{x / t} / s: what is left of c x behind the whole powers of two is rounded as the small number that it is.
-__device__ __forceinline__ float ln_share(float x, const Ref& ref, float s, const Log2& log2, float c, float inv_t) {
+__device__ __forceinline__ float ln_share(float x, const Ref& ref, float s, const Log2& log2, Scale c) {
   // c x may overflow where x / t does not, and beside such numbers the sum's own power of two is nothing
-  if (ref.far || !(fabsf(x) < 1e30f)) return (x - ref.m) * inv_t - logf(s);
-  return (fmaf(x, c, -log2.whole) - log2.part) * kLn2;
+  if (ref.far || !(fabsf(x) < 1e30f)) return (x - ref.m) * c.inv_t - logf(s);
+  return (c.exponent(x, log2.whole) - log2.part) * kLn2;
 }
 
 // L2's treatment of what is read: once, or again soon.
@@ -327,12 +384,13 @@ struct LogitsLossArgs {
   const void* logits;
   int64_t ld, T;
   int V, fp32;
+  Scale scale;  // of the logits (policy gradient: at temperature 1)
   // distillation
   const int32_t* ids;  // [T][k]
   const float* top;    // [T][k]
   const float* top_lse;
   int k;
-  float temperature;
+  float temperature;  // its scale is set by the launch, as verify's
   const float* grad;
   const float* stats_in;
   float* loss;
@@ -352,7 +410,7 @@ enum class LossMode { kLoss, kGrad, kBackward, kPolicy };
 constexpr int kMaxTop = 1024;
 // Bytes of a row that the largest cluster holds on chip.
 constexpr int64_t kMaxLossRowBytes = 3 << 19;
-cudaError_t launch_logits_loss(const LogitsLossArgs& a, LossMode mode, cudaStream_t stream);
+cudaError_t launch_logits_loss(LogitsLossArgs a, LossMode mode, cudaStream_t stream);
 
 struct VerifyArgs {
   const void* target;  // [T + B][V]
@@ -367,6 +425,7 @@ struct VerifyArgs {
   const float* noise;     // [B][V]
   int64_t ld_noise;
   float temperature;  // 0: the likeliest token
+  Scale scale;
   int32_t* tokens;    // [T + B]
   int32_t* accepted;  // [B]
   float* logp;        // [T + B]
@@ -374,6 +433,6 @@ struct VerifyArgs {
   int32_t* status;
 };
 size_t verify_drafts_ws_bytes(int64_t T, int64_t B, int64_t V, int fp32);
-cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t stream);
+cudaError_t launch_verify_drafts(VerifyArgs a, cudaStream_t stream);
 
 }  // namespace qrr

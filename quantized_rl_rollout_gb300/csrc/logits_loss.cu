@@ -113,13 +113,29 @@ struct Slots {
 // mass = sum_j p_j, rest = p_r, and the log-sum-exp that the teacher's logits are measured from: y_sum = sum 2^{c y - r} at
 // the reference of y_max (without a tail) or lse.
 struct Teacher {
-  float mass, rest, y_max, y_sum, lse;
+  float mass, rest, y_max, y_sum, y_low, lse;
+};
+
+// A log-sum-exp in base 2, in two parts.
+struct Lse {
+  float lse, high, low;
+  __device__ __forceinline__ explicit Lse(float lse_) : lse(lse_) {
+    constexpr float kHigh = 1.44269502162933350f, kLow = 1.92596299e-8f;  // log2(e)
+    high = __fmul_rn(lse, kHigh);
+    low = fmaf(lse, kHigh, -high) + lse * kLow;
+  }
+  __device__ __forceinline__ bool small(float y) const { return fabsf(lse) < 1e30f && fabsf(y) < 1e30f; }
+  // e^{y / t - lse}
+  __device__ __forceinline__ Two share(float y, Scale c) const {
+    if (!small(y)) return Two{expf(fmaf(y, c.inv_t, -lse)), 0.0f};
+    const float h = __fmul_rn(y, c);
+    return pow2(h - high, fmaf(y, c, -h) + (y * c.lo - low));
+  }
 };
 
 // By a warp; the slots' p_j are written.
-__device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse, const Slots& s, float c, int lane) {
-  Teacher r{0.0f, 0.0f, 0.0f, 1.0f, 0.0f};
-  const float inv_t = 1.0f / a.temperature;
+__device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse, const Slots& s, Scale c, int lane) {
+  Teacher r{0.0f, 0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
   if (a.top_lse) {
     r.lse = top_lse;
   } else {
@@ -129,23 +145,28 @@ __device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse,
     r.y_max = warp_max(r.y_max);
     if (r.y_max == -INFINITY) r.y_max = 0.0f;
     const Ref ref(r.y_max, c);
-    r.y_sum = 0.0f;
+    Two sum;
     for (int j = lane; j < s.k; j += 32) {
-      const float p = s.id[j] >= 0 ? ref.far ? expf((s.y[j] - ref.m) * inv_t) : exp2f(fmaf(s.y[j], c, -ref.r)) : 0.0f;
-      s.p[j] = p;
-      r.y_sum += p;
+      Two p;
+      if (s.id[j] >= 0) p = ref.far ? Two{expf((s.y[j] - ref.m) * c.inv_t), 0.0f} : ref.exactly(s.y[j], c);
+      s.p[j] = p.high;
+      sum.add(p);
     }
-    r.y_sum = warp_sum(r.y_sum);
+    sum.add_warp();
+    r.y_sum = sum.high, r.y_low = sum.low;
   }
   const float norm = 1.0f / r.y_sum;
+  const Lse lse(r.lse);
+  Two mass;  // (what it leaves of 1 may be little)
   for (int j = lane; j < s.k; j += 32) {
-    float p = 0.0f;
-    if (s.id[j] >= 0) p = a.top_lse ? expf(fmaf(s.y[j], inv_t, -r.lse)) : s.p[j] * norm;
-    r.mass += p;
-    s.p[j] = p;
+    Two p;
+    if (s.id[j] >= 0) p = a.top_lse ? lse.share(s.y[j], c) : Two{__fmul_rn(s.p[j], norm), 0.0f};
+    mass.add(p);
+    s.p[j] = p.high;
   }
-  r.mass = warp_sum(r.mass);
-  r.rest = a.top_lse ? fmaxf(1.0f - r.mass, 0.0f) : 0.0f;
+  mass.add_warp();
+  r.mass = mass.high;
+  r.rest = a.top_lse ? fmaxf((1.0f - mass.high) - mass.low, 0.0f) : 0.0f;
   return r;
 }
 
@@ -175,16 +196,18 @@ __device__ __forceinline__ void store_zeros(E* out, const Part<E>& part, int tid
 // The gradient outside the ids: e^{x / t} over that at `at`, times `scale`.
 struct Gradient {
   Ref at;
-  float c, scale;
+  Scale c;
+  float scale;
   __device__ __forceinline__ float operator()(float x) const { return at(x, c) * scale; }
   template <int N>
   __device__ __forceinline__ uint4 block(float (&x)[N]) const {
     if (!at.far) {
-      const uint64_t c2 = f32x2(c, c), nr2 = f32x2(-at.r, -at.r), scale2 = f32x2(scale, scale);
+      const uint64_t c2 = f32x2(c, c), lo2 = f32x2(c.lo, c.lo), nr2 = f32x2(-at.r, -at.r), scale2 = f32x2(scale, scale);
 #pragma unroll
       for (int u = 0; u < N; u += 2) {
         float y, z;
-        f32x2(fma2(f32x2(x[u], x[u + 1]), c2, nr2), y, z);
+        const uint64_t both = f32x2(x[u], x[u + 1]);
+        f32x2(fma2(both, lo2, fma2(both, c2, nr2)), y, z);
         f32x2(mul2(f32x2(ex2_approx(y), ex2_approx(z)), scale2), x[u], x[u + 1]);
       }
     } else {
@@ -225,7 +248,7 @@ __device__ __forceinline__ void store_gradient(E* out, const Part<E>& part, cons
 
 // And at the ids of this part, behind it: factor (q_j - p_j).
 template <class E>
-__device__ __forceinline__ void store_ids(E* out, const Part<E>& part, const Slots& s, bool twice, const Ref& ref, float c, float inv_s,
+__device__ __forceinline__ void store_ids(E* out, const Part<E>& part, const Slots& s, bool twice, const Ref& ref, Scale c, float inv_s,
                                           float factor, int tid, int threads) {
   for (int j = tid; j < s.k; j += threads) {
     if (!part.has(s.id[j]) || (twice && !s.first(j))) continue;
@@ -241,7 +264,7 @@ struct RowInfo {
   float weight, rollout;     // the gradient's, or the advantage; the token's log-probability in the rollout
   int again;                 // whether the sums are to be taken once more
   int twice;                 // whether slots share an id
-  float m, s, m_out, s_out;  // references and sums of the whole row, and of its logits outside the ids (with a tail)
+  float m, s, s_low, m_out, s_out;  // references and sums of the whole row, and of its logits outside the ids (with a tail)
   float m_at, scale;         // the gradient outside the ids
   float inv_s, factor;       // and at them
   float lse, lse_at;         // kBackward: known, of m and m_at
@@ -249,17 +272,26 @@ struct RowInfo {
 
 // The loss of a row, by a warp.
 template <LossMode M>
-__device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, const Slots& s, const RowInfo& info, float c, int lane) {
+__device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, const Slots& s, const RowInfo& info, Scale c, int lane) {
   const bool empty = info.m == -INFINITY, none = info.m_out == -INFINITY;
-  const float sum = empty ? 1.0f : info.s, inv_t = 1.0f / a.temperature;
+  const float sum = empty ? 1.0f : info.s, inv_t = c.inv_t;
   const Ref ref(info.m, c), ref_out(info.m_out, c), ref_y(info.teacher.y_max, c);
-  const Log2 log2(ref, sum), log2_y(ref_y, info.teacher.y_sum);
+  const Log2 log2(ref, sum, empty ? 0.0f : info.s_low), log2_y(ref_y, info.teacher.y_sum, info.teacher.y_low);
   const Teacher& y = info.teacher;
+  // ln p - ln q of one id is rounded as the small number that it mostly is: (y - x) / t less what the log-sum-exps differ by.
+  const Lse teacher_lse(y.lse);
+  const float apart = a.top_lse ? (teacher_lse.high - log2.whole) + (teacher_lse.low - log2.part)
+                                : (log2_y.whole - log2.whole) + (log2_y.part - log2.part);
+  const bool near = !ref.far && !ref_y.far && fabsf(y.lse) < 1e30f;
   float loss = 0.0f;
   for (int j = lane; j < s.k; j += 32)
     if (s.id[j] >= 0 && s.p[j] > 0.0f) {
-      const float ln_p = a.top_lse ? fmaf(s.y[j], inv_t, -y.lse) : ln_share(s.y[j], ref_y, y.y_sum, log2_y, c, inv_t);
-      loss += s.p[j] * (ln_p - ln_share(s.x[j], ref, sum, log2, c, inv_t));
+      if (near && fabsf(s.x[j]) < 1e30f && fabsf(s.y[j]) < 1e30f) {
+        loss += s.p[j] * (c.exponent(s.y[j] - s.x[j], apart) * kLn2);
+        continue;
+      }
+      const float ln_p = a.top_lse ? fmaf(s.y[j], inv_t, -y.lse) : ln_share(s.y[j], ref_y, y.y_sum, log2_y, c);
+      loss += s.p[j] * (ln_p - ln_share(s.x[j], ref, sum, log2, c));
     }
   loss = warp_sum(loss);
   if (lane != 0) return;
@@ -282,28 +314,30 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
   if (!(fabsf(ref.m) < INFINITY) || !(sum < INFINITY) || !(y.mass < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
 }
 
-// The sum at the ids, each once, by a warp.
-__device__ __forceinline__ Sum sum_at_ids(const Slots& slots, const RowInfo& info, float c, int lane) {
-  Sum top{info.m_top, 0.0f};
-  const Ref ref(top.m, c);
+// The sum at the ids, each once, by a warp. `less`: less what the hardware's exponential made of them.
+__device__ __forceinline__ Two sum_at_ids(const Slots& slots, const RowInfo& info, bool less, Scale c, int lane) {
+  Two top;
+  const Ref ref(info.m_top, c);
   for (int j = lane; j < slots.k; j += 32)
-    if (slots.id[j] >= 0 && (!info.twice || slots.first(j))) top.s += ref(slots.x[j], c);
-  top.s = warp_sum(top.s);
+    if (slots.id[j] >= 0 && (!info.twice || slots.first(j))) {
+      top.add(ref.exactly(slots.x[j], c));
+      if (less) top.add(Two{-ref(slots.x[j], c), 0.0f});
+    }
+  top.add_warp();
   return top;
 }
 
-// What follows from the references and sums of the row and (with a tail) outside the ids, whose sum at the row's reference
+// What follows from the references and sums of the row (and a low part) and (with a tail) outside the ids, whose sum at the row's reference
 // is q_rest. By a warp; `writes`: of the row's parts, this one writes what is the row's.
 template <bool kPolicy>
 __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& all,
-                                         const Sum& outside, float q_rest, bool tail, float c, int lane, bool writes) {
-  const float inv_t = kPolicy ? 1.0f : 1.0f / a.temperature;
+                                         float low, const Sum& outside, float q_rest, bool tail, Scale c, int lane, bool writes) {
   const Ref ref(all.m, c);
   const bool bare = all.m == -INFINITY, none = outside.m == -INFINITY;
   const float sum = bare ? 1.0f : all.s;  // a row of -inf alone has no probabilities: q = 0
-  float factor = info.weight * inv_t;
+  float factor = info.weight * c.inv_t;
   if constexpr (kPolicy) {
-    const float lp = ln_share(slots.x[0], ref, sum, Log2(ref, sum), c, inv_t);
+    const float lp = ln_share(slots.x[0], ref, sum, Log2(ref, sum, low), c);
     float w = 1.0f;
     if (a.rollout_logp) {
       w = expf(lp - info.rollout);
@@ -318,7 +352,7 @@ __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, con
   }
   if (lane == 0) {
     const float inv_s = 1.0f / sum;
-    info.m = all.m, info.s = all.s, info.m_out = outside.m, info.s_out = outside.s;
+    info.m = all.m, info.s = all.s, info.s_low = low, info.m_out = outside.m, info.s_out = outside.s;
     info.m_at = tail ? outside.m : all.m;
     info.scale = !tail ? factor * inv_s : none ? 0.0f : factor * (q_rest * inv_s - info.teacher.rest) / outside.s;
     info.inv_s = inv_s;
@@ -329,39 +363,51 @@ __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, con
 // From sums at the reference of the ids. False if that served badly: the sums that are divided by have to be there, far
 // from the ends of fp32's range.
 template <bool kPolicy>
-__device__ __forceinline__ bool conclude_first(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& top,
-                                               float total, bool tail, float c, int lane, bool writes) {
+__device__ __forceinline__ bool conclude_first(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Two& top,
+                                               float total, bool tail, Scale c, int lane, bool writes) {
   auto served = [](float x) { return x > 0x1p-60f && x < 0x1p64f; };
-  const Sum outside{top.m, total}, all{top.m, tail ? total + top.s : total};
-  if (!served(all.s) || (tail && !served(total)) || top.m == -INFINITY) return false;
-  conclude<kPolicy>(a, t, slots, info, all, outside, total, tail, c, lane, writes);
+  Two sum{total, 0.0f};
+  sum.add(top);
+  const Sum outside{info.m_top, tail ? total : sum.high}, all{info.m_top, sum.high};
+  if (!served(all.s) || (tail && !served(total)) || all.m == -INFINITY) return false;
+  conclude<kPolicy>(a, t, slots, info, all, sum.low, outside, total, tail, c, lane, writes);
   return true;
 }
 
 // From sums at the largest logits.
 template <bool kPolicy>
-__device__ __forceinline__ void conclude_largest(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& top,
-                                                 const Sum& outside, bool tail, float c, int lane, bool writes) {
+__device__ __forceinline__ void conclude_largest(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Two& top,
+                                                 const Sum& outside, bool tail, Scale c, int lane, bool writes) {
   Sum all = outside;
-  if (tail) all.merge(top.m, top.s, c);
-  conclude<kPolicy>(a, t, slots, info, all, outside, outside.s * Sum::moved(outside.m, Ref(all.m, c), c), tail, c, lane, writes);
+  if (tail) all.merge(info.m_top, top.high, c);
+  conclude<kPolicy>(a, t, slots, info, all, 0.0f, outside, outside.s * Sum::moved(outside.m, Ref(all.m, c), c), tail, c, lane, writes);
 }
 
-// From known log-sum-exps, which are references themselves, not rounded to whole numbers. By one thread.
-__device__ __forceinline__ void conclude_known(const LogitsLossArgs& a, int64_t t, RowInfo& info) {
+// The reference of a known log-sum-exp, a whole number too, and the factor of its row's shares that is left.
+__device__ __forceinline__ Ref known_ref(float lse, float temperature, Scale c) {
+  Ref ref(lse * temperature, c);
+  if (!ref.far && lse > -INFINITY) ref.r = rintf(Lse(lse).high);
+  return ref;
+}
+__device__ __forceinline__ float known_share(float lse, float temperature, Scale c) {
+  const Ref ref = known_ref(lse, temperature, c);
+  const Lse parts(lse);
+  return !ref.far && lse > -INFINITY ? pow2(ref.r - parts.high, -parts.low).high : 1.0f;
+}
+
+// From known log-sum-exps. By one thread.
+__device__ __forceinline__ void conclude_known(const LogitsLossArgs& a, int64_t t, RowInfo& info, Scale c) {
   const bool tail = a.top_lse;
   const float lse = __ldg(a.stats_in + 2 * t), lse_out = __ldg(a.stats_in + 2 * t + 1);
   info.lse = lse;
   info.lse_at = tail ? lse_out : lse;
-  info.inv_s = 1.0f;
-  info.factor = info.weight / a.temperature;
-  info.scale = !tail ? info.factor : lse_out == -INFINITY ? 0.0f : info.factor * (ex2_approx((lse_out - lse) * kLog2e) - info.teacher.rest);
+  info.factor = info.weight * c.inv_t;
+  info.inv_s = known_share(lse, a.temperature, c);
+  info.scale = !tail                  ? info.factor * info.inv_s
+               : lse_out == -INFINITY ? 0.0f
+                                      : info.factor * (ex2_approx((lse_out - lse) * kLog2e) - info.teacher.rest) *
+                                            known_share(lse_out, a.temperature, c);
   if (!(info.teacher.mass < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
-}
-__device__ __forceinline__ Ref known_ref(float lse, float temperature, float c) {
-  Ref ref(lse * temperature, c);
-  if (lse > -INFINITY) ref.r = lse * kLog2e;
-  return ref;
 }
 
 // Granule g without the marked elements.
@@ -405,7 +451,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   const int rank = blockIdx.x % parts, k = kPolicy ? 1 : a.k;
   const Part<E> part(static_cast<const E*>(a.logits) + t * a.ld, a.V, rank, per);
   E* const out = kWrites ? static_cast<E*>(a.dlogits) + t * a.ldd : nullptr;
-  const float inv_t = kPolicy ? 1.0f : 1.0f / a.temperature, c = kLog2e * inv_t;
+  const Scale c = a.scale;
   const bool tail = !kPolicy && a.top_lse;
 
   extern __shared__ __align__(16) uint8_t smem[];
@@ -492,14 +538,13 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     float2 of = make_float2(0.0f, 0.0f);
     if (warp == 0) of = make_float2(warp_sum(lane < warps ? sums[lane].x : 0.0f), info.twice ? 1.0f : 0.0f);
     of = exchange(0, of);
-    Sum top;
+    Two top;  // at the ids, the largest terms mostly: with a tail they are not in the sum, without they are put right
     if (warp == 0) {
       const float total = warp_sum(of.x);
       const bool twice = __any_sync(kAll, of.y != 0.0f);
       if (lane == 0) info.twice = twice;
       __syncwarp();
-      top = Sum{info.m_top, 0.0f};
-      if (tail) top = sum_at_ids(slots, info, c, lane);
+      top = sum_at_ids(slots, info, !tail, c, lane);
       const bool served = conclude_first<kPolicy>(a, t, slots, info, top, total, tail, c, lane, rank == 0);
       if (lane == 0) info.again = !served;
     }
@@ -557,7 +602,8 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
   __shared__ uint64_t loaded;
   __shared__ int abort;
   __shared__ RowInfo info;
-  const float c = kLog2e / a.temperature, top_lse = a.top_lse ? __ldg(a.top_lse + t) : 0.0f;
+  const Scale c = a.scale;
+  const float top_lse = a.top_lse ? __ldg(a.top_lse + t) : 0.0f;
   if (tid == 0) {
     mbar_init(&loaded, 1);
     fence_barrier_init();
@@ -580,7 +626,7 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
     if (lane == 0) {
       info.teacher = y;
       info.weight = __ldg(a.grad + t);
-      conclude_known(a, t, info);
+      conclude_known(a, t, info, c);
     }
   }
   mbar_wait(&loaded, 0, &abort, a.status);
@@ -604,7 +650,7 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
   const Gradient of{known_ref(info.lse_at, a.temperature, c), c, info.scale};
   store_gradient<1>(out, part, held - part.base, of, tid, threads, [&](int i) { return tile[i - part.g0]; });
   __syncthreads();
-  store_ids(out, part, slots, twice, ref, c, 1.0f, info.factor, tid, threads);
+  store_ids(out, part, slots, twice, ref, c, info.inv_s, info.factor, tid, threads);
 }
 
 constexpr int kMaxSmem = 220 << 10;  // of a CTA, beside what is declared
@@ -661,8 +707,9 @@ cudaError_t launch(const LogitsLossArgs& a, LossMode mode, cudaStream_t stream) 
 
 }  // namespace
 
-cudaError_t launch_logits_loss(const LogitsLossArgs& a, LossMode mode, cudaStream_t stream) {
+cudaError_t launch_logits_loss(LogitsLossArgs a, LossMode mode, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
+  a.scale = scale_of(mode == LossMode::kPolicy ? 1.0f : a.temperature);
   return a.fp32 ? launch<float>(a, mode, stream) : launch<Bf16>(a, mode, stream);
 }
 

@@ -149,7 +149,7 @@ __device__ __forceinline__ RowSum sane(RowSum x) {
 
 // The sum of a row from its parts, by a warp (the same in every lane).
 template <Form F>
-__device__ __forceinline__ RowSum merge_parts(RowSum x, float c, int V) {
+__device__ __forceinline__ RowSum merge_parts(RowSum x, Scale c, int V) {
   Sum sum{x.m, x.s};
   sum.merge_warp(c);
   if constexpr (F == Form::kGreedy) {
@@ -161,7 +161,7 @@ __device__ __forceinline__ RowSum merge_parts(RowSum x, float c, int V) {
   return x;
 }
 template <Form F>
-__device__ __forceinline__ RowSum row_sum(const RowSum* parts_of, int parts, float c, int V) {
+__device__ __forceinline__ RowSum row_sum(const RowSum* parts_of, int parts, Scale c, int V) {
   const int lane = threadIdx.x & 31;
   RowSum x{-INFINITY, 0.0f, -INFINITY, V};
   if (lane < parts) {
@@ -173,11 +173,11 @@ __device__ __forceinline__ RowSum row_sum(const RowSum* parts_of, int parts, flo
 
 // Whether a draft is taken, from the sums of its place and its logits.
 template <Form F>
-__device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float u, float dp, float dq, float c, float inv_t) {
+__device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float u, float dp, float dq, Scale c) {
   if constexpr (F == Form::kGreedy) return drafted == p.arg;
   p = sane(p);
   const Ref at(p.m, c);
-  if constexpr (F == Form::kLookup) return u < expf(ln_share(dp, at, p.s, Log2(at, p.s), c, inv_t));
+  if constexpr (F == Form::kLookup) return u < expf(ln_share(dp, at, p.s, Log2(at, p.s), c));
   // u q < p as u < 2^{c (x_p - x_q) - (r_p - r_q) - (log2 s_p - log2 s_q)}
   q = sane(q);
   const Ref at_q(q.m, c);
@@ -186,7 +186,7 @@ __device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float 
     l = ((dp - at.m) - (dq - at_q.m)) * c - (log2f(p.s) - log2f(q.s));
   } else {
     const Log2 lp(at, p.s), lq(at_q, q.s);
-    l = fmaf(dp - dq, c, -(lp.whole - lq.whole)) - (lp.part - lq.part);
+    l = c.exponent(dp - dq, lp.whole - lq.whole) - (lp.part - lq.part);
   }
   return u < exp2f(l);
 }
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
   constexpr bool kModel = F == Form::kModel, kGreedy = F == Form::kGreedy;
   constexpr int kRows = kModel ? 2 : 1, kWarps = kSumWorkers / 32, kInFlight = 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
-  const float inv_t = kGreedy ? 1.0f : 1.0f / a.temperature, c = kLog2e * inv_t;
+  const Scale c = a.scale;
   const Workspace at(a, parts);
   struct Task {
     const E* row;  // null: no more
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
       q = row_sum<F>(at.sums + (a.T + a.B + w.first + w.place) * parts, parts, c, V);
       dq = to_f32(__ldg(static_cast<const E*>(a.draft) + (w.first + w.place) * a.ld_draft + drafted));
     }
-    if (!taken_by<F>(p, q, drafted, u, dp, dq, c, inv_t) && lane == 0) atomicMin(&at.states[w.b].needed, w.place + 1);
+    if (!taken_by<F>(p, q, drafted, u, dp, dq, c) && lane == 0) atomicMin(&at.states[w.b].needed, w.place + 1);
   };
   Where now{}, then{}, last{};
   bool any = choose(ask(), now, 0);
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
   constexpr int kThreads = kDrawThreads, kWarps = kThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / parts, rank = blockIdx.x % parts, V = a.V;
-  const float inv_t = kGreedy ? 1.0f : 1.0f / a.temperature, c = kLog2e * inv_t;
+  const Scale c = a.scale;
   const Workspace from(a, sum_parts);
   __shared__ RowSum rows[2];
   __shared__ uint64_t best_warps[2][kWarps], best[2][kMaxParts];
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
       const RowSum whole = sane(p);
       const Ref at(whole.m, c);
       tokens[i] = drafted;
-      logp[i] = ln_share(x, at, whole.s, Log2(at, whole.s), c, inv_t);
+      logp[i] = ln_share(x, at, whole.s, Log2(at, whole.s), c);
     }
   }
   __syncthreads();
@@ -467,11 +467,11 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     // The score itself. Both products are rounded: contracted to an FMA, the difference of equal rows would be a rounding
     // error and not 0.
     const bool minus = kModel && refused;
-    auto scale = [&](const RowSum& r, const Ref& at) { return 1.0f / (at.far ? r.s : r.s * ex2_approx(fmaf(-at.m, c, at.r))); };
+    auto scale = [&](const RowSum& r, const Ref& at) { return 1.0f / (at.far ? r.s : r.s * ex2_approx(c.exponent(-at.m, -at.r))); };
     const float inv_p = scale(p_row, p_ref), inv_q = minus ? scale(q_row, q_ref) : 0.0f;
     auto score = [&](float x, float y, float e, int v, bool whole_p) {
-      float r = __fmul_rn(expf((x - p_ref.m) * inv_t), inv_p);
-      if (minus && !whole_p) r -= __fmul_rn(expf((y - q_ref.m) * inv_t), inv_q);
+      float r = __fmul_rn(expf((x - p_ref.m) * c.inv_t), inv_p);
+      if (minus && !whole_p) r -= __fmul_rn(expf((y - q_ref.m) * c.inv_t), inv_q);
       if (v == drafted && !kModel && !whole_p) r = 0.0f;
       return r / e;
     };
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     if (tid == 0) {
       tokens[taken] = token;
       logp[taken] = token < 0 ? 0.0f
-                              : ln_share(to_f32(s.target[taken * a.ld_target + token]), p_ref, p_row.s, Log2(p_ref, p_row.s), c, inv_t);
+                              : ln_share(to_f32(s.target[taken * a.ld_target + token]), p_ref, p_row.s, Log2(p_ref, p_row.s), c);
       a.accepted[b] = taken;
     }
     for (int i = taken + 1 + tid; i <= s.given; i += kThreads) {
@@ -720,8 +720,9 @@ size_t verify_drafts_ws_bytes(int64_t T, int64_t B, int64_t V, int fp32) {
          static_cast<size_t>(T + B) * sizeof(int);
 }
 
-cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t stream) {
+cudaError_t launch_verify_drafts(VerifyArgs a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
+  a.scale = scale_of(a.temperature == 0.0f ? 1.0f : a.temperature);
   return a.fp32 ? launch<float>(a, stream) : launch<Bf16>(a, stream);
 }
 
