@@ -301,3 +301,33 @@ def test_streams_and_graphs(q):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_counts_far_apart(q, form):
+    """One long sequence among short and empty ones, and many sequences: more parts of rows than there are CTAs to sum them."""
+    _check(q, _case([0] * 20 + [120] + [1, 0, 2] * 20, 5000, BF16, form, 31, spread=0.05), enough=0.5)
+    _check(q, _case([3, 1, 0, 2] * 400, 300, FP32, form, 32), enough=0.8)
+
+
+def test_refusals_are_seen_in_time(q):
+    """Sequences that are refused at each place in turn, with rows behind the refusal that would raise a flag if they counted."""
+    n, v = 12, 40000
+    s = _case([n] * (n + 1), v, BF16, "greedy", 33)
+    target = s["target"].clone()
+    s["drafts"] = s["drafts"].view(n + 1, n).clone()
+    best = target.float().argmax(-1).view(n + 1, n + 1)
+    for b in range(n + 1):
+        s["drafts"][b] = best[b, :n].to(torch.int32)
+        if b < n:
+            s["drafts"][b, b] = (best[b, b] + 1) % v
+        target.view(n + 1, n + 1, v)[b, b + 1:] = float("nan")
+    s["drafts"], s["target"] = s["drafts"].view(-1), target
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for _ in range(20):
+        tokens, accepted, logp = _run(q, s, dev_status=st)
+        assert accepted.tolist() == list(range(n + 1))
+        tokens = tokens.view(n + 1, n + 1)
+        for b in range(n + 1):
+            assert torch.equal(tokens[b, :b + 1].long(), best[b, :b + 1]) and torch.all(tokens[b, b + 1:] == -1)
+    assert q.get_last_device_status(st) == 0
