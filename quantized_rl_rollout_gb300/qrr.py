@@ -487,7 +487,7 @@ def _logit_rows(x, rows, v, name, dtype=None):
     """(dtype number, row stride) of logits [rows, v] whose rows are contiguous (a slice of wider rows will do)."""
     if x.dtype not in _DTYPES or not x.is_cuda or (dtype is not None and x.dtype != dtype):
         raise TypeError(f"{name} must be a CUDA {'bfloat16 or float32' if dtype is None else dtype} tensor, got {x.dtype}")
-    if tuple(x.shape) != (rows, v):
+    if x.shape != (rows, v):
         raise ValueError(f"{name} must be {[rows, v]}, got {list(x.shape)}")
     s = x.stride()
     if (v > 1 and s[1] != 1) or (rows > 1 and s[0] < v):
@@ -499,11 +499,19 @@ def _vector(x, n, dtype, name, device):
     """Address of a contiguous vector of n values (None stays)."""
     if x is None:
         return None
-    if x.dtype != dtype or not x.is_cuda or not x.is_contiguous() or x.numel() != n:
+    if x.dtype != dtype or not x.is_contiguous() or x.numel() != n or not x.is_cuda:
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} values")
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, the logits on {device}")
     return x.data_ptr()
+
+
+def _output(x, shape, n, dtype, name, device, stream):
+    """(tensor, address) of an output of n values: the caller's, or a new one."""
+    if x is None:
+        x = _on_stream(shape, dtype, device, stream)
+        return x, x.data_ptr()
+    return x, _vector(x, n, dtype, name, device)
 
 
 def _same_device(device, *tensors):
@@ -546,10 +554,9 @@ def distill_topk(logits, top_ids, top_logits, top_lse=None, temperature=1.0, los
     rows, _, _ = _loss_rows(logits, None, stream, grad=False)
     t, dev = rows[1], logits.device
     teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
-    loss = _on_stream((t,), torch.float32, dev, stream) if loss is None else loss
-    stats = _on_stream((t, 2), torch.float32, dev, stream) if stats is None else stats
-    _check(lib().qrr_distill_topk(logits.data_ptr(), *rows, *teacher, _vector(loss, t, torch.float32, "loss", dev),
-                                  _vector(stats, 2 * t, torch.float32, "stats", dev), _ptr(dev_status), _stream(stream)),
+    loss, loss_ptr = _output(loss, (t,), t, torch.float32, "loss", dev, stream)
+    stats, stats_ptr = _output(stats, (t, 2), 2 * t, torch.float32, "stats", dev, stream)
+    _check(lib().qrr_distill_topk(logits.data_ptr(), *rows, *teacher, loss_ptr, stats_ptr, _ptr(dev_status), _stream(stream)),
            "qrr_distill_topk")
     return loss, stats
 
@@ -574,9 +581,9 @@ def distill_topk_grad(logits, top_ids, top_logits, grad, top_lse=None, temperatu
     rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
     t, dev = rows[1], logits.device
     teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
-    loss = _on_stream((t,), torch.float32, dev, stream) if loss is None else loss
+    loss, loss_ptr = _output(loss, (t,), t, torch.float32, "loss", dev, stream)
     _check(lib().qrr_distill_topk_grad(logits.data_ptr(), *rows, *teacher, _vector(grad, t, torch.float32, "grad", dev),
-                                       _vector(loss, t, torch.float32, "loss", dev), dlogits.data_ptr(), ldd, _ptr(dev_status),
+                                       loss_ptr, dlogits.data_ptr(), ldd, _ptr(dev_status),
                                        _stream(stream)), "qrr_distill_topk_grad")
     return loss, dlogits
 
@@ -587,16 +594,12 @@ def token_logprobs_is_grad(logits, tokens, advantages, rollout_logp=None, cap=0.
     held fixed (None, for 1, without ``rollout_logp``); ``dlogits`` may be ``logits`` itself."""
     rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
     t, dev = rows[1], logits.device
-    logp = _on_stream((t,), torch.float32, dev, stream) if logp is None else logp
-    if rollout_logp is None:
-        w = None
-    elif w is None:
-        w = _on_stream((t,), torch.float32, dev, stream)
+    logp, logp_ptr = _output(logp, (t,), t, torch.float32, "logp", dev, stream)
+    w, w_ptr = (None, None) if rollout_logp is None else _output(w, (t,), t, torch.float32, "w", dev, stream)
     _check(lib().qrr_token_logprobs_is_grad(logits.data_ptr(), *rows, _vector(tokens, t, torch.int32, "tokens", dev),
                                             _vector(advantages, t, torch.float32, "advantages", dev),
                                             _vector(rollout_logp, t, torch.float32, "rollout_logp", dev), float(cap),
-                                            _vector(logp, t, torch.float32, "logp", dev), _vector(w, t, torch.float32, "w", dev),
-                                            dlogits.data_ptr(), ldd, _ptr(dev_status), _stream(stream)),
+                                            logp_ptr, w_ptr, dlogits.data_ptr(), ldd, _ptr(dev_status), _stream(stream)),
            "qrr_token_logprobs_is_grad")
     return logp, w, dlogits
 
@@ -630,17 +633,16 @@ def verify_drafts(target, drafts, uniforms=None, noise=None, draft_logits=None, 
             ld_noise = _logit_rows(noise, b, v, "noise", torch.float32)[1]
     _same_device(dev, draft_logits, noise)
     cu_ptr = _vector(cu, b + 1, torch.int32, "cu", dev)
-    tokens = _on_stream((rows,), torch.int32, dev, stream) if tokens is None else tokens
-    accepted = _on_stream((b,), torch.int32, dev, stream) if accepted is None else accepted
-    logp = _on_stream((rows,), torch.float32, dev, stream) if logp is None else logp
+    tokens, tokens_ptr = _output(tokens, (rows,), rows, torch.int32, "tokens", dev, stream)
+    accepted, accepted_ptr = _output(accepted, (b,), b, torch.int32, "accepted", dev, stream)
+    logp, logp_ptr = _output(logp, (rows,), rows, torch.float32, "logp", dev, stream)
     if workspace is None:
         workspace = _workspace(lib().qrr_verify_drafts_workspace_bytes(t, b, v, dtype), dev, stream)
     _check(lib().qrr_verify_drafts(target.data_ptr(), ld_target, _ptr(draft_logits), ld_draft, dtype, t, b, v,
                                    _vector(drafts, t, torch.int32, "drafts", dev), cu_ptr,
                                    _vector(uniforms, t, torch.float32, "uniforms", dev), _ptr(noise), ld_noise,
-                                   float(temperature), _vector(tokens, rows, torch.int32, "tokens", dev),
-                                   _vector(accepted, b, torch.int32, "accepted", dev),
-                                   _vector(logp, rows, torch.float32, "logp", dev), workspace.data_ptr(), workspace.numel(),
+                                   float(temperature), tokens_ptr, accepted_ptr, logp_ptr, workspace.data_ptr(),
+                                   workspace.numel(),
                                    _ptr(dev_status), _stream(stream)), "qrr_verify_drafts")
     return tokens, accepted, logp
 
