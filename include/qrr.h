@@ -443,7 +443,8 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * masked out (q = 0); a row of nothing but -inf has q = 0 everywhere.  A row
  * with a NaN or +inf raises QRR_DEV_NONFINITE, its outputs unspecified.
  * Sums are fp32 with the hardware's base-2 exponential (about 2^-22 relative);
- * results do not depend on timing.
+ * terms at the ids are within an ulp.  Results do not depend on timing, but on
+ * a row's alignment (the order in which its values are added).
  *
  * Teacher.  top_ids int32 [T][k], top_logits fp32 [T][k], 0 <= k <= 1024: the
  * teacher's logits at k tokens of each row, in any order; a slot with a
@@ -466,7 +467,8 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * of the forward call with the same arguments.  (q is taken from the fp32
  * log-sum-exp: its rounding is a relative error of q.)
  * qrr_distill_topk_grad: loss and dlogits at once, where grad [T] (a weight a
- * row) is known before the loss: each logit is read once. */
+ * row) is known before the loss: a row is read from memory once (the second
+ * time it comes from L2 mostly). */
 #define QRR_MAX_LOSS_ROW_BYTES (3u << 19)
 typedef enum qrr_dtype { QRR_DTYPE_BF16 = 0, QRR_DTYPE_FP32 = 1 } qrr_dtype;
 

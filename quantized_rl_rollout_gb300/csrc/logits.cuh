@@ -408,7 +408,7 @@ struct LogitsLossArgs {
 };
 enum class LossMode { kLoss, kGrad, kBackward, kPolicy };
 constexpr int kMaxTop = 1024;
-// Bytes of a row that the largest cluster holds on chip.
+// Bytes of a row: the marks of its granules, a byte each, leave room in shared memory for two CTAs.
 constexpr int64_t kMaxLossRowBytes = 3 << 19;
 cudaError_t launch_logits_loss(LogitsLossArgs a, LossMode mode, cudaStream_t stream);
 

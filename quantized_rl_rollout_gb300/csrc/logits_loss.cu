@@ -17,9 +17,14 @@
 // shared memory.
 //
 // With a tail, the logits at the teacher's ids are left out of the sum (marked in shared memory, a byte a granule), so that
-// the sum outside them is one of positive terms, not a difference. Sums are fp32; e^x is the hardware's base-2 approximation (about 2^-22 relative)
-// where it is taken a logit and expf where it is taken an id. A loss is a small difference of large logarithms: each is
-// taken from a whole power of two, so that it is rounded as a small number.
+// the sum outside them is one of positive terms, not a difference. Sums are fp32; e^x is the hardware's base-2 approximation
+// (about 2^-22 relative) where it is taken a logit. What makes up most of a row and of a loss is the ids, a few terms whose
+// errors do not average out: their exponentials are within an ulp and summed in two parts (without a tail they replace what
+// the hardware made of them), and a logarithm's difference is rounded as the small number that it is. A loss of 0.1 is off by
+// 2.6e-8 so (root mean square; 6.3e-8 without), the log-sum-exps by their own rounding.
+//
+// Measured, rows of 128256 bf16: loss alone, 2048 rows, 77 us (80% of a copy's rate); loss and gradient of 4096, 388 us (74%);
+// policy gradient of 4096, 351 us (82%); 2048 rows' gradient from known log-sum-exps 142 us (98%).
 #include <algorithm>
 
 #include "logits.cuh"
@@ -434,7 +439,7 @@ __device__ __forceinline__ bool mark(uint32_t* marks, int id, int base) {
 // A CTA takes part blockIdx.x % parts of row blockIdx.x / parts: `per` granules. The parts of a row are a cluster.
 //
 // A gradient reads its row again, so what counts is that it is still in L2: two CTAs of 512 threads an SM with eight
-// granules a thread under way (step batch below: 375 us; three and four CTAs of 256: 400 and 419). A loss alone reads once:
+// granules a thread under way (loss and gradient of 4096 rows: 375 us; three and four CTAs of 256 threads: 400 and 419). A loss alone reads once:
 // six CTAs of 256 threads hide one another's ends (2048 rows of 128256 bf16: 74 us; two of 512: 89).
 template <LossMode M>
 struct Shape {
