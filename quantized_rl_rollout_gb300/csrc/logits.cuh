@@ -262,18 +262,6 @@ struct FixedSum {
   }
 };
 
-// The sum of n granules load(0) .. load(n - 1), once more with the largest of them.
-template <class E, class Load>
-__device__ __noinline__ Sum sum_largest(int n, Load load, Scale c) {
-  Sum sum;
-  for (int i = 0; i < n; ++i) {
-    float x[kPer<E>];
-    unpack(load(i), x);
-    sum.add_largest(x, max_of(x), c);
-  }
-  return sum;
-}
-
 // A sum s = sum 2^{c x - r} (and a low part of it) as a power of two and a small logarithm: log2 of it and its reference =
 // whole + part, |part| <= 1/2.
 struct Log2 {
@@ -408,7 +396,7 @@ struct LogitsLossArgs {
 };
 enum class LossMode { kLoss, kGrad, kBackward, kPolicy };
 constexpr int kMaxTop = 1024;
-// Bytes of a row: the marks of its granules, a byte each, leave room in shared memory for two CTAs.
+// Bytes of a row, of which 32 CTAs hold the tiles for its gradient from known log-sum-exps with ease.
 constexpr int64_t kMaxLossRowBytes = 3 << 19;
 cudaError_t launch_logits_loss(LogitsLossArgs a, LossMode mode, cudaStream_t stream);
 

@@ -16,15 +16,16 @@
 // out. Where there are few rows, a cluster of CTAs takes one, a contiguous part each, and joins sums over distributed
 // shared memory.
 //
-// With a tail, the logits at the teacher's ids are left out of the sum (marked in shared memory, a byte a granule), so that
-// the sum outside them is one of positive terms, not a difference. Sums are fp32; e^x is the hardware's base-2 approximation
+// With a tail, the logits at the teacher's ids are left out of the sum (their granules are passed over and added without
+// them), so that the sum outside them is one of positive terms, not a difference. Sums are fp32; e^x is the hardware's base-2 approximation
 // (about 2^-22 relative) where it is taken a logit. What makes up most of a row and of a loss is the ids, a few terms whose
 // errors do not average out: their exponentials are within an ulp and summed in two parts (without a tail they replace what
 // the hardware made of them), and a logarithm's difference is rounded as the small number that it is. A loss of 0.1 is off by
 // 2.6e-8 so (root mean square; 6.3e-8 without), the log-sum-exps by their own rounding.
 //
-// Measured, rows of 128256 bf16: loss alone, 2048 rows, 77 us (80% of a copy's rate); loss and gradient of 4096, 388 us (74%);
-// policy gradient of 4096, 351 us (82%); 2048 rows' gradient from known log-sum-exps 142 us (98%).
+// Measured, rows of 128256 bf16: loss alone, 2048 rows, 77 us (81% of a copy's rate); loss and gradient of 4096, 346 us (83%);
+// policy gradient of 4096, 329 us (87%); 2048 rows' gradient from known log-sum-exps 142 us (98%). What is rare is called
+// with copies of what it needs: closures by reference put the hot loops' variables on the stack (346 us: 388, 329: 351).
 #include <algorithm>
 
 #include "logits.cuh"
@@ -55,6 +56,7 @@ struct Part {
     e1 = min(g1 * kPer<E> - lead, V);
   }
   __device__ __forceinline__ bool has(int id) const { return id >= e0 && id < e1; }
+  __device__ __forceinline__ int granule_of(int id) const { return has(id) ? g0 + (id - base) / kPer<E> : -1; }  // -1: not here
   // the granules that lie in the row as a whole
   __device__ __forceinline__ int whole0() const { return base < 0 ? g0 + 1 : g0; }
   __device__ __forceinline__ int whole1() const { return g1 > g0 && g1 * kPer<E> - lead > V ? g1 - 1 : g1; }
@@ -269,6 +271,7 @@ struct RowInfo {
   float weight, rollout;     // the gradient's, or the advantage; the token's log-probability in the rollout
   int again;                 // whether the sums are to be taken once more
   int twice;                 // whether slots share an id
+  int shared;                // whether slots of this part share a granule
   float m, s, s_low, m_out, s_out;  // references and sums of the whole row, and of its logits outside the ids (with a tail)
   float m_at, scale;         // the gradient outside the ids
   float inv_s, factor;       // and at them
@@ -427,11 +430,34 @@ __device__ __forceinline__ uint4 without(uint4 g, uint32_t marked) {
   return pack(x);
 }
 
-// Marks an id of a part (a byte a granule, a bit an element). True if it was marked before, which is another slot's doing.
+// Granule i of a part without the elements at ids.
 template <class E>
-__device__ __forceinline__ bool mark(uint32_t* marks, int id, int base) {
-  const int at = id - base, bit = 8 * (at / kPer<E> % 4) + at % kPer<E>;
-  return atomicOr(&marks[at / kPer<E> / 4], 1u << bit) >> bit & 1u;
+__device__ __noinline__ uint4 without_ids(const Part<E> part, const Slots slots, int i, uint4 g) {
+  uint32_t marked = 0;
+  for (int j = 0; j < slots.k; ++j)
+    if (part.granule_of(slots.id[j]) == i) marked |= 1u << (slots.id[j] - part.base) % kPer<E>;
+  return without<E>(g, marked);
+}
+
+// A warp's sum of a part, outside the ids if that is wanted, once more at its largest logits.
+template <class E>
+__device__ __noinline__ Sum sum_again(const Part<E> part, const Slots slots, bool outside, int tid, int threads, Scale c) {
+  Sum sum;
+  auto add = [&](int i, uint4 g) {
+    if (outside) g = without_ids(part, slots, i, g);
+    float x[kPer<E>];
+    unpack(g, x);
+    sum.add_largest(x, max_of(x), c);
+  };
+  for (int i = part.whole0() + tid; i < part.whole1(); i += threads) add(i, __ldg(part.granules() + i));
+  part.cut(tid, threads, [&](int i) { add(i, part.load_cut(i)); });
+  sum.merge_warp(c);
+  return sum;
+}
+
+// Bytes that say which granules a thread passes over, one for `in_flight` of them.
+__host__ __device__ __forceinline__ int skip_bytes(int per, int threads, int in_flight) {
+  return (per + threads * in_flight - 1) / (threads * in_flight) * threads;
 }
 
 // ---- losses -------------------------------------------------------------------------
@@ -439,12 +465,13 @@ __device__ __forceinline__ bool mark(uint32_t* marks, int id, int base) {
 // A CTA takes part blockIdx.x % parts of row blockIdx.x / parts: `per` granules. The parts of a row are a cluster.
 //
 // A gradient reads its row again, so what counts is that it is still in L2: two CTAs of 512 threads an SM with eight
-// granules a thread under way (loss and gradient of 4096 rows: 375 us; three and four CTAs of 256 threads: 400 and 419). A loss alone reads once:
-// six CTAs of 256 threads hide one another's ends (2048 rows of 128256 bf16: 74 us; two of 512: 89).
+// granules a thread under way (three and four CTAs of 256 threads: 375 us became 400 and 419 for loss and gradient of 4096 rows).
+// A loss alone reads once: four CTAs of 256 threads hide one another's ends (2048 rows of 128256 bf16: 76 us; six with four
+// granules 77, eight of 128 threads 78, two of 512 87). Rows cut between CTAs where one each would do: 90 us and more.
 template <LossMode M>
 struct Shape {
   static constexpr bool kTwice = M != LossMode::kLoss;
-  static constexpr int kThreads = kTwice ? 512 : 256, kCtas = kTwice ? 2 : 6, kInFlight = kTwice ? 8 : 4;
+  static constexpr int kThreads = kTwice ? 512 : 256, kCtas = kTwice ? 2 : 4, kInFlight = 8;
 };
 
 template <class E, LossMode M>
@@ -459,9 +486,11 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   const Scale c = a.scale;
   const bool tail = !kPolicy && a.top_lse;
 
+  constexpr int kInFlight = Shape<M>::kInFlight;
   extern __shared__ __align__(16) uint8_t smem[];
   const Slots slots(smem, k);
-  uint32_t* const marks = reinterpret_cast<uint32_t*>(smem + 16 * k);
+  uint32_t* const skips = reinterpret_cast<uint32_t*>(smem + 16 * k);  // a byte for each kInFlight granules of a thread, a bit a granule
+  const int w0 = part.whole0(), w1 = part.whole1();
   __shared__ RowInfo info;
   __shared__ float2 sums[kMaxThreads / 32];
   __shared__ float2 shares[2][kMaxParts];  // of every part: sum and whether slots share an id; the second time reference and sum
@@ -474,11 +503,11 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   for (int j = tid; j < k; j += threads)
     any |= slots.set(j, __ldg(kPolicy ? a.tokens + t : a.ids + t * k + j), kPolicy ? 0.0f : __ldg(a.top + t * k + j), a.V, a.status);
   if constexpr (!kPolicy)
-    for (int i = tid; i < (per + 15) / 16; i += threads) reinterpret_cast<uint4*>(marks)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < skip_bytes(per, threads, kInFlight) / 16; i += threads) reinterpret_cast<uint4*>(skips)[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) {
     info.weight = weight;
     info.rollout = rollout;
-    info.twice = 0;
+    info.twice = info.shared = 0;
     if constexpr (kPolicy) slots.p[0] = 1.0f;
   }
   if (parts > 1) cluster_arrive();  // this CTA runs
@@ -496,14 +525,30 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     return;
   }
 
-  // The logits at the ids, and marks of those here. No part writes a gradient before all have been here, as sums are joined
-  // in between.
+  // The logits at the ids, and marks of their granules here. No part writes a gradient before all have been here, as sums are
+  // joined in between. With a tail, a granule with an id is left to the thread of its first slot: the others have one byte to
+  // look at for kInFlight granules. (With a mark for every element, and a byte a granule to look at by the thread that comes to
+  // it: 388 us in the place of 346 for loss and gradient of 4096 rows.)
+  const uint4* const granules = part.granules();
+  uint4 mine = make_uint4(0, 0, 0, 0);  // of this thread's first slot
   for (int j = tid; j < k; j += threads) {
     const int id = slots.id[j];
     if (id < 0) continue;
-    const bool here = part.has(id);
     slots.x[j] = to_f32(part.row[id]);
-    if (!kPolicy && here && mark<E>(marks, id, part.base)) info.twice = 1;
+    const int g = kPolicy ? -1 : part.granule_of(id);
+    if (g < 0) continue;
+    bool alone = false;  // in its granule, before others come
+    if (g >= w0 && g < w1) {
+      if (tail && j == tid) mine = __ldg(granules + g);
+      const int n = (g - w0) / threads, at = n / kInFlight * threads + (g - w0) % threads;
+      const uint32_t bit = 1u << (8 * (at % 4) + n % kInFlight);
+      alone = (atomicOr(&skips[at / 4], bit) & bit) == 0;
+    }
+    if (!alone) {
+      info.shared = 1;
+      for (int i = 0; i < k; ++i)
+        if (i != j && slots.id[i] == id) info.twice = 1;
+    }
   }
   __syncthreads();
   float m_top = -INFINITY;
@@ -513,16 +558,53 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   if (tid == 0) info.m_top = m_top;
   {
     const Ref ref(m_top, c);
-    const uint4* const granules = part.granules();
+    constexpr uint32_t kNothing = sizeof(E) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+    const uint4 nothing = make_uint4(kNothing, kNothing, kNothing, kNothing);
     const uint64_t hint = kWrites ? read_again() : read_once();
     auto load = [&](int i) { return load_hint(granules + i, hint); };
-    const uint8_t* const marked = reinterpret_cast<const uint8_t*>(marks) - part.g0;
-    auto left = [&](int i, uint4 g) { return !kPolicy && tail ? without<E>(g, marked[i]) : g; };
-    const int w0 = part.whole0() + tid, w1 = part.whole1();
     FixedSum<E> fixed;
     fixed.start(ref, c);
-    stream<Shape<M>::kInFlight>(w0, w1, threads, load, [&](int i, uint4 g) { fixed.add(left(i, g)); });
-    part.cut(tid, threads, [&](int i) { fixed.add(left(i, part.load_cut(i))); });
+    if (!kPolicy && tail)
+      for (int j = tid; j < k; j += threads) {
+        const int id = slots.id[j], g = part.granule_of(id);
+        if (g < w0 || g >= w1) continue;
+        const uint4 raw = j == tid ? mine : load(g);
+        if (!info.shared) {
+          fixed.add(without<E>(raw, 1u << (id - part.base) % N));
+          continue;
+        }
+        bool first = true;  // of the slots in this granule
+        for (int i = 0; i < j && first; ++i) first = part.granule_of(slots.id[i]) != g;
+        if (first) fixed.add(without_ids(part, slots, g, raw));
+      }
+    const uint8_t* skip = reinterpret_cast<const uint8_t*>(skips) + tid;
+    for (int i = w0 + tid; i < w1; i += kInFlight * threads, skip += threads) {
+      uint4 g[kInFlight];
+      if (i + (kInFlight - 1) * threads < w1) {
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) g[u] = load(i + u * threads);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) {
+          g[u] = nothing;
+          if (i + u * threads < w1) g[u] = load(i + u * threads);
+        }
+      }
+      if (!kPolicy && tail) {
+        const uint32_t not_here = *skip;
+        if (not_here != 0) {
+#pragma unroll
+          for (int u = 0; u < kInFlight; ++u)
+            if (not_here >> u & 1u) g[u] = nothing;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) fixed.add(g[u]);
+    }
+    part.cut(tid, threads, [&](int i) {
+      const uint4 g = part.load_cut(i);
+      fixed.add(!kPolicy && tail ? without_ids(part, slots, i, g) : g);
+    });
     const float mine = warp_sum(ref.far ? INFINITY : fixed.total());
     if (lane == 0) sums[warp] = make_float2(mine, 0.0f);
     if (!kPolicy && warp == warps - 1) {
@@ -555,14 +637,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     }
     __syncthreads();
     if (info.again) {
-      Sum largest = sum_largest<E>((w1 - w0 + threads - 1) / threads,
-                                   [&](int n) { return left(w0 + n * threads, load(w0 + n * threads)); }, c);
-      part.cut(tid, threads, [&](int i) {
-        float x[N];
-        unpack(left(i, part.load_cut(i)), x);
-        largest.add_largest(x, max_of(x), c);
-      });
-      largest.merge_warp(c);
+      const Sum largest = sum_again<E>(part, slots, !kPolicy && tail, tid, threads, c);
       if (lane == 0) sums[warp] = make_float2(largest.m, largest.s);
       __syncthreads();
       Sum outside;
@@ -581,7 +656,6 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   }
 
   if constexpr (kWrites) {
-    const uint4* const granules = part.granules();
     const uint64_t hint = read_once();
     store_gradient<Shape<M>::kInFlight>(out, part, part.row, Gradient{Ref(info.m_at, c), c, info.scale}, tid, threads,
                                         [&](int i) { return load_hint(granules + i, hint); });
@@ -675,7 +749,8 @@ cudaError_t launch(const LogitsLossArgs& a, cudaStream_t stream) {
   while (parts < kMaxParts && a.T * parts < sms && granules > parts * 256) parts *= 2;
   const int per = (granules + parts - 1) / parts;
   const int threads = std::min(Shape<M>::kThreads, per >= 2048 ? 512 : per >= 1024 ? 256 : per >= 256 ? 128 : 64);
-  const size_t smem = M == LossMode::kPolicy ? 16 : 16 * static_cast<size_t>(a.k) + (per + 15) / 16 * 16;
+  size_t smem = 16;
+  if (M != LossMode::kPolicy) smem = 16 * static_cast<size_t>(a.k) + skip_bytes(per, threads, Shape<M>::kInFlight);
   static OncePerDevice limit;
   e = limit(dev, [] { return cudaFuncSetAttribute(logits_loss_kernel<E, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
   if (e != cudaSuccess) return e;

@@ -211,6 +211,22 @@ __global__ void __launch_bounds__(256) verify_begin_kernel(const VerifyArgs a, c
   if (!s.valid || (usable < s.given && __ldg(a.drafts + s.first + usable) >= a.V)) flag(a.status, QRR_DEV_BAD_INDEX);
 }
 
+// A warp's sum of a span once more, at its largest logits (called with copies: nothing of the callers' goes to the stack).
+template <class E>
+__device__ __noinline__ Sum sum_again(const Span<E> span, int tid, Scale c) {
+  Sum sum;
+  auto add = [&](uint4 g) {
+    float x[kPer<E>];
+    unpack(g, x);
+    sum.add_largest(x, max_of(x), c);
+  };
+  for (int i = span.w0 + tid; i < span.w1; i += kSumWorkers) add(__ldg(span.granules() + i));
+  if (tid == 0 && span.head >= 0) add(span.cut(0));
+  if (tid == kSumWorkers - 1 && span.tail >= 0) add(span.cut(span.tail));
+  sum.merge_warp(c);
+  return sum;
+}
+
 // Sums of rows. Task ((place * B + b) * kRows + which) * parts + rank is a part of a row, which: the target's (0) or the
 // draft's (1). A CTA takes the tasks blockIdx.x, blockIdx.x + gridDim.x, .. that are needed: eight warps sum a task's granules
 // while one more joins the sums of the task before, decides that place if it is its last part, and looks for the task behind.
@@ -288,16 +304,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
       RowSum x{ref.m, warp_sum(ref.far ? INFINITY : fixed.total()), largest, V};
       // A sum near the ends of fp32's range is taken again, at the warp's largest logit. (It may have no values at all.)
       if (!(x.s > 0x1p-60f && x.s < 0x1p64f)) {
-        Sum again = sum_largest<E>((whole - tid + kSumWorkers - 1) / kSumWorkers,
-                                   [&](int i) { return __ldg(granules + tid + kSumWorkers * i); }, c);
-        auto add_cut = [&](int i) {
-          float v[N];
-          unpack(span.cut(i), v);
-          again.add_largest(v, max_of(v), c);
-        };
-        if (tid == 0 && span.head >= 0) add_cut(0);
-        if (tid == kSumWorkers - 1 && span.tail >= 0) add_cut(span.tail);
-        again.merge_warp(c);
+        const Sum again = sum_again(span, tid, c);
         x.m = again.m, x.s = again.s;
       }
       if constexpr (kGreedy) {
