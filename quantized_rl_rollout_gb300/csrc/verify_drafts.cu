@@ -14,10 +14,11 @@
 // lies behind a refusal that is known by then. So what is read in vain is about as much as is under way at a time. The last
 // of the parts of a place to be summed decides it. A launch before it checks the drafts, one behind it draws the tokens.
 //
-// 64 sequences of 8 drafts over 128256 bf16 logits take 56 us (of which some 38 sum rows: 171 MB at 5 TB/s but for what starts
-// and ends it, where 104 MB would do; the rest draws: 33 MB of noise, and as much of rows again); 36% of a copy's rate by
-// the bytes that have to be read. Launches of their own for places 0 and 1, for 2 .. and for all took 65 to 75 us: a launch that reads
-// a few rows takes as long as one that reads 64 MB. One sequence takes 12 us, three launches that wait for one another.
+// 64 sequences of 8 drafts over 128256 bf16 logits take 53 us (of which some 36 sum rows, half as many again as have to be;
+// the rest draws: 33 MB of noise, and as much of rows again), 38% of a copy's rate by the bytes that have to be read.
+// Launches of their own for places 0 and 1, for 2 .. and for all took 65 to 75 us: a launch that reads a few rows takes as
+// long as one that reads 64 MB. Taking tasks that are known to be needed before others changed nothing. One sequence
+// takes 12 us, three launches that wait for one another.
 //
 // Sums are fp32 with the hardware's base-2 exponential. Drafts are decided, and tokens drawn, from probabilities by the exact
 // one; where a token is drawn, bounds by the hardware's say which few can be the best.
@@ -350,8 +351,11 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
     }
     return x;
   };
-  auto choose = [&](Candidate x, Where& w, int slot) {  // the next task; whether there is one
+  // The next task; whether there is one. It is looked for as late as can be: before the sums of the task before are joined,
+  // 55 us in the place of 53 for 64 sequences, for rows that are summed in vain.
+  auto choose = [&](Where& w, int slot) {
     for (;;) {
+      const Candidate x = ask();
       const uint32_t needed = __ballot_sync(kAll, x.needed);
       if (needed) {
         const int from = __ffs(needed) - 1;
@@ -369,7 +373,6 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
       }
       next += 32 * static_cast<int64_t>(gridDim.x);
       if (next >= total) break;
-      x = ask();
     }
     if (lane == 0) tasks[slot].row = nullptr;
     return false;
@@ -402,14 +405,12 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
     if (!taken_by<F>(p, q, drafted, u, dp, dq, c) && lane == 0) atomicMin(&at.states[w.b].needed, w.place + 1);
   };
   Where now{}, then{}, last{};
-  bool any = choose(ask(), now, 0);
+  bool any = choose(now, 0);
   __syncthreads();
   for (int k = 0;; ++k) {  // task k is being summed
-    Candidate x{};
-    if (any) x = ask();
     if (k > 0) finish(last, sums[(k - 1) & 1]);
     if (!any) return;
-    any = choose(x, then, (k + 1) & 1);
+    any = choose(then, (k + 1) & 1);
     last = now, now = then;
     __syncthreads();
   }
@@ -704,7 +705,7 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(tasks, static_cast<int64_t>(sms) * kSumCtas));
   e = launch_after(true, verify_sums_kernel<E, F>, grid, 1, kSumThreads, stream, a, parts);
   if (e != cudaSuccess) return e;
-  // Enough CTAs for the SMs draw the tokens, a granule a thread at least. (Enough for two an SM: 62 us where this takes 56 for 64
+  // Enough CTAs for the SMs draw the tokens, a granule a thread at least. (Enough for two an SM: 62 us where this took 56 for 64
   // sequences, 57 for 52 with 200: what a CTA does beside its granules costs more.)
   const int granules = granules_of<E>(kPer<E> - 1, a.V);
   int draw_parts = 1;
