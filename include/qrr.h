@@ -449,7 +449,8 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * Teacher.  top_ids int32 [T][k], top_logits fp32 [T][k], 0 <= k <= 1024: the
  * teacher's logits at k tokens of each row, in any order; a slot with a
  * negative id is unused, an id >= V is unused and raises QRR_DEV_BAD_INDEX, slots
- * that name one id add up.  With temperature t (1e-6 .. 1e6):
+ * that name one id add up.  With temperature t (1e-6 .. 1e6; double, so that a
+ * program's 0.8 is what its own formulas take):
  *   q = softmax(logits / t)
  *   top_lse NULL:      p_j = e^{y_j / t} / sum_i e^{y_i / t}
  *   top_lse fp32 [T]:  p_j = e^{y_j / t - top_lse}, top_lse the log-sum-exp of the
@@ -473,15 +474,15 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
 typedef enum qrr_dtype { QRR_DTYPE_BF16 = 0, QRR_DTYPE_FP32 = 1 } qrr_dtype;
 
 qrr_status qrr_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
-                            const float* top_logits, int32_t k, const float* top_lse, float temperature, float* loss,
+                            const float* top_logits, int32_t k, const float* top_lse, double temperature, float* loss,
                             float* stats, int32_t* dev_status, void* stream);
 qrr_status qrr_distill_topk_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
                                      const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
-                                     float temperature, const float* stats, const float* grad, void* dlogits,
+                                     double temperature, const float* stats, const float* grad, void* dlogits,
                                      int64_t ldd, int32_t* dev_status, void* stream);
 qrr_status qrr_distill_topk_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
                                  const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
-                                 float temperature, const float* grad, float* loss, void* dlogits, int64_t ldd,
+                                 double temperature, const float* grad, float* loss, void* dlogits, int64_t ldd,
                                  int32_t* dev_status, void* stream);
 
 /* qrr_token_logprobs_is_grad: qrr_token_logprobs_is and the gradient of
@@ -536,7 +537,7 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
 size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_t dtype);
 qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
                              int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,
-                             const float* uniforms, const float* noise, int64_t ld_noise, float temperature,
+                             const float* uniforms, const float* noise, int64_t ld_noise, double temperature,
                              int32_t* tokens, int32_t* accepted, float* logp, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, void* stream);
 

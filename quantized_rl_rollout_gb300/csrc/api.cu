@@ -875,7 +875,7 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 
 inline bool is_dtype(int32_t d) { return d == QRR_DTYPE_BF16 || d == QRR_DTYPE_FP32; }
 inline size_t dtype_bytes(int32_t d) { return d == QRR_DTYPE_FP32 ? 4 : 2; }
-inline bool is_temperature(float t) { return t >= kMinTemperature && t <= kMaxTemperature; }
+inline bool is_temperature(double t) { return t >= kMinTemperature && t <= kMaxTemperature; }
 
 // Rows of logits [T][V] with `ld` between them.
 qrr_status check_rows(const void* p, int32_t dtype, int64_t T, int64_t V, int64_t ld) {
@@ -909,7 +909,7 @@ qrr_status check_teacher(const LogitsLossArgs& a) {
 }
 
 LogitsLossArgs distill_args(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
-                            const float* top_logits, int32_t k, const float* top_lse, float temperature, int32_t* dev_status) {
+                            const float* top_logits, int32_t k, const float* top_lse, double temperature, int32_t* dev_status) {
   LogitsLossArgs a{};
   a.logits = logits;
   a.fp32 = dtype == QRR_DTYPE_FP32;
@@ -928,7 +928,7 @@ LogitsLossArgs distill_args(const void* logits, int32_t dtype, int64_t T, int64_
 }  // namespace
 
 qrr_status qrr_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
-                            const float* top_logits, int32_t k, const float* top_lse, float temperature, float* loss,
+                            const float* top_logits, int32_t k, const float* top_lse, double temperature, float* loss,
                             float* stats, int32_t* dev_status, void* stream) {
   qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
   if (st != QRR_OK) return st;
@@ -945,7 +945,7 @@ qrr_status qrr_distill_topk(const void* logits, int32_t dtype, int64_t T, int64_
 
 qrr_status qrr_distill_topk_backward(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
                                      const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
-                                     float temperature, const float* stats, const float* grad, void* dlogits,
+                                     double temperature, const float* stats, const float* grad, void* dlogits,
                                      int64_t ldd, int32_t* dev_status, void* stream) {
   qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
   if (st != QRR_OK) return st;
@@ -966,7 +966,7 @@ qrr_status qrr_distill_topk_backward(const void* logits, int32_t dtype, int64_t 
 
 qrr_status qrr_distill_topk_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,
                                  const int32_t* top_ids, const float* top_logits, int32_t k, const float* top_lse,
-                                 float temperature, const float* grad, float* loss, void* dlogits, int64_t ldd,
+                                 double temperature, const float* grad, float* loss, void* dlogits, int64_t ldd,
                                  int32_t* dev_status, void* stream) {
   qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
   if (st != QRR_OK) return st;
@@ -1016,13 +1016,13 @@ size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_
 
 qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
                              int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,
-                             const float* uniforms, const float* noise, int64_t ld_noise, float temperature,
+                             const float* uniforms, const float* noise, int64_t ld_noise, double temperature,
                              int32_t* tokens, int32_t* accepted, float* logp, void* workspace, size_t workspace_bytes,
                              int32_t* dev_status, void* stream) {
   if (!is_dtype(dtype) || T < 0 || B < 0 || V < 1) return QRR_ERR_INVALID_ARG;
   if (!cu && (B == 0 ? T > 0 : T % B != 0)) return QRR_ERR_INVALID_ARG;
-  if (temperature != 0.0f && !is_temperature(temperature)) return QRR_ERR_INVALID_ARG;
-  const bool greedy = temperature == 0.0f;
+  if (temperature != 0.0 && !is_temperature(temperature)) return QRR_ERR_INVALID_ARG;
+  const bool greedy = temperature == 0.0;
   if (T > (int64_t{1} << 30) || B > (1 << 26) || V > (int64_t{1} << 30)) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (B > 0 && (!target || !tokens || !accepted || !logp)) return QRR_ERR_INVALID_ARG;
   if (B > 0 && T > 0 && (!drafts || (!greedy && !uniforms))) return QRR_ERR_INVALID_ARG;

@@ -122,17 +122,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 1 / t, and log2(e) / t in two parts, c rounded down and lo > 0: of a logit of -inf both products are -inf.
+// t and 1 / t, and log2(e) / t in two parts, c rounded down and lo > 0: of a logit of -inf both products are -inf.
 struct Scale {
-  float inv_t, c, lo;
+  float t, inv_t, c, lo;
   __device__ __forceinline__ operator float() const { return c; }
   __device__ __forceinline__ float exponent(float x, float r) const { return fmaf(x, lo, fmaf(x, c, -r)); }
 };
-inline Scale scale_of(float t) {
+inline Scale scale_of(double t) {
   const double k = 1.4426950408889634 / t;
   float c = static_cast<float>(k);
   if (c >= k) c = nextafterf(c, 0.0f);
-  return Scale{1.0f / t, c, static_cast<float>(k - c)};
+  return Scale{static_cast<float>(t), static_cast<float>(1.0 / t), c, static_cast<float>(k - c)};
 }
 
 // A number in two parts, and sums of such.
@@ -345,7 +345,7 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // ---- host -------------------------------------------------------------------
 
-constexpr float kMinTemperature = 1e-6f, kMaxTemperature = 1e6f;
+constexpr double kMinTemperature = 1e-6, kMaxTemperature = 1e6;
 
 // Launch on clusters of `cluster` CTAs along x.
 template <class... K, class... A>
@@ -378,7 +378,7 @@ struct LogitsLossArgs {
   const float* top;    // [T][k]
   const float* top_lse;
   int k;
-  float temperature;  // its scale is set by the launch, as verify's
+  double temperature;  // its scale is set by the launch, as verify's
   const float* grad;
   const float* stats_in;
   float* loss;
@@ -412,7 +412,7 @@ struct VerifyArgs {
   const float* uniforms;  // [T]
   const float* noise;     // [B][V]
   int64_t ld_noise;
-  float temperature;  // 0: the likeliest token
+  double temperature;  // 0: the likeliest token
   Scale scale;
   int32_t* tokens;    // [T + B]
   int32_t* accepted;  // [B]

@@ -120,7 +120,7 @@ struct Slots {
 // mass = sum_j p_j, rest = p_r, and the log-sum-exp that the teacher's logits are measured from: y_sum = sum 2^{c y - r} at
 // the reference of y_max (without a tail) or lse.
 struct Teacher {
-  float mass, rest, y_max, y_sum, y_low, lse;
+  float mass, mass_low, rest, y_max, y_sum, y_low, lse;
 };
 
 // A log-sum-exp in base 2, in two parts.
@@ -142,7 +142,7 @@ struct Lse {
 
 // By a warp; the slots' p_j are written.
 __device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse, const Slots& s, Scale c, int lane) {
-  Teacher r{0.0f, 0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
+  Teacher r{0.0f, 0.0f, 0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
   if (a.top_lse) {
     r.lse = top_lse;
   } else {
@@ -172,7 +172,7 @@ __device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse,
     s.p[j] = p.high;
   }
   mass.add_warp();
-  r.mass = mass.high;
+  r.mass = mass.high, r.mass_low = mass.low;
   r.rest = a.top_lse ? fmaxf((1.0f - mass.high) - mass.low, 0.0f) : 0.0f;
   return r;
 }
@@ -272,7 +272,9 @@ struct RowInfo {
   int again;                 // whether the sums are to be taken once more
   int twice;                 // whether slots share an id
   int shared;                // whether slots of this part share a granule
-  float m, s, s_low, m_out, s_out;  // references and sums of the whole row, and of its logits outside the ids (with a tail)
+  // references and sums of the whole row (and a low part of it), and of its logits outside the ids (with a tail); the sum at
+  // the ids, -1 if it is not at m
+  float m, s, s_low, s_top, m_out, s_out;
   float m_at, scale;         // the gradient outside the ids
   float inv_s, factor;       // and at them
   float lse, lse_at;         // kBackward: known, of m and m_at
@@ -311,7 +313,9 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
     if (y.rest > (none ? kDust : 0.0f)) {
       const float ln_q = none ? -INFINITY : ref.far || ref_out.far ? (ref_out.m - ref.m) * inv_t + logf(info.s_out) - logf(sum)
                                                                    : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
-      loss += y.rest * (logf(y.rest) - ln_q);
+      // Where most is outside the ids, ln (p_r / q_r) is that of 1 and little: (1 - mass) / (1 - q at the ids).
+      const float q_top = info.s_top >= 0.0f ? info.s_top / sum : 1.0f;
+      loss += y.rest * (q_top < 0.5f ? log1pf(((q_top - y.mass) - y.mass_low) / (1.0f - q_top)) : logf(y.rest) - ln_q);
     }
   }
   a.loss[t] = loss;
@@ -339,7 +343,7 @@ __device__ __forceinline__ Two sum_at_ids(const Slots& slots, const RowInfo& inf
 // is q_rest. By a warp; `writes`: of the row's parts, this one writes what is the row's.
 template <bool kPolicy>
 __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& all,
-                                         float low, const Sum& outside, float q_rest, bool tail, Scale c, int lane, bool writes) {
+                                         float low, float top, const Sum& outside, float q_rest, bool tail, Scale c, int lane, bool writes) {
   const Ref ref(all.m, c);
   const bool bare = all.m == -INFINITY, none = outside.m == -INFINITY;
   const float sum = bare ? 1.0f : all.s;  // a row of -inf alone has no probabilities: q = 0
@@ -360,7 +364,7 @@ __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, con
   }
   if (lane == 0) {
     const float inv_s = 1.0f / sum;
-    info.m = all.m, info.s = all.s, info.s_low = low, info.m_out = outside.m, info.s_out = outside.s;
+    info.m = all.m, info.s = all.s, info.s_low = low, info.s_top = top, info.m_out = outside.m, info.s_out = outside.s;
     info.m_at = tail ? outside.m : all.m;
     info.scale = !tail ? factor * inv_s : none ? 0.0f : factor * (q_rest * inv_s - info.teacher.rest) / outside.s;
     info.inv_s = inv_s;
@@ -378,7 +382,7 @@ __device__ __forceinline__ bool conclude_first(const LogitsLossArgs& a, int64_t 
   sum.add(top);
   const Sum outside{info.m_top, tail ? total : sum.high}, all{info.m_top, sum.high};
   if (!served(all.s) || (tail && !served(total)) || all.m == -INFINITY) return false;
-  conclude<kPolicy>(a, t, slots, info, all, sum.low, outside, total, tail, c, lane, writes);
+  conclude<kPolicy>(a, t, slots, info, all, sum.low, top.high, outside, total, tail, c, lane, writes);
   return true;
 }
 
@@ -388,17 +392,17 @@ __device__ __forceinline__ void conclude_largest(const LogitsLossArgs& a, int64_
                                                  const Sum& outside, bool tail, Scale c, int lane, bool writes) {
   Sum all = outside;
   if (tail) all.merge(info.m_top, top.high, c);
-  conclude<kPolicy>(a, t, slots, info, all, 0.0f, outside, outside.s * Sum::moved(outside.m, Ref(all.m, c), c), tail, c, lane, writes);
+  conclude<kPolicy>(a, t, slots, info, all, 0.0f, -1.0f, outside, outside.s * Sum::moved(outside.m, Ref(all.m, c), c), tail, c, lane, writes);
 }
 
 // The reference of a known log-sum-exp, a whole number too, and the factor of its row's shares that is left.
-__device__ __forceinline__ Ref known_ref(float lse, float temperature, Scale c) {
-  Ref ref(lse * temperature, c);
+__device__ __forceinline__ Ref known_ref(float lse, Scale c) {
+  Ref ref(lse * c.t, c);
   if (!ref.far && lse > -INFINITY) ref.r = rintf(Lse(lse).high);
   return ref;
 }
-__device__ __forceinline__ float known_share(float lse, float temperature, Scale c) {
-  const Ref ref = known_ref(lse, temperature, c);
+__device__ __forceinline__ float known_share(float lse, Scale c) {
+  const Ref ref = known_ref(lse, c);
   const Lse parts(lse);
   return !ref.far && lse > -INFINITY ? pow2(ref.r - parts.high, -parts.low).high : 1.0f;
 }
@@ -410,11 +414,11 @@ __device__ __forceinline__ void conclude_known(const LogitsLossArgs& a, int64_t 
   info.lse = lse;
   info.lse_at = tail ? lse_out : lse;
   info.factor = info.weight * c.inv_t;
-  info.inv_s = known_share(lse, a.temperature, c);
+  info.inv_s = known_share(lse, c);
   info.scale = !tail                  ? info.factor * info.inv_s
                : lse_out == -INFINITY ? 0.0f
                                       : info.factor * (ex2_approx((lse_out - lse) * kLog2e) - info.teacher.rest) *
-                                            known_share(lse_out, a.temperature, c);
+                                            known_share(lse_out, c);
   if (!(info.teacher.mass < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
 }
 
@@ -725,8 +729,8 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
     }
   twice = __syncthreads_or(twice);
 
-  const Ref ref = known_ref(info.lse, a.temperature, c);
-  const Gradient of{known_ref(info.lse_at, a.temperature, c), c, info.scale};
+  const Ref ref = known_ref(info.lse, c);
+  const Gradient of{known_ref(info.lse_at, c), c, info.scale};
   store_gradient<1>(out, part, held - part.base, of, tid, threads, [&](int i) { return tile[i - part.g0]; });
   __syncthreads();
   store_ids(out, part, slots, twice, ref, c, info.inv_s, info.factor, tid, threads);
@@ -789,7 +793,7 @@ cudaError_t launch(const LogitsLossArgs& a, LossMode mode, cudaStream_t stream) 
 
 cudaError_t launch_logits_loss(LogitsLossArgs a, LossMode mode, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  a.scale = scale_of(mode == LossMode::kPolicy ? 1.0f : a.temperature);
+  a.scale = scale_of(mode == LossMode::kPolicy ? 1.0 : a.temperature);
   return a.fp32 ? launch<float>(a, mode, stream) : launch<Bf16>(a, mode, stream);
 }
 

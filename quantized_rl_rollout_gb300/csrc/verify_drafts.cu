@@ -717,7 +717,7 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
 
 template <class E>
 cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
-  if (a.temperature == 0.0f) return launch<E, Form::kGreedy>(a, stream);
+  if (a.temperature == 0.0) return launch<E, Form::kGreedy>(a, stream);
   return a.draft ? launch<E, Form::kModel>(a, stream) : launch<E, Form::kLookup>(a, stream);
 }
 
@@ -730,7 +730,7 @@ size_t verify_drafts_ws_bytes(int64_t T, int64_t B, int64_t V, int fp32) {
 
 cudaError_t launch_verify_drafts(VerifyArgs a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
-  a.scale = scale_of(a.temperature == 0.0f ? 1.0f : a.temperature);
+  a.scale = scale_of(a.temperature == 0.0 ? 1.0 : a.temperature);
   return a.fp32 ? launch<float>(a, stream) : launch<Bf16>(a, stream);
 }
 

@@ -105,17 +105,17 @@ SIGNATURES = {
     "qrr_aqn_noise_probe": (ctypes.c_int, [_c_p, _c_i64, _c_i64, ctypes.c_uint64, _c_i32, _c_i32, _c_p]),
     "qrr_token_logprobs_is": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, ctypes.c_float, _c_p, _c_p, _c_p,
                                              _c_p]),
-    "qrr_distill_topk": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, ctypes.c_float, _c_p,
+    "qrr_distill_topk": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, ctypes.c_double, _c_p,
                                         _c_p, _c_p, _c_p]),
     "qrr_distill_topk_backward": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p,
-                                                 ctypes.c_float, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
-    "qrr_distill_topk_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, ctypes.c_float,
+                                                 ctypes.c_double, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
+    "qrr_distill_topk_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_i32, _c_p, ctypes.c_double,
                                              _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
     "qrr_token_logprobs_is_grad": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, ctypes.c_float,
                                                   _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
     "qrr_verify_drafts_workspace_bytes": (_c_sz, [_c_i64, _c_i32, _c_i64, _c_i32]),
     "qrr_verify_drafts": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i32, _c_i64, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p,
-                                         _c_i64, ctypes.c_float, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
+                                         _c_i64, ctypes.c_double, _c_p, _c_p, _c_p, _c_p, _c_sz, _c_p, _c_p]),
     "qrr_workspace_bytes": (_c_sz, [_c_i32, _c_i64, _c_i64, _c_i64, _c_i32]),
     "qrr_wait_probe": (ctypes.c_int, [_c_i64, _c_i32, _c_p, _c_p, _c_p]),
     "qrr_stream_probe": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p]),
