@@ -14,8 +14,9 @@
 // lies behind a refusal that is known by then. So what is read in vain is about as much as is under way at a time. The last
 // of the parts of a place to be summed decides it. A launch before it checks the drafts, one behind it draws the tokens.
 //
-// 64 sequences of 8 drafts over 128256 bf16 logits take 53 us (of which some 36 sum rows, half as many again as have to be;
-// the rest draws: 33 MB of noise, and as much of rows again), 38% of a copy's rate by the bytes that have to be read.
+// 64 sequences of 8 drafts over 128256 bf16 logits take 53 us, 38% of a copy's rate by the bytes that have to be read. Some 36
+// of them sum rows: 171 MB at 4.6 TB/s where 104 MB have to be read, but a place at a time for the sequences that go on would
+// take 9 tasks of 4 us one after another, as long. The rest draws: 33 MB of noise, and as much of rows again.
 // Launches of their own for places 0 and 1, for 2 .. and for all took 65 to 75 us: a launch that reads a few rows takes as
 // long as one that reads 64 MB. Taking tasks that are known to be needed before others changed nothing. One sequence
 // takes 12 us, three launches that wait for one another.
@@ -351,8 +352,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
     }
     return x;
   };
-  // The next task; whether there is one. It is looked for as late as can be: before the sums of the task before are joined,
-  // 55 us in the place of 53 for 64 sequences, for rows that are summed in vain.
+  // The next task; whether there is one. It is looked for behind the join of the task before (64 sequences: 53 us; before it, 55).
   auto choose = [&](Where& w, int slot) {
     for (;;) {
       const Candidate x = ask();
