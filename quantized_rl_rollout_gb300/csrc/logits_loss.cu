@@ -313,9 +313,9 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
     if (y.rest > (none ? kDust : 0.0f)) {
       const float ln_q = none ? -INFINITY : ref.far || ref_out.far ? (ref_out.m - ref.m) * inv_t + logf(info.s_out) - logf(sum)
                                                                    : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
-      // Where most is outside the ids, ln (p_r / q_r) is that of 1 and little: (1 - mass) / (1 - q at the ids).
+      // Where most is outside the ids for both, ln (p_r / q_r) is that of 1 and little: (1 - mass) / (1 - q at the ids).
       const float q_top = info.s_top >= 0.0f ? info.s_top / sum : 1.0f;
-      loss += y.rest * (q_top < 0.5f ? log1pf(((q_top - y.mass) - y.mass_low) / (1.0f - q_top)) : logf(y.rest) - ln_q);
+      loss += y.rest * (q_top < 0.5f && y.mass < 0.5f ? log1pf(((q_top - y.mass) - y.mass_low) / (1.0f - q_top)) : logf(y.rest) - ln_q);
     }
   }
   a.loss[t] = loss;

@@ -387,3 +387,31 @@ def test_streams_and_graphs(q):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("y", [1e-9, 1e-7, 0.3, 0.69, 0.7, 3.0, 20.0])
+@pytest.mark.parametrize("spread", [0.0, 4.0, 9.0])
+def test_rests_of_any_size(q, y, spread):
+    """The teacher's rest from 1e-9 to nearly all, beside students with little and with most at the id."""
+    v = 1000
+    x = torch.zeros(3, v)
+    x[:, 17] = torch.tensor([0.0, 1.0, 2.0]) * spread
+    x = x.to(DEV)
+    ids = torch.full((3, 1), 17, dtype=torch.int32, device=DEV)
+    top = torch.zeros(3, 1, device=DEV)
+    lse = torch.full((3,), y, device=DEV)
+    _check(q, x, ids, top, lse, 1.0)
+    _check(q, x.to(BF16), ids, top, lse, 0.7)
+
+
+def test_slots_in_one_granule(q):
+    """Ids side by side, more of them than threads that have a granule, and some of them twice."""
+    for dtype in (BF16, FP32):
+        x, _ = _rows(3, 2053, dtype, 41, start=3)
+        ids = torch.arange(1000, dtype=torch.int32).repeat(3, 1)
+        ids[1] += 1053
+        ids[2, 500:] = ids[2, :500]
+        top = x.float().cpu().gather(1, ids.long()) + 0.3
+        lse = torch.logsumexp(x.double(), -1).float() + 1.0
+        _check(q, x, ids.to(DEV), top.to(DEV), lse.to(DEV), 1.0)
+        _check(q, x, ids.to(DEV), top.to(DEV), None, 1.0)
