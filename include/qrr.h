@@ -438,7 +438,7 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * Rows.  logits: bf16 or fp32 (qrr_dtype), row t at logits + t ld elements,
  * V values; ld >= V, any alignment of the element type.  The gradient dlogits
  * has the logits' type, row t at dlogits + t ldd; it may be logits itself
- * (with ldd == ld), but must not overlap it in any other way.  V * the
+ * (with ldd == ld) or lie between its rows; any other overlap is refused.  V * the
  * element's size <= QRR_MAX_LOSS_ROW_BYTES, T <= 2^27.  Logits of -inf are
  * masked out (q = 0); a row of nothing but -inf has q = 0 everywhere.  A row
  * with a NaN or +inf raises QRR_DEV_NONFINITE, its outputs unspecified.

@@ -898,7 +898,12 @@ qrr_status check_dlogits(const LogitsLossArgs& a, int32_t dtype) {
   if (st != QRR_OK || a.T == 0) return st;
   const uintptr_t e = dtype_bytes(dtype), x = reinterpret_cast<uintptr_t>(a.logits), y = reinterpret_cast<uintptr_t>(a.dlogits);
   if (x == y) return a.T > 1 && a.ld != a.ldd ? QRR_ERR_INVALID_ARG : QRR_OK;
-  return QRR_OK;
+  const uintptr_t x_end = x + ((a.T - 1) * a.ld + a.V) * e, y_end = y + ((a.T - 1) * a.ldd + a.V) * e;
+  if (x_end <= y || y_end <= x) return QRR_OK;
+  // Rows between one another's, as columns of one buffer are.
+  if (a.ld != a.ldd || a.T == 1) return QRR_ERR_INVALID_ARG;
+  const uintptr_t ld = a.ld, V = a.V, ahead = (y > x ? y - x : x - y) / e % ld;
+  return ahead >= V && ld - ahead >= V ? QRR_OK : QRR_ERR_INVALID_ARG;
 }
 
 qrr_status check_teacher(const LogitsLossArgs& a) {

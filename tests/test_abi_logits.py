@@ -201,3 +201,22 @@ def test_binding_refuses(binding):
             call()
             raise AssertionError(f"call {i} was not refused")
     assert not calls
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dlogits=FAKE + 2), 1), (dict(dlogits=FAKE + 2 * 50), 1), (dict(logits=FAKE + 2 * 250, dlogits=FAKE), 1),  # rows in others
+    (dict(dlogits=FAKE + 2 * 100), 1), (dict(T=1, dlogits=FAKE + 2), 1), (dict(dlogits=FAKE + 2 * 104, ld=104, ldd=108), 1),
+    (dict(dlogits=FAKE + 2 * 100, ld=199, ldd=199), 1), (dict(dlogits=FAKE + 2 * 300, ld=250, ldd=250), 1)])
+def test_gradients_that_overlap_the_logits(qrr, change, status):
+    assert _losses(qrr, **change)[1:] == (status, status)
+    assert _policy(qrr, **change) == status
+
+
+def test_gradients_beside_the_logits(qrr, monkeypatch):
+    """Columns of one buffer, and the logits themselves, pass the checks (an injected fault stops them before a launch)."""
+    monkeypatch.setenv("QRR_INJECT_FAULT", "cuda")
+    ok = _losses(qrr)[2]
+    assert ok not in (0, 1, 2, 3)
+    for change in (dict(dlogits=FAKE + 2 * 100, ld=200, ldd=200), dict(logits=FAKE + 2 * 100, dlogits=FAKE, ld=208, ldd=208),
+                   dict(dlogits=FAKE), dict(dlogits=FAKE + 2 * 300), dict(T=1, dlogits=FAKE, ldd=300)):
+        assert _losses(qrr, **change)[1:] == (ok, ok) and _policy(qrr, **change) == ok, change
