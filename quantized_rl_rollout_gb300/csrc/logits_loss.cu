@@ -271,7 +271,6 @@ struct RowInfo {
   float weight, rollout;     // the gradient's, or the advantage; the token's log-probability in the rollout
   int again;                 // whether the sums are to be taken once more
   int twice;                 // whether slots share an id
-  int shared;                // whether slots of this part share a granule
   // references and sums of the whole row (and a low part of it), and of its logits outside the ids (with a tail); the sum at
   // the ids, -1 if it is not at m
   float m, s, s_low, s_top, m_out, s_out;
@@ -434,21 +433,61 @@ __device__ __forceinline__ uint4 without(uint4 g, uint32_t marked) {
   return pack(x);
 }
 
+// The granules of a part that have ids, in shared memory: a table of a power of two of places, at most half of them used. Of
+// each the elements at ids (a bit each) and its first slot.
+struct Marked {
+  int* granule;  // -1: an empty place
+  uint32_t* bits;
+  int* slot;
+  int places;
+  static __host__ __device__ __forceinline__ int places_for(int k) {
+    int n = 32;
+    while (n < 2 * k) n *= 2;
+    return n;
+  }
+  static __host__ __device__ __forceinline__ int bytes_for(int k) { return 12 * places_for(k); }
+  __device__ __forceinline__ Marked(uint8_t* at, int k) : granule(reinterpret_cast<int*>(at)), places(places_for(k)) {
+    bits = reinterpret_cast<uint32_t*>(granule + places);
+    slot = reinterpret_cast<int*>(bits + places);
+  }
+  __device__ __forceinline__ void clear(int tid, int threads) const {
+    for (int i = tid; i < places; i += threads) granule[i] = -1, bits[i] = 0, slot[i] = kMaxTop;
+  }
+  __device__ __forceinline__ int start(int g) const {  // multiplicative hashing, by the golden ratio
+    return static_cast<int>(static_cast<uint32_t>(g) * 2654435769u >> 16) & (places - 1);
+  }
+  // True if the element was marked before, which is another slot's doing.
+  __device__ __forceinline__ bool mark(int g, int element, int j) const {
+    int i = start(g);
+    for (;; i = (i + 1) & (places - 1)) {
+      const int was = atomicCAS(&granule[i], -1, g);
+      if (was == -1 || was == g) break;
+    }
+    atomicMin(&slot[i], j);
+    return atomicOr(&bits[i], 1u << element) >> element & 1u;
+  }
+  // Its place, -1 if it has no ids.
+  __device__ __forceinline__ int find(int g) const {
+    for (int i = start(g);; i = (i + 1) & (places - 1)) {
+      if (granule[i] == g) return i;
+      if (granule[i] == -1) return -1;
+    }
+  }
+};
+
 // Granule i of a part without the elements at ids.
 template <class E>
-__device__ __noinline__ uint4 without_ids(const Part<E> part, const Slots slots, int i, uint4 g) {
-  uint32_t marked = 0;
-  for (int j = 0; j < slots.k; ++j)
-    if (part.granule_of(slots.id[j]) == i) marked |= 1u << (slots.id[j] - part.base) % kPer<E>;
-  return without<E>(g, marked);
+__device__ __forceinline__ uint4 without_ids(const Marked& marked, int i, uint4 g) {
+  const int at = marked.find(i);
+  return at < 0 ? g : without<E>(g, marked.bits[at]);
 }
 
 // A warp's sum of a part, outside the ids if that is wanted, once more at its largest logits.
 template <class E>
-__device__ __noinline__ Sum sum_again(const Part<E> part, const Slots slots, bool outside, int tid, int threads, Scale c) {
+__device__ __noinline__ Sum sum_again(const Part<E> part, const Marked marked, bool outside, int tid, int threads, Scale c) {
   Sum sum;
   auto add = [&](int i, uint4 g) {
-    if (outside) g = without_ids(part, slots, i, g);
+    if (outside) g = without_ids<E>(marked, i, g);
     float x[kPer<E>];
     unpack(g, x);
     sum.add_largest(x, max_of(x), c);
@@ -493,7 +532,9 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   constexpr int kInFlight = Shape<M>::kInFlight;
   extern __shared__ __align__(16) uint8_t smem[];
   const Slots slots(smem, k);
-  uint32_t* const skips = reinterpret_cast<uint32_t*>(smem + 16 * k);  // a byte for each kInFlight granules of a thread, a bit a granule
+  const Marked marked(smem + 16 * k, k);
+  // a byte for each kInFlight granules of a thread, a bit a granule
+  uint32_t* const skips = reinterpret_cast<uint32_t*>(smem + 16 * k + Marked::bytes_for(k));
   const int w0 = part.whole0(), w1 = part.whole1();
   __shared__ RowInfo info;
   __shared__ float2 sums[kMaxThreads / 32];
@@ -506,12 +547,15 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   bool any = false;
   for (int j = tid; j < k; j += threads)
     any |= slots.set(j, __ldg(kPolicy ? a.tokens + t : a.ids + t * k + j), kPolicy ? 0.0f : __ldg(a.top + t * k + j), a.V, a.status);
-  if constexpr (!kPolicy)
-    for (int i = tid; i < skip_bytes(per, threads, kInFlight) / 16; i += threads) reinterpret_cast<uint4*>(skips)[i] = make_uint4(0, 0, 0, 0);
+  if constexpr (!kPolicy) {
+    marked.clear(tid, threads);
+    for (int i = tid; i < skip_bytes(per, threads, kInFlight) / 16; i += threads)
+      reinterpret_cast<uint4*>(skips)[i] = make_uint4(0, 0, 0, 0);
+  }
   if (tid == 0) {
     info.weight = weight;
     info.rollout = rollout;
-    info.twice = info.shared = 0;
+    info.twice = 0;
     if constexpr (kPolicy) slots.p[0] = 1.0f;
   }
   if (parts > 1) cluster_arrive();  // this CTA runs
@@ -541,17 +585,11 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     slots.x[j] = to_f32(part.row[id]);
     const int g = kPolicy ? -1 : part.granule_of(id);
     if (g < 0) continue;
-    bool alone = false;  // in its granule, before others come
-    if (g >= w0 && g < w1) {
-      if (tail && j == tid) mine = __ldg(granules + g);
+    if (marked.mark(g, (id - part.base) % N, j)) info.twice = 1;
+    if (tail && g >= w0 && g < w1) {
+      if (j == tid) mine = __ldg(granules + g);
       const int n = (g - w0) / threads, at = n / kInFlight * threads + (g - w0) % threads;
-      const uint32_t bit = 1u << (8 * (at % 4) + n % kInFlight);
-      alone = (atomicOr(&skips[at / 4], bit) & bit) == 0;
-    }
-    if (!alone) {
-      info.shared = 1;
-      for (int i = 0; i < k; ++i)
-        if (i != j && slots.id[i] == id) info.twice = 1;
+      atomicOr(&skips[at / 4], 1u << (8 * (at % 4) + n % kInFlight));
     }
   }
   __syncthreads();
@@ -572,14 +610,8 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
       for (int j = tid; j < k; j += threads) {
         const int id = slots.id[j], g = part.granule_of(id);
         if (g < w0 || g >= w1) continue;
-        const uint4 raw = j == tid ? mine : load(g);
-        if (!info.shared) {
-          fixed.add(without<E>(raw, 1u << (id - part.base) % N));
-          continue;
-        }
-        bool first = true;  // of the slots in this granule
-        for (int i = 0; i < j && first; ++i) first = part.granule_of(slots.id[i]) != g;
-        if (first) fixed.add(without_ids(part, slots, g, raw));
+        const int at = marked.find(g);
+        if (marked.slot[at] == j) fixed.add(without<E>(j == tid ? mine : load(g), marked.bits[at]));
       }
     const uint8_t* skip = reinterpret_cast<const uint8_t*>(skips) + tid;
     for (int i = w0 + tid; i < w1; i += kInFlight * threads, skip += threads) {
@@ -607,7 +639,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     }
     part.cut(tid, threads, [&](int i) {
       const uint4 g = part.load_cut(i);
-      fixed.add(!kPolicy && tail ? without_ids(part, slots, i, g) : g);
+      fixed.add(!kPolicy && tail ? without_ids<E>(marked, i, g) : g);
     });
     const float mine = warp_sum(ref.far ? INFINITY : fixed.total());
     if (lane == 0) sums[warp] = make_float2(mine, 0.0f);
@@ -641,7 +673,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     }
     __syncthreads();
     if (info.again) {
-      const Sum largest = sum_again<E>(part, slots, !kPolicy && tail, tid, threads, c);
+      const Sum largest = sum_again<E>(part, marked, !kPolicy && tail, tid, threads, c);
       if (lane == 0) sums[warp] = make_float2(largest.m, largest.s);
       __syncthreads();
       Sum outside;
@@ -754,7 +786,7 @@ cudaError_t launch(const LogitsLossArgs& a, cudaStream_t stream) {
   const int per = (granules + parts - 1) / parts;
   const int threads = std::min(Shape<M>::kThreads, per >= 2048 ? 512 : per >= 1024 ? 256 : per >= 256 ? 128 : 64);
   size_t smem = 16;
-  if (M != LossMode::kPolicy) smem = 16 * static_cast<size_t>(a.k) + skip_bytes(per, threads, Shape<M>::kInFlight);
+  if (M != LossMode::kPolicy) smem = 16 * static_cast<size_t>(a.k) + Marked::bytes_for(a.k) + skip_bytes(per, threads, Shape<M>::kInFlight);
   static OncePerDevice limit;
   e = limit(dev, [] { return cudaFuncSetAttribute(logits_loss_kernel<E, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
   if (e != cudaSuccess) return e;
