@@ -33,12 +33,6 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ Bf16 from_f32(float x, Bf16) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
 __device__ __forceinline__ float from_f32(float x, float) { return x; }
 
-template <class E>
-__device__ __forceinline__ E minus_inf() {
-  if constexpr (sizeof(E) == 2) return 0xFF80u;
-  else return -INFINITY;
-}
-
 __device__ __forceinline__ void unpack(uint4 g, float (&x)[8]) {
   x[0] = bf16_lo(g.x), x[1] = bf16_hi(g.x), x[2] = bf16_lo(g.y), x[3] = bf16_hi(g.y);
   x[4] = bf16_lo(g.z), x[5] = bf16_hi(g.z), x[6] = bf16_lo(g.w), x[7] = bf16_hi(g.w);
@@ -228,8 +222,6 @@ struct Sum {
 #pragma unroll
     for (int u = 0; u < N; ++u) s += ref(x[u], c);
   }
-  // Whether the reference that is kept served.
-  __device__ __forceinline__ bool served() const { return m > -INFINITY && s < 0x1p64f; }
 };
 
 // A thread's sum at a reference that stays, in two accumulators of two values.
@@ -324,18 +316,9 @@ __device__ __forceinline__ void stream(int first, int end, int step, Load load, 
 
 // ---- clusters ---------------------------------------------------------------
 
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 // To the same variable of CTA `rank`.
 __device__ __forceinline__ void st_cluster(const float2* p, uint32_t rank, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y) : "memory");
-}
-__device__ __forceinline__ void st_cluster(const float4* p, uint32_t rank, float4 v) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr(p, rank)), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
 }
 __device__ __forceinline__ void st_cluster(const uint64_t* p, uint32_t rank, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr(p, rank)), "l"(v) : "memory");
@@ -396,8 +379,6 @@ struct LogitsLossArgs {
 };
 enum class LossMode { kLoss, kGrad, kBackward, kPolicy };
 constexpr int kMaxTop = 1024;
-// Bytes of a row, of which 32 CTAs hold the tiles for its gradient from known log-sum-exps with ease.
-constexpr int64_t kMaxLossRowBytes = 3 << 19;
 cudaError_t launch_logits_loss(LogitsLossArgs a, LossMode mode, cudaStream_t stream);
 
 struct VerifyArgs {

@@ -177,27 +177,19 @@ __device__ __forceinline__ Teacher teach(const LogitsLossArgs& a, float top_lse,
   return r;
 }
 
-// out[e0 .. e1) of a row, whole granules at once: block(e) gives kPer elements from e on, one(e) a single one.
-template <class E, class Block, class One>
-__device__ __forceinline__ void store_range(E* out, int e0, int e1, int tid, int threads, Block block, One one) {
-  constexpr int N = kPer<E>;
-  if (e0 >= e1) return;
-  const int lead = lead_of(out);
-  const int first = (e0 + lead) / N, last = (e1 + lead + N - 1) / N;
-  for (int g = first + tid; g < last; g += threads) {
-    const int f = g * N - lead;
-    if (f >= e0 && f + N <= e1) {
-      __stcs(reinterpret_cast<uint4*>(out + f), block(f));
-    } else {
-      for (int e = max(f, e0); e < min(f + N, e1); ++e) out[e] = one(e);
-    }
-  }
-}
-
 template <class E>
 __device__ __forceinline__ void store_zeros(E* out, const Part<E>& part, int tid, int threads) {
-  store_range(out, part.e0, part.e1, tid, threads, [](int) { return make_uint4(0, 0, 0, 0); },
-              [](int) { return from_f32(0.0f, E{}); });
+  constexpr int N = kPer<E>;
+  if (part.e0 >= part.e1) return;
+  const int lead = lead_of(out), last = (part.e1 + lead + N - 1) / N;
+  for (int g = (part.e0 + lead) / N + tid; g < last; g += threads) {
+    const int f = g * N - lead;
+    if (f >= part.e0 && f + N <= part.e1) {
+      __stcs(reinterpret_cast<uint4*>(out + f), make_uint4(0, 0, 0, 0));
+    } else {
+      for (int e = max(f, part.e0); e < min(f + N, part.e1); ++e) out[e] = from_f32(0.0f, E{});
+    }
+  }
 }
 
 // The gradient outside the ids: e^{x / t} over that at `at`, times `scale`.
@@ -383,8 +375,8 @@ __device__ __forceinline__ Two sum_at_ids(const Slots& slots, const RowInfo& inf
   return top;
 }
 
-// What follows from the references and sums of the row (and a low part) and (with a tail) outside the ids, whose sum at the row's reference
-// is q_rest. By a warp; `writes`: of the row's parts, this one writes what is the row's.
+// What follows from the references and sums of the row (and a low part) and (with a tail) outside the ids, whose sum at the
+// row's reference is q_rest. By a warp; `writes`: of the row's parts, this one writes what is the row's.
 template <bool kPolicy>
 __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, const Slots& slots, RowInfo& info, const Sum& all,
                                          float low, float top, const Sum& outside, float q_rest, bool tail, Scale c, int lane, bool writes) {
@@ -563,7 +555,8 @@ struct Shape {
 };
 
 template <class E, LossMode M>
-__global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_loss_kernel(const LogitsLossArgs a, const int parts, const int per) {
+__global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_loss_kernel(const LogitsLossArgs a, const int parts,
+                                                                                              const int per) {
   constexpr int N = kPer<E>;
   constexpr bool kPolicy = M == LossMode::kPolicy, kWrites = M != LossMode::kLoss;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads / 32;
