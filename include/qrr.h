@@ -505,7 +505,8 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
  * [B + 1], ascending; NULL: T / B each) and one row of target logits more than
  * drafts: rows cu[b] + b .. cu[b + 1] + b, the last behind its last draft.
  *   p_i = softmax(target row / t), q_i = softmax(draft row / t)
- * Drafts d_0, d_1, .. are taken in order while u_i q_i(d_i) < p_i(d_i).  At the
+ * Drafts d_0, d_1, .. are taken in order while u_i q_i(d_i) < p_i(d_i) (decided
+ * by the quotient's logarithm: neither need be in fp32's range).  At the
  * first refusal the next token is argmax_v max(p_i(v) - q_i(v), 0) / e_v (p_i in
  * the place of the difference where nothing is left of it), behind the last
  * draft argmax_v p_n(v) / e_v: the lowest index of equals.  With u uniform in

@@ -11,7 +11,9 @@ Drafts without probabilities are ``q_i = [v = d_i]``.  At temperature 0 a draft
 is taken if it is the target's likeliest token, which is also the next token.
 For u uniform and e exponential the tokens are distributed as drawn from p.
 
-Everything is float64 on the logits' values.
+Everything is float64 on the logits' values; drafts are decided by logarithms, as
+their probabilities may be below float64's range (e^-7000 at a temperature of
+0.001) where their quotient is not.
 """
 
 import numpy as np
@@ -21,6 +23,12 @@ def softmax(x: np.ndarray) -> np.ndarray:
     x = np.asarray(x, np.float64)
     e = np.exp(x - np.max(x))
     return e / e.sum()
+
+
+def log_softmax(x: np.ndarray) -> np.ndarray:
+    x = np.asarray(x, np.float64)
+    x = x - np.max(x)
+    return x - np.log(np.exp(x).sum())
 
 
 def sequence(target, drafts, uniforms=None, noise=None, draft_logits=None, temperature: float = 1.0):
@@ -43,14 +51,18 @@ def sequence(target, drafts, uniforms=None, noise=None, draft_logits=None, tempe
             if temperature == 0:
                 ok = d == int(np.argmax(target[i]))
             else:
-                q = softmax(np.asarray(draft_logits[i], np.float64) / t) if draft_logits is not None else np.eye(1, p.size, d)[0]
-                left, right = float(uniforms[i]) * q[d], p[d]
+                q, lnq = np.eye(1, p.size, d)[0], 0.0
+                if draft_logits is not None:
+                    y = np.asarray(draft_logits[i], np.float64) / t
+                    q, lnq = softmax(y), log_softmax(y)[d]
+                with np.errstate(divide="ignore"):
+                    left, right = np.log(float(uniforms[i])) + lnq, log_softmax(target[i] / t)[d]
                 ok = left < right
-                if left and right:  # with a 0 on either side nothing is near
-                    margin = min(margin, abs(left - right) / max(left, right))
+                if np.isfinite(left) and np.isfinite(right):  # with a 0 on either side nothing is near
+                    margin = min(margin, -np.expm1(-abs(left - right)))
             if ok:
                 tokens.append(d)
-                logp.append(np.log(p[d]))
+                logp.append(float(log_softmax(target[i] / t)[d]))
                 continue
         if temperature == 0:
             token = int(np.argmax(target[i]))

@@ -415,3 +415,30 @@ def test_slots_in_one_granule(q):
         lse = torch.logsumexp(x.double(), -1).float() + 1.0
         _check(q, x, ids.to(DEV), top.to(DEV), lse.to(DEV), 1.0)
         _check(q, x, ids.to(DEV), top.to(DEV), None, 1.0)
+
+
+@pytest.mark.parametrize("temperature", [1e-6, 1e-3, 1e3, 1e6])
+def test_extreme_temperatures(q, temperature):
+    """Logits over 1e-6 reach 1e7, where a row is its largest logit alone: differences are taken first, and rounded three times
+    (the difference, 1 / t, their product) beside what holds at ordinary temperatures."""
+    x, _ = _rows(5, 3001, BF16, 51)
+    x[3] = torch.where(torch.arange(3001, device=DEV) % 2 == 0, x[3], -torch.inf)
+    ids, top, _ = _teacher(x.nan_to_num(neginf=-9.0), 12, 52, 1.0, False)
+    ids[3] = ids[3] // 2 * 2
+    grad = torch.ones(5, device=DEV)
+    loss, stats, ref = _oracle(x, ids, top, None, temperature)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got, got_stats = q.distill_topk(x, ids, top, temperature=temperature, dev_status=st)
+    again, d = q.distill_topk_grad(x, ids, top, grad, temperature=temperature, dev_status=st)
+    d2 = q.distill_topk_backward(x, ids, top, got_stats, grad, temperature=temperature, dev_status=st)
+    # of a loss sum p (ln p - ln q) every logarithm is rounded by itself: 3 EPS of (y - y_max) / t and (x - x_max) / t each
+    _close(got, loss, 2 * (LSE + P) + 8 * EPS * np.abs(loss), "loss")
+    _close(again, loss, 2 * (LSE + P) + 8 * EPS * np.abs(loss), "loss with its gradient")
+    _close(got_stats, stats, LSE + 3 * EPS * np.abs(stats), "stats")
+    # q and p each within LSE + P and what 3 EPS of an exponent that still counts (below 100) make of them
+    scale = (LSE + P + 3 * EPS * 100) * 2 / temperature
+    _close(d, ref, scale + np.abs(ref) * 2 ** -8, "gradient")
+    if temperature >= 1e-3:  # (below, a known log-sum-exp of 1e7 is rounded to whole numbers)
+        known = EPS * np.abs(stats[:, :1]) * 2 / temperature
+        _close(d2, ref, scale + 2 * known + np.abs(ref) * 2 ** -8, "backward")
+    assert q.get_last_device_status(st) == 0

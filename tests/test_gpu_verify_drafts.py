@@ -331,3 +331,18 @@ def test_refusals_are_seen_in_time(q):
         for b in range(n + 1):
             assert torch.equal(tokens[b, :b + 1].long(), best[b, :b + 1]) and torch.all(tokens[b, b + 1:] == -1)
     assert q.get_last_device_status(st) == 0
+
+
+@pytest.mark.parametrize("form", ["model", "lookup"])
+@pytest.mark.parametrize("temperature", [1e-6, 1e-3, 1e3, 1e6])
+def test_extreme_temperatures(q, form, temperature):
+    """Near 0 the likeliest token, as if greedy; far above nearly uniform. A log-probability is (x - x_max) / t - ln s: 3 EPS of
+    the first more than at ordinary temperatures, which `_check` grants of the whole."""
+    s = _case([3, 0, 5, 2] * 3, 3001, BF16, form, 61, temperature=1.0, spread=0.2)
+    s["temperature"] = temperature
+    _check(q, s, enough=0.7)
+    if temperature == 1e-6 and form == "lookup":  # (a model's draft is taken by p / q, however unlikely both are)
+        tokens, _, _ = _run(q, s)
+        used, rows = tokens >= 0, s["target"].float()
+        # (an exponential noise of 1e-20 at another token cannot make up for e^-7000)
+        assert torch.equal(rows[used].gather(1, tokens[used].long()[:, None])[:, 0], rows[used].amax(-1))
