@@ -78,30 +78,6 @@ __device__ __forceinline__ uint64_t candidate(float score, int v) {
   return static_cast<uint64_t>(__float_as_uint(score)) << 32 | (kAll - static_cast<uint32_t>(v));
 }
 
-// Elements e .. e + kPer of a row, as granules if they are aligned, one by one if not.
-template <class E>
-__device__ __forceinline__ void load_block(const E* row, int e, float (&x)[kPer<E>]) {
-  if ((reinterpret_cast<uintptr_t>(row + e) & 15u) == 0) {
-    unpack(__ldg(reinterpret_cast<const uint4*>(row + e)), x);
-  } else {
-#pragma unroll
-    for (int u = 0; u < kPer<E>; ++u) x[u] = to_f32(__ldg(row + e + u));
-  }
-}
-template <int N>
-__device__ __forceinline__ void load_noise(const float* row, int e, float (&x)[N]) {
-  if ((reinterpret_cast<uintptr_t>(row + e) & 15u) == 0) {
-#pragma unroll
-    for (int u = 0; u < N; u += 4) {
-      const float4 f = __ldcs(reinterpret_cast<const float4*>(row + e + u));
-      x[u] = f.x, x[u + 1] = f.y, x[u + 2] = f.z, x[u + 3] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int u = 0; u < N; ++u) x[u] = __ldcs(row + e + u);
-  }
-}
-
 // Part `rank` of `parts` of a row's granules: its whole ones, and the row's cut ones if they are here (-1: not).
 template <class E>
 struct Span {
@@ -162,15 +138,14 @@ __device__ __forceinline__ RowSum merge_parts(RowSum x, Scale c, int V) {
   x.m = sum.m, x.s = sum.s;
   return x;
 }
-template <Form F>
-__device__ __forceinline__ RowSum row_sum(const RowSum* parts_of, int parts, Scale c, int V) {
+__device__ __forceinline__ RowSum part_of_row(const RowSum* parts_of, int parts, int V) {  // a lane each
   const int lane = threadIdx.x & 31;
   RowSum x{-INFINITY, 0.0f, -INFINITY, V};
   if (lane < parts) {
     const float4 f = __ldcg(reinterpret_cast<const float4*>(parts_of + lane));
     x = RowSum{f.x, f.y, f.z, __float_as_int(f.w)};
   }
-  return merge_parts<F>(x, c, V);
+  return x;
 }
 
 // Whether a draft is taken, from the sums of its place and its logits.
@@ -378,30 +353,36 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
     return false;
   };
   auto finish = [&](const Where& w, const RowSum* of_warps) {
+    const int64_t row = w.first + w.b + w.place, draft = w.first + w.place;
+    const bool decided = w.place < w.usable;  // by a draft
+    int drafted = 0;
+    float u = 0.0f;
+    if (decided) {
+      drafted = __ldg(a.drafts + draft);
+      if (!kGreedy) u = __ldg(a.uniforms + draft);
+    }
     RowSum x{-INFINITY, 0.0f, -INFINITY, V};
     if (lane < kWarps) x = of_warps[lane];
     x = merge_parts<F>(x, c, V);
-    const int64_t row = w.first + w.b + w.place;
     int before = 0;
     if (lane == 0) {
-      const int64_t i = w.which ? a.T + a.B + w.first + w.place : row;
+      const int64_t i = w.which ? a.T + a.B + draft : row;
       __stcg(reinterpret_cast<float4*>(at.sums + i * parts + w.rank), make_float4(x.m, x.s, x.largest, __int_as_float(x.arg)));
-      if (w.place < w.usable)
-        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(at.summed + row) : "memory");
+      if (decided) asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(at.summed + row) : "memory");
     }
     before = __shfl_sync(kAll, before, 0);
-    if (w.place >= w.usable || before != kRows * parts - 1) return;
+    if (!decided || before != kRows * parts - 1) return;
     __syncwarp();
-    const int drafted = __ldg(a.drafts + w.first + w.place);
-    const float u = kGreedy ? 0.0f : __ldg(a.uniforms + w.first + w.place);
-    const RowSum p = row_sum<F>(at.sums + row * parts, parts, c, V);
-    RowSum q{};
+    // All that is loaded, and then the two joins: others wait for what is decided here.
+    RowSum p = part_of_row(at.sums + row * parts, parts, V), q{};
     float dp = 0.0f, dq = 0.0f;
     if (!kGreedy) dp = to_f32(__ldg(static_cast<const E*>(a.target) + row * a.ld_target + drafted));
     if constexpr (kModel) {
-      q = row_sum<F>(at.sums + (a.T + a.B + w.first + w.place) * parts, parts, c, V);
-      dq = to_f32(__ldg(static_cast<const E*>(a.draft) + (w.first + w.place) * a.ld_draft + drafted));
+      q = part_of_row(at.sums + (a.T + a.B + draft) * parts, parts, V);
+      dq = to_f32(__ldg(static_cast<const E*>(a.draft) + draft * a.ld_draft + drafted));
     }
+    p = merge_parts<F>(p, c, V);
+    if constexpr (kModel) q = merge_parts<F>(q, c, V);
     if (!taken_by<F>(p, q, drafted, u, dp, dq, c) && lane == 0) atomicMin(&at.states[w.b].needed, w.place + 1);
   };
   Where now{}, then{}, last{};
@@ -442,10 +423,12 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
   // The places up to the refusal, a warp each (other CTAs: that one alone).
   for (int i = rank == 0 ? warp : taken + warp; i <= taken; i += kWarps) {
     const int drafted = i < taken ? __ldg(a.drafts + s.first + i) : 0;
+    RowSum p = part_of_row(from.sums + (s.first + b + i) * sum_parts, sum_parts, V), q{-INFINITY, 0.0f, 0.0f, 0};
+    if (kModel && i < n) q = part_of_row(from.sums + (a.T + a.B + s.first + i) * sum_parts, sum_parts, V);
     const float x = to_f32(__ldg(s.target + i * a.ld_target + drafted));
-    const RowSum p = row_sum<F>(from.sums + (s.first + b + i) * sum_parts, sum_parts, c, V);
-    RowSum q{0.0f, 1.0f, 0.0f, 0};
-    if (kModel && i < n) q = row_sum<F>(from.sums + (a.T + a.B + s.first + i) * sum_parts, sum_parts, c, V);
+    p = merge_parts<F>(p, c, V);
+    if (kModel && i < n) q = merge_parts<F>(q, c, V);
+    else q = RowSum{0.0f, 1.0f, 0.0f, 0};
     if (lane != 0) continue;
     auto bad = [](const RowSum& r) { return !(fabsf(r.m) < INFINITY) || !(r.s < INFINITY); };
     if (bad(p) || bad(q)) flag(a.status, QRR_DEV_NONFINITE);
@@ -483,32 +466,16 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
       if (v == drafted && !kModel && !whole_p) r = 0.0f;
       return r / e;
     };
-    // f(granule, its logits, the other row's, its noise) of this thread's granules. Elements beside the row are -inf with
-    // noise 1.
-    auto each_of = [&](int w0, int w1, auto f) {  // of the whole granules w0 .. w1 - 1, and the cut ones
-      auto cut = [&](int i) {
-        float x[N], y[N], z[N];
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-          const int v = i * N - lead + u;
-          const bool in = v >= 0 && v < V;
-          x[u] = in ? to_f32(row[v]) : -INFINITY;
-          y[u] = in && minus ? to_f32(other[v]) : -INFINITY;
-          z[u] = in ? noise[v] : 1.0f;
-        }
-        f(i, x, y, z);
+    // f(token) of this thread's part of the span: for looks that are rare, so by element, with no arrays that loops index.
+    auto each = [&](auto f) {
+      auto granule = [&](int i) {
+#pragma unroll 1
+        for (int v = max(i * N - lead, 0); v < min(i * N - lead + N, V); ++v) f(v);
       };
-      if (tid == 0 && span.head >= 0) cut(0);
-      for (int i = w0 + tid; i < w1; i += kThreads) {
-        float x[N], y[N], z[N];
-        load_noise(noise, i * N - lead, z);
-        unpack(__ldg(span.granules() + i), x);
-        if (minus) load_block(other, i * N - lead, y);
-        f(i, x, y, z);
-      }
-      if (tid == kThreads - 1 && span.tail >= 0) cut(span.tail);
+      if (tid == 0 && span.head >= 0) granule(0);
+      for (int i = span.w0 + tid; i < span.w1; i += kThreads) granule(i);
+      if (tid == kThreads - 1 && span.tail >= 0) granule(span.tail);
     };
-    auto each = [&](auto f) { each_of(span.w0, span.w1, f); };
     // An upper bound of max(p - q, 0) / e by the hardware's exponentials and reciprocal, within kSlack of p and q. A thread
     // keeps the best granule by it, and how good the second is.
     constexpr float kSlack = 0x1p-16f;
@@ -583,7 +550,21 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
                        (!minus || (reinterpret_cast<uintptr_t>(other + e0) & 15u) == 0);
     if (alike) bounds(std::true_type{});
     else bounds(std::false_type{});
-    each_of(0, 0, bound);
+    // The cut granules: -inf beside the row, with noise 1.
+    auto bound_cut = [&](int i) {
+      float x[N], y[N], z[N];
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int v = i * N - lead + u;
+        const bool in = v >= 0 && v < V;
+        x[u] = in ? to_f32(row[v]) : -INFINITY;
+        y[u] = in && minus ? to_f32(other[v]) : -INFINITY;
+        z[u] = in ? noise[v] : 1.0f;
+      }
+      bound(i, x, y, z);
+    };
+    if (tid == 0 && span.head >= 0) bound_cut(0);
+    if (tid == kThreads - 1 && span.tail >= 0) bound_cut(span.tail);
     // The best granule's score is what others have to reach by their bounds.
     float best_score = 0.0f;
     int best_at = 0;
@@ -607,15 +588,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     const float reached = warp_max(scores[min(lane, kWarps - 1)]);
     const bool several = at >= 0 && second >= reached && second > 0.0f;
     look(at >= 0 && upper >= reached && !first && !several);
-    if (several) {
-      each([&](int i, const float(&x)[N], const float(&y)[N], const float(&z)[N]) {
-#pragma unroll 1
-        for (int u = 0; u < N; ++u) {
-          const int v = i * N - lead + u;
-          if (v >= 0 && v < V) take(score(x[u], y[u], z[u], v, false), v);
-        }
-      });
-    }
+    if (several) each([&](int v) { take(score(to_f32(row[v]), minus ? to_f32(other[v]) : 0.0f, noise[v], v, false), v); });
     uint64_t c_left = best_score > 0.0f ? candidate(best_score, best_at) : 0;
     // The best of all parts, in every thread.
     auto best_of_all = [&](uint64_t mine, int round) {
@@ -637,13 +610,7 @@ __global__ void __launch_bounds__(kDrawThreads, 2) verify_draw_kernel(const Veri
     uint64_t found = best_of_all(c_left, 0);
     if (found == 0 && refused) {  // nothing is left of p: from p itself
       best_score = 0.0f;
-      each([&](int i, const float(&x)[N], const float(&)[N], const float(&z)[N]) {
-#pragma unroll 1
-        for (int u = 0; u < N; ++u) {
-          const int v = i * N - lead + u;
-          if (v >= 0 && v < V) take(score(x[u], 0.0f, z[u], v, true), v);
-        }
-      });
+      each([&](int v) { take(score(to_f32(row[v]), 0.0f, noise[v], v, true), v); });
       found = best_of_all(best_score > 0.0f ? candidate(best_score, best_at) : 0, 1);
     }
     if (found) token = static_cast<int>(kAll - static_cast<uint32_t>(found));
