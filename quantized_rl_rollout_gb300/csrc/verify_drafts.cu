@@ -148,6 +148,13 @@ __device__ __forceinline__ RowSum part_of_row(const RowSum* parts_of, int parts,
   return x;
 }
 
+// The base-2 logarithm of p / q where a reference is far: what a logit has above it is taken first, as the numbers
+// themselves have no digits for the difference.
+__device__ __noinline__ float far_apart(RowSum p, RowSum q, float dp, float dq, Scale c) {
+  const Ref at(p.m, c), at_q(q.m, c);
+  return ((dp - at.m) - (dq - at_q.m)) * c + (at.offset(c) - at_q.offset(c)) - (log2f(p.s) - log2f(q.s));
+}
+
 // Whether a draft is taken, from the sums of its place and its logits.
 template <Form F>
 __device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float u, float dp, float dq, Scale c) {
@@ -160,7 +167,7 @@ __device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float 
   const Ref at_q(q.m, c);
   float l;
   if (at.far || at_q.far) {
-    l = ((dp - at.m) - (dq - at_q.m)) * c - (log2f(p.s) - log2f(q.s));
+    l = far_apart(p, q, dp, dq, c);
   } else {
     const Log2 lp(at, p.s), lq(at_q, q.s);
     l = c.exponent(dp - dq, lp.whole - lq.whole) - (lp.part - lq.part);
