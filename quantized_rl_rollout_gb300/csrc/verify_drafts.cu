@@ -161,7 +161,12 @@ __device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float 
   if constexpr (F == Form::kGreedy) return drafted == p.arg;
   p = sane(p);
   const Ref at(p.m, c);
-  if constexpr (F == Form::kLookup) return u < expf(ln_share(dp, at, p.s, Log2(at, p.s), c));
+  // 0 q < p as p > 0, though p / q may be below fp32's range. (NaN: refused.)
+  auto above = [&](float l, float p_by_q) { return u > 0.0f ? u < p_by_q : dp > -INFINITY && l == l; };
+  if constexpr (F == Form::kLookup) {
+    const float l = ln_share(dp, at, p.s, Log2(at, p.s), c);
+    return above(l, expf(l));
+  }
   // u q < p as u < 2^{c (x_p - x_q) - (r_p - r_q) - (log2 s_p - log2 s_q)}
   q = sane(q);
   const Ref at_q(q.m, c);
@@ -172,7 +177,7 @@ __device__ __forceinline__ bool taken_by(RowSum p, RowSum q, int drafted, float 
     const Log2 lp(at, p.s), lq(at_q, q.s);
     l = c.exponent(dp - dq, lp.whole - lq.whole) - (lp.part - lq.part);
   }
-  return u < exp2f(l);
+  return above(l, exp2f(l));
 }
 
 // Checks offsets and drafts, a warp a sequence, and sets up the workspace.

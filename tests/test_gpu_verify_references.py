@@ -68,3 +68,20 @@ def test_rows_across_the_edge(q, form, temperature, sign):  # noqa: F811
     u = torch.rand(n, generator=g) * (1.0 if form == "model" else 2.0 / v)
     s = _given(target, draft if form == "model" else None, drafts, u, noise, temperature)
     _check(q, s, enough=0.6)
+
+
+@pytest.mark.parametrize("form", ["model", "lookup"])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("temperature", [1e-3, 1.0])
+def test_uniforms_of_zero(q, form, dtype, temperature):  # noqa: F811
+    """0 q < p takes every draft that the target does not rule out, however unlikely: p / q down to e^-4000 here."""
+    g = torch.Generator().manual_seed(3)
+    n, v = 12, 500
+    target, draft = torch.randn(2 * n, v, generator=g).to(dtype), torch.randn(n, v, generator=g).to(dtype)
+    target[::2, 17] = -4.0 if temperature < 1 else -300.0
+    draft[:, 17] = 5.0
+    target[4::8, 17] = -torch.inf
+    noise = torch.empty(n, v).exponential_(generator=g).clamp(min=1e-3)
+    s = _given(target, draft if form == "model" else None, [17] * n, torch.zeros(n), noise, temperature)
+    _, accepted, _ = _check(q, s, enough=0.7)
+    assert accepted.tolist() == [0 if b % 4 == 2 else 1 for b in range(n)]
