@@ -132,11 +132,19 @@ struct Lse {
     low = fmaf(lse, kHigh, -high) + lse * kLow;
   }
   __device__ __forceinline__ bool small(float y) const { return fabsf(lse) < 1e30f && fabsf(y) < 1e30f; }
-  // e^{y / t - lse}
+  // The base-2 logarithm of e^{y / t - lse}, and the number.
+  __device__ __forceinline__ Two exponent(float y, Scale c) const {
+    const float h = __fmul_rn(y, c);
+    return Two{h - high, fmaf(y, c, -h) + (y * c.lo - low)};
+  }
   __device__ __forceinline__ Two share(float y, Scale c) const {
     if (!small(y)) return Two{expf(fmaf(y, c.inv_t, -lse)), 0.0f};
-    const float h = __fmul_rn(y, c);
-    return pow2(h - high, fmaf(y, c, -h) + (y * c.lo - low));
+    const Two l = exponent(y, c);
+    return pow2(l.high, l.low);
+  }
+  __device__ __forceinline__ float ln_share(float y, Scale c) const {
+    const Two l = exponent(y, c);
+    return small(y) ? (l.high + l.low) * kLn2 : fmaf(y, c.inv_t, -lse);
   }
 };
 
@@ -336,7 +344,7 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
         loss += s.p[j] * (c.exponent(s.y[j] - s.x[j], apart) * kLn2);
         continue;
       }
-      const float ln_p = a.top_lse ? fmaf(s.y[j], inv_t, -y.lse) : ln_share(s.y[j], ref_y, y.y_sum, log2_y, c);
+      const float ln_p = a.top_lse ? teacher_lse.ln_share(s.y[j], c) : ln_share(s.y[j], ref_y, y.y_sum, log2_y, c);
       loss += s.p[j] * (ln_p - ln_share(s.x[j], ref, sum, log2, c));
     }
   loss = warp_sum(loss);
@@ -347,8 +355,9 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
     const Log2 log2_out(ref_out, none ? 1.0f : info.s_out);
     lse_out = none ? -INFINITY : ref_out.far ? ref_out.m * inv_t + logf(info.s_out) : fmaf(log2_out.whole, kLn2, log2_out.part * kLn2);
     if (y.rest > (none ? kDust : 0.0f)) {
-      const float ln_q = none ? -INFINITY : ref.far || ref_out.far ? (ref_out.m - ref.m) * inv_t + logf(info.s_out) - logf(sum)
-                                                                   : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
+      const float ln_q = none ? -INFINITY
+                         : ref.far || ref_out.far ? fmaf(ref_out.above(ref, c), kLn2, logf(info.s_out) - logf(sum))
+                                                  : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
       // Where most is outside the ids for both, ln (p_r / q_r) is that of 1 and little: (1 - mass) / (1 - q at the ids).
       const float q_top = info.s_top >= 0.0f ? info.s_top / sum : 1.0f;
       loss += y.rest * (q_top < 0.5f && y.mass < 0.5f ? log1pf(((q_top - y.mass) - y.mass_low) / (1.0f - q_top)) : logf(y.rest) - ln_q);
