@@ -532,8 +532,8 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
  * in [0, V).  Rows behind a refusal may go unread.  Offsets that descend or
  * leave [0, T] raise QRR_DEV_BAD_INDEX; nothing is written for that sequence,
  * and what is for sequences that share its places is unspecified.
- * Places outside cu[0] .. cu[B] are left as they were.  B <= 2^26, V <= 2^30, T
- * <= 2^30.  Sums are fp32 with the hardware's base-2 exponential, probabilities
+ * Places outside cu[0] .. cu[B] are left as they were.  B <= 2^24, V <= 2^30, T
+ * <= 2^24 (a sequence's places are given out by one CTA).  Sums are fp32 with the hardware's base-2 exponential, probabilities
  * that decide take expf; results do not depend on timing. */
 size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_t dtype);
 qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,

@@ -1015,7 +1015,7 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
 }
 
 size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_t dtype) {
-  if (!is_dtype(dtype) || T < 0 || B < 0 || V < 1 || T > (int64_t{1} << 30) || B > (1 << 26) || V > (int64_t{1} << 30)) return 0;
+  if (!is_dtype(dtype) || T < 0 || B < 0 || V < 1 || T > kMaxDrafts || B > kMaxDrafts || V > (int64_t{1} << 30)) return 0;
   return verify_drafts_ws_bytes(T, B, V, dtype == QRR_DTYPE_FP32);
 }
 
@@ -1028,7 +1028,7 @@ qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* 
   if (!cu && (B == 0 ? T > 0 : T % B != 0)) return QRR_ERR_INVALID_ARG;
   if (temperature != 0.0 && !is_temperature(temperature)) return QRR_ERR_INVALID_ARG;
   const bool greedy = temperature == 0.0;
-  if (T > (int64_t{1} << 30) || B > (1 << 26) || V > (int64_t{1} << 30)) return QRR_ERR_UNSUPPORTED_SHAPE;
+  if (T > kMaxDrafts || B > kMaxDrafts || V > (int64_t{1} << 30)) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (B > 0 && (!target || !tokens || !accepted || !logp)) return QRR_ERR_INVALID_ARG;
   if (B > 0 && T > 0 && (!drafts || (!greedy && !uniforms))) return QRR_ERR_INVALID_ARG;
   if (B > 0 && !greedy && (!noise || ld_noise < 0 || (B > 1 && ld_noise < V))) return QRR_ERR_INVALID_ARG;

@@ -410,6 +410,7 @@ struct VerifyArgs {
   void* workspace;    // verify_drafts_ws_bytes
   int32_t* status;
 };
+constexpr int64_t kMaxDrafts = 1 << 24;  // drafts and sequences of a call
 size_t verify_drafts_ws_bytes(int64_t T, int64_t B, int64_t V, int fp32);
 cudaError_t launch_verify_drafts(VerifyArgs a, cudaStream_t stream);
 

@@ -30,6 +30,7 @@
 
 #include "logits.cuh"
 #include "once_per_device.cuh"
+#include "verify_order.cuh"
 
 namespace qrr {
 
@@ -52,15 +53,17 @@ struct alignas(8) State {
 };
 
 // The workspace: sums of a target row of each place of every sequence, then of each draft row; states; parts that are summed
-// of each place.
+// of each place; the sequence of each place (with offsets, and of places in sequences alone).
 struct Workspace {
   RowSum* sums;
   State* states;
   int* summed;
+  int* owners;
   __host__ __device__ Workspace(const VerifyArgs& a, int parts) {
     sums = static_cast<RowSum*>(a.workspace);
     states = reinterpret_cast<State*>(sums + (2 * a.T + a.B) * parts);
     summed = reinterpret_cast<int*>(states + a.B);
+    owners = summed + (a.T + a.B);
   }
 };
 
@@ -193,9 +196,11 @@ __global__ void __launch_bounds__(256) verify_begin_kernel(const VerifyArgs a, c
     const int d = __ldg(a.drafts + s.first + i);
     if (d < 0 || d >= a.V) usable = min(usable, i);
     to.summed[s.first + b + i] = 0;
+    if (a.cu) to.owners[s.first + b + i] = b;
   }
   usable = __reduce_min_sync(kAll, usable);
   if (lane != 0) return;
+  if (a.cu && s.valid) to.owners[s.first + b + s.given] = b;
   to.states[b] = State{usable, s.valid ? usable + 1 : 0};
   if (!s.valid || (usable < s.given && __ldg(a.drafts + s.first + usable) >= a.V)) flag(a.status, QRR_DEV_BAD_INDEX);
 }
@@ -216,8 +221,8 @@ __device__ __noinline__ Sum sum_again(const Span<E> span, int tid, Scale c) {
   return sum;
 }
 
-// Sums of rows. Task ((place * B + b) * kRows + which) * parts + rank is a part of a row, which: the target's (0) or the
-// draft's (1). A CTA takes the tasks blockIdx.x, blockIdx.x + gridDim.x, .. that are needed: eight warps sum a task's granules
+// Sums of rows. Task (i * kRows + which) * parts + rank is a part of a row, i the place in the order (PlaceOrder), which: the
+// target's (0) or the draft's (1). A CTA takes the tasks blockIdx.x, blockIdx.x + gridDim.x, .. that are needed: eight warps sum a task's granules
 // while one more joins the sums of the task before, decides that place if it is its last part, and looks for the task behind.
 template <class E, Form F>
 __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(const VerifyArgs a, const int parts) {
@@ -243,7 +248,6 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
   for (int b = tid; b < a.B; b += kSumThreads) longest = max(longest, __ldcg(&at.states[b].usable) + 1);
   atomicMax(&most, longest);
   __syncthreads();
-  const int64_t total = static_cast<int64_t>(most) * a.B * kRows * parts;
 
   if (warp < kWarps) {
     __syncthreads();  // the first task
@@ -321,16 +325,26 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(cons
     bool needed;
   };
   const int log_parts = __ffs(parts) - 1;
+  const PlaceOrder order(most, a.B, a.T + a.B);
+  const int64_t total = order.total * kRows * parts;
   int64_t next = blockIdx.x;  // the first task that is not looked at
   auto ask = [&] {            // a lane each
     Candidate x;
-    const int64_t task = next + static_cast<int64_t>(lane) * gridDim.x, row = task >> log_parts, place_b = row / kRows;
+    const int64_t task = next + static_cast<int64_t>(lane) * gridDim.x, row = task >> log_parts, i = row / kRows;
     x.at.rank = static_cast<int>(task & (parts - 1)), x.at.which = static_cast<int>(row % kRows);
-    x.at.place = total <= INT_MAX ? static_cast<int>(static_cast<uint32_t>(place_b) / static_cast<uint32_t>(a.B))
-                                  : static_cast<int>(place_b / a.B);
-    x.at.b = static_cast<int>(place_b - static_cast<int64_t>(x.at.place) * a.B);
-    x.needed = task < total;
+    x.at.place = total <= INT_MAX ? static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(a.B)) : static_cast<int>(i / a.B);
+    x.at.b = static_cast<int>(i - static_cast<int64_t>(x.at.place) * a.B);
     x.at.first = 0, x.at.usable = 0;
+    x.needed = task < total;
+    if (i >= order.by_place && x.needed) {  // by row: rows outside the sequences have no owner, or whatever stood there
+      x.at.b = __ldcg(at.owners + (i - order.by_place));
+      x.needed = x.at.b >= 0 && x.at.b < a.B;
+      if (x.needed) {
+        const int64_t place = i - order.by_place - x.at.b - __ldg(a.cu + x.at.b);
+        x.needed = place >= order.level && place <= a.T;
+        x.at.place = static_cast<int>(place);
+      }
+    }
     if (x.needed) {
       const int2 state = __ldcg(reinterpret_cast<const int2*>(at.states + x.at.b));
       x.at.first = a.cu ? __ldg(a.cu + x.at.b) : x.at.b * (a.T / a.B);
@@ -704,7 +718,7 @@ cudaError_t launch(const VerifyArgs& a, cudaStream_t stream) {
 
 size_t verify_drafts_ws_bytes(int64_t T, int64_t B, int64_t V, int fp32) {
   return static_cast<size_t>(2 * T + B) * sum_parts(V, fp32) * sizeof(RowSum) + static_cast<size_t>(B) * sizeof(State) +
-         static_cast<size_t>(T + B) * sizeof(int);
+         2 * static_cast<size_t>(T + B) * sizeof(int);
 }
 
 cudaError_t launch_verify_drafts(VerifyArgs a, cudaStream_t stream) {
