@@ -441,7 +441,9 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * (with ldd == ld) or lie between its rows; any other overlap is refused.  V * the
  * element's size <= QRR_MAX_LOSS_ROW_BYTES, T <= 2^27.  Logits of -inf are
  * masked out (q = 0); a row of nothing but -inf has q = 0 everywhere.  A row
- * with a NaN or +inf raises QRR_DEV_NONFINITE, its outputs unspecified.
+ * with a NaN or +inf raises QRR_DEV_NONFINITE, its outputs unspecified; stats with
+ * one, top_logits that are NaN or +inf, and without top_lse top_logits that are
+ * all -inf, likewise.
  * Sums are fp32 with the hardware's base-2 exponential (about 2^-22 relative);
  * terms at the ids are within an ulp.  Results do not depend on timing, but on
  * a row's alignment (the order in which its values are added).

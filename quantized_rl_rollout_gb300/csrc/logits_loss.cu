@@ -225,6 +225,35 @@ struct Gradient {
   }
 };
 
+// Whether a NaN or +inf is among logits, from a maximum that a NaN comes through.
+struct NoWatch {
+  __device__ __forceinline__ void add(uint4) {}
+  __device__ __forceinline__ void add(float) {}
+};
+template <class E>
+struct Watch {
+  uint32_t top = sizeof(E) == 2 ? 0xFF80FF80u : 0xFF800000u;  // -inf
+  static __device__ __forceinline__ uint32_t max_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (sizeof(E) == 2) {
+      asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    } else {
+      float f;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)));
+      r = __float_as_uint(f);
+    }
+    return r;
+  }
+  __device__ __forceinline__ void add(uint4 g) { top = max_nan(top, max_nan(max_nan(g.x, g.y), max_nan(g.z, g.w))); }
+  __device__ __forceinline__ void add(float x) {
+    top = max_nan(top, sizeof(E) == 2 ? __float_as_uint(x) | 0xFF80u : __float_as_uint(x));  // (beside it: -inf)
+  }
+  __device__ __forceinline__ bool finite() const {
+    if constexpr (sizeof(E) == 2) return bf16_lo(top) < INFINITY && bf16_hi(top) < INFINITY;
+    else return __uint_as_float(top) < INFINITY;
+  }
+};
+
 // The N elements of two granules from element r on.
 template <class E>
 __device__ __forceinline__ uint4 window(uint4 a, uint4 b, int r) {
@@ -247,8 +276,9 @@ __device__ __forceinline__ uint4 window(uint4 a, uint4 b, int r) {
 
 // The gradient of a part to its row of it, by load(granule), from a whole granule of the logits each. Where the two rows do
 // not start alike, a granule of the gradient comes of two of the logits, the second from the next lane.
-template <int kInFlight, class E, class Load>
-__device__ __forceinline__ void store_gradient(E* out, const Part<E>& part, const Gradient& of, int tid, int threads, Load load) {
+template <int kInFlight, class E, class W, class Load>
+__device__ __forceinline__ void store_gradient(E* out, const Part<E>& part, const Gradient& of, W& watch, int tid, int threads,
+                                               Load load) {
   constexpr int N = kPer<E>;
   const int lead = lead_of(out);
   // Element e0 .. of a granule, inside the part.
@@ -257,9 +287,13 @@ __device__ __forceinline__ void store_gradient(E* out, const Part<E>& part, cons
     unpack(g, x);
 #pragma unroll
     for (int u = 0; u < N; ++u)
-      if (e + u >= part.e0 && e + u < part.e1) out[e + u] = from_f32(of(x[u]), E{});
+      if (e + u >= part.e0 && e + u < part.e1) {
+        watch.add(x[u]);
+        out[e + u] = from_f32(of(x[u]), E{});
+      }
   };
   auto whole = [&](int e, uint4 g) {
+    watch.add(g);
     float x[N];
     unpack(g, x);
     __stcs(reinterpret_cast<uint4*>(out + e), of.block(x));
@@ -464,7 +498,7 @@ __device__ __forceinline__ void conclude_known(const LogitsLossArgs& a, int64_t 
                : lse_out == -INFINITY ? 0.0f
                                       : info.factor * (ex2_approx((lse_out - lse) * kLog2e) - info.teacher.rest) *
                                             known_share(lse_out, c);
-  if (!(info.teacher.mass < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
+  if (!(info.teacher.mass < INFINITY) || !(lse < INFINITY) || !(info.lse_at < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
 }
 
 // Granule g without the marked elements.
@@ -740,7 +774,8 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
 
   if constexpr (kWrites) {
     const uint64_t hint = read_once();
-    store_gradient<Shape<M>::kInFlight>(out, part, Gradient{Ref(info.m_at, c), c, info.scale}, tid, threads,
+    NoWatch none;  // (the sums have seen them all)
+    store_gradient<Shape<M>::kInFlight>(out, part, Gradient{Ref(info.m_at, c), c, info.scale}, none, tid, threads,
                                         [&](int i) { return load_hint(granules + i, hint); });
     __syncthreads();
     store_ids(out, part, slots, info.twice, Ref(info.m, c), c, info.inv_s, info.factor, tid, threads);
@@ -781,8 +816,9 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
   }
   if (tid == 0) part.copy(tile, &loaded);
   part.cut(tid, threads, [&](int i) { tile[i - part.g0] = part.load_cut(i); });
+  Watch<E> watch;
   for (int j = tid; j < k; j += threads)
-    if (part.has(slots.id[j])) slots.x[j] = to_f32(part.row[slots.id[j]]);
+    if (part.has(slots.id[j])) watch.add(slots.x[j] = to_f32(part.row[slots.id[j]]));
   if (warp == 0) {
     const Teacher y = teach(a, top_lse, slots, c, lane);
     if (lane == 0) {
@@ -793,7 +829,8 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
   }
   mbar_wait(&loaded, 0, &abort, a.status);
   __syncthreads();
-  // Slots that name one id find out by writing their numbers to its place, which store_ids fills in the end.
+  // Slots that name one id find out by writing their numbers to its place, which store_ids fills in the end (small numbers, as
+  // `watch` sees them).
   bool twice = false;
   for (int j = tid; j < k; j += threads)
     if (part.has(slots.id[j])) {
@@ -810,7 +847,8 @@ __global__ void __launch_bounds__(kBackwardThreads) logits_backward_kernel(const
 
   const Ref ref = known_ref(info.lse, c);
   const Gradient of{known_ref(info.lse_at, c), c, info.scale};
-  store_gradient<1>(out, part, of, tid, threads, [&](int i) { return tile[i - part.g0]; });
+  store_gradient<1>(out, part, of, watch, tid, threads, [&](int i) { return tile[i - part.g0]; });
+  if (!watch.finite()) flag(a.status, QRR_DEV_NONFINITE);
   __syncthreads();
   store_ids(out, part, slots, twice, ref, c, info.inv_s, info.factor, tid, threads);
 }
