@@ -492,6 +492,8 @@ qrr_status qrr_distill_topk_grad(const void* logits, int32_t dtype, int64_t T, i
  *   dlogits[t][v] = A_t w_t (softmax(logits[t])[v] - [v == tokens[t]])
  * advantages fp32 [T]; w = min(exp(logp - rollout_logp), cap) (cap <= 0: no
  * cap), 1 where rollout_logp is NULL (w is then not written and may be NULL).
+ * A w that is NaN (rollout_logp is, or both are -inf) or +inf raises
+ * QRR_DEV_NONFINITE, and a NaN is not capped.
  * A negative token is padding: logp = w = 0, gradient 0, not read; a token
  * >= V likewise, and raises QRR_DEV_BAD_INDEX.  Rows as above. */
 qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld,

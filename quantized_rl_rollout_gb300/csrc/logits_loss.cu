@@ -432,13 +432,13 @@ __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, con
     float w = 1.0f;
     if (a.rollout_logp) {
       w = expf(lp - info.rollout);
-      if (a.cap > 0.0f) w = fminf(w, a.cap);
+      if (a.cap > 0.0f && w > a.cap) w = a.cap;  // (a NaN stays one)
     }
     factor *= w;
     if (writes && lane == 0) {
       a.logp[t] = lp;
       if (a.w) a.w[t] = w;
-      if (!(fabsf(ref.m) < INFINITY) || !(sum < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
+      if (!(fabsf(ref.m) < INFINITY) || !(sum < INFINITY) || !(w < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
     }
   }
   if (lane == 0) {

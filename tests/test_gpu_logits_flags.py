@@ -95,3 +95,25 @@ def test_teachers_of_nothing(q, status):  # noqa: F811
                  lambda: q.distill_topk_backward(x, ids, top, stats, grad, dev_status=status)):
         assert _flags(q, status, call) == q.DEV_NONFINITE
     _check(q, x, ids, top, lse, 1.0)
+
+
+@pytest.mark.parametrize("cap", [0.0, 1.5])
+def test_weights_without_a_number(q, status, cap):  # noqa: F811
+    """A rollout's log-probability that is NaN, or -inf where the token is masked here too: the weight is NaN, capped or not, and
+    reported; a weight of +inf without a cap as well, and with one it is the cap."""
+    x, _ = _rows(5, 300, BF16, 9)
+    x[2, 11] = -torch.inf
+    tokens = torch.tensor([4, 8, 11, 15, 16], dtype=torch.int32, device=DEV)
+    adv = torch.ones(5, device=DEV)
+    rollout = torch.tensor([-3.0, float("nan"), -torch.inf, -4.0, -5.0], device=DEV)
+    got = {}
+    assert _flags(q, status, lambda: got.update(r=q.token_logprobs_is_grad(x, tokens, adv, rollout, cap, dev_status=status))) == q.DEV_NONFINITE
+    logp, w, d = got["r"]
+    assert torch.isnan(w).tolist() == [False, True, True, False, False]
+    assert torch.isnan(d).any(1).tolist() == [False, True, True, False, False]
+    want = torch.exp(logp.double() - rollout.double())[[0, 3, 4]]
+    want = want.clamp(max=cap) if cap else want
+    assert np.allclose(w.double()[[0, 3, 4]].cpu().numpy(), want.cpu().numpy(), rtol=1e-6, atol=0)
+    rollout = torch.tensor([-3.0, -torch.inf, -3.0, -4.0, -5.0], device=DEV)
+    flags = _flags(q, status, lambda: got.update(r=q.token_logprobs_is_grad(x, tokens, adv, rollout, cap, dev_status=status)))
+    assert flags == (0 if cap else q.DEV_NONFINITE) and float(got["r"][1][1]) == (cap or np.inf)
