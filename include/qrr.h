@@ -450,8 +450,8 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  *
  * Teacher.  top_ids int32 [T][k], top_logits fp32 [T][k], 0 <= k <= 1024: the
  * teacher's logits at k tokens of each row, in any order; a slot with a
- * negative id is unused, an id >= V is unused and raises QRR_DEV_BAD_INDEX, slots
- * that name one id add up.  With temperature t (1e-6 .. 1e6; double, so that a
+ * negative id is unused, an id >= V is unused and raises QRR_DEV_BAD_INDEX; slots
+ * that name one id are one outcome, whose p_j is the sum of theirs.  With temperature t (1e-6 .. 1e6; double, so that a
  * program's 0.8 is what its own formulas take):
  *   q = softmax(logits / t)
  *   top_lse NULL:      p_j = e^{y_j / t} / sum_i e^{y_i / t}

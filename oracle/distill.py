@@ -4,8 +4,8 @@ teacher's top logits, and the policy gradient of the tokens a rollout took.
 Test infrastructure only (see the package docstring).
 
 With x a row of logits, t the temperature, q = softmax(x / t), and the
-teacher's logits y_j at the ids i_j (a negative id is no slot, slots that name
-one id add up):
+teacher's logits y_j at the ids i_j (a negative id is no slot, the p_j of slots
+that name one id add up to one outcome's):
 
 * without the teacher's log-sum-exp: ``p_j = e^{y_j / t} / sum_i e^{y_i / t}``;
 * with it: ``p_j = e^{y_j / t - lse}``, and what is missing, ``p_r = max(0, 1 -
@@ -50,7 +50,9 @@ def row(x: np.ndarray, ids: np.ndarray, y: np.ndarray, lse, temperature: float):
     inside[ids] = True
     outside = total if lse is None else _lse(z[~inside])
     some = p > 0
-    loss = float(np.sum(p[some] * (lnp[some] - lnq[ids[some]])))
+    whole = np.full(z.shape, -np.inf)  # ln of what the teacher gives an id
+    np.logaddexp.at(whole, ids, lnp)
+    loss = float(np.sum(p[some] * (whole[ids[some]] - lnq[ids[some]])))
     grad = q.copy()
     np.add.at(grad, ids, -p)
     if outside == -np.inf and rest <= 2.0 ** -16:

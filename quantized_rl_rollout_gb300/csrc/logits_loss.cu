@@ -6,7 +6,7 @@
 //   with a tail      p_j = e^{y_j / t - lse_teacher}, p_r = 1 - sum_j p_j, q_r = 1 - sum_j q_{i_j},
 //                    L = sum_j p_j (ln p_j - ln q_{i_j}) + p_r (ln p_r - ln q_r)
 //   dL/dx_v = (q_v - p_v) / t; with a tail, outside the ids, e^{x_v / t - lse_r} (q_r - p_r) / t, lse_r the log-sum-exp of
-//   the logits outside. Slots that name one id add up.
+//   the logits outside. Slots that name one id are one outcome: their p_j add up.
 // Policy gradient of token a with advantage A: logp = x_a - lse, w = min(e^{logp - logp_rollout}, cap),
 //   d(-A w logp)/dx_v = A w (q_v - [v = a]), w held fixed: the same form with p_a = 1 and the factor A w.
 //
@@ -26,6 +26,8 @@
 // Measured, rows of 128256 bf16: loss alone, 2048 rows, 77 us (81% of a copy's rate); loss and gradient of 4096, 346 us (83%);
 // policy gradient of 4096, 329 us (87%); 2048 rows' gradient from known log-sum-exps 142 us (98%). What is rare is called
 // with copies of what it needs: closures by reference put the hot loops' variables on the stack (346 us: 388, 329: 351).
+#include <float.h>
+
 #include <algorithm>
 
 #include "logits.cuh"
@@ -109,10 +111,10 @@ struct Slots {
       if (id[i] == id[j]) return false;
     return true;
   }
-  // What the teacher gives the id of slot j, its first.
-  __device__ __forceinline__ float all(int j) const {
+  // What the teacher gives the id of slot j by the slots from `from` on: j if it is the id's first.
+  __device__ __forceinline__ float all(int j, int from) const {
     float sum = 0.0f;
-    for (int i = j; i < k; ++i) sum += id[i] == id[j] ? p[i] : 0.0f;
+    for (int i = from; i < k; ++i) sum += id[i] == id[j] ? p[i] : 0.0f;
     return sum;
   }
 };
@@ -338,7 +340,7 @@ __device__ __forceinline__ void store_ids(E* out, const Part<E>& part, const Slo
                                           float factor, int tid, int threads) {
   for (int j = tid; j < s.k; j += threads) {
     if (!part.has(s.id[j]) || (twice && !s.first(j))) continue;
-    const float p = twice ? s.all(j) : s.p[j];
+    const float p = twice ? s.all(j, j) : s.p[j];
     out[s.id[j]] = from_f32(factor * (ref(s.x[j], c) * inv_s - p), E{});
   }
 }
@@ -357,6 +359,16 @@ struct RowInfo {
   float inv_s, factor;       // and at them
   float lse, lse_at;         // kBackward: known, of m and m_at
 };
+
+// To a row's loss, of slots that share an id: what p ln p of their sum has above the sum of theirs, each slot its part. (Rare, and
+// behind the rest: within it, it puts the hot loops' variables of loss and gradient on the stack, 358 us for 350.)
+__device__ __noinline__ void add_shared_ids(float* loss, const Slots s, int lane) {
+  float more = 0.0f;
+  for (int j = lane; j < s.k; j += 32)
+    if (s.id[j] >= 0 && s.p[j] > 0.0f) more += s.p[j] * logf(fminf(s.all(j, 0) / s.p[j], FLT_MAX));
+  more = warp_sum(more);
+  if (lane == 0) *loss += more;
+}
 
 // The loss of a row, by a warp.
 template <LossMode M>
@@ -780,7 +792,10 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     __syncthreads();
     store_ids(out, part, slots, info.twice, Ref(info.m, c), c, info.inv_s, info.factor, tid, threads);
   }
-  if ((M == LossMode::kLoss || M == LossMode::kGrad) && rank == 0 && warp == warps - 1) write_loss<M>(a, t, slots, info, c, lane);
+  if ((M == LossMode::kLoss || M == LossMode::kGrad) && rank == 0 && warp == warps - 1) {
+    write_loss<M>(a, t, slots, info, c, lane);
+    if (info.twice) add_shared_ids(a.loss + t, slots, lane);
+  }
 }
 
 // ---- the gradient from known log-sum-exps ------------------------------------------
