@@ -460,6 +460,9 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  *                      max(0, 1 - sum_j p_j), is one outcome more, beside q_r,
  *                      the student's probability outside the ids
  *   loss = sum_j p_j (ln p_j - ln q_j) [+ p_r (ln p_r - ln q_r)]
+ * (top_lse is to be of the same row and temperature: one that makes sum_j p_j > 1
+ * is no distribution and its loss no divergence, but gradients are this loss's:
+ * q sum_j p_j - p)
  * (where a row has nothing but -inf outside the ids, q_r = 0, a p_r of up to
  * 2^-16 counts as rounding: 0).
  * A row without a used slot has no teacher: loss 0, gradient 0, not read.

@@ -11,6 +11,8 @@ that name one id add up to one outcome's):
 * with it: ``p_j = e^{y_j / t - lse}``, and what is missing, ``p_r = max(0, 1 -
   sum_j p_j)``, is one outcome more beside the student's probability outside
   the ids, ``q_r``; where that is 0, a ``p_r`` of up to 2^-16 counts as rounding;
+  a log-sum-exp that is too small for its slots makes ``sum_j p_j > 1``, which
+  is taken as given;
 * ``loss = sum_j p_j (ln p_j - ln q_{i_j}) [+ p_r (ln p_r - ln q_r)]`` with
   0 ln 0 = 0; its gradient in the logits.
 
@@ -53,7 +55,7 @@ def row(x: np.ndarray, ids: np.ndarray, y: np.ndarray, lse, temperature: float):
     whole = np.full(z.shape, -np.inf)  # ln of what the teacher gives an id
     np.logaddexp.at(whole, ids, lnp)
     loss = float(np.sum(p[some] * (whole[ids[some]] - lnq[ids[some]])))
-    grad = q.copy()
+    grad = q * (1.0 if lse is None else max(1.0, float(p.sum())))
     np.add.at(grad, ids, -p)
     if outside == -np.inf and rest <= 2.0 ** -16:
         rest = 0.0

@@ -6,7 +6,8 @@
 //   with a tail      p_j = e^{y_j / t - lse_teacher}, p_r = 1 - sum_j p_j, q_r = 1 - sum_j q_{i_j},
 //                    L = sum_j p_j (ln p_j - ln q_{i_j}) + p_r (ln p_r - ln q_r)
 //   dL/dx_v = (q_v - p_v) / t; with a tail, outside the ids, e^{x_v / t - lse_r} (q_r - p_r) / t, lse_r the log-sum-exp of
-//   the logits outside. Slots that name one id are one outcome: their p_j add up.
+//   the logits outside. Slots that name one id are one outcome: their p_j add up. Where all p_j add up to more than 1 (the
+//   teacher's log-sum-exp is not of these slots), q is weighed with that: (q_v sum_j p_j - p_v) / t.
 // Policy gradient of token a with advantage A: logp = x_a - lse, w = min(e^{logp - logp_rollout}, cap),
 //   d(-A w logp)/dx_v = A w (q_v - [v = a]), w held fixed: the same form with p_a = 1 and the factor A w.
 //
@@ -123,6 +124,8 @@ struct Slots {
 // the reference of y_max (without a tail) or lse.
 struct Teacher {
   float mass, mass_low, rest, y_max, y_sum, y_low, lse;
+  // With a tail: 1, or more if the log-sum-exp is not of these slots.
+  __device__ __forceinline__ float all() const { return fmaxf(mass + mass_low, 1.0f); }
 };
 
 // A log-sum-exp in base 2, in two parts.
@@ -356,7 +359,7 @@ struct RowInfo {
   // the ids, -1 if it is not at m
   float m, s, s_low, s_top, m_out, s_out;
   float m_at, scale;         // the gradient outside the ids
-  float inv_s, factor;       // and at them
+  float inv_s, factor;       // and at them (q as it is weighed)
   float lse, lse_at;         // kBackward: known, of m and m_at
 };
 
@@ -457,8 +460,9 @@ __device__ __forceinline__ void conclude(const LogitsLossArgs& a, int64_t t, con
     const float inv_s = 1.0f / sum;
     info.m = all.m, info.s = all.s, info.s_low = low, info.s_top = top, info.m_out = outside.m, info.s_out = outside.s;
     info.m_at = tail ? outside.m : all.m;
-    info.scale = !tail ? factor * inv_s : none ? 0.0f : factor * (q_rest * inv_s - info.teacher.rest) / outside.s;
-    info.inv_s = inv_s;
+    const float all_by_s = tail ? info.teacher.all() * inv_s : inv_s;
+    info.scale = !tail ? factor * inv_s : none ? 0.0f : factor * (q_rest * all_by_s - info.teacher.rest) / outside.s;
+    info.inv_s = all_by_s;
     info.factor = factor;
   }
 }
@@ -505,10 +509,11 @@ __device__ __forceinline__ void conclude_known(const LogitsLossArgs& a, int64_t 
   info.lse = lse;
   info.lse_at = tail ? lse_out : lse;
   info.factor = info.weight * c.inv_t;
-  info.inv_s = known_share(lse, c);
+  const float all = tail ? info.teacher.all() : 1.0f;
+  info.inv_s = known_share(lse, c) * all;
   info.scale = !tail                  ? info.factor * info.inv_s
                : lse_out == -INFINITY ? 0.0f
-                                      : info.factor * (ex2_approx((lse_out - lse) * kLog2e) - info.teacher.rest) *
+                                      : info.factor * (ex2_approx((lse_out - lse) * kLog2e) * all - info.teacher.rest) *
                                             known_share(lse_out, c);
   if (!(info.teacher.mass < INFINITY) || !(lse < INFINITY) || !(info.lse_at < INFINITY)) flag(a.status, QRR_DEV_NONFINITE);
 }

@@ -40,3 +40,36 @@ def test_slots_of_one_id(q, dtype, tail):  # noqa: F811
         top[:, 20:24:2] = -torch.inf
         lse = torch.logsumexp(torch.where(ids >= 0, top.double(), -torch.inf), -1).float() + 0.2 if tail else None
         _check(q, x, ids, top, lse, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+@pytest.mark.parametrize("shift", [-1e-6, -1e-3, -0.4, -1.0])
+def test_probabilities_that_pass_one(q, dtype, temperature, shift):  # noqa: F811
+    """The teacher's log-sum-exp is smaller than that of its slots alone: there is no rest, and the gradient is the loss's."""
+    for t, v, k in ((5, 1203, 20), (2, 60000, 64), (400, 333, 7)):
+        x, _ = _rows(t, v, dtype, v)
+        ids, top, _ = _teacher(x, k, 6, temperature, False)
+        lse = (torch.logsumexp(torch.where(ids >= 0, top.double() / temperature, -torch.inf), -1) + shift).float()
+        _check(q, x, ids, top, lse, temperature)
+
+
+@pytest.mark.parametrize("shift", [-0.4, -1.0])
+def test_their_gradient_is_the_difference(q, shift):  # noqa: F811
+    """As test_gpu_drafted_update.py takes it, of a loss with the teacher's probabilities summing to e^-shift."""
+    g = torch.Generator().manual_seed(3)
+    t, v, k, h = 7, 1500, 40, 0.05
+    x = (2 * torch.randn(t, v, generator=g)).to(DEV)
+    y = x.cpu() + torch.randn(t, v, generator=g)
+    top, ids = torch.topk(y, k, -1)
+    more = dict(top_lse=(torch.logsumexp(top, -1) + shift).to(DEV))
+    top, ids = top.to(DEV), ids.to(torch.int32).to(DEV)
+    d = torch.where(y > y.median(), 1.0, -1.0).to(DEV) * torch.rand(t, v, generator=g).to(DEV)
+    loss, grad = q.distill_topk_grad(x, ids, top, torch.ones(t, device=DEV), **more)
+    sides = [q.distill_topk(x + s * h * d, ids, top, **more)[0].double() for s in (1, -1)]
+    along = (grad.double() * d.double()).sum(-1)
+    size = (grad.abs().double() * d.abs().double()).sum(-1)
+    # a loss is off by (LSE + P) (2 M + loss) at a mass of M = e^-shift, the difference by h^2 / 6 of M + 1 third cumulants below 1
+    m = float(torch.exp(torch.tensor(-shift)))
+    bound = (LSE + P) * (2 * m + loss.double().abs()) / h + h * h / 6 * (m + 1) + (LSE + P) * (2 + size)
+    assert torch.all(((sides[0] - sides[1]) / (2 * h) - along).abs() <= bound)

@@ -1,8 +1,10 @@
 """Pins of the oracle's distillation loss for teachers that are no plain distribution over different ids: slots that name one
 id, and probabilities that pass 1 together."""
 
+import math
 
 import numpy as np
+import pytest
 
 from oracle import distill as d
 
@@ -32,3 +34,20 @@ def test_the_loss_is_never_below_zero():
         x = g.normal(0, 2, 6)
         assert d.row(x, ids, y, None, 1.0)[0] >= 0
         assert d.row(x, ids, y, float(np.logaddexp.reduce(y)) + 0.2, 1.0)[0] >= 0
+
+
+@pytest.mark.parametrize("temperature", [1.0, 2.5])
+def test_gradient_where_the_teacher_passes_one(temperature):
+    """A log-sum-exp that is too small (of another temperature, or of part of the row): the gradient is still the difference."""
+    g = np.random.default_rng(4)
+    for shift in (-1.0, -0.4, -1e-3):
+        x, y, ids = g.normal(0, 2, 8), g.normal(0, 1, 4), g.permutation(8)[:4]
+        lse = float(np.logaddexp.reduce(y / temperature)) + shift
+        loss, _, _, grad = d.row(x, ids, y, lse, temperature)
+        assert math.isfinite(loss)
+        for v in range(8):
+            up, down = x.copy(), x.copy()
+            up[v] += 1e-5
+            down[v] -= 1e-5
+            diff = (d.row(up, ids, y, lse, temperature)[0] - d.row(down, ids, y, lse, temperature)[0]) / 2e-5
+            assert abs(diff - grad[v]) <= 1e-8
