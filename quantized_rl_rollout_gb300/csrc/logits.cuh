@@ -295,11 +295,13 @@ __device__ __forceinline__ uint64_t read_again() {
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
+// (Of memory that the kernel may write: it stays where it stands among stores.)
 __device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t policy) {
   uint4 v;
   asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p), "l"(policy));
+               : "l"(p), "l"(policy)
+               : "memory");
   return v;
 }
 

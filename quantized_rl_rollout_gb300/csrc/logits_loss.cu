@@ -589,7 +589,7 @@ __device__ __noinline__ Sum sum_again(const Part<E> part, const Marked marked, b
     unpack(g, x);
     sum.add_largest(x, max_of(x), c);
   };
-  for (int i = part.whole0() + tid; i < part.whole1(); i += threads) add(i, __ldg(part.granules() + i));
+  for (int i = part.whole0() + tid; i < part.whole1(); i += threads) add(i, part.granules()[i]);
   part.cut(tid, threads, [&](int i) { add(i, part.load_cut(i)); });
   sum.merge_warp(c);
   return sum;
@@ -603,6 +603,8 @@ __host__ __device__ __forceinline__ int skip_bytes(int per, int threads, int in_
 // ---- losses -------------------------------------------------------------------------
 //
 // A CTA takes part blockIdx.x % parts of row blockIdx.x / parts: `per` granules. The parts of a row are a cluster.
+//
+// The gradient may be written over the logits, which are therefore read by plain loads, not by those of constant memory.
 //
 // A gradient reads its row again, so what counts is that it is still in L2: two CTAs of 512 threads an SM with eight
 // granules a thread under way (three and four CTAs of 256 threads: 375 us became 400 and 419 for loss and gradient of 4096 rows).
@@ -685,7 +687,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
     if (g < 0) continue;
     if (marked.mark(g, (id - part.base) % N, j)) info.twice = 1;
     if (tail && g >= w0 && g < w1) {
-      if (j == tid) mine = __ldg(granules + g);
+      if (j == tid) mine = granules[g];
       const int n = (g - w0) / threads, at = n / kInFlight * threads + (g - w0) % threads;
       atomicOr(&skips[at / 4], 1u << (8 * (at % 4) + n % kInFlight));
     }
