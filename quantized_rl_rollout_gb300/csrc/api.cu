@@ -877,11 +877,13 @@ inline bool is_dtype(int32_t d) { return d == QRR_DTYPE_BF16 || d == QRR_DTYPE_F
 inline size_t dtype_bytes(int32_t d) { return d == QRR_DTYPE_FP32 ? 4 : 2; }
 inline bool is_temperature(double t) { return t >= kMinTemperature && t <= kMaxTemperature; }
 
+// Rows of V that do not overlap, in an address space (so that offsets among them can be counted).
+bool is_stride(int64_t T, int64_t V, int64_t ld) { return ld >= (T > 1 ? V : 0) && ld <= (int64_t{1} << 44) / std::max<int64_t>(T, 1); }
+
 // Rows of logits [T][V] with `ld` between them.
 qrr_status check_rows(const void* p, int32_t dtype, int64_t T, int64_t V, int64_t ld) {
   if (T > 0 && !p) return QRR_ERR_INVALID_ARG;
-  if (T > 1 && ld < V) return QRR_ERR_INVALID_ARG;
-  if (ld < 0 || ld > (int64_t{1} << 40)) return QRR_ERR_INVALID_ARG;
+  if (!is_stride(T, V, ld)) return QRR_ERR_INVALID_ARG;
   return reinterpret_cast<uintptr_t>(p) % dtype_bytes(dtype) ? QRR_ERR_MISALIGNED : QRR_OK;
 }
 
@@ -1031,7 +1033,7 @@ qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* 
   if (T > kMaxDrafts || B > kMaxDrafts || V > (int64_t{1} << 30)) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (B > 0 && (!target || !tokens || !accepted || !logp)) return QRR_ERR_INVALID_ARG;
   if (B > 0 && T > 0 && (!drafts || (!greedy && !uniforms))) return QRR_ERR_INVALID_ARG;
-  if (B > 0 && !greedy && (!noise || ld_noise < 0 || (B > 1 && ld_noise < V))) return QRR_ERR_INVALID_ARG;
+  if (B > 0 && !greedy && (!noise || !is_stride(B, V, ld_noise))) return QRR_ERR_INVALID_ARG;
   qrr_status st = check_rows(target, dtype, T + B, V, ld_target);
   if (st != QRR_OK) return st;
   if (draft && !greedy) {

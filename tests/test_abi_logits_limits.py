@@ -2,7 +2,7 @@
 
 import pytest
 
-from .test_abi_logits import FAKE, _verify, qrr  # noqa: F401
+from .test_abi_logits import FAKE, _losses, _policy, _verify, qrr  # noqa: F401
 
 BIG = 1 << 24
 
@@ -19,3 +19,21 @@ def test_verification_of_the_most_it_takes(qrr, monkeypatch):  # noqa: F811
     assert _verify(qrr, T=BIG, B=BIG, cu=FAKE) == 5
     # a part of a row (16 bytes) of each of its rows, a state (8) a sequence, two numbers (4) a place
     assert qrr.lib().qrr_verify_drafts_workspace_bytes(BIG, BIG, 100, 0) == BIG * (3 * 16 + 8 + 2 * 8)
+
+
+@pytest.mark.parametrize("T,ld", [(1 << 27, 1 << 40), (1 << 24, 1 << 39), (3, 1 << 62), (1 << 27, (1 << 37) + 1), (1, 1 << 45)])
+def test_strides_that_leave_the_address_space(qrr, T, ld):  # noqa: F811
+    """Offsets that pass 64 bits, or come near, are refused before they are counted with."""
+    assert _losses(qrr, T=T, ld=ld) == (1, 1, 1) and _losses(qrr, T=T, ldd=ld)[1:] == (1, 1)
+    assert _policy(qrr, T=T, ld=ld) == 1 and _policy(qrr, T=T, ldd=ld) == 1
+    if T <= BIG:
+        assert _verify(qrr, T=T, cu=FAKE, ld=ld) == 1 and _verify(qrr, T=T, cu=FAKE, ld_draft=ld) == 1
+        assert _verify(qrr, T=T, B=T, cu=FAKE, ld_noise=ld) == 1
+
+
+@pytest.mark.parametrize("T,ld", [(1 << 24, 1 << 19), (3, 1 << 40), (1, 0)])
+def test_strides_of_large_buffers(qrr, monkeypatch, T, ld):  # noqa: F811
+    monkeypatch.setenv("QRR_INJECT_FAULT", "cuda")
+    far = 1 << 50
+    assert _losses(qrr, T=T, ld=ld, ldd=ld, dlogits=far) == (5, 5, 5) and _policy(qrr, T=T, ld=ld, ldd=ld, dlogits=far) == 5
+    assert _verify(qrr, T=T, B=T, cu=FAKE, ld=ld or 100, ld_draft=ld, ld_noise=ld) == 5
