@@ -912,7 +912,7 @@ qrr_status check_teacher(const LogitsLossArgs& a) {
   if (a.k < 0 || !is_temperature(a.temperature)) return QRR_ERR_INVALID_ARG;
   if (a.k > kMaxTop) return QRR_ERR_UNSUPPORTED_SHAPE;
   if (a.T > 0 && a.k > 0 && (!a.ids || !a.top)) return QRR_ERR_INVALID_ARG;
-  return aligned4(a.ids) && aligned4(a.top) && aligned4(a.top_lse) ? QRR_OK : QRR_ERR_MISALIGNED;
+  return aligned4(a.ids) && aligned4(a.top) && aligned4(a.top_lse) && aligned4(a.status) ? QRR_OK : QRR_ERR_MISALIGNED;
 }
 
 LogitsLossArgs distill_args(const void* logits, int32_t dtype, int64_t T, int64_t V, int64_t ld, const int32_t* top_ids,
@@ -999,7 +999,8 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
   qrr_status st = check_loss_rows(logits, dtype, T, V, ld);
   if (st != QRR_OK) return st;
   if (T > 0 && (!tokens || !advantages || !logp || (rollout_logp && !w))) return QRR_ERR_INVALID_ARG;
-  if (!aligned4(tokens) || !aligned4(advantages) || !aligned4(rollout_logp) || !aligned4(logp) || !aligned4(w))
+  if (!aligned4(tokens) || !aligned4(advantages) || !aligned4(rollout_logp) || !aligned4(logp) || !aligned4(w) ||
+      !aligned4(dev_status))
     return QRR_ERR_MISALIGNED;
   LogitsLossArgs a = distill_args(logits, dtype, T, V, ld, nullptr, nullptr, 1, nullptr, 1.0f, dev_status);
   a.tokens = tokens;
@@ -1041,7 +1042,7 @@ qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* 
     if (st != QRR_OK) return st;
   }
   if (!aligned4(drafts) || !aligned4(cu) || !aligned4(uniforms) || !aligned4(noise) || !aligned4(tokens) ||
-      !aligned4(accepted) || !aligned4(logp))
+      !aligned4(accepted) || !aligned4(logp) || !aligned4(dev_status))
     return QRR_ERR_MISALIGNED;
   if (B > 0 && (!workspace || workspace_bytes < qrr_verify_drafts_workspace_bytes(T, B, V, dtype))) return QRR_ERR_WORKSPACE;
   if (!aligned16(workspace)) return QRR_ERR_MISALIGNED;

@@ -506,6 +506,15 @@ def _vector(x, n, dtype, name, device):
     return x.data_ptr()
 
 
+def _status(x, device):
+    """Address of a status word (None stays)."""
+    if x is None:
+        return None
+    if x.dtype != torch.int32 or x.numel() < 1 or x.device != device:
+        raise ValueError(f"dev_status must be an int32 tensor on {device}")
+    return x.data_ptr()
+
+
 def _output(x, shape, n, dtype, name, device, stream):
     """(tensor, address) of an output of n values: the caller's, or a new one."""
     if x is None:
@@ -556,7 +565,7 @@ def distill_topk(logits, top_ids, top_logits, top_lse=None, temperature=1.0, los
     teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
     loss, loss_ptr = _output(loss, (t,), t, torch.float32, "loss", dev, stream)
     stats, stats_ptr = _output(stats, (t, 2), 2 * t, torch.float32, "stats", dev, stream)
-    _check(lib().qrr_distill_topk(logits.data_ptr(), *rows, *teacher, loss_ptr, stats_ptr, _ptr(dev_status), _stream(stream)),
+    _check(lib().qrr_distill_topk(logits.data_ptr(), *rows, *teacher, loss_ptr, stats_ptr, _status(dev_status, dev), _stream(stream)),
            "qrr_distill_topk")
     return loss, stats
 
@@ -570,7 +579,7 @@ def distill_topk_backward(logits, top_ids, top_logits, stats, grad, top_lse=None
     teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
     _check(lib().qrr_distill_topk_backward(logits.data_ptr(), *rows, *teacher, _vector(stats, 2 * t, torch.float32, "stats", dev),
                                            _vector(grad, t, torch.float32, "grad", dev), dlogits.data_ptr(), ldd,
-                                           _ptr(dev_status), _stream(stream)), "qrr_distill_topk_backward")
+                                           _status(dev_status, dev), _stream(stream)), "qrr_distill_topk_backward")
     return dlogits
 
 
@@ -583,7 +592,7 @@ def distill_topk_grad(logits, top_ids, top_logits, grad, top_lse=None, temperatu
     teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
     loss, loss_ptr = _output(loss, (t,), t, torch.float32, "loss", dev, stream)
     _check(lib().qrr_distill_topk_grad(logits.data_ptr(), *rows, *teacher, _vector(grad, t, torch.float32, "grad", dev),
-                                       loss_ptr, dlogits.data_ptr(), ldd, _ptr(dev_status),
+                                       loss_ptr, dlogits.data_ptr(), ldd, _status(dev_status, dev),
                                        _stream(stream)), "qrr_distill_topk_grad")
     return loss, dlogits
 
@@ -599,7 +608,7 @@ def token_logprobs_is_grad(logits, tokens, advantages, rollout_logp=None, cap=0.
     _check(lib().qrr_token_logprobs_is_grad(logits.data_ptr(), *rows, _vector(tokens, t, torch.int32, "tokens", dev),
                                             _vector(advantages, t, torch.float32, "advantages", dev),
                                             _vector(rollout_logp, t, torch.float32, "rollout_logp", dev), float(cap),
-                                            logp_ptr, w_ptr, dlogits.data_ptr(), ldd, _ptr(dev_status), _stream(stream)),
+                                            logp_ptr, w_ptr, dlogits.data_ptr(), ldd, _status(dev_status, dev), _stream(stream)),
            "qrr_token_logprobs_is_grad")
     return logp, w, dlogits
 
@@ -638,12 +647,13 @@ def verify_drafts(target, drafts, uniforms=None, noise=None, draft_logits=None, 
     logp, logp_ptr = _output(logp, (rows,), rows, torch.float32, "logp", dev, stream)
     if workspace is None:
         workspace = _workspace(lib().qrr_verify_drafts_workspace_bytes(t, b, v, dtype), dev, stream)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     _check(lib().qrr_verify_drafts(target.data_ptr(), ld_target, _ptr(draft_logits), ld_draft, dtype, t, b, v,
                                    _vector(drafts, t, torch.int32, "drafts", dev), cu_ptr,
                                    _vector(uniforms, t, torch.float32, "uniforms", dev), _ptr(noise), ld_noise,
                                    float(temperature), tokens_ptr, accepted_ptr, logp_ptr, workspace.data_ptr(),
-                                   workspace.numel(),
-                                   _ptr(dev_status), _stream(stream)), "qrr_verify_drafts")
+                                   workspace.numel(), _status(dev_status, dev), _stream(stream)), "qrr_verify_drafts")
     return tokens, accepted, logp
 
 

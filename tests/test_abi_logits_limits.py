@@ -1,8 +1,11 @@
 """Sizes of the calls on rows of logits that are refused, on the host (see test_abi_logits.py)."""
 
-import pytest
+import types
 
-from .test_abi_logits import FAKE, _losses, _policy, _verify, qrr  # noqa: F401
+import pytest
+import torch
+
+from .test_abi_logits import FAKE, _i, _losses, _policy, _t, _verify, binding, qrr  # noqa: F401
 
 BIG = 1 << 24
 
@@ -37,3 +40,34 @@ def test_strides_of_large_buffers(qrr, monkeypatch, T, ld):  # noqa: F811
     far = 1 << 50
     assert _losses(qrr, T=T, ld=ld, ldd=ld, dlogits=far) == (5, 5, 5) and _policy(qrr, T=T, ld=ld, ldd=ld, dlogits=far) == 5
     assert _verify(qrr, T=T, B=T, cu=FAKE, ld=ld or 100, ld_draft=ld, ld_noise=ld) == 5
+
+
+def test_status_words_off_their_alignment(qrr):  # noqa: F811
+    """An atomic there would be a fault of the GPU."""
+    lib, s = qrr.lib(), FAKE + 2
+    head = (FAKE, 0, 3, 100, 100, FAKE, FAKE, 4, None, 1.0)
+    assert lib.qrr_distill_topk(*head, FAKE, FAKE, s, None) == 3
+    assert lib.qrr_distill_topk_backward(*head, FAKE, FAKE, 2 * FAKE, 100, s, None) == 3
+    assert lib.qrr_distill_topk_grad(*head, FAKE, FAKE, 2 * FAKE, 100, s, None) == 3
+    assert lib.qrr_token_logprobs_is_grad(FAKE, 0, 3, 100, 100, FAKE, FAKE, FAKE, 0.0, FAKE, FAKE, 2 * FAKE, 100, s, None) == 3
+    assert lib.qrr_verify_drafts(FAKE, 100, FAKE, 100, 0, 6, 3, 100, FAKE, None, FAKE, FAKE, 100, 1.0, FAKE, FAKE, FAKE, FAKE, 1 << 50,
+                                 s, None) == 3
+
+
+def test_binding_refuses_status_words_and_workspaces(binding):  # noqa: F811
+    qrr, calls = binding
+    x, ids, top, grad = _t(4, 10), _i(4, 3), _t(4, 3), _t(4)
+    other = types.SimpleNamespace(index=1)
+    verify = lambda **more: qrr.verify_drafts(x, _i(3), _t(3), _t(1, 10), **more)  # noqa: E731
+    for status in (_t(1), _t(1, dtype=torch.uint8), _i(0), _t(1, dtype=torch.int32, device=other)):
+        for call in (lambda: qrr.distill_topk(x, ids, top, dev_status=status), lambda: qrr.distill_topk_grad(x, ids, top, grad, dev_status=status),
+                     lambda: qrr.distill_topk_backward(x, ids, top, _t(4, 2), grad, dev_status=status),
+                     lambda: qrr.token_logprobs_is_grad(x, _i(4), grad, dev_status=status), lambda: verify(dev_status=status)):
+            with pytest.raises(ValueError):
+                call()
+    for workspace in (_t(1 << 20, dtype=torch.uint8, device=other), _t(1 << 10, 1 << 10, dtype=torch.uint8, stride=(1 << 11, 1))):
+        with pytest.raises(ValueError):
+            verify(workspace=workspace)
+    assert not calls
+    verify(workspace=_t(1 << 20, dtype=torch.uint8), dev_status=_i(1))
+    assert len(calls) == 1
