@@ -85,3 +85,41 @@ def test_uniforms_of_zero(q, form, dtype, temperature):  # noqa: F811
     s = _given(target, draft if form == "model" else None, [17] * n, torch.zeros(n), noise, temperature)
     _, accepted, _ = _check(q, s, enough=0.7)
     assert accepted.tolist() == [0 if b % 4 == 2 else 1 for b in range(n)]
+
+
+@pytest.mark.parametrize("v", [700, 704])
+def test_same_logits_nearer_than_rounding(q, v):  # noqa: F811
+    """q = p and u the largest below 1: a draft may go either way where rows start unalike, but what is given out holds together,
+    and every log-probability is the oracle's of its token."""
+    s = _case([5] * 12, v, BF16, "model", 7)
+    s["draft_logits"] = s["target"][[i for i in range(72) if i % 6 != 5]].contiguous()
+    s["uniforms"].fill_(1 - 2.0 ** -24)
+    tokens, accepted, logp = (x.cpu().numpy() for x in _run(q, s))
+    tokens, logp, drafts = tokens.reshape(12, 6), logp.reshape(12, 6), s["drafts"].cpu().numpy().reshape(12, 5)
+    target, noise = s["target"].double().cpu().numpy().reshape(12, 6, v), s["noise"].double().cpu().numpy()
+    if v == 704:
+        assert (accepted == 5).all()
+    for b in range(12):
+        n = int(accepted[b])
+        assert 0 <= n <= 5 and tokens[b, :n].tolist() == drafts[b, :n].tolist() and (tokens[b, n + 1:] == -1).all()
+        assert not logp[b, n + 1:].any() and 0 <= tokens[b, n] < v
+        for i in range(n + 1):
+            want = verify.log_softmax(target[b, i])[tokens[b, i]]
+            assert abs(logp[b, i] - want) <= LSE + 3 * EPS * abs(want)
+        if n == 5:  # behind the last draft: by p and the noise
+            score = verify.softmax(target[b, 5]) / noise[b]
+            assert score[tokens[b, 5]] >= score.max() * (1 - NEAR)
+
+
+def test_lookups_follow_the_target(q):  # noqa: F811
+    """The frequencies of looked-up first tokens are p's whatever the drafts are, among them always one token (5 sigma)."""
+    n, v = 20000, 6
+    g = torch.Generator(device=DEV).manual_seed(12)
+    x = torch.tensor([0.3, 1.0, -1.0, 0.7, 0.0, -2.0], device=DEV)
+    p = torch.softmax(x.double(), -1)
+    for drafts in (torch.full((n,), 1), torch.full((n,), 5), torch.arange(n) % v):
+        tokens, _, _ = q.verify_drafts(x.expand(2 * n, v).contiguous(), drafts.to(torch.int32).to(DEV),
+                                       uniforms=torch.rand(n, generator=g, device=DEV),
+                                       noise=torch.empty(n, v, device=DEV).exponential_(generator=g))
+        got = torch.bincount(tokens[::2].long(), minlength=v).double() / n
+        assert torch.all((got - p).abs() <= 5 * torch.sqrt(p * (1 - p) / n))
