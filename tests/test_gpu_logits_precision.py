@@ -51,3 +51,41 @@ def test_losses_and_log_sum_exps(q, dtype, temperature, tail):  # noqa: F811
     assert np.all(off[:, 0] <= OUTSIDE * r + IDS + 2.0 ** -20)
     if tail:
         assert np.all(off[:, 1] <= OUTSIDE + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("temperature", [0.8, 1.0])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("tail", [False, True])
+def test_two_ids_hold_all(q, dtype, temperature, tail):  # noqa: F811
+    """Rows of two ids about 26 t whose errors do not average out: nothing is outside them but what a tail's logarithm is of.
+
+    Off by: the exponentials at the ids, 2^-24; the logarithm's small part, 2^-25; y - x, below 2, over t, 1.25 2^-24; that with the
+    log-sum-exps' difference, 2^-24; the two products and their sum, 2^-24: 2.9e-7.  A tail's logarithm is off by 2.5e-6 as
+    above, times the rest of 0.03.  Mistakes that these bounds have to find, planted in the oracle: exponents of 37
+    rounded once, and a temperature in 32 bits beside a log-sum-exp that is not."""
+    g = torch.Generator().manual_seed(72)
+    t, n, v = temperature, 200, 513
+    x = 4 + torch.randn(n, v, generator=g)
+    ids = torch.stack([torch.randperm(v, generator=g)[:2] for _ in range(n)])
+    x.scatter_(1, ids, 26 * t + 0.5 * torch.randn(n, 2, generator=g).clamp(-2, 2))
+    x = x.to(dtype)
+    top = x.float().gather(1, ids) + t * torch.tensor([0.4, -1.2]) + 0.05 * torch.randn(n, 2, generator=g)
+    lse = (torch.logsumexp(top.double() / t, -1) + 0.03).float() if tail else None
+    host = lambda a: None if a is None else a.double().numpy()  # noqa: E731
+
+    def of(scaled, temperature=1.0, y=host(top) / t):
+        return distill.distill(scaled, ids.numpy(), y, host(lse), temperature)[0]
+
+    loss = of(host(x) / t)
+    bound = np.full(n, 2.9e-7 + (OUTSIDE * 0.03 if tail else 0.0))
+    once = (x.float() * np.float32(math.log2(math.e) / t)).double().numpy() * math.log(2)
+    assert (np.abs(of(once) - loss) > bound).sum() >= 5
+    if tail and t != 1.0:
+        t32 = float(np.float32(t))
+        assert (np.abs(of(host(x) / t32, y=host(top) / t32) - loss) > bound).sum() >= 5
+    x, ids_, top, lse_ = x.to(DEV), ids.to(torch.int32).to(DEV), top.to(DEV), None if lse is None else lse.to(DEV)
+    more = dict(top_lse=lse_, temperature=t)
+    got, _ = q.distill_topk(x, ids_, top, **more)
+    again, _ = q.distill_topk_grad(x, ids_, top, torch.ones(n, device=DEV), **more)
+    for a in (got, again):
+        assert np.all(np.abs(a.double().cpu().numpy() - loss) <= bound)
