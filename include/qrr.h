@@ -446,7 +446,9 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * all -inf, likewise.
  * Sums are fp32 with the hardware's base-2 exponential (about 2^-22 relative);
  * terms at the ids are within an ulp.  Results do not depend on timing, but on
- * a row's alignment (the order in which its values are added).
+ * the order in which a row's values are added, which goes by its alignment, by the
+ * rows of the call and by the device's SMs: a row's last bits differ between a
+ * batch and its parts.
  *
  * Teacher.  top_ids int32 [T][k], top_logits fp32 [T][k], 0 <= k <= 1024: the
  * teacher's logits at k tokens of each row, in any order; a slot with a
@@ -471,7 +473,10 @@ qrr_status qrr_token_logprobs_is(const void* logits, int64_t T, int64_t V, const
  * / t, that of the logits outside the ids; without top_lse the first again).
  * qrr_distill_topk_backward: dlogits = grad[t] dloss/dlogits, from the stats
  * of the forward call with the same arguments.  (q is taken from the fp32
- * log-sum-exp: its rounding is a relative error of q.)
+ * log-sum-exp: its rounding, 2^-24 |lse|, is a relative error of q.  Where |lse|
+ * passes 2^16 or so, as logits over a temperature of 1e-4 do, that is more than a
+ * bf16's own, and from 2^23 on q has no digits: qrr_distill_topk_grad has no such
+ * limit.)
  * qrr_distill_topk_grad: loss and dlogits at once, where grad [T] (a weight a
  * row) is known before the loss: a row is read from memory once (the second
  * time it comes from L2 mostly). */
@@ -493,6 +498,8 @@ qrr_status qrr_distill_topk_grad(const void* logits, int32_t dtype, int64_t T, i
 /* qrr_token_logprobs_is_grad: qrr_token_logprobs_is and the gradient of
  * -sum_t A_t w_t logp_t at once, w held fixed:
  *   dlogits[t][v] = A_t w_t (softmax(logits[t])[v] - [v == tokens[t]])
+ * at temperature 1: the log-probabilities of a rollout at another one are of another
+ * distribution (its logits over t, whose gradient is to be divided by t again).
  * advantages fp32 [T]; w = min(exp(logp - rollout_logp), cap) (cap <= 0: no
  * cap), 1 where rollout_logp is NULL (w is then not written and may be NULL).
  * A w that is NaN (rollout_logp is, or both are -inf) or +inf raises
@@ -541,7 +548,8 @@ qrr_status qrr_token_logprobs_is_grad(const void* logits, int32_t dtype, int64_t
  * and what is for sequences that share its places is unspecified.
  * Places outside cu[0] .. cu[B] are left as they were.  B <= 2^24, V <= 2^30, T
  * <= 2^24 (a sequence's places are given out by one CTA).  Sums are fp32 with the hardware's base-2 exponential, probabilities
- * that decide take expf; results do not depend on timing. */
+ * that decide take expf; results do not depend on timing, nor a sequence's on the
+ * others, but on its rows' alignment. */
 size_t qrr_verify_drafts_workspace_bytes(int64_t T, int32_t B, int64_t V, int32_t dtype);
 qrr_status qrr_verify_drafts(const void* target, int64_t ld_target, const void* draft, int64_t ld_draft, int32_t dtype,
                              int64_t T, int32_t B, int64_t V, const int32_t* drafts, const int32_t* cu,

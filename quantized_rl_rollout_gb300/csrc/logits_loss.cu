@@ -24,9 +24,10 @@
 // the hardware made of them), and a logarithm's difference is rounded as the small number that it is. A loss of 0.1 is off by
 // 2.6e-8 so (root mean square; 6.3e-8 without), the log-sum-exps by their own rounding.
 //
-// Measured, rows of 128256 bf16: loss alone, 2048 rows, 77 us (81% of a copy's rate); loss and gradient of 4096, 346 us (83%);
-// policy gradient of 4096, 329 us (87%); 2048 rows' gradient from known log-sum-exps 142 us (98%). What is rare is called
-// with copies of what it needs: closures by reference put the hot loops' variables on the stack (346 us: 388, 329: 351).
+// Measured, rows of 128256 bf16: loss alone, 2048 rows, 77 us (81% of a copy's rate); loss and gradient of 4096, 349 us (82%);
+// policy gradient of 4096, 328 us (88%); 2048 rows' gradient from known log-sum-exps 142 us (98%). What is rare is called
+// with copies of what it needs: closures by reference put the hot loops' variables on the stack (389 us for the 349, 351 for
+// the 328).
 #include <float.h>
 
 #include <algorithm>
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(Shape<M>::kThreads, Shape<M>::kCtas) logits_lo
   // The logits at the ids, and marks of their granules here. No part writes a gradient before all have been here, as sums are
   // joined in between. With a tail, a granule with an id is left to the thread of its first slot: the others have one byte to
   // look at for kInFlight granules. (With a mark for every element, and a byte a granule to look at by the thread that comes to
-  // it: 388 us in the place of 346 for loss and gradient of 4096 rows.)
+  // it: 388 us in the place of 349 for loss and gradient of 4096 rows.)
   const uint4* const granules = part.granules();
   uint4 mine = make_uint4(0, 0, 0, 0);  // of this thread's first slot
   for (int j = tid; j < k; j += threads) {
@@ -893,7 +894,7 @@ cudaError_t launch(const LogitsLossArgs& a, cudaStream_t stream) {
   const int per = (granules + parts - 1) / parts;
   // Threads: few rows are done with the soonest by many; where CTAs follow one another, more of them hide what each does
   // beside its granules, so a thread has 32 of these (16 without a teacher). 3174 rows of 32000 bf16: loss and gradient 93 us,
-  // loss 50, policy gradient 66; with 512 (loss: 256) threads 134, 59 and 81. 300 rows of 32003: 12.6 us, with 256 threads 12.8.
+  // loss 51, policy gradient 66; with 512 (loss: 256) threads 134, 59 and 81. 300 rows of 32003: 12.6 us, with 256 threads 12.8.
   int threads = per >= 2048 ? 512 : per >= 1024 ? 256 : per >= 256 ? 128 : 64;
   if (a.T > 2 * sms) {
     threads = 64;

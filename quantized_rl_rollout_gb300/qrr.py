@@ -586,7 +586,7 @@ def distill_topk_backward(logits, top_ids, top_logits, stats, grad, top_lse=None
 def distill_topk_grad(logits, top_ids, top_logits, grad, top_lse=None, temperature=1.0, loss=None, dlogits=None,
                       dev_status=None, stream=None):
     """(loss, dlogits) of ``distill_topk`` and ``distill_topk_backward`` at once, where the rows' weights ``grad`` are known
-    beforehand: the logits are read once."""
+    beforehand: the logits are read from memory once, and a second time from L2 mostly."""
     rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
     t, dev = rows[1], logits.device
     teacher = _teacher(top_ids, top_logits, top_lse, temperature, t, dev)
@@ -600,7 +600,8 @@ def distill_topk_grad(logits, top_ids, top_logits, grad, top_lse=None, temperatu
 def token_logprobs_is_grad(logits, tokens, advantages, rollout_logp=None, cap=0.0, logp=None, w=None, dlogits=None,
                            dev_status=None, stream=None):
     """(logp, w, dlogits): ``token_logprobs_is`` and the gradient of -sum A w logp in the logits (bf16 or fp32) at once, w
-    held fixed (None, for 1, without ``rollout_logp``); ``dlogits`` may be ``logits`` itself."""
+    held fixed (None, for 1, without ``rollout_logp``); ``dlogits`` may be ``logits`` itself.  At temperature 1: of a rollout at
+    another one, take the logits over it, and the gradient over it again."""
     rows, dlogits, ldd = _loss_rows(logits, dlogits, stream)
     t, dev = rows[1], logits.device
     logp, logp_ptr = _output(logp, (t,), t, torch.float32, "logp", dev, stream)

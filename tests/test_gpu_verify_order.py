@@ -55,3 +55,19 @@ def test_among_bad_offsets_and_padding(q):  # noqa: F811
         rows = int(cu[live]) + live
         assert torch.equal(accepted[:live], want[1][:live]) and accepted[300] > 100
         assert torch.equal(tokens[:rows], want[0][:rows]) and torch.equal(logp[:rows], want[2][:rows])
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_a_sequence_alone(q, form):  # noqa: F811
+    """A sequence's outputs are bit for bit those that it has without the others (of rows that start alike)."""
+    counts, v = [3, 0, 5, 1, 2] * 40, 20000
+    s = _case(counts, v, BF16, form, 4)
+    tokens, accepted, logp = _run(q, s)
+    at = 0
+    for b, n in enumerate(counts[:15]):
+        rows, drafts = slice(at + b, at + b + n + 1), slice(at, at + n)
+        of = lambda x, i: None if x is None else x[i]  # noqa: E731
+        one = q.verify_drafts(s["target"][rows], s["drafts"][drafts], uniforms=of(s["uniforms"], drafts), noise=of(s["noise"], slice(b, b + 1)),
+                              draft_logits=of(s["draft_logits"], drafts), temperature=s["temperature"])
+        assert torch.equal(one[0], tokens[rows]) and int(one[1]) == int(accepted[b]) and torch.equal(one[2], logp[rows])
+        at += n
