@@ -222,9 +222,9 @@ __device__ __noinline__ Sum sum_again(const Span<E> span, int tid, Scale c) {
 }
 
 // Sums of rows. Task (i * kRows + which) * parts + rank is a part of a row, i the place in the order (PlaceOrder), which: the
-// target's (0) or the draft's (1). A CTA takes the tasks blockIdx.x, blockIdx.x + gridDim.x, .. that are needed: eight warps sum a task's granules
-// while one more joins the sums of the task before, decides that place if it is its last part, and looks for the task behind.
-// Four CTAs an SM leave a thread 56 registers; 24 to 52 bytes are spilled.
+// target's (0) or the draft's (1). A CTA takes the tasks blockIdx.x, blockIdx.x + gridDim.x, .. that are needed: eight warps
+// sum a task's granules while one more joins the sums of the task before, decides that place if it is its last part, and
+// looks for the task behind. Four CTAs an SM leave a thread 56 registers; 24 to 52 bytes are spilled.
 template <class E, Form F>
 __global__ void __launch_bounds__(kSumThreads, kSumCtas) verify_sums_kernel(const VerifyArgs a, const int parts) {
   constexpr int N = kPer<E>;
