@@ -395,7 +395,9 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
         continue;
       }
       const float ln_p = a.top_lse ? teacher_lse.ln_share(s.y[j], c) : ln_share(s.y[j], ref_y, y.y_sum, log2_y, c);
-      loss += s.p[j] * (ln_p - ln_share(s.x[j], ref, sum, log2, c));
+      // (a share of a logit over t that is beyond fp32's range may be within)
+      if (ref.far || !(fabsf(s.x[j]) < 1e30f)) loss += s.p[j] * (ln_p + logf(sum)) - s.p[j] * (s.x[j] - ref.m) * inv_t;
+      else loss += s.p[j] * (ln_p - ln_share(s.x[j], ref, sum, log2, c));
     }
   loss = warp_sum(loss);
   if (lane != 0) return;
@@ -405,9 +407,11 @@ __device__ __forceinline__ void write_loss(const LogitsLossArgs& a, int64_t t, c
     const Log2 log2_out(ref_out, none ? 1.0f : info.s_out);
     lse_out = none ? -INFINITY : ref_out.far ? ref_out.m * inv_t + logf(info.s_out) : fmaf(log2_out.whole, kLn2, log2_out.part * kLn2);
     if (y.rest > (none ? kDust : 0.0f)) {
-      const float ln_q = none ? -INFINITY
-                         : ref.far || ref_out.far ? fmaf(ref_out.above(ref, c), kLn2, logf(info.s_out) - logf(sum))
-                                                  : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
+      const bool far = ref.far || ref_out.far;
+      const float ln_q = none  ? -INFINITY
+                         : far ? logf(info.s_out) - logf(sum) + (ref.offset(c) - ref_out.offset(c)) * kLn2
+                               : ((log2_out.whole - log2.whole) + (log2_out.part - log2.part)) * kLn2;
+      if (far && !none) loss -= y.rest * (ref_out.m - ref.m) * inv_t;
       // Where most is outside the ids for both, ln (p_r / q_r) is that of 1 and little: (1 - mass) / (1 - q at the ids).
       const float q_top = info.s_top >= 0.0f ? info.s_top / sum : 1.0f;
       loss += y.rest * (q_top < 0.5f && y.mass < 0.5f ? log1pf(((q_top - y.mass) - y.mass_low) / (1.0f - q_top)) : logf(y.rest) - ln_q);
